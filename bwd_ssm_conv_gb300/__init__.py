@@ -10,3 +10,8 @@ from .binding import (  # noqa: F401
     ssm_decode_step, ssm_scan_bwd, ssm_scan_fwd, ssm_scan_status, ssm_scan_workspace_size,
     ssm_status_string,
 )
+from .block import (  # noqa: F401
+    AddNorm, Ckpt8, GatedNorm, ssm_add_norm_bwd, ssm_add_norm_fwd, ssm_ckpt8_load,
+    ssm_ckpt8_save, ssm_ckpt8_wgrad, ssm_ckpt8_wgrad_workspace_size, ssm_gated_norm_bwd,
+    ssm_gated_norm_fwd, ssm_norm_bwd_workspace_size,
+)

@@ -1,0 +1,393 @@
+"""ctypes binding of include/ssm_block.h: the norms before and after the scan and 8-bit
+activation checkpoints.
+
+As in ``binding``: argument marshalling only, every step of the computation runs in the
+library's CUDA kernels on PyTorch's current stream (or ``stream``), and a missing library raises.
+Activations are CUDA tensors [..., cols], float32 or bfloat16, whose last dimension is dense and
+whose rows lie at one stride (a slice of a wider tensor is fine); parameters are contiguous fp32.
+"""
+from __future__ import annotations
+
+import ctypes
+from typing import NamedTuple
+
+import torch
+
+from . import binding
+from .binding import SSM_BF16, SSM_F32, _check
+
+SSM_NORM_FIRST = 1        # gated_norm: norm of y, then the gate
+SSM_WGRAD_ACCUMULATE = 1  # wgrad: add to d_W
+SSM_MAX_NORM_COLS = 32768
+SSM_CKPT8_BLOCK = 32
+
+EXPORTED = ("ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
+            "ssm_norm_bwd_workspace_size", "ssm_ckpt8_save", "ssm_ckpt8_load",
+            "ssm_ckpt8_wgrad_workspace_size", "ssm_ckpt8_wgrad")
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_longlong), ("cols", ctypes.c_int), ("group", ctypes.c_int),
+                ("io", ctypes.c_int), ("res_io", ctypes.c_int), ("flags", ctypes.c_uint),
+                ("eps", ctypes.c_float)]
+
+
+class Ckpt8(NamedTuple):
+    """An activation held in 8 bits: q int8 [..., cols], e uint8 [..., ceil(cols / 32)]; the value
+    is q * 2^(e - 133), NaN where e is 255."""
+    q: torch.Tensor
+    e: torch.Tensor
+
+
+class AddNorm(NamedTuple):
+    out: torch.Tensor
+    res_out: torch.Tensor | None
+    rstd: torch.Tensor | None
+    res8: Ckpt8 | None
+    x8: Ckpt8 | None
+    out8: Ckpt8 | None
+
+
+class GatedNorm(NamedTuple):
+    out: torch.Tensor
+    rstd: torch.Tensor | None
+    y8: Ckpt8 | None
+    z8: Ckpt8 | None
+    out8: Ckpt8 | None
+
+
+_vp, _sz, _i, _u, _ll = (ctypes.c_void_p, ctypes.c_size_t, ctypes.c_int, ctypes.c_uint,
+                         ctypes.c_longlong)
+_L = None
+
+
+def lib():
+    """The loaded library with this header's argument types set (raises if it is missing)."""
+    global _L
+    if _L is None:
+        L = binding.lib()
+        d = ctypes.POINTER(NormDesc)
+        L.ssm_add_norm_fwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp, _ll] +
+                                       [_vp] * 8)
+        L.ssm_add_norm_bwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll] +
+                                       [_vp] * 5 + [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _sz, _vp])
+        L.ssm_gated_norm_fwd.argtypes = [d, _vp, _ll, _vp, _ll, _vp, _vp, _ll] + [_vp] * 8
+        L.ssm_gated_norm_bwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp, _vp,
+                                          _vp, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _sz, _vp])
+        L.ssm_norm_bwd_workspace_size.argtypes = [d, _i]
+        L.ssm_norm_bwd_workspace_size.restype = _sz
+        L.ssm_ckpt8_save.argtypes = [_vp, _ll, _vp, _vp, _ll, _i, _i, _vp]
+        L.ssm_ckpt8_load.argtypes = [_vp, _vp, _vp, _ll, _ll, _i, _i, _vp]
+        L.ssm_ckpt8_wgrad_workspace_size.argtypes = [_ll, _i, _i, _i]
+        L.ssm_ckpt8_wgrad_workspace_size.restype = _sz
+        L.ssm_ckpt8_wgrad.argtypes = [_vp, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _u, _vp, _sz, _vp]
+        _L = L
+    return _L
+
+
+_IO = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
+
+
+def _io(t: torch.Tensor, name: str) -> int:
+    io = _IO.get(t.dtype)
+    if io is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {t.dtype}")
+    return io
+
+
+def _rows(t, name, shape=None, dtype=None):
+    """(pointer, row stride) of an activation [..., cols]; (None, 0) for None."""
+    if t is None:
+        return None, 0
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    cols = t.shape[-1]
+    if t.is_contiguous():
+        return t.data_ptr(), cols
+    if cols > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    ld, span = None, None  # one stride for all rows: outer dimensions step over whole inner ones
+    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+        if size == 1:
+            continue
+        if ld is None:
+            ld, span = stride, size * stride
+        elif stride != span:
+            raise ValueError(f"{name}'s rows must lie at one stride")
+        else:
+            span *= size
+    if ld is None:
+        ld = cols
+    if ld < cols:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return t.data_ptr(), ld
+
+
+def _f32(t, name, n):
+    """Pointer of a contiguous fp32 tensor of n elements; None for None."""
+    if t is None:
+        return None
+    if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+        raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of {n} elements")
+    return t.data_ptr()
+
+
+def _kept(c, name, shape):
+    """Pointers of a checkpoint of an activation of that shape."""
+    if c is None:
+        return None, None
+    q, e = c
+    eshape = (*shape[:-1], -(-shape[-1] // SSM_CKPT8_BLOCK))
+    if not (q.is_cuda and e.is_cuda and q.dtype == torch.int8 and e.dtype == torch.uint8 and
+            q.is_contiguous() and e.is_contiguous()):
+        raise ValueError(f"{name} must hold contiguous int8 and uint8 CUDA tensors")
+    if tuple(q.shape) != tuple(shape) or tuple(e.shape) != eshape:
+        raise ValueError(f"{name} must hold shapes {tuple(shape)} and {eshape}, got "
+                         f"{tuple(q.shape)} and {tuple(e.shape)}")
+    return q.data_ptr(), e.data_ptr()
+
+
+def _new_ckpt8(shape, device):
+    return Ckpt8(torch.empty(shape, dtype=torch.int8, device=device),
+                 torch.empty(*shape[:-1], -(-shape[-1] // SSM_CKPT8_BLOCK), dtype=torch.uint8,
+                             device=device))
+
+
+def _on(stream, *made):
+    """The call's stream; tensors made here for a stream other than the current one are marked as
+    used there, so that their memory is not given out again before that stream is done."""
+    cur = torch.cuda.current_stream()
+    if stream is None or stream == cur:
+        return cur.cuda_stream
+    for t in made:
+        for u in t if isinstance(t, tuple) else (t,):
+            if u is not None:
+                u.record_stream(stream)
+    return stream.cuda_stream
+
+
+def _workspace(nbytes, device, ws):
+    """(workspace, made here)"""
+    if ws is not None:
+        if not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+            raise ValueError("workspace too small (or not a contiguous CUDA tensor)")
+        return ws, None
+    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+    return ws, ws
+
+
+def _rows_of(shape):
+    n = 1
+    for s in shape[:-1]:
+        n *= s
+    return n
+
+
+# ---- residual add + RMSNorm -----------------------------------------------------------------
+
+def ssm_add_norm_fwd(x, w=None, residual=None, scale=None, eps=1e-5, res_dtype=None, save8=False,
+                     save_x8=False, save_out8=False, want_res=True, want_rstd=True, out=None,
+                     stream=None) -> AddNorm:
+    """s = residual + scale * x; out = w * s / sqrt(mean(s^2) + eps), per row of x [..., cols].
+
+    ``residual`` (and s, returned as ``res_out``) is fp32 or of x's type; without a residual
+    ``res_dtype`` sets that type.  ``save8`` / ``save_x8`` / ``save_out8``: also keep s, x or out as
+    8-bit checkpoints (for ssm_add_norm_bwd, its d_scale, and the next projection's
+    ssm_ckpt8_wgrad).  ``out`` = (out, res_out), preallocated, optional."""
+    io = _io(x, "x")
+    shape, dev = x.shape, x.device
+    cols = shape[-1]
+    rdt = residual.dtype if residual is not None else (res_dtype or x.dtype)
+    if out is None:
+        o = torch.empty(shape, dtype=x.dtype, device=dev)
+        res = torch.empty(shape, dtype=rdt, device=dev) if want_res else None
+        made = (o, res)
+    else:
+        o, res = out
+        made = ()
+    rows = _rows_of(shape)
+    rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if want_rstd else None
+    res8 = _new_ckpt8(shape, dev) if save8 else None
+    x8 = _new_ckpt8(shape, dev) if save_x8 else None
+    out8 = _new_ckpt8(shape, dev) if save_out8 else None
+    d = NormDesc(rows, cols, 0, io, _IO.get(rdt, -1), 0, eps)
+    L = _L or lib()
+    rc = L.ssm_add_norm_fwd(
+        d, *_rows(x, "x"), *_rows(residual, "residual", shape), _f32(scale, "scale", cols),
+        _f32(w, "w", cols), *_rows(o, "out", shape, x.dtype), *_rows(res, "res_out", shape, rdt),
+        None if rstd is None else rstd.data_ptr(), *_kept(res8, "res8", shape),
+        *_kept(x8, "x8", shape), *_kept(out8, "out8", shape),
+        _on(stream, *made, rstd, res8, x8, out8))
+    _check("ssm_add_norm_fwd", rc)
+    return AddNorm(o, res, rstd, res8, x8, out8)
+
+
+def ssm_norm_bwd_workspace_size(rows, cols, sums=1, group=0, io=SSM_BF16, res_io=SSM_F32) -> int:
+    d = NormDesc(rows, cols, group, io, res_io, 0, 1.0)
+    return int(lib().ssm_norm_bwd_workspace_size(d, sums))
+
+
+def ssm_add_norm_bwd(d_out, res, rstd, w=None, d_res_out=None, scale=None, x=None, res_dtype=None,
+                     want_dres=True, want_dx=True, ws=None, out=None, stream=None) -> dict:
+    """Backward of ssm_add_norm_fwd; returns {"d_res", "d_x", "d_w", "d_scale"} (None where not
+    wanted or not applicable).
+
+    ``res``: the forward's res_out, or its 8-bit checkpoint res8.  ``x`` (a tensor or a Ckpt8)
+    is needed for d_scale only.  ``d_res_out``: the gradient that reaches res_out past the norm.
+    The stream's type is that of ``res`` or ``d_res_out``, else ``res_dtype``, else d_out's.
+    ``out`` = a dict of preallocated outputs with the same keys, optional."""
+    io = _io(d_out, "d_out")
+    shape, dev, f32 = d_out.shape, d_out.device, torch.float32
+    cols = shape[-1]
+    res8 = isinstance(res, tuple)
+    rdt = (d_res_out.dtype if d_res_out is not None else
+           res.dtype if not res8 else res_dtype or d_out.dtype)
+    if out is None:
+        g = dict(d_res=torch.empty(shape, dtype=rdt, device=dev) if want_dres else None,
+                 d_x=torch.empty(shape, dtype=d_out.dtype, device=dev) if want_dx else None,
+                 d_w=torch.empty(cols, dtype=f32, device=dev) if w is not None else None,
+                 d_scale=(torch.empty(cols, dtype=f32, device=dev)
+                          if scale is not None and x is not None else None))
+        made = tuple(g.values())
+    else:
+        g, made = out, ()
+    rows = _rows_of(shape)
+    d = NormDesc(rows, cols, 0, io, _IO.get(rdt, -1), 0, 1.0)
+    L = _L or lib()
+    sums = (g["d_w"] is not None) + (g["d_scale"] is not None)
+    wsz = L.ssm_norm_bwd_workspace_size(d, sums) if sums else 0
+    ws, mine = _workspace(wsz, dev, ws)
+    x8 = isinstance(x, tuple)
+    rc = L.ssm_add_norm_bwd(
+        d, *_rows(d_out, "d_out"), *_rows(d_res_out, "d_res_out", shape, rdt),
+        *_rows(None if res8 else res, "res", shape, rdt),
+        *_kept(res if res8 else None, "res", shape),
+        *_rows(None if x8 else x, "x", shape, d_out.dtype), *_kept(x if x8 else None, "x", shape),
+        _f32(rstd, "rstd", rows), _f32(scale, "scale", cols), _f32(w, "w", cols),
+        *_rows(g["d_res"], "d_res", shape, rdt), *_rows(g["d_x"], "d_x", shape, d_out.dtype),
+        _f32(g["d_w"], "d_w", cols), _f32(g["d_scale"], "d_scale", cols), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _on(stream, *made, mine))
+    _check("ssm_add_norm_bwd", rc)
+    return g
+
+
+# ---- gated RMSNorm ----------------------------------------------------------------------------
+
+def ssm_gated_norm_fwd(y, z, w=None, group=0, eps=1e-5, norm_first=False, save8=False,
+                       save_out8=False, want_rstd=True, out=None, stream=None) -> GatedNorm:
+    """Per group of ``group`` columns (0: all) of y, z [..., cols]:
+    out = w * v / sqrt(mean(v^2) + eps) with v = y silu(z), or, with ``norm_first``,
+    out = w * y / sqrt(mean(y^2) + eps) * silu(z).
+
+    ``save8``: keep y and z as 8-bit checkpoints for ssm_gated_norm_bwd; ``save_out8``: keep out
+    for the next projection's ssm_ckpt8_wgrad.  ``out``: preallocated, optional."""
+    io = _io(y, "y")
+    shape, dev = y.shape, y.device
+    cols = shape[-1]
+    o = torch.empty(shape, dtype=y.dtype, device=dev) if out is None else out
+    made = (o,) if out is None else ()
+    groups = cols // group if group else 1
+    rstd = (torch.empty(*shape[:-1], max(groups, 1), dtype=torch.float32, device=dev)
+            if want_rstd else None)
+    y8 = _new_ckpt8(shape, dev) if save8 else None
+    z8 = _new_ckpt8(shape, dev) if save8 else None
+    out8 = _new_ckpt8(shape, dev) if save_out8 else None
+    d = NormDesc(_rows_of(shape), cols, group, io, io, SSM_NORM_FIRST if norm_first else 0, eps)
+    L = _L or lib()
+    rc = L.ssm_gated_norm_fwd(
+        d, *_rows(y, "y"), *_rows(z, "z", shape, y.dtype), _f32(w, "w", cols),
+        *_rows(o, "out", shape, y.dtype), None if rstd is None else rstd.data_ptr(),
+        *_kept(y8, "y8", shape), *_kept(z8, "z8", shape), *_kept(out8, "out8", shape),
+        _on(stream, *made, rstd, y8, z8, out8))
+    _check("ssm_gated_norm_fwd", rc)
+    return GatedNorm(o, rstd, y8, z8, out8)
+
+
+def ssm_gated_norm_bwd(d_out, y, z, rstd, w=None, group=0, norm_first=False, ws=None, out=None,
+                       stream=None) -> dict:
+    """Backward of ssm_gated_norm_fwd; returns {"d_y", "d_z", "d_w"} (d_w None without w).
+
+    ``y`` and ``z``: the forward's inputs, or their 8-bit checkpoints y8 and z8.  ``out`` = a dict
+    of preallocated outputs with the same keys, optional (d_z may be a slice of the gradient of a
+    wider projection)."""
+    io = _io(d_out, "d_out")
+    shape, dev, f32 = d_out.shape, d_out.device, torch.float32
+    cols = shape[-1]
+    if out is None:
+        g = dict(d_y=torch.empty(shape, dtype=d_out.dtype, device=dev),
+                 d_z=torch.empty(shape, dtype=d_out.dtype, device=dev),
+                 d_w=torch.empty(cols, dtype=f32, device=dev) if w is not None else None)
+        made = tuple(g.values())
+    else:
+        g, made = out, ()
+    rows, groups = _rows_of(shape), cols // group if group else 1
+    d = NormDesc(rows, cols, group, io, io, SSM_NORM_FIRST if norm_first else 0, 1.0)
+    L = _L or lib()
+    wsz = L.ssm_norm_bwd_workspace_size(d, 1) if g["d_w"] is not None else 0
+    ws, mine = _workspace(wsz, dev, ws)
+    y8, z8 = isinstance(y, tuple), isinstance(z, tuple)
+    rc = L.ssm_gated_norm_bwd(
+        d, *_rows(d_out, "d_out"), *_rows(None if y8 else y, "y", shape, d_out.dtype),
+        *_kept(y if y8 else None, "y", shape), *_rows(None if z8 else z, "z", shape, d_out.dtype),
+        *_kept(z if z8 else None, "z", shape), _f32(rstd, "rstd", rows * groups),
+        _f32(w, "w", cols), *_rows(g["d_y"], "d_y", shape, d_out.dtype),
+        *_rows(g["d_z"], "d_z", shape, d_out.dtype), _f32(g["d_w"], "d_w", cols), ws.data_ptr(),
+        ws.numel() * ws.element_size(), _on(stream, *made, mine))
+    _check("ssm_gated_norm_bwd", rc)
+    return g
+
+
+# ---- 8-bit activation checkpoints ---------------------------------------------------------------
+
+def ssm_ckpt8_save(x, out=None, stream=None) -> Ckpt8:
+    """x [..., cols] as an 8-bit checkpoint (int8 values, one power-of-two scale per 32 columns)."""
+    io = _io(x, "x")
+    shape = x.shape
+    c = _new_ckpt8(shape, x.device) if out is None else out
+    L = _L or lib()
+    rc = L.ssm_ckpt8_save(*_rows(x, "x"), *_kept(c, "out", shape), _rows_of(shape), shape[-1], io,
+                          _on(stream, c if out is None else None))
+    _check("ssm_ckpt8_save", rc)
+    return c
+
+
+def ssm_ckpt8_load(c, dtype=torch.bfloat16, out=None, stream=None):
+    """The values of a checkpoint, as ``dtype`` (both types hold them exactly)."""
+    shape = c[0].shape
+    o = torch.empty(shape, dtype=dtype, device=c[0].device) if out is None else out
+    L = _L or lib()
+    rc = L.ssm_ckpt8_load(*_kept(c, "c", shape), *_rows(o, "out", shape), _rows_of(shape),
+                          shape[-1], _io(o, "out"), _on(stream, o if out is None else None))
+    _check("ssm_ckpt8_load", rc)
+    return o
+
+
+def ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io=SSM_BF16) -> int:
+    return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io))
+
+
+def ssm_ckpt8_wgrad(g, x8, accumulate=False, ws=None, out=None, stream=None):
+    """The gradient d_W [m][k] (fp32) of a projection y = x W^T from g = dL/dy [..., m] and the
+    8-bit checkpoint x8 of x [..., k]: d_W = sum over rows of g x^T.  ``accumulate`` adds it to
+    ``out``."""
+    io = _io(g, "g")
+    m, k = g.shape[-1], x8[0].shape[-1]
+    tokens = _rows_of(g.shape)
+    if accumulate and out is None:
+        raise ValueError("accumulate needs the tensor to add to (out)")
+    o = torch.empty(m, k, dtype=torch.float32, device=g.device) if out is None else out
+    if tuple(o.shape) != (m, k):
+        raise ValueError(f"out must have shape {(m, k)}, got {tuple(o.shape)}")
+    L = _L or lib()
+    ws, mine = _workspace(L.ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io), g.device, ws)
+    rc = L.ssm_ckpt8_wgrad(*_rows(g, "g"), *_kept(x8, "x8", (*g.shape[:-1], k)),
+                           _f32(o, "out", m * k), tokens, m, k, io,
+                           SSM_WGRAD_ACCUMULATE if accumulate else 0, ws.data_ptr(),
+                           ws.numel() * ws.element_size(),
+                           _on(stream, o if out is None else None, mine))
+    _check("ssm_ckpt8_wgrad", rc)
+    return o

@@ -1,0 +1,155 @@
+// block.cuh -- launchers of the operators around the scan (norm_add.cu, norm_gated.cu, ckpt8.cu,
+// wgrad8.cu), called by the C ABI in block_api.cu, and what the norms' kernels share.
+#pragma once
+
+#include <cuda_runtime.h>
+
+#include "kernels.cuh"
+#include "rows.cuh"
+
+namespace ssm {
+
+// ---- the norms' launches ----------------------------------------------------------------------
+// Column widths and chunks per thread of the kernel instances, and the plan of a launch.
+enum NormVariant { kVec8x1, kVec8x2, kVec8x4, kVec8x4Wide, kOne2, kOne8, kOne32 };
+struct NormShape {
+  NormVariant variant;
+  RowPlan plan;
+};
+NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, bool backward);
+
+// A backward's column sums: each block's own over its rows, [nbx][cols], then their sum.
+size_t column_sums_bytes(long long rows, int group, int groups, int sms, int sums);
+cudaError_t launch_column_sums(const float* part, int n, int cols, float* out, cudaStream_t st);
+
+inline size_t slots_bytes(const RowPlan& p, int vec, int nj) {
+  return p.rpb > 1 ? sizeof(float) * (size_t)p.threads * vec * nj : 0;
+}
+
+// Adds a block's rpb rows' column sums in order and stores them at part[blockIdx.x][col].  Every
+// thread of the block calls it.
+template <int VEC, int NJ>
+__device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPos& pos,
+                                              const RowPlan& pl, const int (&col)[NJ],
+                                              const bool (&okc)[NJ], int cols, float* part,
+                                              float* slots) {
+  if (pl.rpb > 1) {
+    __syncthreads();  // the area may still be read for an earlier sum
+#pragma unroll
+    for (int j = 0; j < NJ; j++)
+#pragma unroll
+      for (int i = 0; i < VEC; i++) slots[(j * VEC + i) * blockDim.x + threadIdx.x] = v[j][i];
+    __syncthreads();
+    if (pos.slot != 0) return;
+    const int step = pl.tpr * pl.gpb;  // threads of one row
+#pragma unroll
+    for (int j = 0; j < NJ; j++)
+#pragma unroll
+      for (int i = 0; i < VEC; i++)
+        for (int s = 1; s < pl.rpb; s++)
+          v[j][i] += slots[(j * VEC + i) * blockDim.x + threadIdx.x + s * step];
+  }
+#pragma unroll
+  for (int j = 0; j < NJ; j++)
+    if (okc[j])
+#pragma unroll
+      for (int i = 0; i < VEC; i++)
+        part[(long long)blockIdx.x * cols + pos.col0 + col[j] + i] = v[j][i];
+}
+
+// ---- add_norm -----------------------------------------------------------------------------------
+struct AddNormFwd {
+  long long rows;
+  int cols;
+  float eps;
+  const void* x;
+  const void* residual;
+  const float* scale;
+  const float* w;
+  void* out;
+  void* res_out;
+  float* rstd;
+  long long ld_x, ld_residual, ld_out, ld_res_out;
+  int8_t *res_q, *x_q, *out_q;
+  uint8_t *res_e, *x_e, *out_e;
+};
+struct AddNormBwd {
+  long long rows;
+  int cols;
+  const void* d_out;
+  const void* d_res_out;
+  const void* res;
+  const void* x;
+  long long ld_d_out, ld_d_res_out, ld_res, ld_x;
+  const int8_t *res_q, *x_q;
+  const uint8_t *res_e, *x_e;
+  const float* rstd_in;
+  const float* scale;
+  const float* w;
+  void* d_res;
+  void* d_x;
+  long long ld_d_res, ld_d_x;
+  float* d_w;
+  float* d_scale;
+  float* part;
+};
+// vec: widths, strides and pointers allow 8 columns at a time
+cudaError_t launch_add_norm_fwd(const AddNormFwd& a, int io, int res_io, bool vec, int sms,
+                                cudaStream_t st);
+cudaError_t launch_add_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
+                                cudaStream_t st);
+
+// ---- gated_norm ---------------------------------------------------------------------------------
+struct GatedNormFwd {
+  long long rows;
+  int cols, group, norm_first;
+  float eps;
+  const void* y;
+  const void* z;
+  const float* w;
+  void* out;
+  long long ld_y, ld_z, ld_out;
+  float* rstd;
+  int8_t *y_q, *z_q, *out_q;
+  uint8_t *y_e, *z_e, *out_e;
+};
+struct GatedNormBwd {
+  long long rows;
+  int cols, group, norm_first;
+  const void* d_out;
+  const void* y;
+  const void* z;
+  long long ld_d_out, ld_y, ld_z;
+  const int8_t *y_q, *z_q;
+  const uint8_t *y_e, *z_e;
+  const float* rstd_in;
+  const float* w;
+  void* d_y;
+  void* d_z;
+  long long ld_d_y, ld_d_z;
+  float* d_w;
+  float* part;
+};
+cudaError_t launch_gated_norm_fwd(const GatedNormFwd& a, int io, bool vec, int sms,
+                                  cudaStream_t st);
+cudaError_t launch_gated_norm_bwd(const GatedNormBwd& a, int io, bool vec, int sms,
+                                  cudaStream_t st);
+
+// ---- 8-bit checkpoints ----------------------------------------------------------------------------
+cudaError_t launch_ckpt8_save(const void* x, long long ld, int8_t* q, uint8_t* e, long long rows,
+                              int cols, int io, int sms, cudaStream_t st);
+cudaError_t launch_ckpt8_load(const int8_t* q, const uint8_t* e, void* out, long long ld,
+                              long long rows, int cols, int io, int sms, cudaStream_t st);
+struct Wgrad {
+  const void* g;
+  long long ld_g;
+  const int8_t* q;
+  const uint8_t* e;
+  float* d_W;
+  long long tokens;
+  int m, k, io, accumulate;
+};
+size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, int sms);
+cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st);
+
+}  // namespace ssm
