@@ -151,5 +151,10 @@ struct Wgrad {
 };
 size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, int sms);
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st);
+// The tensor-core kernel (wgrad8_tc.cu): bf16 g whose rows TMA can read.  part: the splits' tiles,
+// [splits][m][k], or NULL with one split.
+bool wgrad_tc_applies(const Wgrad& a);
+int wgrad_tc_splits(long long tokens, int m, int k, int sms);
+cudaError_t launch_wgrad_tc(const Wgrad& a, float* part, int splits, int* status, cudaStream_t st);
 
 }  // namespace ssm

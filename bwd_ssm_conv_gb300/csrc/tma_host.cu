@@ -28,7 +28,9 @@ bool encode_tmap_3d(CUtensorMap* map, const void* base, int esize, uint64_t d0, 
   auto fn = encode_fn();
   if (!fn) return false;
   const CUtensorMapDataType dt =
-      esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+      esize == 1   ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+      : esize == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16
+                   : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   cuuint64_t dims[3] = {d0, d1, d2};
   cuuint64_t strides[2] = {stride1 * (uint64_t)esize, stride2 * (uint64_t)esize};  // bytes
   cuuint32_t box[3] = {b0, b1, b2};

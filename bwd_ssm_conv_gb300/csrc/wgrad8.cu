@@ -87,21 +87,31 @@ int splits_of(long long tokens, int m, int k, int sms) {
 }  // namespace
 
 size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, int sms) {
-  const int s = splits_of(tokens, m, k, sms);
+  // the larger of the two kernels': which one a call takes depends on its pointers and strides
+  int s = splits_of(tokens, m, k, sms);
+  if (io == SSM_BF16) {
+    const int t = wgrad_tc_splits(tokens, m, k, sms);
+    if (t > s) s = t;
+  }
   return kStatusBytes + (s > 1 ? sizeof(float) * (size_t)s * m * k : 0);
 }
 
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
-  const int s = splits_of(a.tokens, a.m, a.k, sms);
+  const bool tc = wgrad_tc_applies(a);
+  const int s = tc ? wgrad_tc_splits(a.tokens, a.m, a.k, sms) : splits_of(a.tokens, a.m, a.k, sms);
   float* part = s > 1 ? (float*)((char*)ws + kStatusBytes) : nullptr;
-  const long long per = ((a.tokens + s - 1) / s + kDepth - 1) / kDepth * kDepth;
-  const dim3 grid((a.k + kTile - 1) / kTile, (a.m + kTile - 1) / kTile, s);
-  if (a.io == SSM_F32)
-    wgrad8_kernel<float><<<grid, kThreads, 0, st>>>(a, part, per);
-  else
-    wgrad8_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, part, per);
-  count_launches(1);
-  if (cudaError_t e = cudaGetLastError()) return e;
+  if (tc) {
+    if (cudaError_t e = launch_wgrad_tc(a, part, s, (int*)ws, st)) return e;
+  } else {
+    const long long per = ((a.tokens + s - 1) / s + kDepth - 1) / kDepth * kDepth;
+    const dim3 grid((a.k + kTile - 1) / kTile, (a.m + kTile - 1) / kTile, s);
+    if (a.io == SSM_F32)
+      wgrad8_kernel<float><<<grid, kThreads, 0, st>>>(a, part, per);
+    else
+      wgrad8_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, part, per);
+    count_launches(1);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
   if (part) {
     const long long n = (long long)a.m * a.k, b = (n + 255) / 256;
     wgrad8_sum_kernel<<<(int)(b < 8LL * sms ? b : 8LL * sms), 256, 0, st>>>(part, s, n, a.d_W,
