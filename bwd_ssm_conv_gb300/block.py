@@ -9,6 +9,7 @@ whose rows lie at one stride (a slice of a wider tensor is fine); parameters are
 from __future__ import annotations
 
 import ctypes
+from functools import lru_cache
 from typing import NamedTuple
 
 import torch
@@ -88,6 +89,27 @@ def lib():
 _IO = {torch.float32: SSM_F32, torch.bfloat16: SSM_BF16}
 
 
+# What a call of given sizes needs besides its tensors; the same for every call of those sizes on a
+# device, so it is worked out once.
+
+@lru_cache(maxsize=1024)
+def _desc(rows, cols, group, io, res_io, flags, eps):
+    return NormDesc(rows, cols, group, io, res_io, flags, eps)
+
+
+@lru_cache(maxsize=1024)
+def _norm_ws(rows, cols, group, sums, device):
+    with torch.cuda.device(device):
+        return int(lib().ssm_norm_bwd_workspace_size(
+            NormDesc(rows, cols, group, SSM_F32, SSM_F32, 0, 1.0), sums))
+
+
+@lru_cache(maxsize=1024)
+def _wgrad_ws(tokens, m, k, io, device):
+    with torch.cuda.device(device):
+        return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io))
+
+
 def _io(t: torch.Tensor, name: str) -> int:
     io = _IO.get(t.dtype)
     if io is None:
@@ -105,13 +127,19 @@ def _rows(t, name, shape=None, dtype=None):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    cols = t.shape[-1]
     if t.is_contiguous():
-        return t.data_ptr(), cols
-    if cols > 1 and t.stride(-1) != 1:
+        return t.data_ptr(), 0
+    return t.data_ptr(), _row_stride(name, t.shape, t.stride())
+
+
+@lru_cache(maxsize=1024)
+def _row_stride(name, shape, strides):
+    """The one stride between the rows of a tensor that is not contiguous."""
+    cols = shape[-1]
+    if cols > 1 and strides[-1] != 1:
         raise ValueError(f"{name}'s last dimension must be dense")
     ld, span = None, None  # one stride for all rows: outer dimensions step over whole inner ones
-    for size, stride in zip(reversed(t.shape[:-1]), reversed(t.stride()[:-1])):
+    for size, stride in zip(reversed(shape[:-1]), reversed(strides[:-1])):
         if size == 1:
             continue
         if ld is None:
@@ -124,14 +152,14 @@ def _rows(t, name, shape=None, dtype=None):
         ld = cols
     if ld < cols:
         raise ValueError(f"{name}'s rows must not overlap")
-    return t.data_ptr(), ld
+    return ld
 
 
 def _f32(t, name, n):
     """Pointer of a contiguous fp32 tensor of n elements; None for None."""
     if t is None:
         return None
-    if not t.is_cuda or t.dtype != torch.float32 or not t.is_contiguous() or t.numel() != n:
+    if t.dtype != torch.float32 or not t.is_cuda or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous fp32 CUDA tensor of {n} elements")
     return t.data_ptr()
 
@@ -141,13 +169,12 @@ def _kept(c, name, shape):
     if c is None:
         return None, None
     q, e = c
-    eshape = (*shape[:-1], -(-shape[-1] // SSM_CKPT8_BLOCK))
-    if not (q.is_cuda and e.is_cuda and q.dtype == torch.int8 and e.dtype == torch.uint8 and
+    if not (q.dtype == torch.int8 and e.dtype == torch.uint8 and q.is_cuda and e.is_cuda and
             q.is_contiguous() and e.is_contiguous()):
         raise ValueError(f"{name} must hold contiguous int8 and uint8 CUDA tensors")
-    if tuple(q.shape) != tuple(shape) or tuple(e.shape) != eshape:
-        raise ValueError(f"{name} must hold shapes {tuple(shape)} and {eshape}, got "
-                         f"{tuple(q.shape)} and {tuple(e.shape)}")
+    if q.shape != shape or e.shape != (*shape[:-1], -(-shape[-1] // SSM_CKPT8_BLOCK)):
+        raise ValueError(f"{name} must hold an activation of shape {tuple(shape)}, got "
+                         f"{tuple(q.shape)} with scales {tuple(e.shape)}")
     return q.data_ptr(), e.data_ptr()
 
 
@@ -157,34 +184,35 @@ def _new_ckpt8(shape, device):
                              device=device))
 
 
-def _on(stream, *made):
-    """The call's stream; tensors made here for a stream other than the current one are marked as
-    used there, so that their memory is not given out again before that stream is done."""
-    cur = torch.cuda.current_stream()
-    if stream is None or stream == cur:
-        return cur.cuda_stream
-    for t in made:
-        for u in t if isinstance(t, tuple) else (t,):
-            if u is not None:
-                u.record_stream(stream)
+def _ptrs(c):
+    return (None, None) if c is None else (c.q.data_ptr(), c.e.data_ptr())
+
+
+def _on(stream, t, *made):
+    """The call's stream (by default the current one of t's device); tensors made here for a stream
+    other than the current one are marked as used there, so that their memory is not given out
+    again before that stream is done."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream != torch.cuda.current_stream(t.device):
+        for m in made:
+            for u in m if isinstance(m, tuple) else (m,):
+                if u is not None:
+                    u.record_stream(stream)
     return stream.cuda_stream
 
 
 def _workspace(nbytes, device, ws):
-    """(workspace, made here)"""
+    """(workspace, its bytes, the one made here)"""
     if ws is not None:
-        if not ws.is_cuda or not ws.is_contiguous() or ws.numel() * ws.element_size() < nbytes:
+        size = ws.numel() * ws.element_size()
+        if not ws.is_cuda or not ws.is_contiguous() or size < nbytes:
             raise ValueError("workspace too small (or not a contiguous CUDA tensor)")
-        return ws, None
-    ws = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
-    return ws, ws
-
-
-def _rows_of(shape):
-    n = 1
-    for s in shape[:-1]:
-        n *= s
-    return n
+        return ws, size, None
+    if nbytes < 256:
+        nbytes = 256
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, nbytes, ws
 
 
 # ---- residual add + RMSNorm -----------------------------------------------------------------
@@ -205,30 +233,28 @@ def ssm_add_norm_fwd(x, w=None, residual=None, scale=None, eps=1e-5, res_dtype=N
     if out is None:
         o = torch.empty(shape, dtype=x.dtype, device=dev)
         res = torch.empty(shape, dtype=rdt, device=dev) if want_res else None
-        made = (o, res)
+        po, pr = (o.data_ptr(), 0), (None if res is None else res.data_ptr(), 0)
     else:
         o, res = out
-        made = ()
-    rows = _rows_of(shape)
+        po, pr = _rows(o, "out", shape, x.dtype), _rows(res, "res_out", shape, rdt)
+    rows = x.numel() // cols if cols else 0
     rstd = torch.empty(shape[:-1], dtype=torch.float32, device=dev) if want_rstd else None
     res8 = _new_ckpt8(shape, dev) if save8 else None
     x8 = _new_ckpt8(shape, dev) if save_x8 else None
     out8 = _new_ckpt8(shape, dev) if save_out8 else None
-    d = NormDesc(rows, cols, 0, io, _IO.get(rdt, -1), 0, eps)
-    L = _L or lib()
-    rc = L.ssm_add_norm_fwd(
-        d, *_rows(x, "x"), *_rows(residual, "residual", shape), _f32(scale, "scale", cols),
-        _f32(w, "w", cols), *_rows(o, "out", shape, x.dtype), *_rows(res, "res_out", shape, rdt),
-        None if rstd is None else rstd.data_ptr(), *_kept(res8, "res8", shape),
-        *_kept(x8, "x8", shape), *_kept(out8, "out8", shape),
-        _on(stream, *made, rstd, res8, x8, out8))
-    _check("ssm_add_norm_fwd", rc)
+    rc = (_L or lib()).ssm_add_norm_fwd(
+        _desc(rows, cols, 0, io, _IO.get(rdt, -1), 0, eps), *_rows(x, "x"),
+        *_rows(residual, "residual", shape), _f32(scale, "scale", cols), _f32(w, "w", cols), *po,
+        *pr, None if rstd is None else rstd.data_ptr(), *_ptrs(res8), *_ptrs(x8), *_ptrs(out8),
+        _on(stream, x, *(() if out is not None else (o, res)), rstd, res8, x8, out8))
+    if rc:
+        _check("ssm_add_norm_fwd", rc)
     return AddNorm(o, res, rstd, res8, x8, out8)
 
 
 def ssm_norm_bwd_workspace_size(rows, cols, sums=1, group=0, io=SSM_BF16, res_io=SSM_F32) -> int:
-    d = NormDesc(rows, cols, group, io, res_io, 0, 1.0)
-    return int(lib().ssm_norm_bwd_workspace_size(d, sums))
+    return int(lib().ssm_norm_bwd_workspace_size(NormDesc(rows, cols, group, io, res_io, 0, 1.0),
+                                                 sums))
 
 
 def ssm_add_norm_bwd(d_out, res, rstd, w=None, d_res_out=None, scale=None, x=None, res_dtype=None,
@@ -243,35 +269,35 @@ def ssm_add_norm_bwd(d_out, res, rstd, w=None, d_res_out=None, scale=None, x=Non
     io = _io(d_out, "d_out")
     shape, dev, f32 = d_out.shape, d_out.device, torch.float32
     cols = shape[-1]
-    res8 = isinstance(res, tuple)
+    res8, x8 = isinstance(res, tuple), isinstance(x, tuple)
     rdt = (d_res_out.dtype if d_res_out is not None else
            res.dtype if not res8 else res_dtype or d_out.dtype)
     if out is None:
-        g = dict(d_res=torch.empty(shape, dtype=rdt, device=dev) if want_dres else None,
-                 d_x=torch.empty(shape, dtype=d_out.dtype, device=dev) if want_dx else None,
-                 d_w=torch.empty(cols, dtype=f32, device=dev) if w is not None else None,
-                 d_scale=(torch.empty(cols, dtype=f32, device=dev)
-                          if scale is not None and x is not None else None))
-        made = tuple(g.values())
+        d_res = torch.empty(shape, dtype=rdt, device=dev) if want_dres else None
+        d_x = torch.empty(shape, dtype=d_out.dtype, device=dev) if want_dx else None
+        d_w = torch.empty(cols, dtype=f32, device=dev) if w is not None else None
+        d_scale = (torch.empty(cols, dtype=f32, device=dev)
+                   if scale is not None and x is not None else None)
+        g = dict(d_res=d_res, d_x=d_x, d_w=d_w, d_scale=d_scale)
+        made = (d_res, d_x, d_w, d_scale)
     else:
         g, made = out, ()
-    rows = _rows_of(shape)
-    d = NormDesc(rows, cols, 0, io, _IO.get(rdt, -1), 0, 1.0)
-    L = _L or lib()
-    sums = (g["d_w"] is not None) + (g["d_scale"] is not None)
-    wsz = L.ssm_norm_bwd_workspace_size(d, sums) if sums else 0
-    ws, mine = _workspace(wsz, dev, ws)
-    x8 = isinstance(x, tuple)
-    rc = L.ssm_add_norm_bwd(
-        d, *_rows(d_out, "d_out"), *_rows(d_res_out, "d_res_out", shape, rdt),
+        d_res, d_x, d_w, d_scale = g["d_res"], g["d_x"], g["d_w"], g["d_scale"]
+    rows = d_out.numel() // cols if cols else 0
+    sums = (d_w is not None) + (d_scale is not None)
+    ws, size, mine = _workspace(_norm_ws(rows, cols, 0, sums, dev) if sums else 0, dev, ws)
+    rc = (_L or lib()).ssm_add_norm_bwd(
+        _desc(rows, cols, 0, io, _IO.get(rdt, -1), 0, 1.0), *_rows(d_out, "d_out"),
+        *_rows(d_res_out, "d_res_out", shape, rdt),
         *_rows(None if res8 else res, "res", shape, rdt),
         *_kept(res if res8 else None, "res", shape),
         *_rows(None if x8 else x, "x", shape, d_out.dtype), *_kept(x if x8 else None, "x", shape),
         _f32(rstd, "rstd", rows), _f32(scale, "scale", cols), _f32(w, "w", cols),
-        *_rows(g["d_res"], "d_res", shape, rdt), *_rows(g["d_x"], "d_x", shape, d_out.dtype),
-        _f32(g["d_w"], "d_w", cols), _f32(g["d_scale"], "d_scale", cols), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _on(stream, *made, mine))
-    _check("ssm_add_norm_bwd", rc)
+        *_rows(d_res, "d_res", shape, rdt), *_rows(d_x, "d_x", shape, d_out.dtype),
+        _f32(d_w, "d_w", cols), _f32(d_scale, "d_scale", cols), ws.data_ptr(), size,
+        _on(stream, d_out, *made, mine))
+    if rc:
+        _check("ssm_add_norm_bwd", rc)
     return g
 
 
@@ -288,22 +314,24 @@ def ssm_gated_norm_fwd(y, z, w=None, group=0, eps=1e-5, norm_first=False, save8=
     io = _io(y, "y")
     shape, dev = y.shape, y.device
     cols = shape[-1]
-    o = torch.empty(shape, dtype=y.dtype, device=dev) if out is None else out
-    made = (o,) if out is None else ()
-    groups = cols // group if group else 1
-    rstd = (torch.empty(*shape[:-1], max(groups, 1), dtype=torch.float32, device=dev)
-            if want_rstd else None)
+    if out is None:
+        o = torch.empty(shape, dtype=y.dtype, device=dev)
+        po = (o.data_ptr(), 0)
+    else:
+        o, po = out, _rows(out, "out", shape, y.dtype)
+    groups = max(cols // group, 1) if group else 1
+    rstd = torch.empty(*shape[:-1], groups, dtype=torch.float32, device=dev) if want_rstd else None
     y8 = _new_ckpt8(shape, dev) if save8 else None
     z8 = _new_ckpt8(shape, dev) if save8 else None
     out8 = _new_ckpt8(shape, dev) if save_out8 else None
-    d = NormDesc(_rows_of(shape), cols, group, io, io, SSM_NORM_FIRST if norm_first else 0, eps)
-    L = _L or lib()
-    rc = L.ssm_gated_norm_fwd(
-        d, *_rows(y, "y"), *_rows(z, "z", shape, y.dtype), _f32(w, "w", cols),
-        *_rows(o, "out", shape, y.dtype), None if rstd is None else rstd.data_ptr(),
-        *_kept(y8, "y8", shape), *_kept(z8, "z8", shape), *_kept(out8, "out8", shape),
-        _on(stream, *made, rstd, y8, z8, out8))
-    _check("ssm_gated_norm_fwd", rc)
+    rc = (_L or lib()).ssm_gated_norm_fwd(
+        _desc(y.numel() // cols if cols else 0, cols, group, io, io,
+              SSM_NORM_FIRST if norm_first else 0, eps),
+        *_rows(y, "y"), *_rows(z, "z", shape, y.dtype), _f32(w, "w", cols), *po,
+        None if rstd is None else rstd.data_ptr(), *_ptrs(y8), *_ptrs(z8), *_ptrs(out8),
+        _on(stream, y, None if out is not None else o, rstd, y8, z8, out8))
+    if rc:
+        _check("ssm_gated_norm_fwd", rc)
     return GatedNorm(o, rstd, y8, z8, out8)
 
 
@@ -318,26 +346,28 @@ def ssm_gated_norm_bwd(d_out, y, z, rstd, w=None, group=0, norm_first=False, ws=
     shape, dev, f32 = d_out.shape, d_out.device, torch.float32
     cols = shape[-1]
     if out is None:
-        g = dict(d_y=torch.empty(shape, dtype=d_out.dtype, device=dev),
-                 d_z=torch.empty(shape, dtype=d_out.dtype, device=dev),
-                 d_w=torch.empty(cols, dtype=f32, device=dev) if w is not None else None)
-        made = tuple(g.values())
+        d_y = torch.empty(shape, dtype=d_out.dtype, device=dev)
+        d_z = torch.empty(shape, dtype=d_out.dtype, device=dev)
+        d_w = torch.empty(cols, dtype=f32, device=dev) if w is not None else None
+        g = dict(d_y=d_y, d_z=d_z, d_w=d_w)
+        made = (d_y, d_z, d_w)
     else:
         g, made = out, ()
-    rows, groups = _rows_of(shape), cols // group if group else 1
-    d = NormDesc(rows, cols, group, io, io, SSM_NORM_FIRST if norm_first else 0, 1.0)
-    L = _L or lib()
-    wsz = L.ssm_norm_bwd_workspace_size(d, 1) if g["d_w"] is not None else 0
-    ws, mine = _workspace(wsz, dev, ws)
+        d_y, d_z, d_w = g["d_y"], g["d_z"], g["d_w"]
+    rows, groups = d_out.numel() // cols if cols else 0, cols // group if group else 1
+    ws, size, mine = _workspace(_norm_ws(rows, cols, group, 1, dev) if d_w is not None else 0, dev,
+                                ws)
     y8, z8 = isinstance(y, tuple), isinstance(z, tuple)
-    rc = L.ssm_gated_norm_bwd(
-        d, *_rows(d_out, "d_out"), *_rows(None if y8 else y, "y", shape, d_out.dtype),
+    rc = (_L or lib()).ssm_gated_norm_bwd(
+        _desc(rows, cols, group, io, io, SSM_NORM_FIRST if norm_first else 0, 1.0),
+        *_rows(d_out, "d_out"), *_rows(None if y8 else y, "y", shape, d_out.dtype),
         *_kept(y if y8 else None, "y", shape), *_rows(None if z8 else z, "z", shape, d_out.dtype),
         *_kept(z if z8 else None, "z", shape), _f32(rstd, "rstd", rows * groups),
-        _f32(w, "w", cols), *_rows(g["d_y"], "d_y", shape, d_out.dtype),
-        *_rows(g["d_z"], "d_z", shape, d_out.dtype), _f32(g["d_w"], "d_w", cols), ws.data_ptr(),
-        ws.numel() * ws.element_size(), _on(stream, *made, mine))
-    _check("ssm_gated_norm_bwd", rc)
+        _f32(w, "w", cols), *_rows(d_y, "d_y", shape, d_out.dtype),
+        *_rows(d_z, "d_z", shape, d_out.dtype), _f32(d_w, "d_w", cols), ws.data_ptr(), size,
+        _on(stream, d_out, *made, mine))
+    if rc:
+        _check("ssm_gated_norm_bwd", rc)
     return g
 
 
@@ -347,22 +377,31 @@ def ssm_ckpt8_save(x, out=None, stream=None) -> Ckpt8:
     """x [..., cols] as an 8-bit checkpoint (int8 values, one power-of-two scale per 32 columns)."""
     io = _io(x, "x")
     shape = x.shape
+    cols = shape[-1]
     c = _new_ckpt8(shape, x.device) if out is None else out
-    L = _L or lib()
-    rc = L.ssm_ckpt8_save(*_rows(x, "x"), *_kept(c, "out", shape), _rows_of(shape), shape[-1], io,
-                          _on(stream, c if out is None else None))
-    _check("ssm_ckpt8_save", rc)
+    rc = (_L or lib()).ssm_ckpt8_save(
+        *_rows(x, "x"), *(_ptrs(c) if out is None else _kept(c, "out", shape)),
+        x.numel() // cols if cols else 0, cols, io, _on(stream, x, c if out is None else None))
+    if rc:
+        _check("ssm_ckpt8_save", rc)
     return c
 
 
 def ssm_ckpt8_load(c, dtype=torch.bfloat16, out=None, stream=None):
     """The values of a checkpoint, as ``dtype`` (both types hold them exactly)."""
-    shape = c[0].shape
-    o = torch.empty(shape, dtype=dtype, device=c[0].device) if out is None else out
-    L = _L or lib()
-    rc = L.ssm_ckpt8_load(*_kept(c, "c", shape), *_rows(o, "out", shape), _rows_of(shape),
-                          shape[-1], _io(o, "out"), _on(stream, o if out is None else None))
-    _check("ssm_ckpt8_load", rc)
+    q = c[0]
+    shape = q.shape
+    cols = shape[-1]
+    if out is None:
+        o = torch.empty(shape, dtype=dtype, device=q.device)
+        po = (o.data_ptr(), 0)
+    else:
+        o, po = out, _rows(out, "out", shape)
+    rc = (_L or lib()).ssm_ckpt8_load(*_kept(c, "c", shape), *po, q.numel() // cols if cols else 0,
+                                      cols, _io(o, "out"),
+                                      _on(stream, q, o if out is None else None))
+    if rc:
+        _check("ssm_ckpt8_load", rc)
     return o
 
 
@@ -376,18 +415,17 @@ def ssm_ckpt8_wgrad(g, x8, accumulate=False, ws=None, out=None, stream=None):
     ``out``."""
     io = _io(g, "g")
     m, k = g.shape[-1], x8[0].shape[-1]
-    tokens = _rows_of(g.shape)
+    tokens = g.numel() // m if m else 0
     if accumulate and out is None:
         raise ValueError("accumulate needs the tensor to add to (out)")
     o = torch.empty(m, k, dtype=torch.float32, device=g.device) if out is None else out
-    if tuple(o.shape) != (m, k):
-        raise ValueError(f"out must have shape {(m, k)}, got {tuple(o.shape)}")
-    L = _L or lib()
-    ws, mine = _workspace(L.ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io), g.device, ws)
-    rc = L.ssm_ckpt8_wgrad(*_rows(g, "g"), *_kept(x8, "x8", (*g.shape[:-1], k)),
-                           _f32(o, "out", m * k), tokens, m, k, io,
-                           SSM_WGRAD_ACCUMULATE if accumulate else 0, ws.data_ptr(),
-                           ws.numel() * ws.element_size(),
-                           _on(stream, o if out is None else None, mine))
-    _check("ssm_ckpt8_wgrad", rc)
+    if out is not None and out.shape != (m, k):
+        raise ValueError(f"out must have shape {(m, k)}, got {tuple(out.shape)}")
+    ws, size, mine = _workspace(_wgrad_ws(tokens, m, k, io, g.device), g.device, ws)
+    rc = (_L or lib()).ssm_ckpt8_wgrad(
+        *_rows(g, "g"), *_kept(x8, "x8", (*g.shape[:-1], k)), _f32(o, "out", m * k), tokens, m, k,
+        io, SSM_WGRAD_ACCUMULATE if accumulate else 0, ws.data_ptr(), size,
+        _on(stream, g, o if out is None else None, mine))
+    if rc:
+        _check("ssm_ckpt8_wgrad", rc)
     return o

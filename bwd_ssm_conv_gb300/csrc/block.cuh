@@ -10,8 +10,35 @@
 namespace ssm {
 
 // ---- the norms' launches ----------------------------------------------------------------------
-// Column widths and chunks per thread of the kernel instances, and the plan of a launch.
-enum NormVariant { kVec8x1, kVec8x2, kVec8x4, kVec8x4Wide, kOne2, kOne8, kOne32 };
+// The kernel instances: columns of an access, accesses per thread, most threads of a block and
+// blocks of that size that the registers leave room for.
+enum NormVariant { kVec1, kVec1Wide, kVec2, kVec2Wide, kVec3, kVec4, kVec4Wide, kOne2, kOne4,
+                   kOne8Wide, kOne32 };
+#define SSM_NORM_CASES(LAUNCH)                        \
+    case ssm::kVec1: LAUNCH(8, 1, 256, 4); break;      \
+    case ssm::kVec1Wide: LAUNCH(8, 1, 1024, 1); break; \
+    case ssm::kVec2: LAUNCH(8, 2, 256, 2); break;      \
+    case ssm::kVec4Wide: LAUNCH(8, 4, 1024, 1); break; \
+    case ssm::kOne2: LAUNCH(1, 2, 128, 4); break;      \
+    case ssm::kOne4: LAUNCH(1, 4, 256, 4); break;      \
+    case ssm::kOne8Wide: LAUNCH(1, 8, 1024, 1); break; \
+    default: LAUNCH(1, 32, 1024, 1); break;
+#define SSM_NORM_FWD_SWITCH(variant, LAUNCH)           \
+  switch (variant) {                                   \
+    case ssm::kVec3: LAUNCH(8, 3, 256, 2); break;      \
+    case ssm::kVec4: LAUNCH(8, 4, 256, 2); break;      \
+    SSM_NORM_CASES(LAUNCH)                             \
+  }
+#define SSM_NORM_BWD_SWITCH(variant, LAUNCH)           \
+  switch (variant) {                                   \
+    case ssm::kVec2Wide: LAUNCH(8, 2, 512, 1); break;  \
+    SSM_NORM_CASES(LAUNCH)                             \
+  }
+// Threads per SM of a launch's blocks, which all fit at once (registers: the instances above).
+inline int norm_threads_per_sm(NormVariant v) {
+  return v == kVec1 ? 768 : (v == kVec1Wide || v == kVec4Wide || v == kOne4 || v == kOne8Wide || v == kOne32 ? 1024 : 512);
+}
+// The plan of a launch.
 struct NormShape {
   NormVariant variant;
   RowPlan plan;
@@ -20,7 +47,9 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
 
 // A backward's column sums: each block's own over its rows, [nbx][cols], then their sum.
 size_t column_sums_bytes(long long rows, int group, int groups, int sms, int sums);
-cudaError_t launch_column_sums(const float* part, int n, int cols, float* out, cudaStream_t st);
+// out0 and out1 (either may be NULL) from part [sums][n][cols], in that order.
+cudaError_t launch_column_sums(const float* part, int n, int cols, float* out0, float* out1,
+                               cudaStream_t st);
 
 inline size_t slots_bytes(const RowPlan& p, int vec, int nj) {
   return p.rpb > 1 ? sizeof(float) * (size_t)p.threads * vec * nj : 0;
@@ -29,8 +58,8 @@ inline size_t slots_bytes(const RowPlan& p, int vec, int nj) {
 // Adds a block's rpb rows' column sums in order and stores them at part[blockIdx.x][col].  Every
 // thread of the block calls it.
 template <int VEC, int NJ>
-__device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPos& pos,
-                                              const RowPlan& pl, const int (&col)[NJ],
+__device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPlan& pl,
+                                              const RowPos& pos, const int (&col)[NJ],
                                               const bool (&okc)[NJ], int cols, float* part,
                                               float* slots) {
   if (pl.rpb > 1) {
@@ -51,10 +80,7 @@ __device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPos&
   }
 #pragma unroll
   for (int j = 0; j < NJ; j++)
-    if (okc[j])
-#pragma unroll
-      for (int i = 0; i < VEC; i++)
-        part[(long long)blockIdx.x * cols + pos.col0 + col[j] + i] = v[j][i];
+    if (okc[j]) st_cols(part + (long long)blockIdx.x * cols + col[j], v[j]);
 }
 
 // ---- add_norm -----------------------------------------------------------------------------------

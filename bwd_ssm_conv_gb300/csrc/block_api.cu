@@ -4,6 +4,8 @@
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "block.cuh"
 #include "ssm_block.h"
 
@@ -15,10 +17,15 @@ constexpr int kMaxDim = 1 << 20;  // m and k of the weight gradient, columns of 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t io_size(int io) { return io == SSM_BF16 ? 2 : (io == SSM_F32 ? 4 : 0); }
 
+// SMs of the current device, asked for once per device (the answer never changes).
 int num_sms() {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[kDevices];
   int dev = 0, sms = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return 0;
+  if (dev < kDevices && (sms = known[dev].load(std::memory_order_relaxed)) > 0) return sms;
   if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (dev < kDevices) known[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
 
@@ -38,8 +45,9 @@ struct Rows {
     if ((q == nullptr) != (e == nullptr)) ok = false;
     if (q && !aligned(q, 8)) vec = false;
   }
-  void f32(const void* p) {
+  void f32(const void* p) {  // a parameter or its gradient
     if (p && !aligned(p, 4)) ok = false;
+    if (p && !aligned(p, 16)) vec = false;
   }
 };
 
@@ -87,8 +95,7 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
   r.kept(out_q, out_e);
   r.f32(scale);
   r.f32(w);
-  r.f32(rstd);
-  if (!r.ok) return SSM_ERR_INVALID_ARG;
+  if (!r.ok || (rstd && !aligned(rstd, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_x, ld_residual, ld_out, ld_res_out})
     if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
@@ -132,10 +139,10 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
   r.arg(d_x, ld_d_x, io);
   r.kept(res_q, res_e);
   r.kept(x_q, x_e);
-  for (const void* p : {(const void*)rstd, (const void*)scale, (const void*)w, (const void*)d_w,
-                        (const void*)d_scale})
-    r.f32(p);
-  if (!r.ok) return SSM_ERR_INVALID_ARG;
+  r.f32(scale);
+  r.f32(w);
+  if (!r.ok || !aligned(rstd, 4) || (d_w && !aligned(d_w, 4)) || (d_scale && !aligned(d_scale, 4)))
+    return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_d_out, ld_d_res_out, ld_res, ld_x, ld_d_res, ld_d_x})
     if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
@@ -167,8 +174,7 @@ int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y,
   r.kept(z_q, z_e);
   r.kept(out_q, out_e);
   r.f32(w);
-  r.f32(rstd);
-  if (!r.ok) return SSM_ERR_INVALID_ARG;
+  if (!r.ok || (rstd && !aligned(rstd, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_y, ld_z, ld_out})
     if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
@@ -213,10 +219,8 @@ int ssm_gated_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long l
   r.arg(d_z, ld_d_z, io);
   r.kept(y_q, y_e);
   r.kept(z_q, z_e);
-  r.f32(rstd);
   r.f32(w);
-  r.f32(d_w);
-  if (!r.ok) return SSM_ERR_INVALID_ARG;
+  if (!r.ok || !aligned(rstd, 4) || (d_w && !aligned(d_w, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_d_out, ld_y, ld_z, ld_d_y, ld_d_z})
     if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();

@@ -11,47 +11,66 @@ namespace ssm {
 
 namespace {
 
-template <typename IO, int VEC, int NJ, int MAXT>
-__global__ void __launch_bounds__(MAXT) gated_norm_fwd_kernel(const GatedNormFwd a,
-                                                              const RowPlan pl) {
+template <typename IO, int VEC, int NJ, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedNormFwd a,
+                                                                    const RowPlan pl) {
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float part[2][32];
   const RowPos pos = row_pos(pl);
   const int nb = (a.cols + 31) / 32;
   const float inv = 1.0f / (float)a.group;
   bool okc[NJ];
   int col[NJ];
+  float w[NJ][VEC];
 #pragma unroll
   for (int j = 0; j < NJ; j++) {
-    col[j] = (pos.lane + j * pl.tpr) * VEC;
-    okc[j] = pos.ok && col[j] < a.group;
-    col[j] += pos.col0;
+    const int c = (pos.lane + j * pl.tpr) * VEC;
+    okc[j] = pos.ok && c < a.group;
+    col[j] = pos.col0 + c;
+    ld_param<VEC>(a.w, col[j], okc[j], w[j]);
   }
-  int half = 0;
-  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += (long long)gridDim.x * pl.rpb, half ^= 1) {
-    const long long row = base + pos.slot;
-    const bool rok = row < a.rows;
-    Cols<IO, VEC> yr[NJ], zr[NJ];
-#pragma unroll
-    for (int j = 0; j < NJ; j++) {
-      yr[j].zero();
-      zr[j].zero();
-      if (rok && okc[j]) {
-        yr[j].load((const IO*)a.y + row * a.ld_y + col[j]);
-        zr[j].load((const IO*)a.z + row * a.ld_z + col[j]);
-      }
+  typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
+  const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
+  const Op y{a.y, nullptr, nullptr, a.ld_y, at}, z{a.z, nullptr, nullptr, a.ld_z, at + bytes};
+  const long long step = (long long)gridDim.x * pl.rpb;
+  long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
+  auto issue = [&](long long r, int slot) {
+    if (r < a.rows) {
+      y.issue(slot * 2 * bytes, r, col, okc, a.cols);
+      z.issue(slot * 2 * bytes, r, col, okc, a.cols);
     }
-    float v[NJ][VEC];
-    float sq = 0.0f;
+    cp_async_commit();
+  };
+  for (int i = 0; i < pl.slots; i++) {
+    y.clear(i * 2 * bytes, okc, false);
+    z.clear(i * 2 * bytes, okc, false);
+  }
+  const int ahead = pl.slots - 1;
+  for (int i = 0; i < ahead; i++) issue(row + i * step, i);
+  int half = 0, slot = 0;
+  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
+       base += step, row += step, half ^= 1) {
+    const bool rok = row < a.rows;
+    issue(row + ahead * step, slot == 0 ? ahead : slot - 1);
+    cp_async_wait(ahead);
+    const uint32_t s = slot * 2 * bytes;
+    slot = slot == ahead ? 0 : slot + 1;
+    const long long qrow = row * a.cols, erow = row * nb;
+    float v[NJ][VEC], sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
-      yr[j].get(v[j]);
-      if (!a.norm_first) {
-        float z[VEC];
-        zr[j].get(z);
-#pragma unroll
-        for (int i = 0; i < VEC; i++) v[j][i] *= siluf_(z[i]);
+      const bool ok = rok && okc[j];
+      float zv[VEC];
+      y.get(s, j, ok, row, col[j], a.cols, 7u, v[j]);
+      z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
+      if (a.y_q) {
+        const uint32_t ytop = y.top(s, j, v[j]), ztop = z.top(s, j, zv);
+        store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + col[j] / 32);
+        store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + col[j] / 32);
       }
+      if (!a.norm_first)
+#pragma unroll
+        for (int i = 0; i < VEC; i++) v[j][i] *= siluf_(zv[i]);
 #pragma unroll
       for (int i = 0; i < VEC; i++) sq = fmaf(v[j][i], v[j][i], sq);
     }
@@ -61,32 +80,30 @@ __global__ void __launch_bounds__(MAXT) gated_norm_fwd_kernel(const GatedNormFwd
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
-      float w[VEC], o[VEC], z[VEC];
-      ld_param<VEC>(a.w, col[j], okc[j], w);
-      zr[j].get(z);
+      float o[VEC];
 #pragma unroll
-      for (int i = 0; i < VEC; i++) {
-        o[i] = w[i] * (v[j][i] * rstd);
-        if (a.norm_first) o[i] *= siluf_(z[i]);
-        o[i] = rounded<IO>(o[i]);
+      for (int i = 0; i < VEC; i++) o[i] = w[j][i] * (v[j][i] * rstd);
+      if (a.norm_first) {
+        float zv[VEC];
+        z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
+#pragma unroll
+        for (int i = 0; i < VEC; i++) o[i] *= siluf_(zv[i]);
       }
-      if (ok) st_cols((IO*)a.out + row * a.ld_out + col[j], o);
-      const long long q = row * a.cols + col[j], e = row * nb + col[j] / 32;
-      if (a.y_q) {
-        float y[VEC];
-        yr[j].get(y);
-        store_ckpt8<VEC>(y, ok, a.y_q + q, a.y_e + e);
+      Cols<IO, VEC> oc;
+      to_cols(o, oc);
+      if (ok) st_cols((IO*)a.out + row * a.ld_out + col[j], oc);
+      if (a.out_q) {
+        oc.get(o);
+        store_ckpt8<VEC>(o, ok, a.out_q + qrow + col[j], a.out_e + erow + col[j] / 32);
       }
-      if (a.z_q) store_ckpt8<VEC>(z, ok, a.z_q + q, a.z_e + e);
-      if (a.out_q) store_ckpt8<VEC>(o, ok, a.out_q + q, a.out_e + e);
     }
   }
 }
 
-template <typename IO, int VEC, int NJ, int MAXT>
-__global__ void __launch_bounds__(MAXT) gated_norm_bwd_kernel(const GatedNormBwd a,
-                                                              const RowPlan pl) {
-  extern __shared__ float slots[];
+template <typename IO, int VEC, int NJ, int MAXT, int MINB>
+__global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedNormBwd a,
+                                                                    const RowPlan pl) {
+  extern __shared__ __align__(16) unsigned char ring[];  // at the end: the slots' column sums
   __shared__ float part[2][32];
   const RowPos pos = row_pos(pl);
   const int nb = (a.cols + 31) / 32;
@@ -96,136 +113,151 @@ __global__ void __launch_bounds__(MAXT) gated_norm_bwd_kernel(const GatedNormBwd
   float w[NJ][VEC], dw[NJ][VEC];
 #pragma unroll
   for (int j = 0; j < NJ; j++) {
-    col[j] = (pos.lane + j * pl.tpr) * VEC;
-    okc[j] = pos.ok && col[j] < a.group;
-    ld_param<VEC>(a.w, pos.col0 + col[j], okc[j], w[j]);
+    const int c = (pos.lane + j * pl.tpr) * VEC;
+    okc[j] = pos.ok && c < a.group;
+    col[j] = pos.col0 + c;
+    ld_param<VEC>(a.w, col[j], okc[j], w[j]);
 #pragma unroll
     for (int i = 0; i < VEC; i++) dw[j][i] = 0.0f;
   }
-  int half = 0;
+  typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
+  const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
+  const Op d{a.d_out, nullptr, nullptr, a.ld_d_out, at}, y{a.y, a.y_q, a.y_e, a.ld_y, at + bytes},
+      z{a.z, a.z_q, a.z_e, a.ld_z, at + 2 * bytes};
+  const long long step = (long long)gridDim.x * pl.rpb;
+  long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
+  auto issue = [&](long long r, int slot) {
+    const uint32_t s = slot * 3 * bytes;
+    if (r < a.rows) {
+      d.issue(s, r, col, okc, a.cols);
+      y.issue(s, r, col, okc, a.cols);
+      z.issue(s, r, col, okc, a.cols);
+    } else {  // adds nothing to the column sums
+      d.clear(s, okc, true);
+      y.clear(s, okc, true);
+      z.clear(s, okc, true);
+    }
+    cp_async_commit();
+  };
+  // what a row needs besides: read one row ahead
+  float rstd_next = 0.0f;
+  uint32_t ey_next[NJ], ez_next[NJ];
+  auto small = [&](long long r) {
+    const bool rok = r < a.rows;
+    rstd_next = rok && pos.ok ? a.rstd_in[r * pl.groups + pos.col0 / a.group] : 0.0f;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      ey_next[j] = y.scale(rok && okc[j], r, col[j], nb);
+      ez_next[j] = z.scale(rok && okc[j], r, col[j], nb);
+    }
+  };
+  for (int i = 0; i < pl.slots; i++) {
+    d.clear(i * 3 * bytes, okc, false);
+    y.clear(i * 3 * bytes, okc, false);
+    z.clear(i * 3 * bytes, okc, false);
+  }
+  const int ahead = pl.slots - 1;
+  for (int i = 0; i < ahead; i++) issue(row + i * step, i);
+  small(row);
+  int half = 0, slot = 0;
   for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += (long long)gridDim.x * pl.rpb, half ^= 1) {
-    const long long row = base + pos.slot;
+       base += step, row += step, half ^= 1) {
     const bool rok = row < a.rows;
-    const float rstd =
-        rok && pos.ok ? a.rstd_in[row * pl.groups + pos.col0 / a.group] : 0.0f;
-    Cols<IO, VEC> dr[NJ];
-    float y[NJ][VEC], z[NJ][VEC];
+    const float rstd = rstd_next;
+    uint32_t ey[NJ], ez[NJ];
+#pragma unroll
+    for (int j = 0; j < NJ; j++) ey[j] = ey_next[j], ez[j] = ez_next[j];
+    small(row + step);
+    issue(row + ahead * step, slot == 0 ? ahead : slot - 1);
+    cp_async_wait(ahead);
+    const uint32_t s = slot * 3 * bytes;
+    slot = slot == ahead ? 0 : slot + 1;
+    // What the second pass needs of y and z, so that it does not unpack them again:
+    //   gate first: g = silu(z), b = y silu'(z), m = n / rstd;  norm first: g = silu(z),
+    //   b = w d_out silu'(z) n (d_z already), m = n / rstd
+    float g[NJ][VEC], b[NJ][VEC], m[NJ][VEC], dot = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
-      const int c = pos.col0 + col[j];
-      dr[j].zero();
-      if (ok) dr[j].load((const IO*)a.d_out + row * a.ld_d_out + c);
-      if (a.y_q) {
-        Kept<VEC> ky, kz;
-        ky.zero();
-        kz.zero();
-        if (ok) {
-          ky.load(a.y_q + row * a.cols + c, a.y_e + row * nb + c / 32);
-          kz.load(a.z_q + row * a.cols + c, a.z_e + row * nb + c / 32);
-        }
-        ky.get(y[j]);
-        kz.get(z[j]);
+      float dv[VEC], yv[VEC], zv[VEC];
+      d.get(s, j, ok, row, col[j], a.cols, 7u, dv);
+      y.get(s, j, ok, row, col[j], a.cols, ey[j], yv);
+      z.get(s, j, ok, row, col[j], a.cols, ez[j], zv);
+#pragma unroll
+      for (int i = 0; i < VEC; i++) {
+        const float sg = sigmoidf_(zv[i]);
+        g[j][i] = zv[i] * sg;
+        const float slope = fmaf(g[j][i], 1.0f - sg, sg);  // d silu(z) / d z
+        const float yg = yv[i] * g[j][i], t = dv[i] * rstd * yg;  // d_out times n and gate
+        dw[j][i] += t;
+        dot = fmaf(w[j][i], t, dot);
+        m[j][i] = a.norm_first ? yv[i] : yg;
+        b[j][i] = a.norm_first ? w[j][i] * (dv[i] * rstd) * yv[i] * slope : yv[i] * slope;
+      }
+    }
+    const float c = -row_sum(dot, pl.tpr, part, half) * inv * rstd;
+#pragma unroll
+    for (int j = 0; j < NJ; j++) {
+      const bool ok = rok && okc[j];
+      float dv[VEC], dy[VEC];
+      d.get(s, j, ok, row, col[j], a.cols, 7u, dv);
+      if (a.norm_first) {
+#pragma unroll
+        for (int i = 0; i < VEC; i++)
+          dy[i] = rstd * fmaf(m[j][i], c, w[j][i] * dv[i] * g[j][i]);
       } else {
-        Cols<IO, VEC> ky, kz;
-        ky.zero();
-        kz.zero();
-        if (ok) {
-          ky.load((const IO*)a.y + row * a.ld_y + c);
-          kz.load((const IO*)a.z + row * a.ld_z + c);
-        }
-        ky.get(y[j]);
-        kz.get(z[j]);
-      }
-    }
-    // y becomes n; z stays
-    float dot = 0.0f;
 #pragma unroll
-    for (int j = 0; j < NJ; j++) {
-      float d[VEC];
-      dr[j].get(d);
-#pragma unroll
-      for (int i = 0; i < VEC; i++) {
-        const float gate = siluf_(z[j][i]);
-        const float n = a.norm_first ? y[j][i] * rstd : y[j][i] * gate * rstd;
-        const float up = a.norm_first ? d[i] * gate : d[i];  // the gradient of w n
-        dw[j][i] = fmaf(up, n, dw[j][i]);
-        dot = fmaf(w[j][i] * up, n, dot);
-      }
-    }
-    const float mean = row_sum(dot, pl.tpr, part, half) * inv;
-#pragma unroll
-    for (int j = 0; j < NJ; j++) {
-      float d[VEC], dy[VEC], dz[VEC];
-      dr[j].get(d);
-#pragma unroll
-      for (int i = 0; i < VEC; i++) {
-        const float sg = sigmoidf_(z[j][i]), gate = z[j][i] * sg;
-        const float slope = sg * (1.0f + z[j][i] * (1.0f - sg));
-        const float wd = w[j][i] * d[i];
-        if (a.norm_first) {
-          const float n = y[j][i] * rstd;
-          dy[i] = rstd * fmaf(-n, mean, wd * gate);
-          dz[i] = wd * n * slope;
-        } else {
-          const float n = y[j][i] * gate * rstd;
-          const float dv = rstd * fmaf(-n, mean, wd);
-          dy[i] = dv * gate;
-          dz[i] = dv * y[j][i] * slope;
+        for (int i = 0; i < VEC; i++) {
+          const float t = rstd * fmaf(m[j][i], c, w[j][i] * dv[i]);
+          dy[i] = t * g[j][i];
+          b[j][i] *= t;
         }
       }
-      if (rok && okc[j]) {
-        st_cols((IO*)a.d_y + row * a.ld_d_y + pos.col0 + col[j], dy);
-        st_cols((IO*)a.d_z + row * a.ld_d_z + pos.col0 + col[j], dz);
+      if (ok) {
+        st_cols((IO*)a.d_y + row * a.ld_d_y + col[j], dy);
+        st_cols((IO*)a.d_z + row * a.ld_d_z + col[j], b[j]);
       }
     }
   }
-  if (a.d_w) store_partial<VEC, NJ>(dw, pos, pl, col, okc, a.cols, a.part, slots);
+  cp_async_wait(0);
+  if (a.d_w) store_partial<VEC, NJ>(dw, pl, pos, col, okc, a.cols, a.part, (float*)ring);
 }
 
-template <typename IO, int VEC, int NJ, int MAXT>
-void fwd_launch(const GatedNormFwd& a, const RowPlan& pl, cudaStream_t st) {
-  gated_norm_fwd_kernel<IO, VEC, NJ, MAXT><<<dim3(pl.nbx, pl.nby), pl.threads, 0, st>>>(a, pl);
+template <typename IO, int VEC, int NJ, int MAXT, int MINB>
+cudaError_t fwd_launch(const GatedNormFwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
+  const uint32_t slot = 2 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
+  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  return launch_rows(gated_norm_fwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl, pl.slots * slot, st);
 }
-template <typename IO, int VEC, int NJ, int MAXT>
-void bwd_launch(const GatedNormBwd& a, const RowPlan& pl, cudaStream_t st) {
-  gated_norm_bwd_kernel<IO, VEC, NJ, MAXT>
-      <<<dim3(pl.nbx, pl.nby), pl.threads, slots_bytes(pl, VEC, NJ), st>>>(a, pl);
+template <typename IO, int VEC, int NJ, int MAXT, int MINB>
+cudaError_t bwd_launch(const GatedNormBwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
+  const uint32_t slot = 3 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
+  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
+  return launch_rows(gated_norm_bwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl,
+                     ring > sums ? ring : sums, st);
 }
 
 template <typename IO>
 cudaError_t fwd_types(const GatedNormFwd& a, bool vec, int sms, cudaStream_t st) {
   const NormShape s = norm_shape(a.rows, a.group, a.cols / a.group, vec, sms, false);
-  const RowPlan& p = s.plan;
-  switch (s.variant) {
-    case kVec8x1: fwd_launch<IO, 8, 1, 1024>(a, p, st); break;
-    case kVec8x2: fwd_launch<IO, 8, 2, 256>(a, p, st); break;
-    case kVec8x4: fwd_launch<IO, 8, 4, 256>(a, p, st); break;
-    case kVec8x4Wide: fwd_launch<IO, 8, 4, 1024>(a, p, st); break;
-    case kOne2: fwd_launch<IO, 1, 2, 128>(a, p, st); break;
-    case kOne8: fwd_launch<IO, 1, 8, 1024>(a, p, st); break;
-    default: fwd_launch<IO, 1, 32, 1024>(a, p, st); break;
-  }
   count_launches(1);
-  return cudaGetLastError();
+#define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
+  return fwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant), st)
+  SSM_NORM_FWD_SWITCH(s.variant, SSM_LAUNCH)
+#undef SSM_LAUNCH
 }
 template <typename IO>
 cudaError_t bwd_types(const GatedNormBwd& a, bool vec, int sms, cudaStream_t st) {
   const NormShape s = norm_shape(a.rows, a.group, a.cols / a.group, vec, sms, true);
-  const RowPlan& p = s.plan;
-  switch (s.variant) {
-    case kVec8x1: bwd_launch<IO, 8, 1, 1024>(a, p, st); break;
-    case kVec8x2: bwd_launch<IO, 8, 2, 256>(a, p, st); break;
-    case kVec8x4: bwd_launch<IO, 8, 4, 256>(a, p, st); break;
-    case kVec8x4Wide: bwd_launch<IO, 8, 4, 1024>(a, p, st); break;
-    case kOne2: bwd_launch<IO, 1, 2, 128>(a, p, st); break;
-    case kOne8: bwd_launch<IO, 1, 8, 1024>(a, p, st); break;
-    default: bwd_launch<IO, 1, 32, 1024>(a, p, st); break;
-  }
   count_launches(1);
-  if (cudaError_t e = cudaGetLastError()) return e;
-  return a.d_w ? launch_column_sums(a.part, p.nbx, a.cols, a.d_w, st) : cudaSuccess;
+  cudaError_t e;
+#define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
+  e = bwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant), st)
+  SSM_NORM_BWD_SWITCH(s.variant, SSM_LAUNCH)
+#undef SSM_LAUNCH
+  if (e != cudaSuccess || !a.d_w) return e;
+  return launch_column_sums(a.part, s.plan.nbx, a.cols, a.d_w, nullptr, st);
 }
 
 }  // namespace

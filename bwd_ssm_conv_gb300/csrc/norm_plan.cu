@@ -8,53 +8,77 @@ namespace {
 
 constexpr int kFewRows = 4;  // rows per SM below which a row is spread over more threads
 
-// out[c] = sum_b part[b][c]: 32 columns x 32 slices per block, every slice in order, then the
-// slices in order.
-__global__ void __launch_bounds__(1024) column_sums_kernel(const float* __restrict__ part, int n,
-                                                           int cols, float* __restrict__ out) {
-  __shared__ float s[32][33];
-  const int c = blockIdx.x * 32 + threadIdx.x;
-  float v = 0.0f;
-  if (c < cols) {
-#pragma unroll 8
-    for (int b = threadIdx.y; b < n; b += 32) v += __ldg(part + (long long)b * cols + c);
-  }
-  s[threadIdx.y][threadIdx.x] = v;
-  __syncthreads();
-  if (threadIdx.y == 0 && c < cols) {
-    float t = 0.0f;
+// out[c] = sum_b part[b][c]: a block sums 32 columns (blockIdx.x) of one of the sums (blockIdx.y),
+// 8 threads x 4 columns across and 128 slices of the rows, every slice in order, then the slices in
+// order.  Launched so that it may start while the kernel that writes `part` is still running; it
+// waits for that one's end here.
+__global__ void __launch_bounds__(1024) column_sums_kernel(const float* part, int n, int cols,
+                                                           float* out0, float* out1) {
+  __shared__ float s[128][33];
+  const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, c = blockIdx.x * 32 + 4 * tx;
+  float* out = blockIdx.y == 0 && out0 ? out0 : out1;
+  part += (long long)blockIdx.y * n * cols;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  float v[4] = {};
+  if (cols % 4 == 0) {
+    if (c < cols) {
+#pragma unroll 4
+      for (int b = ty; b < n; b += 128) {
+        const float4 p = *reinterpret_cast<const float4*>(part + (long long)b * cols + c);
+        v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      }
+    }
+  } else {
+#pragma unroll 4
+    for (int b = ty; b < n; b += 128)
 #pragma unroll
-    for (int i = 0; i < 32; i++) t += s[i][threadIdx.x];
-    out[c] = t;
+      for (int i = 0; i < 4; i++)
+        if (c + i < cols) v[i] += part[(long long)b * cols + c + i];
   }
+#pragma unroll
+  for (int i = 0; i < 4; i++) s[ty][4 * tx + i] = v[i];
+  __syncthreads();
+  // 32 threads per column: 4 slices each, then over the warp
+  const int w = threadIdx.x >> 5, l = threadIdx.x & 31;
+  float t = (s[4 * l][w] + s[4 * l + 1][w]) + (s[4 * l + 2][w] + s[4 * l + 3][w]);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  if (l == 0 && blockIdx.x * 32 + w < cols) out[blockIdx.x * 32 + w] = t;
 }
 
 }  // namespace
 
 NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, bool backward) {
   NormShape s{};
-  int nj, per_sm;
+  int nj;
   if (vec) {
     const int nch = group / 8;
     const bool few = rows * groups < (long long)kFewRows * sms;
     if (nch <= 32 || (few && nch <= 1024)) {
-      s.variant = kVec8x1, nj = 1;
-    } else if (nch <= 512 && (backward || nch <= 64)) {
-      s.variant = kVec8x2, nj = 2;
-    } else if (nch <= 1024) {
-      s.variant = kVec8x4, nj = 4;
+      nj = 1, s.variant = nch <= 256 ? kVec1 : kVec1Wide;
+    } else if (nch > 1024) {
+      nj = 4, s.variant = kVec4Wide;
+    } else if (backward && nch > 512) {
+      nj = 2, s.variant = kVec2Wide;
     } else {
-      s.variant = kVec8x4Wide, nj = 4;
+      // Of 4, 3 and 2 chunks per thread (2 and 1 in the backward, which keeps more of each) the one
+      // that leaves the fewest threads without a chunk, then the larger: on 32768 rows of 1536 bf16
+      // columns the forward takes 74 us with 3, 83 with 2 and 128 with 1, the backward 119, 108, 165.
+      int best = -1;
+      nj = 2;
+      for (int k = backward ? 2 : 4; k >= (backward ? 1 : 2); k--) {
+        const int tpr = row_threads(nch, k, 8), idle = tpr * k - nch;
+        if (tpr <= 256 && (best < 0 || idle < best)) nj = k, best = idle;
+      }
+      s.variant = nj == 1 ? kVec1 : (nj == 2 ? kVec2 : (nj == 3 ? kVec3 : kVec4));
     }
-    const int tpr = row_threads(nch, nj, 8);
-    per_sm = tpr <= 128 ? 8 : (tpr <= 256 ? 6 : 2);
-    s.plan = row_plan(rows, group, groups, tpr, 128, per_sm, sms);
+    s.plan = row_plan(rows, group, groups, row_threads(nch, nj, 8), 128,
+                      norm_threads_per_sm(s.variant), sms);
   } else {
-    nj = group <= 64 ? 2 : (group <= 8192 ? 8 : 32);
-    s.variant = nj == 2 ? kOne2 : (nj == 8 ? kOne8 : kOne32);
-    const int tpr = row_threads(group, nj, 1);
-    per_sm = tpr <= 128 ? 8 : (tpr <= 256 ? 6 : 2);
-    s.plan = row_plan(rows, group, groups, tpr, 128, per_sm, sms);
+    nj = group <= 64 ? 2 : (group <= 1024 ? 4 : (group <= 8192 ? 8 : 32));
+    s.variant = nj == 2 ? kOne2 : (nj == 4 ? kOne4 : (nj == 8 ? kOne8Wide : kOne32));
+    s.plan = row_plan(rows, group, groups, row_threads(group, nj, 1), 128,
+                      norm_threads_per_sm(s.variant), sms);
   }
   return s;
 }
@@ -69,10 +93,20 @@ size_t column_sums_bytes(long long rows, int group, int groups, int sms, int sum
   return sizeof(float) * (size_t)sums * n * group * groups;
 }
 
-cudaError_t launch_column_sums(const float* part, int n, int cols, float* out, cudaStream_t st) {
-  column_sums_kernel<<<(cols + 31) / 32, dim3(32, 32), 0, st>>>(part, n, cols, out);
+cudaError_t launch_column_sums(const float* part, int n, int cols, float* out0, float* out1,
+                               cudaStream_t st) {
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3((cols + 31) / 32, (out0 ? 1 : 0) + (out1 ? 1 : 0));
+  c.blockDim = dim3(1024);
+  c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, column_sums_kernel, part, n, cols, out0, out1);
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 }  // namespace ssm

@@ -77,34 +77,64 @@ __device__ __forceinline__ void st_cols(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]),
                                             bf16x2_rn(v[4], v[5]), bf16x2_rn(v[6], v[7]));
 }
-// The value as the type stores it.
-template <typename IO> __device__ __forceinline__ float rounded(float v);
-template <> __device__ __forceinline__ float rounded<float>(float v) { return v; }
-template <> __device__ __forceinline__ float rounded<__nv_bfloat16>(float v) {
-  return __bfloat162float(__float2bfloat16_rn(v));
+// Values as the type stores them: rounded once, here.
+__device__ __forceinline__ void to_cols(const float (&v)[1], Cols<float, 1>& c) { c.a = v[0]; }
+__device__ __forceinline__ void to_cols(const float (&v)[1], Cols<__nv_bfloat16, 1>& c) {
+  c.a = __float2bfloat16_rn(v[0]);
 }
-// fp32 parameters of VEC columns (1 where there are none).
+__device__ __forceinline__ void to_cols(const float (&v)[8], Cols<float, 8>& c) {
+#pragma unroll
+  for (int i = 0; i < 8; i++) c.a[i] = v[i];
+}
+__device__ __forceinline__ void to_cols(const float (&v)[8], Cols<__nv_bfloat16, 8>& c) {
+  c.a = make_uint4(bf16x2_rn(v[0], v[1]), bf16x2_rn(v[2], v[3]), bf16x2_rn(v[4], v[5]),
+                   bf16x2_rn(v[6], v[7]));
+}
+__device__ __forceinline__ void st_cols(float* p, const Cols<float, 1>& c) { *p = c.a; }
+__device__ __forceinline__ void st_cols(__nv_bfloat16* p, const Cols<__nv_bfloat16, 1>& c) {
+  *p = c.a;
+}
+__device__ __forceinline__ void st_cols(float* p, const Cols<float, 8>& c) { st_cols(p, c.a); }
+__device__ __forceinline__ void st_cols(__nv_bfloat16* p, const Cols<__nv_bfloat16, 8>& c) {
+  *reinterpret_cast<uint4*>(p) = c.a;
+}
+// fp32 parameters of VEC columns (1 where there are none), 16-byte aligned for VEC = 8.
 template <int VEC>
 __device__ __forceinline__ void ld_param(const float* p, int col, bool ok, float (&v)[VEC]) {
 #pragma unroll
-  for (int i = 0; i < VEC; i++) v[i] = (ok && p) ? __ldg(p + col + i) : 1.0f;
+  for (int i = 0; i < VEC; i++) v[i] = 1.0f;
+  if (ok && p) {
+    if constexpr (VEC == 1) {
+      v[0] = __ldg(p + col);
+    } else {
+      const float4 a = __ldg(reinterpret_cast<const float4*>(p + col));
+      const float4 b = __ldg(reinterpret_cast<const float4*>(p + col) + 1);
+      v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w;
+      v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+  }
 }
 
 // ---- the 8-bit block format (ssm_block.h) ------------------------------------------------------
-// A block's 32 columns lie in 32 / VEC consecutive lanes.  The largest magnitude is taken as an
-// unsigned comparison of the bits, which orders NaN above infinity above every finite value.
+// A block's 32 columns lie in 32 / VEC consecutive lanes.
+// The larger magnitude, NaN if either is one (its sign is left undefined).
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float r;
+  asm("max.NaN.xorsign.abs.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+// The bits of the block's largest magnitude (0x7f800000 and above: not finite).
 template <int VEC>
 __device__ __forceinline__ uint32_t block_top(const float (&v)[VEC]) {
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < VEC; i++) top = max(top, __float_as_uint(v[i]) & 0x7fffffffu);
   if constexpr (VEC == 1) {
-    top = __reduce_max_sync(0xffffffffu, top);
+    return __reduce_max_sync(0xffffffffu, __float_as_uint(v[0]) & 0x7fffffffu);
   } else {
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    float t = max_abs(max_abs(max_abs(v[0], v[1]), max_abs(v[2], v[3])),
+                      max_abs(max_abs(v[4], v[5]), max_abs(v[6], v[7])));
+    t = max_abs(t, __shfl_xor_sync(0xffffffffu, t, 1));
+    t = max_abs(t, __shfl_xor_sync(0xffffffffu, t, 2));
+    return __float_as_uint(t) & 0x7fffffffu;
   }
-  return top;
 }
 // E + 127 of a block, 255 where a value is not finite.
 __device__ __forceinline__ uint32_t block_exp(uint32_t top) {
@@ -116,35 +146,64 @@ __device__ __forceinline__ float block_up(uint32_t e) { return __uint_as_float((
 __device__ __forceinline__ float block_step(uint32_t e) {
   return __uint_as_float(e == 255u ? 0x7fc00000u : (e - 6u) << 23);
 }
-// Four values of a block as bytes: v 2^(6 - E) lies within +-128, is limited to +-127 and rounded to
-// the nearest even integer by adding 1.5 2^23, whose low byte is then the two's complement value.
-__device__ __forceinline__ uint32_t quant_bits(float v, float up) {
-  return __float_as_uint(fminf(fmaxf(v * up, -127.0f), 127.0f) + 12582912.0f);
+// A value as a byte: v 2^(6 - E), within +-128, is rounded to the nearest even integer by adding
+// 1.5 2^23 (one rounding, the product being exact); the low byte is then the two's complement value.
+// Only where the block's largest magnitude rounds up to 128 (its leading 8 bits are ones) does the
+// limit of +-127 matter: kLimit.
+template <bool kLimit> __device__ __forceinline__ uint32_t quant_bits(float v, float up) {
+  if constexpr (kLimit) v = fminf(fmaxf(v * up, -127.0f), 127.0f), up = 1.0f;
+  return __float_as_uint(fmaf(v, up, 12582912.0f));
 }
 __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
-// Quantises VEC columns of a row and stores them at q (and, in the block's first lane, *e).  Every
-// lane of the warp calls it; lanes with !ok hold zeros and store nothing.
+template <bool kLimit> __device__ __forceinline__ uint2 quant8(const float (&v)[8], float up) {
+  return make_uint2(pack_low_bytes(quant_bits<kLimit>(v[0], up), quant_bits<kLimit>(v[1], up),
+                                   quant_bits<kLimit>(v[2], up), quant_bits<kLimit>(v[3], up)),
+                    pack_low_bytes(quant_bits<kLimit>(v[4], up), quant_bits<kLimit>(v[5], up),
+                                   quant_bits<kLimit>(v[6], up), quant_bits<kLimit>(v[7], up)));
+}
+// The same from 8 values as bf16 pairs, which hold the largest magnitude as they are.
+__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b) {
+  uint32_t r;
+  asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+  return r;
+}
+__device__ __forceinline__ uint32_t block_top(const uint4& v) {
+  uint32_t t = max_abs2(max_abs2(v.x, v.y), max_abs2(v.z, v.w));
+  t = max_abs2(t, __shfl_xor_sync(0xffffffffu, t, 1));
+  t = max_abs2(t, __shfl_xor_sync(0xffffffffu, t, 2));
+  const uint32_t lo = (t << 16) & 0x7fffffffu, hi = t & 0x7fff0000u;
+  return lo > hi ? lo : hi;
+}
+// Quantises VEC columns of a row, whose block's largest magnitude is `top`, and stores them at q
+// (and, in the block's first lane, *e).  Every lane of the warp calls it; lanes with !ok hold zeros
+// and store nothing.
+template <int VEC>
+__device__ __forceinline__ void store_ckpt8_top(const float (&v)[VEC], uint32_t top, bool ok,
+                                                int8_t* q, uint8_t* e) {
+  const uint32_t x = block_exp(top);
+  const float up = block_up(x);
+  if constexpr (VEC == 1) {
+    if (ok) *q = x == 255u ? (int8_t)0 : (int8_t)(quant_bits<true>(v[0], up) & 0xffu);
+  } else {
+    uint2 w;
+    // rare: a block that holds 1.9921875 2^E (127.5 steps) or more, or what is not finite
+    if (__any_sync(0xffffffffu, (top & 0x7fffffu) >= 0x7f0000u || x == 255u)) {
+      w = quant8<true>(v, up);
+      if (x == 255u) w = make_uint2(0u, 0u);
+    } else {
+      w = quant8<false>(v, up);
+    }
+    if (ok) *reinterpret_cast<uint2*>(q) = w;
+  }
+  if (ok && (threadIdx.x & (32 / VEC - 1)) == 0) *e = (uint8_t)x;
+}
 template <int VEC>
 __device__ __forceinline__ void store_ckpt8(const float (&v)[VEC], bool ok, int8_t* q, uint8_t* e) {
-  const uint32_t x = block_exp(block_top<VEC>(v));
-  const float up = block_up(x);
-  if (ok) {
-    if constexpr (VEC == 1) {
-      *q = x == 255u ? (int8_t)0 : (int8_t)(quant_bits(v[0], up) & 0xffu);
-    } else {
-      uint2 w;
-      w.x = pack_low_bytes(quant_bits(v[0], up), quant_bits(v[1], up), quant_bits(v[2], up),
-                           quant_bits(v[3], up));
-      w.y = pack_low_bytes(quant_bits(v[4], up), quant_bits(v[5], up), quant_bits(v[6], up),
-                           quant_bits(v[7], up));
-      if (x == 255u) w = make_uint2(0u, 0u);
-      *reinterpret_cast<uint2*>(q) = w;
-    }
-    if ((threadIdx.x & (32 / VEC - 1)) == 0) *e = (uint8_t)x;
-  }
+  store_ckpt8_top<VEC>(v, block_top<VEC>(v), ok, q, e);
 }
+
 // VEC columns of a checkpoint: the loaded bits, and their values.
 template <int VEC> struct Kept;
 template <> struct Kept<1> {
@@ -181,6 +240,7 @@ struct RowPlan {
   int tpr, gpb, rpb;  // tpr > 32: gpb = rpb = 1
   int group, groups;
   int threads, nbx, nby;
+  int slots;  // rows in shared memory at a time (1 .. 3)
 };
 
 struct RowPos {
@@ -215,6 +275,159 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*part)[32], in
   return s;
 }
 
+// ---- rows ahead ---------------------------------------------------------------------------------
+// A thread's own chunks of the rows to come are copied to shared memory while it works on the
+// current one (cp.async, 8 columns at a time, RowPlan::slots rows in all).  It alone reads what it
+// copied, so no barrier is needed, and it may read a row twice, before and after the row's sum,
+// instead of holding it in registers.  Without RING (single columns, and rows too wide for it) it
+// reads global memory each time.
+
+__device__ __forceinline__ uint32_t shared_addr(const void* p) {
+  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+// The same through L1, for a thread's two halves of a 32-byte sector: the second finds it there.
+__device__ __forceinline__ void cp_async16_l1(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async8(uint32_t dst, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() {
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
+// Waits until at most the newest n (0 .. 2) groups are pending.
+__device__ __forceinline__ void cp_async_wait(int n) {
+  if (n == 2) asm volatile("cp.async.wait_group 2;" ::: "memory");
+  else if (n == 1) asm volatile("cp.async.wait_group 1;" ::: "memory");
+  else asm volatile("cp.async.wait_group 0;" ::: "memory");
+}
+__device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
+  uint4 v;
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// One operand, a tensor t or (q given) its checkpoint, and a thread's NJ chunks of its rows.
+template <typename IO, int VEC, int NJ, bool RING> struct Operand {
+  static constexpr int kUnits = RING ? (int)sizeof(IO) / 2 : 0;  // 16 bytes per chunk and row
+  const void* t;
+  const int8_t* q;
+  const uint8_t* e;
+  long long ld;
+  uint32_t at;  // this thread's place in the first slot of the ring
+
+  __device__ __forceinline__ bool given() const { return t || q; }
+  // Bytes that a block's threads need per slot of the ring.
+  static __host__ __device__ constexpr uint32_t slot_bytes(int threads) {
+    return 16u * kUnits * NJ * threads;
+  }
+  // Starts the copies of a row; col: the thread's chunks, `s` the byte offset of the ring slot.
+  __device__ __forceinline__ void issue(uint32_t s, long long row, const int (&col)[NJ],
+                                        const bool (&okc)[NJ], int cols) const {
+    if constexpr (RING) {
+      const uint32_t unit = 16 * blockDim.x;
+      if (q) {
+        const int8_t* p = q + row * cols;
+#pragma unroll
+        for (int j = 0; j < NJ; j++)
+          if (okc[j]) cp_async8(at + s + j * kUnits * unit, p + col[j]);
+      } else if (t) {
+        const IO* p = (const IO*)t + row * ld;
+#pragma unroll
+        for (int j = 0; j < NJ; j++)
+          if (okc[j])
+#pragma unroll
+            for (int u = 0; u < kUnits; u++) {
+              const uint32_t dst = at + s + (j * kUnits + u) * unit;
+              const char* src = (const char*)(p + col[j]) + 16 * u;
+              if constexpr (kUnits == 1) cp_async16(dst, src);
+              else cp_async16_l1(dst, src);
+            }
+      }
+    }
+  }
+  // Zeros in the slot at s: for the chunks that the thread does not have, which are never copied to
+  // (so once is enough), or for all of them, where there is no row to copy.
+  __device__ __forceinline__ void clear(uint32_t s, const bool (&okc)[NJ], bool all) const {
+    if constexpr (RING) {
+#pragma unroll
+      for (int j = 0; j < NJ; j++)
+        if (all || !okc[j] || !given())
+#pragma unroll
+          for (int u = 0; u < kUnits; u++)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(
+                             at + s + (j * kUnits + u) * 16 * blockDim.x),
+                         "r"(0u)
+                         : "memory");
+    }
+  }
+  // The scale byte of a chunk (a checkpoint's; 7 otherwise).
+  __device__ __forceinline__ uint32_t scale(bool ok, long long row, int col, int nb) const {
+    return q && ok ? e[row * nb + col / 32] : 7u;
+  }
+  // The largest magnitude's bits of the block that a tensor's chunk lies in; v holds its values.
+  __device__ __forceinline__ uint32_t top(uint32_t s, int j, const float (&v)[VEC]) const {
+    if constexpr (RING && sizeof(IO) == 2)
+      return block_top(ld_shared16(at + s + j * kUnits * 16 * blockDim.x));
+    else
+      return block_top<VEC>(v);
+  }
+  // A chunk's values (x is its scale byte); zeros for a chunk that the thread does not have.
+  __device__ __forceinline__ void get(uint32_t s, int j, bool ok, long long row, int col, int cols,
+                                      uint32_t x, float (&v)[VEC]) const {
+    if constexpr (VEC == 1) {
+      if (!ok || !given()) {
+        v[0] = 0.0f;
+      } else if (q) {
+        v[0] = (float)q[row * cols + col] * block_step(x);
+      } else {
+        Cols<IO, 1> c;
+        c.load((const IO*)t + row * ld + col);
+        c.get(v);
+      }
+    } else if constexpr (!RING) {
+      if (!ok || !given()) {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) v[i] = 0.0f;
+      } else if (q) {
+        Kept<8> k;
+        k.q = *reinterpret_cast<const uint2*>(q + row * cols + col);
+        k.e = (uint8_t)x;
+        k.get(v);
+      } else {
+        Cols<IO, 8> c;
+        c.load((const IO*)t + row * ld + col);
+        c.get(v);
+      }
+    } else {
+      const uint32_t unit = 16 * blockDim.x, a = at + s + j * kUnits * unit;
+      const uint4 w = ld_shared16(a);
+      if (q) {
+        Kept<8> k;
+        k.q = make_uint2(w.x, w.y);
+        k.e = (uint8_t)x;
+        k.get(v);
+      } else if constexpr (sizeof(IO) == 2) {
+        Cols<IO, 8> c;
+        c.a = w;
+        c.get(v);
+      } else {
+        const uint4 w2 = ld_shared16(a + unit);
+        v[0] = __uint_as_float(w.x), v[1] = __uint_as_float(w.y);
+        v[2] = __uint_as_float(w.z), v[3] = __uint_as_float(w.w);
+        v[4] = __uint_as_float(w2.x), v[5] = __uint_as_float(w2.y);
+        v[6] = __uint_as_float(w2.z), v[7] = __uint_as_float(w2.w);
+      }
+    }
+  }
+};
+
 // ---- host: launch plans ---------------------------------------------------------------------
 inline int round_up32(int v) { return (v + 31) / 32 * 32; }
 
@@ -227,13 +440,13 @@ inline int row_threads(int nch, int nj, int vec) {
   return p;
 }
 
-inline RowPlan row_plan(long long rows, int group, int groups, int tpr, int block, int per_sm,
+inline RowPlan row_plan(long long rows, int group, int groups, int tpr, int block, int per_sm_threads,
                         int sms) {
   RowPlan p{};
   p.tpr = tpr;
   p.group = group;
   p.groups = groups;
-  p.gpb = p.rpb = 1;
+  p.gpb = p.rpb = p.slots = 1;
   if (tpr <= 32) {
     const int teams = block / tpr > 0 ? block / tpr : 1;
     p.gpb = groups < teams ? groups : teams;
@@ -243,10 +456,32 @@ inline RowPlan row_plan(long long rows, int group, int groups, int tpr, int bloc
   p.threads = round_up32(p.tpr * p.gpb * p.rpb);
   p.nby = (groups + p.gpb - 1) / p.gpb;
   const long long need = (rows + p.rpb - 1) / p.rpb;
+  // one round of blocks, each stepping over the rows
+  const int per_sm = p.threads >= per_sm_threads ? 1 : per_sm_threads / p.threads;
   const long long most = ((long long)sms * per_sm + p.nby - 1) / p.nby;
   p.nbx = (int)(need < most ? need : most);
   if (p.nbx < 1) p.nbx = 1;
   return p;
+}
+
+// Rows in shared memory: as many, up to 3, as leave room for per_sm_threads threads on an SM.
+constexpr int kRingBytesPerSm = 208 * 1024;
+inline int ring_slots(uint32_t slot_bytes, int threads, int per_sm_threads) {
+  if (!slot_bytes) return 1;
+  const int blocks = threads >= per_sm_threads ? 1 : per_sm_threads / threads;
+  const int n = (int)(kRingBytesPerSm / ((long long)slot_bytes * blocks));
+  return n < 1 ? 1 : (n > 3 ? 3 : n);
+}
+// Launches with `smem` bytes of dynamic shared memory; more than 48 KB in all has to be asked for.
+template <typename K, typename A>
+inline cudaError_t launch_rows(K kernel, const A& a, const RowPlan& p, size_t smem,
+                               cudaStream_t st) {
+  if (smem > 40 * 1024)  // with the static part, 48 KB at most without asking
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)smem))
+      return e;
+  kernel<<<dim3(p.nbx, p.nby), p.threads, smem, st>>>(a, p);
+  return cudaGetLastError();
 }
 
 }  // namespace ssm
