@@ -79,7 +79,7 @@ def lib():
         L.ssm_norm_bwd_workspace_size.restype = _sz
         L.ssm_ckpt8_save.argtypes = [_vp, _ll, _vp, _vp, _ll, _i, _i, _vp]
         L.ssm_ckpt8_load.argtypes = [_vp, _vp, _vp, _ll, _ll, _i, _i, _vp]
-        L.ssm_ckpt8_wgrad_workspace_size.argtypes = [_ll, _i, _i, _i]
+        L.ssm_ckpt8_wgrad_workspace_size.argtypes = [_ll, _i, _i, _i, _i]
         L.ssm_ckpt8_wgrad_workspace_size.restype = _sz
         L.ssm_ckpt8_wgrad.argtypes = [_vp, _ll, _vp, _vp, _vp, _ll, _i, _i, _i, _u, _vp, _sz, _vp]
         _L = L
@@ -105,9 +105,9 @@ def _norm_ws(rows, cols, group, sums, device):
 
 
 @lru_cache(maxsize=1024)
-def _wgrad_ws(tokens, m, k, io, device):
+def _wgrad_ws(tokens, m, k, io, aligned, device):
     with torch.cuda.device(device):
-        return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io))
+        return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io, aligned))
 
 
 def _io(t: torch.Tensor, name: str) -> int:
@@ -405,8 +405,8 @@ def ssm_ckpt8_load(c, dtype=torch.bfloat16, out=None, stream=None):
     return o
 
 
-def ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io=SSM_BF16) -> int:
-    return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io))
+def ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io=SSM_BF16, aligned=True) -> int:
+    return int(lib().ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io, 1 if aligned else 0))
 
 
 def ssm_ckpt8_wgrad(g, x8, accumulate=False, ws=None, out=None, stream=None):
@@ -421,10 +421,13 @@ def ssm_ckpt8_wgrad(g, x8, accumulate=False, ws=None, out=None, stream=None):
     o = torch.empty(m, k, dtype=torch.float32, device=g.device) if out is None else out
     if out is not None and out.shape != (m, k):
         raise ValueError(f"out must have shape {(m, k)}, got {tuple(out.shape)}")
-    ws, size, mine = _workspace(_wgrad_ws(tokens, m, k, io, g.device), g.device, ws)
+    pg, ld = _rows(g, "g")
+    pq, pe = _kept(x8, "x8", (*g.shape[:-1], k))
+    aligned = not ((pg | pq) & 15 or (ld or m) & 7)
+    ws, size, mine = _workspace(_wgrad_ws(tokens, m, k, io, aligned, g.device), g.device, ws)
     rc = (_L or lib()).ssm_ckpt8_wgrad(
-        *_rows(g, "g"), *_kept(x8, "x8", (*g.shape[:-1], k)), _f32(o, "out", m * k), tokens, m, k,
-        io, SSM_WGRAD_ACCUMULATE if accumulate else 0, ws.data_ptr(), size,
+        pg, ld, pq, pe, _f32(o, "out", m * k), tokens, m, k, io,
+        SSM_WGRAD_ACCUMULATE if accumulate else 0, ws.data_ptr(), size,
         _on(stream, g, o if out is None else None, mine))
     if rc:
         _check("ssm_ckpt8_wgrad", rc)

@@ -175,12 +175,14 @@ struct Wgrad {
   long long tokens;
   int m, k, io, accumulate;
 };
-size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, int sms);
+bool wgrad_aligned(const Wgrad& a);  // g's and q's rows are 16-byte aligned, widths permitting
+size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int sms);
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st);
-// The tensor-core kernel (wgrad8_tc.cu): bf16 g whose rows TMA can read.  part: the splits' tiles,
-// [splits][m][k], or NULL with one split.
-bool wgrad_tc_applies(const Wgrad& a);
-int wgrad_tc_splits(long long tokens, int m, int k, int sms);
-cudaError_t launch_wgrad_tc(const Wgrad& a, float* part, int splits, int* status, cudaStream_t st);
+// The tensor-core kernel (wgrad8_tc.cu): g as `terms` bf16 planes [tokens] x ld_g, q with rows of ld_q
+// bytes.  part: the splits' tiles, [splits][m][k], or NULL with one split.
+int wgrad_tc_splits(long long tokens, int terms, int m, int k, int sms);
+cudaError_t launch_wgrad_tc(const void* g, long long ld_g, int terms, const int8_t* q,
+                            long long ld_q, const Wgrad& a, float* part, int splits, int* status,
+                            cudaStream_t st);
 
 }  // namespace ssm

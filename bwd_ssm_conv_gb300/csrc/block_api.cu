@@ -12,6 +12,8 @@
 namespace {
 
 constexpr long long kMaxTotal = 1LL << 40;
+constexpr long long kMaxWgrad = 1LL << 38;  // elements of g and of X there
+constexpr long long kMaxTokens = 1LL << 29;  // of the weight gradient
 constexpr int kMaxDim = 1 << 20;  // m and k of the weight gradient, columns of a checkpoint
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -265,15 +267,16 @@ int ssm_ckpt8_load(const int8_t* q, const uint8_t* e, void* out, long long ld_ou
 
 static int wgrad_check(long long tokens, int m, int k, int io) {
   if (tokens <= 0 || m <= 0 || k <= 0 || !io_size(io)) return SSM_ERR_INVALID_ARG;
-  if (m > kMaxDim || k > kMaxDim || tokens > kMaxTotal / m || tokens > kMaxTotal / k)
+  if (m > kMaxDim || k > kMaxDim || tokens > kMaxTokens || tokens > kMaxWgrad / m ||
+      tokens > kMaxWgrad / k)
     return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
-size_t ssm_ckpt8_wgrad_workspace_size(long long tokens, int m, int k, int io) {
+size_t ssm_ckpt8_wgrad_workspace_size(long long tokens, int m, int k, int io, int aligned) {
   if (wgrad_check(tokens, m, k, io) != SSM_OK) return 0;
   const int sms = num_sms();
-  return sms <= 0 ? 0 : ssm::wgrad_ws_bytes(tokens, m, k, io, sms);
+  return sms <= 0 ? 0 : ssm::wgrad_ws_bytes(tokens, m, k, io, aligned != 0, sms);
 }
 
 int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_t* e, float* d_W,
@@ -285,14 +288,15 @@ int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_
     return SSM_ERR_INVALID_ARG;
   if (ld_g == 0) ld_g = m;
   if (ld_g < m || !aligned(g, io_size(io)) || !aligned(d_W, 4)) return SSM_ERR_INVALID_ARG;
-  if (!ld_fits(ld_g, tokens)) return SSM_ERR_UNSUPPORTED;
+  if (ld_g > kMaxWgrad / tokens) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
-  if (!ws || !aligned(ws, 256) || ws_bytes < ssm::wgrad_ws_bytes(tokens, m, k, io, sms))
+  ssm::Wgrad a{g, ld_g, q, e, d_W, tokens, m, k, io, (flags & SSM_WGRAD_ACCUMULATE) ? 1 : 0};
+  if (!ws || !aligned(ws, 256) ||
+      ws_bytes < ssm::wgrad_ws_bytes(tokens, m, k, io, ssm::wgrad_aligned(a), sms))
     return SSM_ERR_WORKSPACE;
   cudaStream_t st = (cudaStream_t)stream;
   if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return SSM_ERR_CUDA;
-  ssm::Wgrad a{g, ld_g, q, e, d_W, tokens, m, k, io, (flags & SSM_WGRAD_ACCUMULATE) ? 1 : 0};
   return status_of(ssm::launch_wgrad(a, ws, sms, st));
 }
 

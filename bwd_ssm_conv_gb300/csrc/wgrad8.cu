@@ -1,9 +1,10 @@
-// wgrad8.cu -- d_W[i][j] (+)= sum_t g[t][i] X[t][j] with X read from its 8-bit checkpoint: the
-// general kernel, in fp32 arithmetic, for any size, stride and type.
-//
-// A block forms a 64 x 64 tile of d_W over a range of tokens, 4 x 4 values per thread, from
-// tiles of 16 tokens staged in shared memory as fp32.  Where the tiles alone leave SMs idle the
-// tokens are split over blocks; the splits' tiles go to the workspace and are added in order.
+// wgrad8.cu -- d_W[i][j] (+)= sum_t g[t][i] X[t][j] with X read from its 8-bit checkpoint: what
+// happens around the tensor-core kernel of wgrad8_tc.cu.
+//   before  operands that it cannot read as they are go to the workspace in a form that it can:
+//           fp32 g as three bf16 terms, rows that are not 16-byte aligned with their rows padded
+//   after   where the tokens are split over blocks, the splits' tiles are added in order
+// The copies read and write each value once: on g 4096 x 1024 fp32 that is 42 MB beside the 3 x 8.6
+// GFLOP per 1024 columns of X.
 #include "block.cuh"
 #include "rows.cuh"
 
@@ -11,114 +12,193 @@ namespace ssm {
 
 namespace {
 
-constexpr int kTile = 64, kDepth = 16, kThreads = 256;
+constexpr int kThreads = 256;
 
-__device__ __forceinline__ float as_f(float v) { return v; }
-__device__ __forceinline__ float as_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-
-template <typename IO>
-__global__ void __launch_bounds__(kThreads) wgrad8_kernel(const Wgrad a, float* part,
-                                                          long long per_split) {
-  __shared__ float sg[kDepth][kTile + 4], sx[kDepth][kTile + 4];
-  const int tid = threadIdx.x, i0 = blockIdx.y * kTile, j0 = blockIdx.x * kTile;
-  const long long t_begin = blockIdx.z * per_split;
-  const long long t_end = t_begin + per_split < a.tokens ? t_begin + per_split : a.tokens;
-  const int nb = (a.k + 31) / 32;
-  const int ti = tid / 16, tj = tid % 16;
-  float acc[4][4] = {};
-  for (long long t0 = t_begin; t0 < t_end; t0 += kDepth) {
+// A thread pads 8 columns of a row of bf16 g.
+__global__ void __launch_bounds__(kThreads) pad_g_kernel(const __nv_bfloat16* g, long long ld,
+                                                         __nv_bfloat16* out, int m, int m8,
+                                                         long long n) {
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kThreads) {
+    const long long t = i / (m8 / 8);
+    const int c = (int)(i - t * (m8 / 8)) * 8;
+    const __nv_bfloat16* p = g + t * ld + c;
+    uint32_t w[4];
 #pragma unroll
-    for (int r = 0; r < kDepth * kTile / kThreads; r++) {
-      const int at = tid + r * kThreads, tt = at / kTile, c = at % kTile;
-      const long long t = t0 + tt;
-      float gv = 0.0f, xv = 0.0f;
-      if (t < t_end) {
-        if (i0 + c < a.m) gv = as_f(((const IO*)a.g)[t * a.ld_g + i0 + c]);
-        if (j0 + c < a.k)
-          xv = (float)a.q[t * a.k + j0 + c] * block_step(a.e[t * nb + (j0 + c) / 32]);
-      }
-      sg[tt][c] = gv;
-      sx[tt][c] = xv;
+    for (int j = 0; j < 4; j++) {
+      const uint32_t lo = c + 2 * j < m ? __bfloat16_as_ushort(p[2 * j]) : 0u;
+      const uint32_t hi = c + 2 * j + 1 < m ? __bfloat16_as_ushort(p[2 * j + 1]) : 0u;
+      w[j] = lo | hi << 16;
     }
-    __syncthreads();
-#pragma unroll
-    for (int tt = 0; tt < kDepth; tt++) {
-      const float4 gv = *reinterpret_cast<const float4*>(&sg[tt][4 * ti]);
-      const float4 xv = *reinterpret_cast<const float4*>(&sx[tt][4 * tj]);
-      const float gs[4] = {gv.x, gv.y, gv.z, gv.w}, xs[4] = {xv.x, xv.y, xv.z, xv.w};
-#pragma unroll
-      for (int u = 0; u < 4; u++)
-#pragma unroll
-        for (int v = 0; v < 4; v++) acc[u][v] = fmaf(gs[u], xs[v], acc[u][v]);
-    }
-    __syncthreads();
+    *reinterpret_cast<uint4*>(out + t * m8 + c) = make_uint4(w[0], w[1], w[2], w[3]);
   }
-  float* dst = part ? part + (long long)blockIdx.z * a.m * a.k : a.d_W;
-#pragma unroll
-  for (int u = 0; u < 4; u++)
-#pragma unroll
-    for (int v = 0; v < 4; v++) {
-      const int i = i0 + 4 * ti + u, j = j0 + 4 * tj + v;
-      if (i < a.m && j < a.k) {
-        const long long at = (long long)i * a.k + j;
-        dst[at] = !part && a.accumulate ? dst[at] + acc[u][v] : acc[u][v];
-      }
-    }
 }
 
-__global__ void wgrad8_sum_kernel(const float* __restrict__ part, int splits, long long n,
-                                  float* d_W, int accumulate) {
-  for (long long i = blockIdx.x * (long long)blockDim.x + threadIdx.x; i < n;
-       i += (long long)gridDim.x * blockDim.x) {
+// fp32 as three bf16 terms: 8 leading bits of the 24, the next 8 and the last 8, cut off rather than
+// rounded, so that the terms' sum is the value exactly (above the smallest normal numbers).  What is
+// not finite stays so in the first term.
+__device__ __forceinline__ void three_bf16(float v, uint32_t (&h)[3]) {
+  const uint32_t b = __float_as_uint(v);
+  h[0] = b >> 16, h[1] = h[2] = 0u;
+  if ((b & 0x7f800000u) == 0x7f800000u) {
+    if (b & 0x7fffffu) h[0] = 0x7fc0u;
+    return;
+  }
+  const float r = v - __uint_as_float(b & 0xffff0000u);
+  const uint32_t rb = __float_as_uint(r);
+  h[1] = rb >> 16;
+  h[2] = __float_as_uint(r - __uint_as_float(rb & 0xffff0000u)) >> 16;
+}
+
+// A thread splits 8 columns of a row of fp32 g into planes [3][tokens][m8].
+template <bool VEC>
+__global__ void __launch_bounds__(kThreads) split_g_kernel(const float* g, long long ld,
+                                                           __nv_bfloat16* out, long long plane,
+                                                           int m, int m8, long long n) {
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kThreads) {
+    const long long t = i / (m8 / 8);
+    const int c = (int)(i - t * (m8 / 8)) * 8;
+    const float* p = g + t * ld + c;
+    float v[8];
+    if constexpr (VEC) {
+      Cols<float, 8> x;
+      x.load(p);
+      x.get(v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; j++) v[j] = c + j < m ? p[j] : 0.0f;
+    }
+    uint32_t w[3][4];
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+      uint32_t a[3], b[3];
+      three_bf16(v[2 * j], a);
+      three_bf16(v[2 * j + 1], b);
+#pragma unroll
+      for (int r = 0; r < 3; r++) w[r][j] = a[r] | b[r] << 16;
+    }
+#pragma unroll
+    for (int r = 0; r < 3; r++)
+      *reinterpret_cast<uint4*>(out + r * plane + t * m8 + c) =
+          make_uint4(w[r][0], w[r][1], w[r][2], w[r][3]);
+  }
+}
+
+// A thread pads 16 columns of a row of q.
+__global__ void __launch_bounds__(kThreads) pad_q_kernel(const int8_t* q, int8_t* out, int k,
+                                                         int k16, long long n) {
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kThreads) {
+    const long long t = i / (k16 / 16);
+    const int c = (int)(i - t * (k16 / 16)) * 16;
+    const uint8_t* p = (const uint8_t*)q + t * k + c;
+    uint32_t w[4] = {};
+#pragma unroll
+    for (int j = 0; j < 16; j++)
+      if (c + j < k) w[j / 4] |= (uint32_t)p[j] << (8 * (j % 4));
+    *reinterpret_cast<uint4*>(out + t * k16 + c) = make_uint4(w[0], w[1], w[2], w[3]);
+  }
+}
+
+__global__ void __launch_bounds__(kThreads) wgrad8_sum_kernel(const float* part, int splits,
+                                                              long long n, float* d_W,
+                                                              int accumulate) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the tiles are complete
+  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
+       i += (long long)gridDim.x * kThreads) {
     float v = 0.0f;
-    for (int s = 0; s < splits; s++) v += __ldg(part + s * n + i);
+#pragma unroll 4
+    for (int s = 0; s < splits; s++) v += part[s * n + i];
     d_W[i] = accumulate ? d_W[i] + v : v;
   }
 }
 
-// Splits of the tokens: enough for two blocks per SM, at least 256 tokens each.
-int splits_of(long long tokens, int m, int k, int sms) {
-  const long long tiles = (long long)((m + kTile - 1) / kTile) * ((k + kTile - 1) / kTile);
-  long long s = (2LL * sms + tiles - 1) / tiles, most = (tokens + 255) / 256;
-  if (s > most) s = most;
-  return (int)(s < 1 ? 1 : s);
+int blocks_of(long long n, int sms) {
+  const long long b = (n + kThreads - 1) / kThreads;
+  return (int)(b < 16LL * sms ? b : 16LL * sms);
+}
+
+// The workspace after the status word: g's copy, q's copy, the splits' tiles.
+struct Plan {
+  int terms, splits, m8, k16;
+  bool copy_g, copy_q;
+  size_t g, q, part, bytes;
+};
+Plan plan_of(long long tokens, int m, int k, int io, bool aligned, int sms) {
+  Plan p{};
+  p.terms = io == SSM_F32 ? 3 : 1;
+  p.m8 = (m + 7) / 8 * 8;
+  p.k16 = (k + 15) / 16 * 16;
+  p.copy_g = io == SSM_F32 || p.m8 != m || !aligned;
+  p.copy_q = p.k16 != k || !aligned;
+  p.splits = wgrad_tc_splits(tokens, p.terms, m, k, sms);
+  p.g = kStatusBytes;
+  p.q = p.g + (p.copy_g ? align_up((size_t)p.terms * tokens * p.m8 * 2, 256) : 0);
+  p.part = p.q + (p.copy_q ? align_up((size_t)tokens * p.k16, 256) : 0);
+  p.bytes = p.part + (p.splits > 1 ? sizeof(float) * (size_t)p.splits * m * k : 0);
+  return p;
 }
 
 }  // namespace
 
-size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, int sms) {
-  // the larger of the two kernels': which one a call takes depends on its pointers and strides
-  int s = splits_of(tokens, m, k, sms);
-  if (io == SSM_BF16) {
-    const int t = wgrad_tc_splits(tokens, m, k, sms);
-    if (t > s) s = t;
-  }
-  return kStatusBytes + (s > 1 ? sizeof(float) * (size_t)s * m * k : 0);
+bool wgrad_aligned(const Wgrad& a) {
+  return a.ld_g % 8 == 0 && (uintptr_t)a.g % 16 == 0 && (uintptr_t)a.q % 16 == 0;
+}
+
+size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int sms) {
+  return plan_of(tokens, m, k, io, aligned, sms).bytes;
 }
 
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
-  const bool tc = wgrad_tc_applies(a);
-  const int s = tc ? wgrad_tc_splits(a.tokens, a.m, a.k, sms) : splits_of(a.tokens, a.m, a.k, sms);
-  float* part = s > 1 ? (float*)((char*)ws + kStatusBytes) : nullptr;
-  if (tc) {
-    if (cudaError_t e = launch_wgrad_tc(a, part, s, (int*)ws, st)) return e;
-  } else {
-    const long long per = ((a.tokens + s - 1) / s + kDepth - 1) / kDepth * kDepth;
-    const dim3 grid((a.k + kTile - 1) / kTile, (a.m + kTile - 1) / kTile, s);
-    if (a.io == SSM_F32)
-      wgrad8_kernel<float><<<grid, kThreads, 0, st>>>(a, part, per);
-    else
-      wgrad8_kernel<__nv_bfloat16><<<grid, kThreads, 0, st>>>(a, part, per);
+  const Plan p = plan_of(a.tokens, a.m, a.k, a.io, wgrad_aligned(a), sms);
+  char* w = (char*)ws;
+  const void* g = a.g;
+  long long ld_g = a.ld_g, ld_q = a.k;
+  const int8_t* q = a.q;
+  if (p.copy_g) {
+    __nv_bfloat16* out = (__nv_bfloat16*)(w + p.g);
+    const long long n = a.tokens * (p.m8 / 8);
+    if (a.io == SSM_F32) {
+      const bool vec = p.m8 == a.m && a.ld_g % 8 == 0 && (uintptr_t)a.g % 32 == 0;
+      auto kernel = vec ? split_g_kernel<true> : split_g_kernel<false>;
+      kernel<<<blocks_of(n, sms), kThreads, 0, st>>>((const float*)a.g, a.ld_g, out,
+                                                     a.tokens * p.m8, a.m, p.m8, n);
+    } else {
+      pad_g_kernel<<<blocks_of(n, sms), kThreads, 0, st>>>((const __nv_bfloat16*)a.g, a.ld_g, out,
+                                                           a.m, p.m8, n);
+    }
     count_launches(1);
     if (cudaError_t e = cudaGetLastError()) return e;
+    g = out;
+    ld_g = p.m8;
   }
-  if (part) {
-    const long long n = (long long)a.m * a.k, b = (n + 255) / 256;
-    wgrad8_sum_kernel<<<(int)(b < 8LL * sms ? b : 8LL * sms), 256, 0, st>>>(part, s, n, a.d_W,
-                                                                          a.accumulate);
+  if (p.copy_q) {
+    int8_t* out = (int8_t*)(w + p.q);
+    const long long n = a.tokens * (p.k16 / 16);
+    pad_q_kernel<<<blocks_of(n, sms), kThreads, 0, st>>>(a.q, out, a.k, p.k16, n);
     count_launches(1);
+    if (cudaError_t e = cudaGetLastError()) return e;
+    q = out;
+    ld_q = p.k16;
   }
-  return cudaGetLastError();
+  float* part = p.splits > 1 ? (float*)(w + p.part) : nullptr;
+  if (cudaError_t e = launch_wgrad_tc(g, ld_g, p.terms, q, ld_q, a, part, p.splits, (int*)ws, st))
+    return e;
+  if (!part) return cudaSuccess;
+  const long long n = (long long)a.m * a.k;
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks_of(n, sms));
+  c.blockDim = dim3(kThreads);
+  c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  count_launches(1);
+  return cudaLaunchKernelEx(&c, wgrad8_sum_kernel, (const float*)part, p.splits, n, a.d_W,
+                            a.accumulate);
 }
 
 }  // namespace ssm

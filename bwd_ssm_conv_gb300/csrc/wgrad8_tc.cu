@@ -1,10 +1,13 @@
 // wgrad8_tc.cu -- d_W[i][j] (+)= sum_t g[t][i] X[t][j] on the tensor cores, with X read from its
-// 8-bit checkpoint and g in bf16.
+// 8-bit checkpoint and g in bf16, or in fp32 as three bf16 terms (wgrad8.cu splits it).
 //
 // Both operands run along the tokens in memory's slow direction, so both are staged as they lie,
 // [tokens][columns] with the columns contiguous (the MMA's MN-major form, 128-byte swizzle): no
 // transposition anywhere.  A kept value q 2^(E-6) is exact in bf16, so the products are exact in
 // fp32 and the result differs from an fp32 one by the order and rounding of its additions only.
+//
+// The sum runs over stages of 64 tokens; with three terms, over the tokens three times, g's terms one
+// after the other and X again each time (its conversion costs nothing beside the MMAs).
 //
 // One or two CTAs (CG) form a 128 CG x 256 tile of d_W over a range of tokens, 64 tokens per stage.
 // With two, each holds its 128 rows' g and half of X's columns, and the MMAs (cta_group::2, issued
@@ -74,7 +77,8 @@ struct TcArgs {
   CUtensorMap g, q;
   const uint8_t* e;
   float* out;  // d_W, or the splits' partial tiles
-  long long tokens, per_split;
+  long long tokens;
+  int stages, per_term, per_split;  // in all, of one term of g, of one split
   int m, k, nb, accumulate, vec_out;
   int* status;
 };
@@ -281,9 +285,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
   const int rank = CG == 1 ? 0 : (blockIdx.x & 1);
   const int m0 = (blockIdx.y * CG + rank) * kTM, n0 = (blockIdx.x / CG) * kTN;
   const int nq = n0 + rank * L::NB;  // first column of X staged here
-  const long long t_begin = blockIdx.z * a.per_split;
-  const long long t_end = t_begin + a.per_split < a.tokens ? t_begin + a.per_split : a.tokens;
-  const int iters = (int)((t_end - t_begin + kTT - 1) / kTT);
+  const int s_begin = blockIdx.z * a.per_split;  // its stages: s_begin ... s_begin + iters - 1
+  const int iters = a.stages - s_begin < a.per_split ? a.stages - s_begin : a.per_split;
   const int segs = (iters + kSegment - 1) / kSegment;
   if (tid == 0) {
     for (int i = 0; i < S; i++) {
@@ -315,15 +318,15 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
       Ring<S> r;
-      int it = 0, t = (int)t_begin;
-      for (; it < iters; it++, t += kTT, r.next()) {
+      int it = 0, st = s_begin % a.per_term;
+      for (; it < iters; it++, st = st + 1 == a.per_term ? 0 : st + 1, r.next()) {
         if (it >= S && !mbar_wait(&q_empty[r.s], r.phase ^ 1)) {
           atomicExch(&bad, 1);
           break;
         }
         if (elect_one()) {
           mbar_expect_tx(&q_here[r.s], L::bytes_q);
-          tma_load_3d(smem + L::at_q + r.s * L::bytes_q, &a.q, nq, t, 0, &q_here[r.s]);
+          tma_load_3d(smem + L::at_q + r.s * L::bytes_q, &a.q, nq, st * kTT, 0, &q_here[r.s]);
         }
         __syncwarp();
       }
@@ -333,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     } else if (warp == 3) {
       uint64_t* here = rank == 0 ? full : g_here;
       Ring<S> r;
-      int it = 0, t = (int)t_begin;
-      for (; it < iters; it++, t += kTT, r.next()) {
+      int it = 0, term = s_begin / a.per_term, st = s_begin - term * a.per_term;
+      for (; it < iters; it++, r.next()) {
         if (it >= S && !mbar_wait(&empty[r.s], r.phase ^ 1)) {
           atomicExch(&bad, 1);
           break;
@@ -343,9 +346,11 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
           mbar_expect_tx(&here[r.s], kBytesA);
 #pragma unroll
           for (int c = 0; c < kTM / 64; c++)
-            tma_load_3d(smem + r.s * L::stage + c * kSlab, &a.g, m0 + 64 * c, t, 0, &here[r.s]);
+            tma_load_3d(smem + r.s * L::stage + c * kSlab, &a.g, m0 + 64 * c, st * kTT, term,
+                        &here[r.s]);
         }
         __syncwarp();
+        if (++st == a.per_term) st = 0, term++;
       }
       for (int j = it > S ? it - S : 0; j < it; j++)
         if (!mbar_wait(&here[j % S], (j / S) & 1)) break;
@@ -438,14 +443,14 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     const bool words = a.nb % 4 == 0 && (uintptr_t)a.e % 4 == 0;
     auto load_scales = [&](int seg) {
       uint2* dst = reinterpret_cast<uint2*>(scales + (seg & 1) * L::scales);
-      const long long t0 = t_begin + (long long)seg * kSegTokens;
       uint32_t v[kBatch];
 #pragma unroll
       for (int b = 0; b < kBatch; b++) {
         const int i = (tid - 128) + 32 * kSumWarps * b, blk = blk0 + 4 * (i % W);
-        const long long t = t0 + i / W;
+        const int st = (s_begin + seg * kSegment + i / W / kTT) % a.per_term;
+        const long long t = (long long)st * kTT + i / W % kTT;
         v[b] = 0x07070707u;
-        if (t < t_end && blk < a.nb) {
+        if (t < a.tokens && blk < a.nb) {
           const uint8_t* p = a.e + t * a.nb + blk;
           if (words) {
             v[b] = *reinterpret_cast<const uint32_t*>(p);
@@ -530,10 +535,6 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
   if (tid == 0 && bad) record_status(a.status, SSM_ERR_TIMEOUT);
 }
 
-long long tokens_per_split(long long tokens, int splits) {
-  return ((tokens + splits - 1) / splits + kTT - 1) / kTT * kTT;
-}
-
 // A tile of two CTAs where a row tile of one would be full.
 int ctas_of(int m) { return m > kTM ? 2 : 1; }
 
@@ -558,37 +559,39 @@ template <int CG> cudaError_t launch(const TcArgs& t, int splits, cudaStream_t s
   return e;
 }
 
+int per_split_of(int stages, int splits) { return (stages + splits - 1) / splits; }
+
 }  // namespace
 
-// Splits of the tokens: as many as fill the SMs once, at least 4 stages each.
-int wgrad_tc_splits(long long tokens, int m, int k, int sms) {
+// Splits of the stages: as many as fill the SMs once, at least 4 stages each.
+int wgrad_tc_splits(long long tokens, int terms, int m, int k, int sms) {
   const int cg = ctas_of(m);
   const long long tiles = (long long)((m + cg * kTM - 1) / (cg * kTM)) * ((k + kTN - 1) / kTN);
+  const int stages = terms * (int)((tokens + kTT - 1) / kTT);
   long long s = sms / cg / tiles;
-  const long long most = (tokens + 4 * kTT - 1) / (4 * kTT);
+  const int most = (stages + 3) / 4;
   if (s > most) s = most;
   if (s < 1) s = 1;
-  const long long per = tokens_per_split(tokens, (int)s);
-  return (int)((tokens + per - 1) / per);  // none of them empty
+  const int per = per_split_of(stages, (int)s);
+  return (stages + per - 1) / per;  // none of them empty
 }
 
-// What TMA can read: 16-byte aligned rows.
-bool wgrad_tc_applies(const Wgrad& a) {
-  return a.io == SSM_BF16 && a.ld_g % 8 == 0 && (uintptr_t)a.g % 16 == 0 && a.k % 16 == 0 &&
-         (uintptr_t)a.q % 16 == 0 && a.tokens < (1LL << 31);
-}
-
-cudaError_t launch_wgrad_tc(const Wgrad& a, float* part, int splits, int* status,
+// g: [terms][tokens] rows of ld_g elements, q: rows of ld_q bytes; both 16-byte aligned.
+cudaError_t launch_wgrad_tc(const void* g, long long ld_g, int terms, const int8_t* q,
+                            long long ld_q, const Wgrad& a, float* part, int splits, int* status,
                             cudaStream_t st) {
   const int cg = ctas_of(a.m);
   TcArgs t{};
-  if (!encode_tmap_3d(&t.g, a.g, 2, a.m, a.tokens, 1, a.ld_g, a.ld_g, 64, kTT, 1, 128) ||
-      !encode_tmap_3d(&t.q, a.q, 1, a.k, a.tokens, 1, a.k, a.k, kTN / cg, kTT, 1))
+  if (!encode_tmap_3d(&t.g, g, 2, a.m, a.tokens, terms, ld_g,
+                      terms > 1 ? ld_g * a.tokens : ld_g, 64, kTT, 1, 128) ||
+      !encode_tmap_3d(&t.q, q, 1, a.k, a.tokens, 1, ld_q, ld_q, kTN / cg, kTT, 1))
     return cudaErrorInvalidValue;
   t.e = a.e;
   t.out = part ? part : a.d_W;
   t.tokens = a.tokens;
-  t.per_split = tokens_per_split(a.tokens, splits);
+  t.per_term = (int)((a.tokens + kTT - 1) / kTT);
+  t.stages = terms * t.per_term;
+  t.per_split = per_split_of(t.stages, splits);
   t.m = a.m;
   t.k = a.k;
   t.nb = (a.k + 31) / 32;

@@ -186,8 +186,8 @@ def test_ckpt8_and_wgrad_refusals(L):
         assert wgrad(**{name: None}) == INV, name
     assert wgrad(t=0) == INV and wgrad(m=0) == INV and wgrad(k=-1) == INV and wgrad(io=2) == INV
     assert wgrad(flags=2) == INV and wgrad(ld=63) == INV and wgrad(d_W=FAKE + 2) == INV
-    assert wgrad(m=(1 << 20) + 1) == UNS and wgrad(t=1 << 40) == UNS
-    assert L.ssm_ckpt8_wgrad_workspace_size(0, 64, 64, 0) == 0
+    assert wgrad(m=(1 << 20) + 1) == UNS and wgrad(t=(1 << 29) + 1) == UNS
+    assert L.ssm_ckpt8_wgrad_workspace_size(0, 64, 64, 0, 1) == 0
 
 
 def test_binding_refuses_what_the_library_cannot_see():
