@@ -13,14 +13,15 @@ namespace ssm {
 // The kernel instances: columns of an access, accesses per thread, most threads of a block and
 // blocks of that size that the registers leave room for.
 enum NormVariant { kVec1, kVec1Wide, kVec2, kVec2Wide, kVec3, kVec4, kVec4Wide, kOne2, kOne4,
-                   kOne8Wide, kOne32 };
+                   kOne8, kOne8Wide, kOne32 };
 #define SSM_NORM_CASES(LAUNCH)                        \
     case ssm::kVec1: LAUNCH(8, 1, 256, 4); break;      \
     case ssm::kVec1Wide: LAUNCH(8, 1, 1024, 1); break; \
     case ssm::kVec2: LAUNCH(8, 2, 256, 2); break;      \
     case ssm::kVec4Wide: LAUNCH(8, 4, 1024, 1); break; \
     case ssm::kOne2: LAUNCH(1, 2, 128, 4); break;      \
-    case ssm::kOne4: LAUNCH(1, 4, 256, 4); break;      \
+    case ssm::kOne4: LAUNCH(1, 4, 256, 3); break;      \
+    case ssm::kOne8: LAUNCH(1, 8, 512, 1); break;      \
     case ssm::kOne8Wide: LAUNCH(1, 8, 1024, 1); break; \
     default: LAUNCH(1, 32, 1024, 1); break;
 #define SSM_NORM_FWD_SWITCH(variant, LAUNCH)           \
@@ -36,7 +37,11 @@ enum NormVariant { kVec1, kVec1Wide, kVec2, kVec2Wide, kVec3, kVec4, kVec4Wide, 
   }
 // Threads per SM of a launch's blocks, which all fit at once (registers: the instances above).
 inline int norm_threads_per_sm(NormVariant v) {
-  return v == kVec1 ? 768 : (v == kVec1Wide || v == kVec4Wide || v == kOne4 || v == kOne8Wide || v == kOne32 ? 1024 : 512);
+  switch (v) {
+    case kVec1: case kOne4: return 768;
+    case kVec1Wide: case kVec4Wide: case kOne8Wide: case kOne32: return 1024;
+    default: return 512;
+  }
 }
 // The plan of a launch.
 struct NormShape {

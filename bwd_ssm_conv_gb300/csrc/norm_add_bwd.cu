@@ -34,10 +34,10 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
   const uint32_t act = Act::slot_bytes(blockDim.x), res = Res::slot_bytes(blockDim.x);
   const uint32_t at = shared_addr(ring) + 16 * threadIdx.x, bytes = 2 * act + 2 * res;
   const bool want_ds = a.d_scale != nullptr;
-  const Act d{a.d_out, nullptr, nullptr, a.ld_d_out, at};
-  const Act x{want_ds ? a.x : nullptr, want_ds ? a.x_q : nullptr, a.x_e, a.ld_x, at + act};
-  const Res sv{a.res, a.res_q, a.res_e, a.ld_res, at + 2 * act};
-  const Res up{a.d_res_out, nullptr, nullptr, a.ld_d_res_out, at + 2 * act + res};
+  Act d{a.d_out, nullptr, nullptr, a.ld_d_out, at};
+  Act x{want_ds ? a.x : nullptr, want_ds ? a.x_q : nullptr, a.x_e, a.ld_x, at + act};
+  Res sv{a.res, a.res_q, a.res_e, a.ld_res, at + 2 * act};
+  Res up{a.d_res_out, nullptr, nullptr, a.ld_d_res_out, at + 2 * act + res};
   const long long step = (long long)gridDim.x * pl.rpb;
   long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
   auto issue = [&](long long r, int slot) {
@@ -85,6 +85,10 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
 #pragma unroll
     for (int j = 0; j < NJ; j++) es[j] = es_next[j], ex[j] = ex_next[j];
     small(row + step);
+    d.advance();
+    x.advance();
+    sv.advance();
+    up.advance();
     issue(row + ahead * step, slot == 0 ? ahead : slot - 1);
     cp_async_wait(ahead);
     const uint32_t s = slot * bytes;
@@ -142,7 +146,7 @@ cudaError_t bwd_launch(const AddNormBwd& a, RowPlan pl, int per_sm, cudaStream_t
   constexpr bool kRing = VEC == 8 && MAXT <= 256;
   const uint32_t slot = 2 * (Operand<IO, VEC, NJ, kRing>::slot_bytes(pl.threads) +
                              Operand<RES, VEC, NJ, kRing>::slot_bytes(pl.threads));
-  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
   return launch_rows(add_norm_bwd_kernel<IO, RES, VEC, NJ, MAXT, MINB>, a, pl,
                      ring > sums ? ring : sums, st);

@@ -31,7 +31,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
   }
   typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
-  const Op y{a.y, nullptr, nullptr, a.ld_y, at}, z{a.z, nullptr, nullptr, a.ld_z, at + bytes};
+  Op y{a.y, nullptr, nullptr, a.ld_y, at}, z{a.z, nullptr, nullptr, a.ld_z, at + bytes};
   const long long step = (long long)gridDim.x * pl.rpb;
   long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
   auto issue = [&](long long r, int slot) {
@@ -51,6 +51,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
   for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
        base += step, row += step, half ^= 1) {
     const bool rok = row < a.rows;
+    y.advance();
+    z.advance();
     issue(row + ahead * step, slot == 0 ? ahead : slot - 1);
     cp_async_wait(ahead);
     const uint32_t s = slot * 2 * bytes;
@@ -122,7 +124,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   }
   typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
-  const Op d{a.d_out, nullptr, nullptr, a.ld_d_out, at}, y{a.y, a.y_q, a.y_e, a.ld_y, at + bytes},
+  Op d{a.d_out, nullptr, nullptr, a.ld_d_out, at}, y{a.y, a.y_q, a.y_e, a.ld_y, at + bytes},
       z{a.z, a.z_q, a.z_e, a.ld_z, at + 2 * bytes};
   const long long step = (long long)gridDim.x * pl.rpb;
   long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
@@ -168,6 +170,9 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
 #pragma unroll
     for (int j = 0; j < NJ; j++) ey[j] = ey_next[j], ez[j] = ez_next[j];
     small(row + step);
+    d.advance();
+    y.advance();
+    z.advance();
     issue(row + ahead * step, slot == 0 ? ahead : slot - 1);
     cp_async_wait(ahead);
     const uint32_t s = slot * 3 * bytes;
@@ -226,13 +231,13 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
 template <typename IO, int VEC, int NJ, int MAXT, int MINB>
 cudaError_t fwd_launch(const GatedNormFwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
   const uint32_t slot = 2 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
-  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   return launch_rows(gated_norm_fwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl, pl.slots * slot, st);
 }
 template <typename IO, int VEC, int NJ, int MAXT, int MINB>
 cudaError_t bwd_launch(const GatedNormBwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
   const uint32_t slot = 3 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
-  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
   return launch_rows(gated_norm_bwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl,
                      ring > sums ? ring : sums, st);

@@ -76,7 +76,10 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
                       norm_threads_per_sm(s.variant), sms);
   } else {
     nj = group <= 64 ? 2 : (group <= 1024 ? 4 : (group <= 8192 ? 8 : 32));
-    s.variant = nj == 2 ? kOne2 : (nj == 4 ? kOne4 : (nj == 8 ? kOne8Wide : kOne32));
+    s.variant = nj == 2   ? kOne2
+                : nj == 4 ? kOne4
+                : nj == 8 ? (group <= 4096 ? kOne8 : kOne8Wide)
+                          : kOne32;
     s.plan = row_plan(rows, group, groups, row_threads(group, nj, 1), 128,
                       norm_threads_per_sm(s.variant), sms);
   }

@@ -279,8 +279,8 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*part)[32], in
 // A thread's own chunks of the rows to come are copied to shared memory while it works on the
 // current one (cp.async, 8 columns at a time, RowPlan::slots rows in all).  It alone reads what it
 // copied, so no barrier is needed, and it may read a row twice, before and after the row's sum,
-// instead of holding it in registers.  Without RING (single columns, and rows too wide for it) it
-// reads global memory each time.
+// instead of holding it in registers.  Single columns (VEC = 1) are loaded one row ahead into
+// registers instead; rows too wide for the ring (VEC = 8 without RING) are read where they are used.
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -321,15 +321,43 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   const uint8_t* e;
   long long ld;
   uint32_t at;  // this thread's place in the first slot of the ring
+  float cur[VEC == 1 ? NJ : 1], next[VEC == 1 ? NJ : 1];  // single columns: this row and the next
 
   __device__ __forceinline__ bool given() const { return t || q; }
   // Bytes that a block's threads need per slot of the ring.
   static __host__ __device__ constexpr uint32_t slot_bytes(int threads) {
     return 16u * kUnits * NJ * threads;
   }
+  // The row that was asked for last becomes the current one.
+  __device__ __forceinline__ void advance() {
+    if constexpr (VEC == 1)
+#pragma unroll
+      for (int j = 0; j < NJ; j++) cur[j] = next[j];
+  }
   // Starts the copies of a row; col: the thread's chunks, `s` the byte offset of the ring slot.
   __device__ __forceinline__ void issue(uint32_t s, long long row, const int (&col)[NJ],
-                                        const bool (&okc)[NJ], int cols) const {
+                                        const bool (&okc)[NJ], int cols) {
+    if constexpr (VEC == 1) {
+      if (q) {
+        const int8_t* p = q + row * cols;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) next[j] = okc[j] ? (float)p[col[j]] : 0.0f;
+      } else if (t) {
+        const IO* p = (const IO*)t + row * ld;
+#pragma unroll
+        for (int j = 0; j < NJ; j++) {
+          Cols<IO, 1> c;
+          float v[1];
+          c.zero();
+          if (okc[j]) c.load(p + col[j]);
+          c.get(v);
+          next[j] = v[0];
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < NJ; j++) next[j] = 0.0f;
+      }
+    }
     if constexpr (RING) {
       const uint32_t unit = 16 * blockDim.x;
       if (q) {
@@ -354,7 +382,10 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   }
   // Zeros in the slot at s: for the chunks that the thread does not have, which are never copied to
   // (so once is enough), or for all of them, where there is no row to copy.
-  __device__ __forceinline__ void clear(uint32_t s, const bool (&okc)[NJ], bool all) const {
+  __device__ __forceinline__ void clear(uint32_t s, const bool (&okc)[NJ], bool all) {
+    if constexpr (VEC == 1)
+#pragma unroll
+      for (int j = 0; j < NJ; j++) next[j] = 0.0f;
     if constexpr (RING) {
 #pragma unroll
       for (int j = 0; j < NJ; j++)
@@ -382,15 +413,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   __device__ __forceinline__ void get(uint32_t s, int j, bool ok, long long row, int col, int cols,
                                       uint32_t x, float (&v)[VEC]) const {
     if constexpr (VEC == 1) {
-      if (!ok || !given()) {
-        v[0] = 0.0f;
-      } else if (q) {
-        v[0] = (float)q[row * cols + col] * block_step(x);
-      } else {
-        Cols<IO, 1> c;
-        c.load((const IO*)t + row * ld + col);
-        c.get(v);
-      }
+      v[0] = q ? cur[j] * block_step(x) : cur[j];
     } else if constexpr (!RING) {
       if (!ok || !given()) {
 #pragma unroll
