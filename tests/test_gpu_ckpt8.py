@@ -160,3 +160,32 @@ def test_wgrad_same_bits_every_time_status_and_workspace(io):
         block.ssm_ckpt8_wgrad(gv, c, ws=ws[:128])
     with pytest.raises(ValueError, match="x8 must hold"):
         block.ssm_ckpt8_wgrad(gv[:-1], c)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_wgrad_of_long_sums_of_one_sign(io):
+    """Where every addition could lose up to 2^-23 of the sum to one side, 32768 tokens of positive
+    terms accumulated 16 at a time would lose up to 2048 2^-23 = 2.4e-4.  The accumulator is emptied
+    every 1024 tokens into sums rounded to nearest: at most 64 2^-23 = 7.7e-6 in each part, and 96
+    additions of parts at 2^-24 (three terms of g), 5.8e-6."""
+    g = torch.Generator().manual_seed(9)
+    gv = (1.0 + torch.rand(32768, 136, generator=g)).to(DT[io])
+    q = torch.randint(64, 128, (32768, 272), generator=g).to(torch.int8)
+    e = torch.full((32768, 9), 127, dtype=torch.uint8)
+    got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda())).cpu().double()
+    want = gv.double().t() @ ref.kept(q, e)
+    assert float(((got - want).abs() / want).max()) < 1.4e-5
+
+
+def test_wgrad_of_large_and_not_finite_gradients():
+    """fp32 g at the ends of its range is split exactly; infinities and NaN reach their columns."""
+    gv = torch.ones(70, 24)
+    gv[3, 1], gv[5, 2] = torch.finfo(torch.float32).max, -torch.finfo(torch.float32).max
+    gv[7, 3], gv[9, 4] = float("inf"), float("nan")
+    gv[:, 5] = 2.0 ** -120 * (1.0 + 2.0 ** -23)
+    c = block.ssm_ckpt8_save(torch.full((70, 32), 0.25).cuda())
+    got = block.ssm_ckpt8_wgrad(gv.cuda(), c).cpu()
+    want = gv.double().t() @ torch.full((70, 32), 0.25, dtype=torch.float64)
+    fine = [i for i in range(24) if i not in (3, 4)]
+    assert torch.allclose(got[fine].double(), want[fine], rtol=1e-5, atol=0)
+    assert bool(torch.isinf(got[3]).all()) and bool(torch.isnan(got[4]).all())
