@@ -90,8 +90,7 @@ __device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPlan
 
 // ---- add_norm -----------------------------------------------------------------------------------
 struct AddNormFwd {
-  long long rows;
-  int cols;
+  int rows, cols;
   float eps;
   const void* x;
   const void* residual;
@@ -100,18 +99,17 @@ struct AddNormFwd {
   void* out;
   void* res_out;
   float* rstd;
-  long long ld_x, ld_residual, ld_out, ld_res_out;
+  int ld_x, ld_residual, ld_out, ld_res_out;
   int8_t *res_q, *x_q, *out_q;
   uint8_t *res_e, *x_e, *out_e;
 };
 struct AddNormBwd {
-  long long rows;
-  int cols;
+  int rows, cols;
   const void* d_out;
   const void* d_res_out;
   const void* res;
   const void* x;
-  long long ld_d_out, ld_d_res_out, ld_res, ld_x;
+  int ld_d_out, ld_d_res_out, ld_res, ld_x;
   const int8_t *res_q, *x_q;
   const uint8_t *res_e, *x_e;
   const float* rstd_in;
@@ -119,7 +117,7 @@ struct AddNormBwd {
   const float* w;
   void* d_res;
   void* d_x;
-  long long ld_d_res, ld_d_x;
+  int ld_d_res, ld_d_x;
   float* d_w;
   float* d_scale;
   float* part;
@@ -132,32 +130,30 @@ cudaError_t launch_add_norm_bwd(const AddNormBwd& a, int io, int res_io, bool ve
 
 // ---- gated_norm ---------------------------------------------------------------------------------
 struct GatedNormFwd {
-  long long rows;
-  int cols, group, norm_first;
+  int rows, cols, group, norm_first;
   float eps;
   const void* y;
   const void* z;
   const float* w;
   void* out;
-  long long ld_y, ld_z, ld_out;
+  int ld_y, ld_z, ld_out;
   float* rstd;
   int8_t *y_q, *z_q, *out_q;
   uint8_t *y_e, *z_e, *out_e;
 };
 struct GatedNormBwd {
-  long long rows;
-  int cols, group, norm_first;
+  int rows, cols, group, norm_first;
   const void* d_out;
   const void* y;
   const void* z;
-  long long ld_d_out, ld_y, ld_z;
+  int ld_d_out, ld_y, ld_z;
   const int8_t *y_q, *z_q;
   const uint8_t *y_e, *z_e;
   const float* rstd_in;
   const float* w;
   void* d_y;
   void* d_z;
-  long long ld_d_y, ld_d_z;
+  int ld_d_y, ld_d_z;
   float* d_w;
   float* part;
 };

@@ -14,6 +14,7 @@ namespace {
 constexpr long long kMaxTotal = 1LL << 40;
 constexpr long long kMaxWgrad = 1LL << 38;  // elements of g and of X there
 constexpr long long kMaxTokens = 1LL << 29;  // of the weight gradient
+constexpr long long kMaxStride = 0x7fffffff;  // of the norms' rows
 constexpr int kMaxDim = 1 << 20;  // m and k of the weight gradient, columns of a checkpoint
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
@@ -65,7 +66,7 @@ int norm_check(const ssm_norm_desc* d, bool add, int* group) {
   } else if (d->flags & ~(unsigned)SSM_NORM_FIRST) {
     return SSM_ERR_INVALID_ARG;
   }
-  if (d->cols > SSM_MAX_NORM_COLS || d->rows > kMaxTotal / d->cols) return SSM_ERR_UNSUPPORTED;
+  if (d->cols > SSM_MAX_NORM_COLS || d->rows > SSM_MAX_NORM_ROWS) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 
@@ -99,11 +100,11 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
   r.f32(w);
   if (!r.ok || (rstd && !aligned(rstd, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_x, ld_residual, ld_out, ld_res_out})
-    if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
+    if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
-  ssm::AddNormFwd a{desc->rows, desc->cols, desc->eps, x, residual, scale, w, out, res_out, rstd,
-                    ld_x, ld_residual, ld_out, ld_res_out, res_q, x_q, out_q, res_e, x_e, out_e};
+  ssm::AddNormFwd a{(int)desc->rows, desc->cols, desc->eps, x, residual, scale, w, out, res_out, rstd,
+                    (int)ld_x, (int)ld_residual, (int)ld_out, (int)ld_res_out, res_q, x_q, out_q, res_e, x_e, out_e};
   return status_of(ssm::launch_add_norm_fwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
 }
 
@@ -146,16 +147,16 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
   if (!r.ok || !aligned(rstd, 4) || (d_w && !aligned(d_w, 4)) || (d_scale && !aligned(d_scale, 4)))
     return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_d_out, ld_d_res_out, ld_res, ld_x, ld_d_res, ld_d_x})
-    if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
+    if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
   const int sums = (d_w ? 1 : 0) + (d_scale ? 1 : 0);
   if (sums && (!ws || !aligned(ws, 256) ||
                ws_bytes < 256 + ssm::column_sums_bytes(desc->rows, group, 1, sms, sums)))
     return SSM_ERR_WORKSPACE;
-  ssm::AddNormBwd a{desc->rows, desc->cols, d_out, d_res_out, res, x, ld_d_out, ld_d_res_out,
-                    ld_res, ld_x, res_q, x_q, res_e, x_e, rstd, scale, w, d_res, d_x, ld_d_res,
-                    ld_d_x, d_w, d_scale, sums ? (float*)((char*)ws + 256) : nullptr};
+  ssm::AddNormBwd a{(int)desc->rows, desc->cols, d_out, d_res_out, res, x, (int)ld_d_out,
+                    (int)ld_d_res_out, (int)ld_res, (int)ld_x, res_q, x_q, res_e, x_e, rstd, scale, w,
+                    d_res, d_x, (int)ld_d_res, (int)ld_d_x, d_w, d_scale, sums ? (float*)((char*)ws + 256) : nullptr};
   return status_of(ssm::launch_add_norm_bwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
 }
 
@@ -178,12 +179,12 @@ int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y,
   r.f32(w);
   if (!r.ok || (rstd && !aligned(rstd, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_y, ld_z, ld_out})
-    if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
+    if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  ssm::GatedNormFwd a{desc->rows, cols, group, (desc->flags & SSM_NORM_FIRST) ? 1 : 0, desc->eps,
-                      y, z, w, out, ld_y, ld_z, ld_out, rstd, y_q, z_q, out_q, y_e, z_e, out_e};
+  ssm::GatedNormFwd a{(int)desc->rows, cols, group, (desc->flags & SSM_NORM_FIRST) ? 1 : 0, desc->eps,
+                      y, z, w, out, (int)ld_y, (int)ld_z, (int)ld_out, rstd, y_q, z_q, out_q, y_e, z_e, out_e};
   // Blocks of 32 columns that straddle groups belong to no group's threads: such checkpoints are
   // saved by their own kernel, the inputs' before out is written.
   const bool straddle = group != cols && group % SSM_CKPT8_BLOCK != 0;
@@ -224,14 +225,15 @@ int ssm_gated_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long l
   r.f32(w);
   if (!r.ok || !aligned(rstd, 4) || (d_w && !aligned(d_w, 4))) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_d_out, ld_y, ld_z, ld_d_y, ld_d_z})
-    if (!ld_fits(ld, desc->rows)) return SSM_ERR_UNSUPPORTED;
+    if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
   if (d_w && (!ws || !aligned(ws, 256) ||
               ws_bytes < 256 + ssm::column_sums_bytes(desc->rows, group, cols / group, sms, 1)))
     return SSM_ERR_WORKSPACE;
-  ssm::GatedNormBwd a{desc->rows, cols, group, (desc->flags & SSM_NORM_FIRST) ? 1 : 0, d_out, y, z,
-                      ld_d_out, ld_y, ld_z, y_q, z_q, y_e, z_e, rstd, w, d_y, d_z, ld_d_y, ld_d_z,
+  ssm::GatedNormBwd a{(int)desc->rows, cols, group, (desc->flags & SSM_NORM_FIRST) ? 1 : 0, d_out, y, z,
+                      (int)ld_d_out, (int)ld_y, (int)ld_z, y_q, z_q, y_e, z_e, rstd, w, d_y, d_z,
+                      (int)ld_d_y, (int)ld_d_z,
                       d_w, d_w ? (float*)((char*)ws + 256) : nullptr};
   return status_of(ssm::launch_gated_norm_bwd(a, io, r.vec, sms, (cudaStream_t)stream));
 }

@@ -28,9 +28,8 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
     ld_param<VEC>(a.scale, col[j], okc[j], sc[j]);
   }
   int half = 0;
-  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += (long long)gridDim.x * pl.rpb, half ^= 1) {
-    const long long row = base + pos.slot;
+  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += gridDim.x * pl.rpb, half ^= 1) {
+    const int row = base + pos.slot;
     const bool rok = row < a.rows;
     float s[NJ][VEC];
     Cols<IO, VEC> xr[NJ];
@@ -40,8 +39,8 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
       xr[j].zero();
       rr[j].zero();
       if (rok && okc[j]) {
-        xr[j].load((const IO*)a.x + row * a.ld_x + col[j]);
-        if (a.residual) rr[j].load((const RES*)a.residual + row * a.ld_residual + col[j]);
+        xr[j].load((const IO*)a.x + (long long)row * a.ld_x + col[j]);
+        if (a.residual) rr[j].load((const RES*)a.residual + (long long)row * a.ld_residual + col[j]);
       }
     }
     float sq = 0.0f;
@@ -69,10 +68,11 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
       to_cols(o, oc);
       to_cols(s[j], stored);
       if (ok) {
-        st_cols((IO*)a.out + row * a.ld_out + col[j], oc);
-        if (a.res_out) st_cols((RES*)a.res_out + row * a.ld_res_out + col[j], stored);
+        st_cols((IO*)a.out + (long long)row * a.ld_out + col[j], oc);
+        if (a.res_out) st_cols((RES*)a.res_out + (long long)row * a.ld_res_out + col[j], stored);
       }
-      const long long q = row * cols + col[j], e = row * nb + col[j] / 32;
+      const long long q = (long long)row * cols + col[j],
+                      e = (long long)row * nb + (int)((unsigned)col[j] / 32);
       if (a.res_q) {
         float kept[VEC];
         stored.get(kept);

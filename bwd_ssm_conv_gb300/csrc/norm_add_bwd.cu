@@ -38,9 +38,9 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
   Act x{want_ds ? a.x : nullptr, want_ds ? a.x_q : nullptr, a.x_e, a.ld_x, at + act};
   Res sv{a.res, a.res_q, a.res_e, a.ld_res, at + 2 * act};
   Res up{a.d_res_out, nullptr, nullptr, a.ld_d_res_out, at + 2 * act + res};
-  const long long step = (long long)gridDim.x * pl.rpb;
-  long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
-  auto issue = [&](long long r, int slot) {
+  const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
+  int row = blockIdx.x * pl.rpb + pos.slot;
+  auto issue = [&](int r, int slot) {
     const uint32_t s = slot * bytes;
     if (r < a.rows) {
       d.issue(s, r, col, okc, cols);
@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
   // what a row needs besides: read one row ahead
   float rstd_next = 0.0f;
   uint32_t es_next[NJ], ex_next[NJ];
-  auto small = [&](long long r) {
+  auto small = [&](int r) {
     const bool rok = r < a.rows;
     rstd_next = rok ? a.rstd_in[r] : 0.0f;
 #pragma unroll
@@ -77,8 +77,7 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
   for (int i = 0; i < ahead; i++) issue(row + i * step, i);
   small(row);
   int half = 0, slot = 0;
-  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += step, row += step, half ^= 1) {
+  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, row += step, half ^= 1) {
     const bool rok = row < a.rows;
     const float rstd = rstd_next;
     uint32_t es[NJ], ex[NJ];
@@ -123,13 +122,13 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
         for (int i = 0; i < VEC; i++) ds[j][i] = fmaf(r[i], xv[i], ds[j][i]);
       }
       if (ok) {
-        if (a.d_res) st_cols((RES*)a.d_res + row * a.ld_d_res + col[j], r);
+        if (a.d_res) st_cols((RES*)a.d_res + (long long)row * a.ld_d_res + col[j], r);
         if (a.d_x) {
           float sc[VEC];
           ld_param<VEC>(a.scale, col[j], true, sc);
 #pragma unroll
           for (int i = 0; i < VEC; i++) r[i] *= sc[i];
-          st_cols((IO*)a.d_x + row * a.ld_d_x + col[j], r);
+          st_cols((IO*)a.d_x + (long long)row * a.ld_d_x + col[j], r);
         }
       }
     }

@@ -19,6 +19,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
   const RowPos pos = row_pos(pl);
   const int nb = (a.cols + 31) / 32;
   const float inv = 1.0f / (float)a.group;
+  const int grp = pos.col0 / a.group;
   bool okc[NJ];
   int col[NJ];
   float w[NJ][VEC];
@@ -32,9 +33,9 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
   typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
   Op y{a.y, nullptr, nullptr, a.ld_y, at}, z{a.z, nullptr, nullptr, a.ld_z, at + bytes};
-  const long long step = (long long)gridDim.x * pl.rpb;
-  long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
-  auto issue = [&](long long r, int slot) {
+  const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
+  int row = blockIdx.x * pl.rpb + pos.slot;
+  auto issue = [&](int r, int slot) {
     if (r < a.rows) {
       y.issue(slot * 2 * bytes, r, col, okc, a.cols);
       z.issue(slot * 2 * bytes, r, col, okc, a.cols);
@@ -48,8 +49,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
   const int ahead = pl.slots - 1;
   for (int i = 0; i < ahead; i++) issue(row + i * step, i);
   int half = 0, slot = 0;
-  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += step, row += step, half ^= 1) {
+  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, row += step, half ^= 1) {
     const bool rok = row < a.rows;
     y.advance();
     z.advance();
@@ -57,7 +57,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
     cp_async_wait(ahead);
     const uint32_t s = slot * 2 * bytes;
     slot = slot == ahead ? 0 : slot + 1;
-    const long long qrow = row * a.cols, erow = row * nb;
+    const long long qrow = (long long)row * a.cols, erow = (long long)row * nb;
     float v[NJ][VEC], sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
@@ -67,8 +67,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
       z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
       if (a.y_q) {
         const uint32_t ytop = y.top(s, j, v[j]), ztop = z.top(s, j, zv);
-        store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + col[j] / 32);
-        store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + col[j] / 32);
+        store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + (int)((unsigned)col[j] / 32));
+        store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + (int)((unsigned)col[j] / 32));
       }
       if (!a.norm_first)
 #pragma unroll
@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
     }
     const float rstd = 1.0f / sqrtf(row_sum(sq, pl.tpr, part, half) * inv + a.eps);
     if (a.rstd && rok && pos.ok && pos.lane == 0)
-      a.rstd[row * pl.groups + pos.col0 / a.group] = rstd;
+      a.rstd[(long long)row * pl.groups + grp] = rstd;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
@@ -93,10 +93,10 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
       }
       Cols<IO, VEC> oc;
       to_cols(o, oc);
-      if (ok) st_cols((IO*)a.out + row * a.ld_out + col[j], oc);
+      if (ok) st_cols((IO*)a.out + (long long)row * a.ld_out + col[j], oc);
       if (a.out_q) {
         oc.get(o);
-        store_ckpt8<VEC>(o, ok, a.out_q + qrow + col[j], a.out_e + erow + col[j] / 32);
+        store_ckpt8<VEC>(o, ok, a.out_q + qrow + col[j], a.out_e + erow + (int)((unsigned)col[j] / 32));
       }
     }
   }
@@ -110,6 +110,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   const RowPos pos = row_pos(pl);
   const int nb = (a.cols + 31) / 32;
   const float inv = 1.0f / (float)a.group;
+  const int grp = pos.col0 / a.group;
   bool okc[NJ];
   int col[NJ];
   float w[NJ][VEC], dw[NJ][VEC];
@@ -126,9 +127,9 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
   Op d{a.d_out, nullptr, nullptr, a.ld_d_out, at}, y{a.y, a.y_q, a.y_e, a.ld_y, at + bytes},
       z{a.z, a.z_q, a.z_e, a.ld_z, at + 2 * bytes};
-  const long long step = (long long)gridDim.x * pl.rpb;
-  long long row = (long long)blockIdx.x * pl.rpb + pos.slot;
-  auto issue = [&](long long r, int slot) {
+  const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
+  int row = blockIdx.x * pl.rpb + pos.slot;
+  auto issue = [&](int r, int slot) {
     const uint32_t s = slot * 3 * bytes;
     if (r < a.rows) {
       d.issue(s, r, col, okc, a.cols);
@@ -144,9 +145,9 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   // what a row needs besides: read one row ahead
   float rstd_next = 0.0f;
   uint32_t ey_next[NJ], ez_next[NJ];
-  auto small = [&](long long r) {
+  auto small = [&](int r) {
     const bool rok = r < a.rows;
-    rstd_next = rok && pos.ok ? a.rstd_in[r * pl.groups + pos.col0 / a.group] : 0.0f;
+    rstd_next = rok && pos.ok ? a.rstd_in[(long long)r * pl.groups + grp] : 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       ey_next[j] = y.scale(rok && okc[j], r, col[j], nb);
@@ -162,8 +163,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   for (int i = 0; i < ahead; i++) issue(row + i * step, i);
   small(row);
   int half = 0, slot = 0;
-  for (long long base = (long long)blockIdx.x * pl.rpb; base < a.rows;
-       base += step, row += step, half ^= 1) {
+  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, row += step, half ^= 1) {
     const bool rok = row < a.rows;
     const float rstd = rstd_next;
     uint32_t ey[NJ], ez[NJ];
@@ -192,12 +192,15 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
       for (int i = 0; i < VEC; i++) {
         const float sg = sigmoidf_(zv[i]);
         g[j][i] = zv[i] * sg;
-        const float slope = fmaf(g[j][i], 1.0f - sg, sg);  // d silu(z) / d z
-        const float yg = yv[i] * g[j][i], t = dv[i] * rstd * yg;  // d_out times n and gate
+        b[j][i] = yv[i] * fmaf(g[j][i], 1.0f - sg, sg);  // y times d silu(z) / d z
+        m[j][i] = yv[i] * g[j][i];
+        const float t = dv[i] * rstd * m[j][i];  // d_out times n and gate
         dw[j][i] += t;
         dot = fmaf(w[j][i], t, dot);
-        m[j][i] = a.norm_first ? yv[i] : yg;
-        b[j][i] = a.norm_first ? w[j][i] * (dv[i] * rstd) * yv[i] * slope : yv[i] * slope;
+      }
+      if (a.norm_first) {
+#pragma unroll
+        for (int i = 0; i < VEC; i++) m[j][i] = yv[i], b[j][i] *= w[j][i] * dv[i] * rstd;
       }
     }
     const float c = -row_sum(dot, pl.tpr, part, half) * inv * rstd;
@@ -219,8 +222,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
         }
       }
       if (ok) {
-        st_cols((IO*)a.d_y + row * a.ld_d_y + col[j], dy);
-        st_cols((IO*)a.d_z + row * a.ld_d_z + col[j], b[j]);
+        st_cols((IO*)a.d_y + (long long)row * a.ld_d_y + col[j], dy);
+        st_cols((IO*)a.d_z + (long long)row * a.ld_d_z + col[j], b[j]);
       }
     }
   }

@@ -319,7 +319,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   const void* t;
   const int8_t* q;
   const uint8_t* e;
-  long long ld;
+  int ld;
   uint32_t at;  // this thread's place in the first slot of the ring
   float cur[VEC == 1 ? NJ : 1], next[VEC == 1 ? NJ : 1];  // single columns: this row and the next
 
@@ -335,15 +335,15 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
       for (int j = 0; j < NJ; j++) cur[j] = next[j];
   }
   // Starts the copies of a row; col: the thread's chunks, `s` the byte offset of the ring slot.
-  __device__ __forceinline__ void issue(uint32_t s, long long row, const int (&col)[NJ],
+  __device__ __forceinline__ void issue(uint32_t s, int row, const int (&col)[NJ],
                                         const bool (&okc)[NJ], int cols) {
     if constexpr (VEC == 1) {
       if (q) {
-        const int8_t* p = q + row * cols;
+        const int8_t* p = q + (long long)row * cols;
 #pragma unroll
         for (int j = 0; j < NJ; j++) next[j] = okc[j] ? (float)p[col[j]] : 0.0f;
       } else if (t) {
-        const IO* p = (const IO*)t + row * ld;
+        const IO* p = (const IO*)t + (long long)row * ld;
 #pragma unroll
         for (int j = 0; j < NJ; j++) {
           Cols<IO, 1> c;
@@ -361,12 +361,12 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
     if constexpr (RING) {
       const uint32_t unit = 16 * blockDim.x;
       if (q) {
-        const int8_t* p = q + row * cols;
+        const int8_t* p = q + (long long)row * cols;
 #pragma unroll
         for (int j = 0; j < NJ; j++)
           if (okc[j]) cp_async8(at + s + j * kUnits * unit, p + col[j]);
       } else if (t) {
-        const IO* p = (const IO*)t + row * ld;
+        const IO* p = (const IO*)t + (long long)row * ld;
 #pragma unroll
         for (int j = 0; j < NJ; j++)
           if (okc[j])
@@ -399,8 +399,8 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
     }
   }
   // The scale byte of a chunk (a checkpoint's; 7 otherwise).
-  __device__ __forceinline__ uint32_t scale(bool ok, long long row, int col, int nb) const {
-    return q && ok ? e[row * nb + col / 32] : 7u;
+  __device__ __forceinline__ uint32_t scale(bool ok, int row, int col, int nb) const {
+    return q && ok ? e[(long long)row * nb + (int)((unsigned)col / 32)] : 7u;
   }
   // The largest magnitude's bits of the block that a tensor's chunk lies in; v holds its values.
   __device__ __forceinline__ uint32_t top(uint32_t s, int j, const float (&v)[VEC]) const {
@@ -410,7 +410,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
       return block_top<VEC>(v);
   }
   // A chunk's values (x is its scale byte); zeros for a chunk that the thread does not have.
-  __device__ __forceinline__ void get(uint32_t s, int j, bool ok, long long row, int col, int cols,
+  __device__ __forceinline__ void get(uint32_t s, int j, bool ok, int row, int col, int cols,
                                       uint32_t x, float (&v)[VEC]) const {
     if constexpr (VEC == 1) {
       v[0] = q ? cur[j] * block_step(x) : cur[j];
@@ -420,12 +420,12 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
         for (int i = 0; i < VEC; i++) v[i] = 0.0f;
       } else if (q) {
         Kept<8> k;
-        k.q = *reinterpret_cast<const uint2*>(q + row * cols + col);
+        k.q = *reinterpret_cast<const uint2*>(q + (long long)row * cols + col);
         k.e = (uint8_t)x;
         k.get(v);
       } else {
         Cols<IO, 8> c;
-        c.load((const IO*)t + row * ld + col);
+        c.load((const IO*)t + (long long)row * ld + col);
         c.get(v);
       }
     } else {

@@ -41,6 +41,7 @@ extern "C" {
 #endif
 
 #define SSM_MAX_NORM_COLS 32768 /* columns of a row of the norms (SSM_ERR_UNSUPPORTED beyond) */
+#define SSM_MAX_NORM_ROWS 0x7ff00000 /* rows of the norms; their strides: below 2^31 elements */
 #define SSM_CKPT8_BLOCK 32      /* columns that share a scale */
 
 enum {
