@@ -231,8 +231,9 @@ def ssm_add_norm_fwd(x, w=None, residual=None, scale=None, eps=1e-5, res_dtype=N
     cols = shape[-1]
     rdt = residual.dtype if residual is not None else (res_dtype or x.dtype)
     if out is None:
-        o = torch.empty(shape, dtype=x.dtype, device=dev)
-        res = torch.empty(shape, dtype=rdt, device=dev) if want_res else None
+        o = torch.empty_like(x)
+        res = (None if not want_res else torch.empty_like(residual) if residual is not None else
+               torch.empty(shape, dtype=rdt, device=dev))
         po, pr = (o.data_ptr(), 0), (None if res is None else res.data_ptr(), 0)
     else:
         o, res = out
@@ -267,17 +268,18 @@ def ssm_add_norm_bwd(d_out, res, rstd, w=None, d_res_out=None, scale=None, x=Non
     The stream's type is that of ``res`` or ``d_res_out``, else ``res_dtype``, else d_out's.
     ``out`` = a dict of preallocated outputs with the same keys, optional."""
     io = _io(d_out, "d_out")
-    shape, dev, f32 = d_out.shape, d_out.device, torch.float32
+    shape, dev = d_out.shape, d_out.device
     cols = shape[-1]
     res8, x8 = isinstance(res, tuple), isinstance(x, tuple)
     rdt = (d_res_out.dtype if d_res_out is not None else
            res.dtype if not res8 else res_dtype or d_out.dtype)
     if out is None:
-        d_res = torch.empty(shape, dtype=rdt, device=dev) if want_dres else None
-        d_x = torch.empty(shape, dtype=d_out.dtype, device=dev) if want_dx else None
-        d_w = torch.empty(cols, dtype=f32, device=dev) if w is not None else None
-        d_scale = (torch.empty(cols, dtype=f32, device=dev)
-                   if scale is not None and x is not None else None)
+        d_res = (None if not want_dres else
+                 torch.empty_like(d_res_out) if d_res_out is not None else
+                 torch.empty(shape, dtype=rdt, device=dev))
+        d_x = torch.empty_like(d_out) if want_dx else None
+        d_w = torch.empty_like(w) if w is not None else None
+        d_scale = torch.empty_like(scale) if scale is not None and x is not None else None
         g = dict(d_res=d_res, d_x=d_x, d_w=d_w, d_scale=d_scale)
         made = (d_res, d_x, d_w, d_scale)
     else:
@@ -315,7 +317,7 @@ def ssm_gated_norm_fwd(y, z, w=None, group=0, eps=1e-5, norm_first=False, save8=
     shape, dev = y.shape, y.device
     cols = shape[-1]
     if out is None:
-        o = torch.empty(shape, dtype=y.dtype, device=dev)
+        o = torch.empty_like(y)
         po = (o.data_ptr(), 0)
     else:
         o, po = out, _rows(out, "out", shape, y.dtype)
@@ -343,12 +345,11 @@ def ssm_gated_norm_bwd(d_out, y, z, rstd, w=None, group=0, norm_first=False, ws=
     of preallocated outputs with the same keys, optional (d_z may be a slice of the gradient of a
     wider projection)."""
     io = _io(d_out, "d_out")
-    shape, dev, f32 = d_out.shape, d_out.device, torch.float32
+    shape, dev = d_out.shape, d_out.device
     cols = shape[-1]
     if out is None:
-        d_y = torch.empty(shape, dtype=d_out.dtype, device=dev)
-        d_z = torch.empty(shape, dtype=d_out.dtype, device=dev)
-        d_w = torch.empty(cols, dtype=f32, device=dev) if w is not None else None
+        d_y, d_z = torch.empty_like(d_out), torch.empty_like(d_out)
+        d_w = torch.empty_like(w) if w is not None else None
         g = dict(d_y=d_y, d_z=d_z, d_w=d_w)
         made = (d_y, d_z, d_w)
     else:

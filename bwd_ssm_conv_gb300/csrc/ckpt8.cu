@@ -8,57 +8,80 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // chunks of VEC columns per thread
+constexpr int kUnroll = 4;  // chunks of VEC columns per thread, all loaded before the first is used
 
-// A warp takes a segment of 32 VEC kUnroll columns of one row.
+// A warp takes a segment of 32 VEC kUnroll columns of one row: unit u is segment u % segs of row
+// u / segs.  FLAT: rows without gaps between them are one long row, and nothing is divided.
+template <bool FLAT, int VEC> struct Place {
+  long long row, c0;
+  __device__ __forceinline__ Place(long long u, unsigned segs, int lane) {
+    if constexpr (FLAT) {
+      row = 0;
+      c0 = u * (32 * VEC * kUnroll) + lane * VEC;
+    } else {
+      row = (unsigned)u / segs;
+      c0 = (long long)((unsigned)u - (unsigned)row * segs) * (32 * VEC * kUnroll) + lane * VEC;
+    }
+  }
+};
+
 template <typename IO, int VEC>
-__global__ void __launch_bounds__(kThreads) ckpt8_save_kernel(
-    const IO* x, long long ld, int8_t* q, uint8_t* e, long long rows, long long cols,
-    long long nb, long long segs) {
+__device__ __forceinline__ uint32_t top_of(const Cols<IO, VEC>& c, const float (&v)[VEC]) {
+  if constexpr (VEC == 8 && sizeof(IO) == 2) return block_top(c.a);
+  else return block_top<VEC>(v);
+}
+
+template <typename IO, int VEC, bool FLAT>
+__global__ void __launch_bounds__(kThreads) ckpt8_save_kernel(const IO* x, long long ld, int8_t* q,
+                                                              uint8_t* e, long long cols,
+                                                              long long nb, unsigned segs,
+                                                              long long units) {
   const int lane = threadIdx.x & 31;
-  const long long units = rows * segs;
   for (long long u = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5; u < units;
        u += (long long)gridDim.x * (kThreads / 32)) {
-    const long long row = u / segs, c0 = (u - row * segs) * (32 * VEC * kUnroll) + lane * VEC;
+    const Place<FLAT, VEC> at(u, segs, lane);
+    const IO* xr = x + at.row * ld + at.c0;
+    int8_t* qr = q + at.row * cols + at.c0;
+    uint8_t* er = e + at.row * nb + at.c0 / 32;
     Cols<IO, VEC> r[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; j++) {
-      const long long c = c0 + j * 32 * VEC;
       r[j].zero();
-      if (c < cols) r[j].load(x + row * ld + c);
+      if (at.c0 + j * 32 * VEC < cols) r[j].load(xr + j * 32 * VEC);
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; j++) {
-      const long long c = c0 + j * 32 * VEC;
       float v[VEC];
       r[j].get(v);
-      store_ckpt8<VEC>(v, c < cols, q + row * cols + c, e + row * nb + c / 32);
+      store_ckpt8_top<VEC>(v, top_of<IO, VEC>(r[j], v), at.c0 + j * 32 * VEC < cols,
+                           qr + j * 32 * VEC, er + j * VEC);
     }
   }
 }
 
-template <typename IO, int VEC>
-__global__ void __launch_bounds__(kThreads) ckpt8_load_kernel(
-    const int8_t* q, const uint8_t* e, IO* out, long long ld, long long rows, long long cols,
-    long long nb, long long segs) {
+template <typename IO, int VEC, bool FLAT>
+__global__ void __launch_bounds__(kThreads) ckpt8_load_kernel(const int8_t* q, const uint8_t* e,
+                                                              IO* out, long long ld,
+                                                              long long cols, long long nb,
+                                                              unsigned segs, long long units) {
   const int lane = threadIdx.x & 31;
-  const long long units = rows * segs;
   for (long long u = (blockIdx.x * (long long)kThreads + threadIdx.x) >> 5; u < units;
        u += (long long)gridDim.x * (kThreads / 32)) {
-    const long long row = u / segs, c0 = (u - row * segs) * (32 * VEC * kUnroll) + lane * VEC;
+    const Place<FLAT, VEC> at(u, segs, lane);
+    IO* o = out + at.row * ld + at.c0;
+    const int8_t* qr = q + at.row * cols + at.c0;
+    const uint8_t* er = e + at.row * nb + at.c0 / 32;
     Kept<VEC> r[kUnroll];
 #pragma unroll
     for (int j = 0; j < kUnroll; j++) {
-      const long long c = c0 + j * 32 * VEC;
       r[j].zero();
-      if (c < cols) r[j].load(q + row * cols + c, e + row * nb + c / 32);
+      if (at.c0 + j * 32 * VEC < cols) r[j].load(qr + j * 32 * VEC, er + j * VEC);
     }
 #pragma unroll
     for (int j = 0; j < kUnroll; j++) {
-      const long long c = c0 + j * 32 * VEC;
       float v[VEC];
       r[j].get(v);
-      if (c < cols) st_cols(out + row * ld + c, v);
+      if (at.c0 + j * 32 * VEC < cols) st_cols(o + j * 32 * VEC, v);
     }
   }
 }
@@ -68,28 +91,52 @@ bool vec_ok(const void* act, long long ld, const void* q, int cols, int io) {
   return cols % 8 == 0 && ld % 8 == 0 && (uintptr_t)act % bytes == 0 && (uintptr_t)q % 8 == 0;
 }
 
+// Calls launch(first row, rows, columns, stride, segments, units, flat) for the whole activation:
+// once, unless the units of rows with gaps between them pass 32 bits.
+template <int VEC, typename F>
+cudaError_t for_rows(long long rows, long long cols, long long ld, F launch) {
+  constexpr int kSeg = 32 * VEC * kUnroll;
+  if (ld == cols && cols % 32 == 0) {  // no gaps, and blocks that end with their rows
+    const long long n = rows * cols;
+    return launch(0, n, n, (unsigned)1, (n + kSeg - 1) / kSeg, true);
+  }
+  const long long segs = (cols + kSeg - 1) / kSeg, most = 0x7fffffffLL / segs;
+  for (long long r = 0; r < rows; r += most) {
+    const long long n = rows - r < most ? rows - r : most;
+    if (cudaError_t e = launch(r, cols, ld, (unsigned)segs, n * segs, false)) return e;
+  }
+  return cudaSuccess;
+}
+int blocks_of(long long units, int sms) {
+  const long long need = (units + kThreads / 32 - 1) / (kThreads / 32), most = sms * 32LL;
+  return (int)(need < most ? need : most);
+}
+
 template <typename IO, int VEC>
 cudaError_t save(const void* x, long long ld, int8_t* q, uint8_t* e, long long rows,
                  long long cols, int sms, cudaStream_t st) {
-  // rows without gaps whose blocks are whole are one long row
-  if (ld == cols && cols % 32 == 0) cols *= rows, ld = cols, rows = 1;
-  const long long segs = (cols + 32 * VEC * kUnroll - 1) / (32 * VEC * kUnroll);
-  const long long need = (rows * segs + kThreads / 32 - 1) / (kThreads / 32), most = sms * 32LL;
-  ckpt8_save_kernel<IO, VEC><<<(int)(need < most ? need : most), kThreads, 0, st>>>(
-      (const IO*)x, ld, q, e, rows, cols, (cols + 31) / 32, segs);
-  count_launches(1);
-  return cudaGetLastError();
+  const long long nb = (cols + 31) / 32;
+  return for_rows<VEC>(rows, cols, ld, [&](long long r, long long c, long long l, unsigned segs,
+                                           long long units, bool flat) {
+    auto kernel = flat ? ckpt8_save_kernel<IO, VEC, true> : ckpt8_save_kernel<IO, VEC, false>;
+    kernel<<<blocks_of(units, sms), kThreads, 0, st>>>((const IO*)x + r * ld, l, q + r * cols,
+                                                       e + r * nb, c, nb, segs, units);
+    count_launches(1);
+    return cudaGetLastError();
+  });
 }
 template <typename IO, int VEC>
 cudaError_t load(const int8_t* q, const uint8_t* e, void* out, long long ld, long long rows,
                  long long cols, int sms, cudaStream_t st) {
-  if (ld == cols && cols % 32 == 0) cols *= rows, ld = cols, rows = 1;
-  const long long segs = (cols + 32 * VEC * kUnroll - 1) / (32 * VEC * kUnroll);
-  const long long need = (rows * segs + kThreads / 32 - 1) / (kThreads / 32), most = sms * 32LL;
-  ckpt8_load_kernel<IO, VEC><<<(int)(need < most ? need : most), kThreads, 0, st>>>(
-      q, e, (IO*)out, ld, rows, cols, (cols + 31) / 32, segs);
-  count_launches(1);
-  return cudaGetLastError();
+  const long long nb = (cols + 31) / 32;
+  return for_rows<VEC>(rows, cols, ld, [&](long long r, long long c, long long l, unsigned segs,
+                                           long long units, bool flat) {
+    auto kernel = flat ? ckpt8_load_kernel<IO, VEC, true> : ckpt8_load_kernel<IO, VEC, false>;
+    kernel<<<blocks_of(units, sms), kThreads, 0, st>>>(q + r * cols, e + r * nb,
+                                                       (IO*)out + r * ld, l, c, nb, segs, units);
+    count_launches(1);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace

@@ -101,17 +101,42 @@ __global__ void __launch_bounds__(kThreads) pad_q_kernel(const int8_t* q, int8_t
   }
 }
 
+// d_W (+)= the splits' tiles: a block adds 32 x VEC values in kThreads / 32 slices of the splits, every
+// slice in order, then the slices in order (`slices` of them: one where the splits are few).
+template <int VEC>
 __global__ void __launch_bounds__(kThreads) wgrad8_sum_kernel(const float* part, int splits,
-                                                              long long n, float* d_W,
+                                                              int slices, long long n, float* d_W,
                                                               int accumulate) {
+  __shared__ float s[kThreads / 32][32 * VEC + 1];
+  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
+  // slices == 1: every warp takes 32 x VEC values of its own
+  const long long i = (slices == 1 ? (long long)blockIdx.x * (kThreads / 32) + y : blockIdx.x) *
+                          (32LL * VEC) + x * VEC;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched before the tiles are complete
-  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
-       i += (long long)gridDim.x * kThreads) {
-    float v = 0.0f;
+  float v[VEC] = {};
+  if (i < n) {
 #pragma unroll 4
-    for (int s = 0; s < splits; s++) v += part[s * n + i];
-    d_W[i] = accumulate ? d_W[i] + v : v;
+    for (int t = slices == 1 ? 0 : y; t < splits; t += slices) {
+      if constexpr (VEC == 4) {
+        const float4 p = *reinterpret_cast<const float4*>(part + t * n + i);
+        v[0] += p.x, v[1] += p.y, v[2] += p.z, v[3] += p.w;
+      } else {
+        v[0] += part[t * n + i];
+      }
+    }
   }
+  if (slices > 1) {
+#pragma unroll
+    for (int j = 0; j < VEC; j++) s[y][x * VEC + j] = v[j];
+    __syncthreads();
+    if (y != 0) return;
+    for (int t = 1; t < slices; t++)
+#pragma unroll
+      for (int j = 0; j < VEC; j++) v[j] += s[t][x * VEC + j];
+  }
+  if (i < n)
+#pragma unroll
+    for (int j = 0; j < VEC; j++) d_W[i + j] = accumulate ? d_W[i + j] + v[j] : v[j];
 }
 
 int blocks_of(long long n, int sms) {
@@ -187,8 +212,11 @@ cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
     return e;
   if (!part) return cudaSuccess;
   const long long n = (long long)a.m * a.k;
+  const bool vec = n % 4 == 0;
+  const int slices = p.splits >= 16 ? kThreads / 32 : 1;
+  const long long per = (vec ? 128 : 32) * (slices == 1 ? kThreads / 32 : 1);
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3(blocks_of(n, sms));
+  c.gridDim = dim3((unsigned)((n + per - 1) / per));
   c.blockDim = dim3(kThreads);
   c.stream = st;
   cudaLaunchAttribute at{};
@@ -197,8 +225,8 @@ cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
   c.attrs = &at;
   c.numAttrs = 1;
   count_launches(1);
-  return cudaLaunchKernelEx(&c, wgrad8_sum_kernel, (const float*)part, p.splits, n, a.d_W,
-                            a.accumulate);
+  return cudaLaunchKernelEx(&c, vec ? wgrad8_sum_kernel<4> : wgrad8_sum_kernel<1>,
+                            (const float*)part, p.splits, slices, n, a.d_W, a.accumulate);
 }
 
 }  // namespace ssm
