@@ -147,8 +147,8 @@ cudaError_t bwd_launch(const AddNormBwd& a, RowPlan pl, int per_sm, cudaStream_t
                              Operand<RES, VEC, NJ, kRing>::slot_bytes(pl.threads));
   pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
-  return launch_rows(add_norm_bwd_kernel<IO, RES, VEC, NJ, MAXT, MINB>, a, pl,
-                     ring > sums ? ring : sums, st);
+  return launch_rows<add_norm_bwd_kernel<IO, RES, VEC, NJ, MAXT, MINB>>(
+      a, pl, ring > sums ? ring : sums, st);
 }
 
 template <typename IO, typename RES>

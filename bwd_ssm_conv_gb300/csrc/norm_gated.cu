@@ -235,15 +235,15 @@ template <typename IO, int VEC, int NJ, int MAXT, int MINB>
 cudaError_t fwd_launch(const GatedNormFwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
   const uint32_t slot = 2 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
   pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
-  return launch_rows(gated_norm_fwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl, pl.slots * slot, st);
+  return launch_rows<gated_norm_fwd_kernel<IO, VEC, NJ, MAXT, MINB>>(a, pl, pl.slots * slot, st);
 }
 template <typename IO, int VEC, int NJ, int MAXT, int MINB>
 cudaError_t bwd_launch(const GatedNormBwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
   const uint32_t slot = 3 * Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)>::slot_bytes(pl.threads);
   pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
-  return launch_rows(gated_norm_bwd_kernel<IO, VEC, NJ, MAXT, MINB>, a, pl,
-                     ring > sums ? ring : sums, st);
+  return launch_rows<gated_norm_bwd_kernel<IO, VEC, NJ, MAXT, MINB>>(
+      a, pl, ring > sums ? ring : sums, st);
 }
 
 template <typename IO>

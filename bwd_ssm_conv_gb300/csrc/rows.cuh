@@ -5,6 +5,8 @@
 // (one 16- or 32-byte access), else 1.
 #pragma once
 
+#include <atomic>
+
 #include "common.cuh"
 #include "ssm_block.h"
 
@@ -489,21 +491,30 @@ inline RowPlan row_plan(long long rows, int group, int groups, int tpr, int bloc
 
 // Rows in shared memory: as many, up to 3, as leave room for per_sm_threads threads on an SM.
 constexpr int kRingBytesPerSm = 208 * 1024;
+constexpr int kRingBytesMost = 224 * 1024;  // of one block
 inline int ring_slots(uint32_t slot_bytes, int threads, int per_sm_threads) {
   if (!slot_bytes) return 1;
   const int blocks = threads >= per_sm_threads ? 1 : per_sm_threads / threads;
   const int n = (int)(kRingBytesPerSm / ((long long)slot_bytes * blocks));
   return n < 1 ? 1 : (n > 3 ? 3 : n);
 }
-// Launches with `smem` bytes of dynamic shared memory; more than 48 KB in all has to be asked for.
-template <typename K, typename A>
-inline cudaError_t launch_rows(K kernel, const A& a, const RowPlan& p, size_t smem,
-                               cudaStream_t st) {
-  if (smem > 40 * 1024)  // with the static part, 48 KB at most without asking
-    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)smem))
-      return e;
-  kernel<<<dim3(p.nbx, p.nby), p.threads, smem, st>>>(a, p);
+// Launches Kernel with `smem` bytes of dynamic shared memory.  More than 48 KB in all has to be asked
+// for, once per kernel and device (the first 64 devices remember it).
+template <auto Kernel, typename A>
+inline cudaError_t launch_rows(const A& a, const RowPlan& p, size_t smem, cudaStream_t st) {
+  if (smem > 40 * 1024) {  // with the static part, 48 KB at most without asking
+    static std::atomic<unsigned long long> asked{0};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(asked.load(std::memory_order_relaxed) & bit)) {
+      if (cudaError_t e = cudaFuncSetAttribute(Kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               kRingBytesMost))
+        return e;
+      asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  Kernel<<<dim3(p.nbx, p.nby), p.threads, smem, st>>>(a, p);
   return cudaGetLastError();
 }
 

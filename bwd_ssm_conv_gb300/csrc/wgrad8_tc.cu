@@ -540,9 +540,17 @@ int ctas_of(int m) { return m > kTM ? 2 : 1; }
 
 template <int CG> cudaError_t launch(const TcArgs& t, int splits, cudaStream_t st) {
   auto kernel = wgrad8_tc_kernel<CG>;
-  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                           (int)Lay<CG>::smem))
-    return e;
+  // asked for once per device (the first 64 remember it)
+  static std::atomic<unsigned long long> asked{0};
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Lay<CG>::smem))
+      return e;
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
   cudaLaunchConfig_t c{};
   c.gridDim = dim3((t.k + kTN - 1) / kTN * CG, (t.m + kTM * CG - 1) / (kTM * CG), splits);
   c.blockDim = dim3(kThreads);
