@@ -2,22 +2,26 @@
 
 Usage: ``python -m bwd_ssm_conv_gb300.build`` (or ``build()`` from Python).  Objects are
 compiled in parallel; the library links the shared CUDA runtime so that it and PyTorch use
-one runtime instance in a process.
+one runtime instance in a process.  Beside it goes _block.so, the Python module that marshals the
+calls of ssm_block.h: host code against PyTorch's headers.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 LIB = os.path.join(HERE, "libssm_gb300.so")
+MODULE = os.path.join(HERE, "_block.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -36,6 +40,42 @@ def _cuda_lib_dir(nvcc: str) -> str:
     return os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc))), "lib64")
 
 
+def _torch_dir() -> str:
+    return os.path.dirname(importlib.util.find_spec("torch").origin)
+
+
+def _module_source() -> str:
+    return os.path.join(CSRC, "block_binding.cpp")
+
+
+def _compile_module(nvcc: str) -> str:
+    """The module's object; a C++ compiler, as it holds no device code."""
+    obj = os.path.join(BUILD_DIR, "block_binding.o")
+    torch_include = os.path.join(_torch_dir(), "include")
+    cuda_include = os.path.join(os.path.dirname(_cuda_lib_dir(nvcc)), "include")
+    _run([os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-I", INCLUDE,
+          "-isystem", torch_include,
+          "-isystem", os.path.join(torch_include, "torch", "csrc", "api", "include"),
+          "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda_include,
+          "-c", _module_source(), "-o", obj])
+    return obj
+
+
+def _link_module(obj: str) -> None:
+    tmp = MODULE + f".{os.getpid()}.tmp"
+    _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", HERE,
+          "-l:" + os.path.basename(LIB), "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
+          "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"])
+    os.replace(tmp, MODULE)
+
+
+def _run(cmd) -> str:
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{' '.join(cmd)} failed:\n{r.stdout}\n{r.stderr}")
+    return r.stderr
+
+
 def _sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
@@ -46,10 +86,13 @@ def _deps():
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(MODULE):
         return False
-    t = os.path.getmtime(LIB)
-    return all(os.path.getmtime(p) <= t for p in _deps())
+    t, m = os.path.getmtime(LIB), os.path.getmtime(MODULE)
+    # the module also goes with the PyTorch that it was compiled against
+    torch_version = os.path.join(_torch_dir(), "version.py")
+    return (all(os.path.getmtime(p) <= t for p in _deps()) and
+            all(os.path.getmtime(p) <= m for p in [LIB, _module_source(), torch_version]))
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -68,6 +111,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 4)) as ex:
+        module = ex.submit(_compile_module, nvcc)
         results = list(ex.map(compile_one, _sources()))
     if verbose or ptxas_info:
         for _, err in results:
@@ -80,6 +124,7 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_module(module.result())
     return LIB
 
 
