@@ -7,13 +7,14 @@
 // threads.  The sigmoid is taken once per value in each direction.
 //
 // What bounds them (32768 rows of 1536 bf16 columns, checkpoints of y and z, GB300):
-//   forward   67 us, 406 MB: 6.0 TB/s of 6.7 measured for a copy, and 62 % of the issue slots.
+//   forward   66 us, 406 MB: 6.2 TB/s of 6.7 measured for a copy, and 57 % of the issue slots.
 //             Largest magnitudes of bf16 blocks taken two at a time, and one fused rounding per
 //             value, brought 94 -> 74 us; rows and strides in 32 bits 74 -> 67 us.
-//   backward  93 us, 406 MB: the issue slots (62 % busy at 14 warps per SM; about 44 instructions
-//             per value), at 4.4 TB/s.  The rows read with plain loads took 191 us, the next row
+//   backward  90 us, 406 MB at 4.5 TB/s: issue slots (58 % busy at 14 warps per SM, which wait for
+//             their own results).  The rows read with plain loads took 191 us, the next row
 //             loaded ahead into registers (which spill) 252 us, copied ahead 134 us; fewer chunks per
-//             thread (norm_shape) and all blocks resident 108 us, 32-bit rows and strides 93 us.
+//             thread (norm_shape) and all blocks resident 108 us, 32-bit rows and strides 93 us,
+//             pairs of values per instruction 90 us.  One chunk per thread, for twice the warps: 101.
 #include "block.cuh"
 #include "rows.cuh"
 
@@ -41,6 +42,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
     ld_param<VEC>(a.w, col[j], okc[j], w[j]);
   }
   typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
+  typedef Packed<VEC> P;
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
   Op y{a.y, nullptr, nullptr, a.ld_y, at}, z{a.z, nullptr, nullptr, a.ld_z, at + bytes};
   const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
@@ -68,7 +70,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
     const uint32_t s = slot * 2 * bytes;
     slot = slot == ahead ? 0 : slot + 1;
     const long long qrow = (long long)row * a.cols, erow = (long long)row * nb;
-    float v[NJ][VEC], sq = 0.0f;
+    float v[NJ][VEC];
+    typename P::T sq = P::of(0.0f);
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
@@ -80,26 +83,33 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
         store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + (int)((unsigned)col[j] / 32));
         store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + (int)((unsigned)col[j] / 32));
       }
-      if (!a.norm_first)
 #pragma unroll
-        for (int i = 0; i < VEC; i++) v[j][i] *= siluf_(zv[i]);
-#pragma unroll
-      for (int i = 0; i < VEC; i++) sq = fmaf(v[j][i], v[j][i], sq);
+      for (int i = 0; i < P::N; i++) {
+        typename P::T t = P::at(v[j], i);
+        if (!a.norm_first) {
+          const typename P::T z2 = P::at(zv, i);
+          t = mul_(t, mul_(z2, sigmoid_(z2)));
+          P::put(v[j], i, t);
+        }
+        sq = fma_(t, t, sq);
+      }
     }
-    const float rstd = 1.0f / sqrtf(row_sum(sq, pl.tpr, part, half) * inv + a.eps);
+    const float rstd = 1.0f / sqrtf(row_sum(P::sum(sq), pl.tpr, part, half) * inv + a.eps);
     if (a.rstd && rok && pos.ok && pos.lane == 0)
       a.rstd[(long long)row * pl.groups + grp] = rstd;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
-      float o[VEC];
+      float o[VEC], zv[VEC];
+      if (a.norm_first) z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
 #pragma unroll
-      for (int i = 0; i < VEC; i++) o[i] = w[j][i] * (v[j][i] * rstd);
-      if (a.norm_first) {
-        float zv[VEC];
-        z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
-#pragma unroll
-        for (int i = 0; i < VEC; i++) o[i] *= siluf_(zv[i]);
+      for (int i = 0; i < P::N; i++) {
+        typename P::T t = mul_(P::at(w[j], i), mul_(P::at(v[j], i), P::of(rstd)));
+        if (a.norm_first) {
+          const typename P::T z2 = P::at(zv, i);
+          t = mul_(t, mul_(z2, sigmoid_(z2)));
+        }
+        P::put(o, i, t);
       }
       Cols<IO, VEC> oc;
       to_cols(o, oc);
@@ -123,15 +133,18 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
   const int grp = pos.col0 / a.group;
   bool okc[NJ];
   int col[NJ];
-  float w[NJ][VEC], dw[NJ][VEC];
+  typedef Packed<VEC> P;
+  typedef typename P::T T;
+  T w[NJ][P::N], dw[NJ][P::N];
 #pragma unroll
   for (int j = 0; j < NJ; j++) {
     const int c = (pos.lane + j * pl.tpr) * VEC;
     okc[j] = pos.ok && c < a.group;
     col[j] = pos.col0 + c;
-    ld_param<VEC>(a.w, col[j], okc[j], w[j]);
+    float wv[VEC];
+    ld_param<VEC>(a.w, col[j], okc[j], wv);
 #pragma unroll
-    for (int i = 0; i < VEC; i++) dw[j][i] = 0.0f;
+    for (int i = 0; i < P::N; i++) w[j][i] = P::at(wv, i), dw[j][i] = P::of(0.0f);
   }
   typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Op;
   const uint32_t bytes = Op::slot_bytes(blockDim.x), at = shared_addr(ring) + 16 * threadIdx.x;
@@ -189,7 +202,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
     slot = slot == ahead ? 0 : slot + 1;
     // What the second pass needs of y and z, so that it does not unpack them again: g = silu(z),
     // m = n / rstd, b = y silu'(z) (gate first) or d_z already (norm first)
-    float g[NJ][VEC], b[NJ][VEC], m[NJ][VEC], dot = 0.0f;
+    T g[NJ][P::N], b[NJ][P::N], m[NJ][P::N], dot = P::of(0.0f);
+    const T rs = P::of(rstd);
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
@@ -198,46 +212,51 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_bwd_kernel(const GatedN
       y.get(s, j, ok, row, col[j], a.cols, ey[j], yv);
       z.get(s, j, ok, row, col[j], a.cols, ez[j], zv);
 #pragma unroll
-      for (int i = 0; i < VEC; i++) {
-        const float sg = sigmoidf_(zv[i]);
-        g[j][i] = zv[i] * sg;
-        b[j][i] = yv[i] * fmaf(g[j][i], 1.0f - sg, sg);  // y times d silu(z) / d z
-        m[j][i] = yv[i] * g[j][i];
-        const float t = dv[i] * rstd * m[j][i];  // d_out times n and gate
-        dw[j][i] += t;
-        dot = fmaf(w[j][i], t, dot);
-      }
-      if (a.norm_first) {
-#pragma unroll
-        for (int i = 0; i < VEC; i++) m[j][i] = yv[i], b[j][i] *= w[j][i] * dv[i] * rstd;
+      for (int i = 0; i < P::N; i++) {
+        const T y2 = P::at(yv, i), z2 = P::at(zv, i), sg = sigmoid_(z2);
+        const T dr = mul_(P::at(dv, i), rs);
+        g[j][i] = mul_(z2, sg);
+        b[j][i] = mul_(y2, fma_(g[j][i], fma_(sg, P::of(-1.0f), P::of(1.0f)), sg));
+        m[j][i] = mul_(y2, g[j][i]);
+        const T t = mul_(dr, m[j][i]);  // d_out times n and gate
+        dw[j][i] = add_(dw[j][i], t);
+        dot = fma_(w[j][i], t, dot);
+        if (a.norm_first) m[j][i] = y2, b[j][i] = mul_(b[j][i], mul_(w[j][i], dr));
       }
     }
-    const float c = -row_sum(dot, pl.tpr, part, half) * inv * rstd;
+    const T c = P::of(-row_sum(P::sum(dot), pl.tpr, part, half) * inv * rstd);
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       const bool ok = rok && okc[j];
-      float dv[VEC], dy[VEC];
+      float dv[VEC], dy[VEC], dz[VEC];
       d.get(s, j, ok, row, col[j], a.cols, 7u, dv);
-      if (a.norm_first) {
 #pragma unroll
-        for (int i = 0; i < VEC; i++)
-          dy[i] = rstd * fmaf(m[j][i], c, w[j][i] * dv[i] * g[j][i]);
-      } else {
-#pragma unroll
-        for (int i = 0; i < VEC; i++) {
-          const float t = rstd * fmaf(m[j][i], c, w[j][i] * dv[i]);
-          dy[i] = t * g[j][i];
-          b[j][i] *= t;
+      for (int i = 0; i < P::N; i++) {
+        T t = mul_(w[j][i], P::at(dv, i));
+        if (a.norm_first) {
+          P::put(dy, i, mul_(rs, fma_(m[j][i], c, mul_(t, g[j][i]))));
+          P::put(dz, i, b[j][i]);
+        } else {
+          t = mul_(rs, fma_(m[j][i], c, t));
+          P::put(dy, i, mul_(t, g[j][i]));
+          P::put(dz, i, mul_(t, b[j][i]));
         }
       }
       if (ok) {
         st_cols((IO*)a.d_y + (long long)row * a.ld_d_y + col[j], dy);
-        st_cols((IO*)a.d_z + (long long)row * a.ld_d_z + col[j], b[j]);
+        st_cols((IO*)a.d_z + (long long)row * a.ld_d_z + col[j], dz);
       }
     }
   }
   cp_async_wait(0);
-  if (a.d_w) store_partial<VEC, NJ>(dw, pl, pos, col, okc, a.cols, a.part, (float*)ring);
+  if (a.d_w) {
+    float sums[NJ][VEC];
+#pragma unroll
+    for (int j = 0; j < NJ; j++)
+#pragma unroll
+      for (int i = 0; i < P::N; i++) P::put(sums[j], i, dw[j][i]);
+    store_partial<VEC, NJ>(sums, pl, pos, col, okc, a.cols, a.part, (float*)ring);
+  }
 }
 
 template <typename IO, int VEC, int NJ, int MAXT, int MINB>

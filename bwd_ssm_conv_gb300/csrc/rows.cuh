@@ -117,6 +117,45 @@ __device__ __forceinline__ void ld_param(const float* p, int col, bool ok, float
   }
 }
 
+// A chunk's values for arithmetic: pairs of columns (one instruction for two) or the single one.
+template <int VEC> struct Packed {
+  typedef f2_t T;
+  static constexpr int N = VEC / 2;
+  static __device__ __forceinline__ T of(float v) { return f2_pack(v, v); }
+  static __device__ __forceinline__ T at(const float (&v)[VEC], int i) {
+    return f2_pack(v[2 * i], v[2 * i + 1]);
+  }
+  static __device__ __forceinline__ void put(float (&v)[VEC], int i, T x) {
+    f2_unpack(x, v[2 * i], v[2 * i + 1]);
+  }
+  static __device__ __forceinline__ float sum(T x) {
+    float a, b;
+    f2_unpack(x, a, b);
+    return a + b;
+  }
+};
+template <> struct Packed<1> {
+  typedef float T;
+  static constexpr int N = 1;
+  static __device__ __forceinline__ T of(float v) { return v; }
+  static __device__ __forceinline__ T at(const float (&v)[1], int) { return v[0]; }
+  static __device__ __forceinline__ void put(float (&v)[1], int, T x) { v[0] = x; }
+  static __device__ __forceinline__ float sum(T x) { return x; }
+};
+__device__ __forceinline__ float mul_(float a, float b) { return a * b; }
+__device__ __forceinline__ float add_(float a, float b) { return a + b; }
+__device__ __forceinline__ float fma_(float a, float b, float c) { return fmaf(a, b, c); }
+__device__ __forceinline__ f2_t mul_(f2_t a, f2_t b) { return f2_mul(a, b); }
+__device__ __forceinline__ f2_t add_(f2_t a, f2_t b) { return f2_add(a, b); }
+__device__ __forceinline__ f2_t fma_(f2_t a, f2_t b, f2_t c) { return f2_fma(a, b, c); }
+__device__ __forceinline__ float sigmoid_(float v) { return sigmoidf_(v); }
+__device__ __forceinline__ f2_t sigmoid_(f2_t v) {
+  float a, b;
+  f2_unpack(f2_mul(v, f2_pack(-kLog2e, -kLog2e)), a, b);
+  f2_unpack(f2_add(f2_pack(ex2(a), ex2(b)), f2_pack(1.0f, 1.0f)), a, b);
+  return f2_pack(rcp_approx(a), rcp_approx(b));
+}
+
 // ---- the 8-bit block format (ssm_block.h) ------------------------------------------------------
 // A block's 32 columns lie in 32 / VEC consecutive lanes.
 // The larger magnitude, NaN if either is one (its sign is left undefined).
@@ -160,6 +199,19 @@ __device__ __forceinline__ uint32_t pack_low_bytes(uint32_t a, uint32_t b, uint3
   return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 template <bool kLimit> __device__ __forceinline__ uint2 quant8(const float (&v)[8], float up) {
+  if constexpr (!kLimit) {
+    float r[8];
+#pragma unroll
+    for (int i = 0; i < 4; i++)
+      f2_unpack(f2_fma(f2_pack(v[2 * i], v[2 * i + 1]), f2_pack(up, up),
+                       f2_pack(12582912.0f, 12582912.0f)),
+                r[2 * i], r[2 * i + 1]);
+    uint32_t b[8];
+#pragma unroll
+    for (int i = 0; i < 8; i++) b[i] = __float_as_uint(r[i]);
+    return make_uint2(pack_low_bytes(b[0], b[1], b[2], b[3]),
+                      pack_low_bytes(b[4], b[5], b[6], b[7]));
+  }
   return make_uint2(pack_low_bytes(quant_bits<kLimit>(v[0], up), quant_bits<kLimit>(v[1], up),
                                    quant_bits<kLimit>(v[2], up), quant_bits<kLimit>(v[3], up)),
                     pack_low_bytes(quant_bits<kLimit>(v[4], up), quant_bits<kLimit>(v[5], up),
@@ -226,10 +278,13 @@ template <> struct Kept<8> {
   __device__ __forceinline__ void get(float (&v)[8]) const {
     const float step = block_step(e);
     const uint32_t w[2] = {q.x ^ 0x80808080u, q.y ^ 0x80808080u};  // q + 128 in each byte
+    const f2_t step2 = f2_pack(step, step), off = f2_pack(-8388736.0f, -8388736.0f);
 #pragma unroll
-    for (int i = 0; i < 8; i++) {  // 2^23 + (q + 128) as a float, minus 2^23 + 128: exactly q
-      const uint32_t b = __byte_perm(w[i >> 2], 0x4b000000u, 0x7650u + (i & 3));
-      v[i] = (__uint_as_float(b) - 8388736.0f) * step;
+    for (int i = 0; i < 8; i += 2) {  // 2^23 + (q + 128) as a float, minus 2^23 + 128: exactly q
+      const uint32_t a = __byte_perm(w[i >> 2], 0x4b000000u, 0x7650u + (i & 3));
+      const uint32_t b = __byte_perm(w[i >> 2], 0x4b000000u, 0x7651u + (i & 3));
+      f2_unpack(f2_mul(f2_add(f2_pack(__uint_as_float(a), __uint_as_float(b)), off), step2), v[i],
+                v[i + 1]);
     }
   }
 };
