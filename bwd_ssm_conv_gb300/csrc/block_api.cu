@@ -297,9 +297,7 @@ int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_
   if (!ws || !aligned(ws, 256) ||
       ws_bytes < ssm::wgrad_ws_bytes(tokens, m, k, io, ssm::wgrad_aligned(a), sms))
     return SSM_ERR_WORKSPACE;
-  cudaStream_t st = (cudaStream_t)stream;
-  if (cudaMemsetAsync(ws, 0, sizeof(int), st) != cudaSuccess) return SSM_ERR_CUDA;
-  return status_of(ssm::launch_wgrad(a, ws, sms, st));
+  return status_of(ssm::launch_wgrad(a, ws, sms, (cudaStream_t)stream));
 }
 
 }  // extern "C"

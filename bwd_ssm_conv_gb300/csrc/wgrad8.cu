@@ -3,9 +3,11 @@
 //   before  operands that it cannot read as they are go to the workspace in a form that it can:
 //           fp32 g as three bf16 terms, rows that are not 16-byte aligned with their rows padded
 //   after   where the tokens are split over blocks, the splits' tiles are added in order
-// The copies read and write each value once.  8189 tokens x 64 x 512, fp32 g (GB300): split 2.1 us,
-// product 9.8 us, sum 3.0 us; 8192 x 2048 x 1024: 102 us in all, 1010 TFLOP/s of bf16 products for
-// 337 of fp32 (a plain fp32 product: 54).
+// The copies read and write each value once.  8189 tokens x 64 x 512, fp32 g (GB300): 17.6 us, of
+// which the copy 2.1, the product 9.8 and the sum 3.0 by themselves; each is set up while the one
+// before it runs (one after the other, with the status word cleared by a copy of its own: 20.5).
+// 8192 x 2048 x 1024: 102 us, 1010 TFLOP/s of bf16 products for 337 of fp32 (a plain fp32 product:
+// 54).
 #include "block.cuh"
 #include "rows.cuh"
 
@@ -15,10 +17,19 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// A call's first kernel clears its status word; the tensor-core kernel may be set up meanwhile (it
+// waits where it needs the copies).
+__device__ __forceinline__ void first_of_call(int* status) {
+  if (blockIdx.x == 0 && threadIdx.x == 0) *status = 0;
+  asm volatile("griddepcontrol.launch_dependents;");
+}
+__global__ void clear_status_kernel(int* status) { first_of_call(status); }
+
 // A thread pads 8 columns of a row of bf16 g.
 __global__ void __launch_bounds__(kThreads) pad_g_kernel(const __nv_bfloat16* g, long long ld,
                                                          __nv_bfloat16* out, int m, int m8,
-                                                         long long n) {
+                                                         long long n, int* status) {
+  first_of_call(status);
   for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kThreads) {
     const long long t = i / (m8 / 8);
@@ -55,7 +66,9 @@ __device__ __forceinline__ void three_bf16(float v, uint32_t (&h)[3]) {
 template <bool VEC>
 __global__ void __launch_bounds__(kThreads) split_g_kernel(const float* g, long long ld,
                                                            __nv_bfloat16* out, long long plane,
-                                                           int m, int m8, long long n) {
+                                                           int m, int m8, long long n,
+                                                           int* status) {
+  first_of_call(status);
   for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kThreads) {
     const long long t = i / (m8 / 8);
@@ -88,7 +101,8 @@ __global__ void __launch_bounds__(kThreads) split_g_kernel(const float* g, long 
 
 // A thread pads 16 columns of a row of q.
 __global__ void __launch_bounds__(kThreads) pad_q_kernel(const int8_t* q, int8_t* out, int k,
-                                                         int k16, long long n) {
+                                                         int k16, long long n, int* status) {
+  first_of_call(status);
   for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
        i += (long long)gridDim.x * kThreads) {
     const long long t = i / (k16 / 16);
@@ -179,6 +193,7 @@ size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int 
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
   const Plan p = plan_of(a.tokens, a.m, a.k, a.io, wgrad_aligned(a), sms);
   char* w = (char*)ws;
+  int* status = (int*)ws;
   const void* g = a.g;
   long long ld_g = a.ld_g, ld_q = a.k;
   const int8_t* q = a.q;
@@ -189,10 +204,10 @@ cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
       const bool vec = p.m8 == a.m && a.ld_g % 8 == 0 && (uintptr_t)a.g % 32 == 0;
       auto kernel = vec ? split_g_kernel<true> : split_g_kernel<false>;
       kernel<<<blocks_of(n, sms), kThreads, 0, st>>>((const float*)a.g, a.ld_g, out,
-                                                     a.tokens * p.m8, a.m, p.m8, n);
+                                                     a.tokens * p.m8, a.m, p.m8, n, status);
     } else {
       pad_g_kernel<<<blocks_of(n, sms), kThreads, 0, st>>>((const __nv_bfloat16*)a.g, a.ld_g, out,
-                                                           a.m, p.m8, n);
+                                                           a.m, p.m8, n, status);
     }
     count_launches(1);
     if (cudaError_t e = cudaGetLastError()) return e;
@@ -202,14 +217,19 @@ cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
   if (p.copy_q) {
     int8_t* out = (int8_t*)(w + p.q);
     const long long n = a.tokens * (p.k16 / 16);
-    pad_q_kernel<<<blocks_of(n, sms), kThreads, 0, st>>>(a.q, out, a.k, p.k16, n);
+    pad_q_kernel<<<blocks_of(n, sms), kThreads, 0, st>>>(a.q, out, a.k, p.k16, n, status);
     count_launches(1);
     if (cudaError_t e = cudaGetLastError()) return e;
     q = out;
     ld_q = p.k16;
   }
+  if (!p.copy_g && !p.copy_q) {
+    clear_status_kernel<<<1, 32, 0, st>>>(status);
+    count_launches(1);
+    if (cudaError_t e = cudaGetLastError()) return e;
+  }
   float* part = p.splits > 1 ? (float*)(w + p.part) : nullptr;
-  if (cudaError_t e = launch_wgrad_tc(g, ld_g, p.terms, q, ld_q, a, part, p.splits, (int*)ws, st))
+  if (cudaError_t e = launch_wgrad_tc(g, ld_g, p.terms, q, ld_q, a, part, p.splits, status, st))
     return e;
   if (!part) return cudaSuccess;
   const long long n = (long long)a.m * a.k;

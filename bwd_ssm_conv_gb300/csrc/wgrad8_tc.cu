@@ -79,7 +79,7 @@ struct TcArgs {
   float* out;  // d_W, or the splits' partial tiles
   long long tokens;
   int stages, per_term, per_split;  // in all, of one term of g, of one split
-  int m, k, nb, accumulate, vec_out;
+  int m, k, nb, accumulate, vec_out, q_copied;
   int* status;
 };
 
@@ -174,6 +174,12 @@ template <int S> struct Ring {
     if (++s == S) s = 0, phase ^= 1;
   }
 };
+// This kernel may start while the one before it in the call runs (wgrad8.cu): here its results are
+// complete, also for TMA.
+__device__ __forceinline__ void wait_for_copies() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("fence.proxy.async.global;" ::: "memory");
+}
 template <int CG> __device__ __forceinline__ void sync_tile() {  // every thread of the tile's CTAs
   if constexpr (CG == 1) {
     __syncthreads();
@@ -313,10 +319,12 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
   sync_tile<CG>();
   tmem_fence_after_sync();
   const uint32_t tm = tbase;
+  asm volatile("griddepcontrol.launch_dependents;");  // the kernel that adds the splits, if any
 
   if (warp < 4) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
     if (warp == 0) {
+      if (a.q_copied) wait_for_copies();
       Ring<S> r;
       int it = 0, st = s_begin % a.per_term;
       for (; it < iters; it++, st = st + 1 == a.per_term ? 0 : st + 1, r.next()) {
@@ -335,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
         if (!mbar_wait(&q_here[j % S], (j / S) & 1)) break;
     } else if (warp == 3) {
       uint64_t* here = rank == 0 ? full : g_here;
+      wait_for_copies();
       Ring<S> r;
       int it = 0, term = s_begin / a.per_term, st = s_begin - term * a.per_term;
       for (; it < iters; it++, r.next()) {
@@ -532,7 +541,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     tmem_fence_after_sync();
     Mma<CG>::dealloc(tm);
   }
-  if (tid == 0 && bad) record_status(a.status, SSM_ERR_TIMEOUT);
+  if (tid == 0) {
+    wait_for_copies();  // the kernel before clears the status; this one does not end ahead of it
+    if (bad) record_status(a.status, SSM_ERR_TIMEOUT);
+  }
 }
 
 // A tile of two CTAs where a row tile of one would be full.
@@ -556,12 +568,14 @@ template <int CG> cudaError_t launch(const TcArgs& t, int splits, cudaStream_t s
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = Lay<CG>::smem;
   c.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim.x = CG;
-  at.val.clusterDim.y = at.val.clusterDim.z = 1;
-  c.attrs = &at;
-  c.numAttrs = CG > 1 ? 1 : 0;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = CG;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = CG > 1 ? 2 : 1;
   const cudaError_t e = cudaLaunchKernelEx(&c, kernel, t);
   count_launches(1);
   return e;
@@ -584,7 +598,8 @@ int wgrad_tc_splits(long long tokens, int terms, int m, int k, int sms) {
   return (stages + per - 1) / per;  // none of them empty
 }
 
-// g: [terms][tokens] rows of ld_g elements, q: rows of ld_q bytes; both 16-byte aligned.
+// To be called right after a kernel of the same call that clears `status` and lets this one start
+// early.  g: [terms][tokens] rows of ld_g elements, q: rows of ld_q bytes; both 16-byte aligned.
 cudaError_t launch_wgrad_tc(const void* g, long long ld_g, int terms, const int8_t* q,
                             long long ld_q, const Wgrad& a, float* part, int splits, int* status,
                             cudaStream_t st) {
@@ -604,6 +619,7 @@ cudaError_t launch_wgrad_tc(const void* g, long long ld_g, int terms, const int8
   t.k = a.k;
   t.nb = (a.k + 31) / 32;
   t.accumulate = part ? 0 : a.accumulate;
+  t.q_copied = q != a.q;
   t.vec_out = a.k % 8 == 0 && (uintptr_t)t.out % 32 == 0;
   t.status = status;
   return cg == 1 ? launch<1>(t, splits, st) : launch<2>(t, splits, st);
