@@ -65,7 +65,7 @@ def _link_module(obj: str) -> None:
     tmp = MODULE + f".{os.getpid()}.tmp"
     _run([os.environ.get("CXX", "g++"), "-shared", "-o", tmp, obj, "-L", HERE,
           "-l:" + os.path.basename(LIB), "-L", os.path.join(_torch_dir(), "lib"), "-ltorch_python",
-          "-ltorch_cpu", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"])
+          "-ltorch_cpu", "-ltorch_cuda", "-lc10_cuda", "-lc10", "-Wl,-rpath,$ORIGIN"])
     os.replace(tmp, MODULE)
 
 

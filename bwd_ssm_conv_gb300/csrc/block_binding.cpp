@@ -9,6 +9,7 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -140,7 +141,7 @@ Kept kept(const Pair& c, const char* name, IntArrayRef shape) {
 
 // ---- results ------------------------------------------------------------------------------------
 Tensor make(IntArrayRef shape, ScalarType dtype, const Tensor& like) {
-  return at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
+  return at::Tensor(at::detail::empty_cuda(shape, dtype, like.device(), std::nullopt));
 }
 struct NewCkpt8 {
   Tensor q, e;
