@@ -199,3 +199,25 @@ def test_binding_refuses_what_the_library_cannot_see():
     with pytest.raises(ValueError, match="accumulate"):
         block.ssm_ckpt8_wgrad(t, block.Ckpt8(t.to(torch.int8), t[:, :2].to(torch.uint8)),
                               accumulate=True)
+
+
+def test_binding_names_the_argument_that_is_not_a_tensor():
+    t = torch.zeros(4, 64)
+    c = block.Ckpt8(t.to(torch.int8), t[:, :2].to(torch.uint8))
+    for call, name in ((lambda: block.ssm_add_norm_fwd([1.0]), "x"),
+                       (lambda: block.ssm_add_norm_fwd(t, w=2.0), "w"),
+                       (lambda: block.ssm_add_norm_bwd(t, None, t), "res"),
+                       (lambda: block.ssm_gated_norm_fwd(t, None), "z"),
+                       (lambda: block.ssm_gated_norm_bwd(t, t, None, t), "z"),
+                       (lambda: block.ssm_ckpt8_load(t), "c"),
+                       (lambda: block.ssm_ckpt8_save(t, out=t), "out|x"),
+                       (lambda: block.ssm_ckpt8_wgrad(t, t), "x8"),
+                       (lambda: block.ssm_ckpt8_wgrad(None, c), "g")):
+        with pytest.raises((TypeError, ValueError), match=name):
+            call()
+    with pytest.raises(ValueError, match="dimension"):
+        block.ssm_ckpt8_save(torch.tensor(1.0))
+    with pytest.raises(TypeError, match="dtype"):
+        block.ssm_add_norm_fwd(t, res_dtype="float32")
+    with pytest.raises(ValueError, match="pair"):
+        block.ssm_ckpt8_load((c.q,))

@@ -8,7 +8,7 @@ import pytest
 import torch
 
 import block_ref as ref
-from bwd_ssm_conv_gb300 import block
+from bwd_ssm_conv_gb300 import SsmError, block
 from gpu_util import TOL_F32_FWD, TOL_F32_GRAD, assert_close
 
 pytestmark = pytest.mark.gpu
@@ -252,3 +252,31 @@ def test_rows_past_32_bit_offsets():
     want = ref.gated_norm_bwd(last, y8, z8, a.rstd[-4:].cpu(), None, 0, False)
     close("d_y", b["d_y"][-4:], want[0], grad=True)
     close("d_z", b["d_z"][-4:], want[1], grad=True)
+
+
+def test_what_a_call_makes_is_freed_with_its_results():
+    x = torch.randn(40, 96, device="cuda")
+    w = torch.ones(96, device="cuda")
+
+    def step():
+        a = block.ssm_add_norm_fwd(x, w, x, w, save8=True, save_x8=True, save_out8=True)
+        g = block.ssm_add_norm_bwd(x, a.res8, a.rstd, w, d_res_out=x, scale=w, x=a.x8)
+        b = block.ssm_gated_norm_fwd(x, x, w, save8=True, save_out8=True)
+        h = block.ssm_gated_norm_bwd(x, b.y8, b.z8, b.rstd, w)
+        d = block.ssm_ckpt8_wgrad(x, b.out8)
+        e = block.ssm_ckpt8_load(block.ssm_ckpt8_save(x))
+        with pytest.raises(ValueError):
+            block.ssm_add_norm_fwd(x, w[:5])
+        with pytest.raises(SsmError):
+            block.ssm_gated_norm_fwd(x, x, w, group=7)
+        return a, g, b, h, d, e
+
+    step()
+    before = torch.cuda.memory_allocated()
+    kept = step()
+    assert torch.cuda.memory_allocated() > before
+    assert type(kept[0].res8) is block.Ckpt8 and type(kept[0]) is block.AddNorm
+    del kept
+    for _ in range(20):
+        step()
+    assert torch.cuda.memory_allocated() == before
