@@ -1,5 +1,7 @@
 // norm_plan.cu -- how the norms' launches are laid out, and the sums over rows that their
 // backwards share.
+#include <stdlib.h>
+
 #include "block.cuh"
 
 namespace ssm {
@@ -64,13 +66,18 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
       nj = 2, s.variant = kVec2Wide;
     } else {
       // Of 4, 3 and 2 chunks per thread (2 and 1 in the backward, which keeps more of each) the one
-      // that leaves the fewest threads without a chunk, then the larger: on 32768 rows of 1536 bf16
-      // columns the forward takes 74 us with 3, 83 with 2 and 128 with 1, the backward 119, 108, 165.
-      int best = -1;
+      // that leaves the fewest threads without a chunk: on 32768 rows of 1536 bf16 columns the
+      // forward takes 74 us with 3, 83 with 2 and 128 with 1, the backward 119, 108, 165.  Among
+      // equals the forward takes the one nearest to two warps per row (add_norm of bf16 rows and an
+      // fp32 stream, 2 and 4 chunks: 16384 x 512 17.9 and 20.3 us, 16384 x 1024 34.4 and 37.1; both
+      // bf16, 8192 x 2048: 30.1 and 28.0), the backward the larger, whose fewer rows at a time leave
+      // fewer column sums to add (8192 x 512 fp32, 2 and 1: 18.7 and 20.2 us with them).
+      int best = -1, from64 = 0;
       nj = 2;
       for (int k = backward ? 2 : 4; k >= (backward ? 1 : 2); k--) {
-        const int tpr = row_threads(nch, k, 8), idle = tpr * k - nch;
-        if (tpr <= 256 && (best < 0 || idle < best)) nj = k, best = idle;
+        const int tpr = row_threads(nch, k, 8), idle = tpr * k - nch, off = abs(tpr - 64);
+        if (tpr <= 256 && (best < 0 || idle < best || (!backward && idle == best && off < from64)))
+          nj = k, best = idle, from64 = off;
       }
       s.variant = nj == 1 ? kVec1 : (nj == 2 ? kVec2 : (nj == 3 ? kVec3 : kVec4));
     }
