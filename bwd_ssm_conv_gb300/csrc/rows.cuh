@@ -378,7 +378,8 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   const uint8_t* e;
   int ld;
   uint32_t at;  // this thread's place in the first slot of the ring
-  float cur[VEC == 1 ? NJ : 1], next[VEC == 1 ? NJ : 1];  // single columns: this row and the next
+  // single columns of this row and the next, as loaded: nothing waits for the next row's
+  uint32_t cur[VEC == 1 ? NJ : 1], next[VEC == 1 ? NJ : 1];
 
   __device__ __forceinline__ bool given() const { return t || q; }
   // Bytes that a block's threads need per slot of the ring.
@@ -395,24 +396,15 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   __device__ __forceinline__ void issue(uint32_t s, int row, const int (&col)[NJ],
                                         const bool (&okc)[NJ], int cols) {
     if constexpr (VEC == 1) {
-      if (q) {
-        const int8_t* p = q + (long long)row * cols;
+      const int8_t* pq = q + (long long)row * cols;
+      const IO* pt = (const IO*)t + (long long)row * ld;
 #pragma unroll
-        for (int j = 0; j < NJ; j++) next[j] = okc[j] ? (float)p[col[j]] : 0.0f;
-      } else if (t) {
-        const IO* p = (const IO*)t + (long long)row * ld;
-#pragma unroll
-        for (int j = 0; j < NJ; j++) {
-          Cols<IO, 1> c;
-          float v[1];
-          c.zero();
-          if (okc[j]) c.load(p + col[j]);
-          c.get(v);
-          next[j] = v[0];
-        }
-      } else {
-#pragma unroll
-        for (int j = 0; j < NJ; j++) next[j] = 0.0f;
+      for (int j = 0; j < NJ; j++) {
+        next[j] = 0u;
+        if (!okc[j] || !given()) continue;
+        if (q) next[j] = (uint32_t)(int)pq[col[j]];
+        else if constexpr (sizeof(IO) == 2) next[j] = reinterpret_cast<const uint16_t*>(pt)[col[j]];
+        else next[j] = reinterpret_cast<const uint32_t*>(pt)[col[j]];
       }
     }
     if constexpr (RING) {
@@ -442,7 +434,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   __device__ __forceinline__ void clear(uint32_t s, const bool (&okc)[NJ], bool all) {
     if constexpr (VEC == 1)
 #pragma unroll
-      for (int j = 0; j < NJ; j++) next[j] = 0.0f;
+      for (int j = 0; j < NJ; j++) next[j] = 0u;
     if constexpr (RING) {
 #pragma unroll
       for (int j = 0; j < NJ; j++)
@@ -470,7 +462,8 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   __device__ __forceinline__ void get(uint32_t s, int j, bool ok, int row, int col, int cols,
                                       uint32_t x, float (&v)[VEC]) const {
     if constexpr (VEC == 1) {
-      v[0] = q ? cur[j] * block_step(x) : cur[j];
+      v[0] = q ? (float)(int)cur[j] * block_step(x) :
+             __uint_as_float(sizeof(IO) == 2 ? cur[j] << 16 : cur[j]);
     } else if constexpr (!RING) {
       if (!ok || !given()) {
 #pragma unroll
