@@ -103,8 +103,9 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
     if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
-  ssm::AddNormFwd a{(int)desc->rows, desc->cols, desc->eps, x, residual, scale, w, out, res_out, rstd,
-                    (int)ld_x, (int)ld_residual, (int)ld_out, (int)ld_res_out, res_q, x_q, out_q, res_e, x_e, out_e};
+  ssm::AddNormFwd a{(int)desc->rows, desc->cols, desc->eps, x, residual, scale, w, out, res_out,
+                    rstd, (int)ld_x, (int)ld_residual, (int)ld_out, (int)ld_res_out, res_q, x_q,
+                    out_q, res_e, x_e, out_e};
   return status_of(ssm::launch_add_norm_fwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
 }
 
@@ -155,8 +156,9 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
                ws_bytes < 256 + ssm::column_sums_bytes(desc->rows, group, 1, sms, sums)))
     return SSM_ERR_WORKSPACE;
   ssm::AddNormBwd a{(int)desc->rows, desc->cols, d_out, d_res_out, res, x, (int)ld_d_out,
-                    (int)ld_d_res_out, (int)ld_res, (int)ld_x, res_q, x_q, res_e, x_e, rstd, scale, w,
-                    d_res, d_x, (int)ld_d_res, (int)ld_d_x, d_w, d_scale, sums ? (float*)((char*)ws + 256) : nullptr};
+                    (int)ld_d_res_out, (int)ld_res, (int)ld_x, res_q, x_q, res_e, x_e, rstd, scale,
+                    w, d_res, d_x, (int)ld_d_res, (int)ld_d_x, d_w, d_scale,
+                    sums ? (float*)((char*)ws + 256) : nullptr};
   return status_of(ssm::launch_add_norm_bwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
 }
 
@@ -183,8 +185,9 @@ int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y,
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
   cudaStream_t st = (cudaStream_t)stream;
-  ssm::GatedNormFwd a{(int)desc->rows, cols, group, (desc->flags & SSM_NORM_FIRST) ? 1 : 0, desc->eps,
-                      y, z, w, out, (int)ld_y, (int)ld_z, (int)ld_out, rstd, y_q, z_q, out_q, y_e, z_e, out_e};
+  const int norm_first = (desc->flags & SSM_NORM_FIRST) ? 1 : 0;
+  ssm::GatedNormFwd a{(int)desc->rows, cols, group, norm_first, desc->eps, y, z, w, out, (int)ld_y,
+                      (int)ld_z, (int)ld_out, rstd, y_q, z_q, out_q, y_e, z_e, out_e};
   // Blocks of 32 columns that straddle groups belong to no group's threads: such checkpoints are
   // saved by their own kernel, the inputs' before out is written.
   const bool straddle = group != cols && group % SSM_CKPT8_BLOCK != 0;

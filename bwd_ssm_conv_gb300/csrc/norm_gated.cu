@@ -80,8 +80,9 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
       z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
       if (a.y_q) {
         const uint32_t ytop = y.top(s, j, v[j]), ztop = z.top(s, j, zv);
-        store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + (int)((unsigned)col[j] / 32));
-        store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + (int)((unsigned)col[j] / 32));
+        const int blk = (int)((unsigned)col[j] / 32);
+        store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + blk);
+        store_ckpt8_top<VEC>(zv, ztop, ok, a.z_q + qrow + col[j], a.z_e + erow + blk);
       }
 #pragma unroll
       for (int i = 0; i < P::N; i++) {
@@ -116,7 +117,8 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
       if (ok) st_cols((IO*)a.out + (long long)row * a.ld_out + col[j], oc);
       if (a.out_q) {
         oc.get(o);
-        store_ckpt8<VEC>(o, ok, a.out_q + qrow + col[j], a.out_e + erow + (int)((unsigned)col[j] / 32));
+        store_ckpt8<VEC>(o, ok, a.out_q + qrow + col[j],
+                         a.out_e + erow + (int)((unsigned)col[j] / 32));
       }
     }
   }
