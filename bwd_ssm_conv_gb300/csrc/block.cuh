@@ -20,7 +20,6 @@ enum NormVariant { kVec1, kVec1Wide, kVec2, kVec2Wide, kVec3, kVec4, kVec4Wide, 
     case ssm::kVec2: LAUNCH(8, 2, 256, 2); break;      \
     case ssm::kVec4Wide: LAUNCH(8, 4, 1024, 1); break; \
     case ssm::kOne2: LAUNCH(1, 2, 128, 4); break;      \
-    case ssm::kOne4: LAUNCH(1, 4, 256, 3); break;      \
     case ssm::kOne8: LAUNCH(1, 8, 512, 1); break;      \
     case ssm::kOne8Wide: LAUNCH(1, 8, 1024, 1); break; \
     default: LAUNCH(1, 32, 1024, 1); break;
@@ -28,17 +27,20 @@ enum NormVariant { kVec1, kVec1Wide, kVec2, kVec2Wide, kVec3, kVec4, kVec4Wide, 
   switch (variant) {                                   \
     case ssm::kVec3: LAUNCH(8, 3, 256, 2); break;      \
     case ssm::kVec4: LAUNCH(8, 4, 256, 2); break;      \
+    case ssm::kOne4: LAUNCH(1, 4, 256, 4); break;      \
     SSM_NORM_CASES(LAUNCH)                             \
   }
 #define SSM_NORM_BWD_SWITCH(variant, LAUNCH)           \
   switch (variant) {                                   \
     case ssm::kVec2Wide: LAUNCH(8, 2, 512, 1); break;  \
+    case ssm::kOne4: LAUNCH(1, 4, 256, 3); break;      \
     SSM_NORM_CASES(LAUNCH)                             \
   }
 // Threads per SM of a launch's blocks, which all fit at once (registers: the instances above).
-inline int norm_threads_per_sm(NormVariant v) {
+inline int norm_threads_per_sm(NormVariant v, bool backward) {
   switch (v) {
-    case kVec1: case kOne4: return 768;
+    case kVec1: return 768;
+    case kOne4: return backward ? 768 : 1024;
     case kVec1Wide: case kVec4Wide: case kOne8Wide: case kOne32: return 1024;
     default: return 512;
   }

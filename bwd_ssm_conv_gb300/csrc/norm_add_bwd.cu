@@ -162,7 +162,7 @@ cudaError_t bwd_types(const AddNormBwd& a, bool vec, int sms, cudaStream_t st) {
   count_launches(1);
   cudaError_t e;
 #define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
-  e = bwd_launch<IO, RES, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant), st)
+  e = bwd_launch<IO, RES, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant, true), st)
   SSM_NORM_BWD_SWITCH(s.variant, SSM_LAUNCH)
 #undef SSM_LAUNCH
   if (e != cudaSuccess || (!a.d_w && !a.d_scale)) return e;

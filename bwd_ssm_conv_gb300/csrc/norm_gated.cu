@@ -281,7 +281,7 @@ cudaError_t fwd_types(const GatedNormFwd& a, bool vec, int sms, cudaStream_t st)
   const NormShape s = norm_shape(a.rows, a.group, a.cols / a.group, vec, sms, false);
   count_launches(1);
 #define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
-  return fwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant), st)
+  return fwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant, false), st)
   SSM_NORM_FWD_SWITCH(s.variant, SSM_LAUNCH)
 #undef SSM_LAUNCH
 }
@@ -291,7 +291,7 @@ cudaError_t bwd_types(const GatedNormBwd& a, bool vec, int sms, cudaStream_t st)
   count_launches(1);
   cudaError_t e;
 #define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
-  e = bwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant), st)
+  e = bwd_launch<IO, VEC, NJ, MAXT, MINB>(a, s.plan, norm_threads_per_sm(s.variant, true), st)
   SSM_NORM_BWD_SWITCH(s.variant, SSM_LAUNCH)
 #undef SSM_LAUNCH
   if (e != cudaSuccess || !a.d_w) return e;

@@ -82,7 +82,7 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
       s.variant = nj == 1 ? kVec1 : (nj == 2 ? kVec2 : (nj == 3 ? kVec3 : kVec4));
     }
     s.plan = row_plan(rows, group, groups, row_threads(nch, nj, 8), 128,
-                      norm_threads_per_sm(s.variant), sms);
+                      norm_threads_per_sm(s.variant, backward), sms);
   } else {
     nj = group <= 64 ? 2 : (group <= 1024 ? 4 : (group <= 8192 ? 8 : 32));
     s.variant = nj == 2   ? kOne2
@@ -90,7 +90,7 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
                 : nj == 8 ? (group <= 4096 ? kOne8 : kOne8Wide)
                           : kOne32;
     s.plan = row_plan(rows, group, groups, row_threads(group, nj, 1), 128,
-                      norm_threads_per_sm(s.variant), sms);
+                      norm_threads_per_sm(s.variant, backward), sms);
   }
   return s;
 }
