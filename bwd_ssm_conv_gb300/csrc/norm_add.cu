@@ -30,28 +30,58 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
     ld_param<VEC>(a.w, col[j], okc[j], w[j]);
     ld_param<VEC>(a.scale, col[j], okc[j], sc[j]);
   }
+  // Single columns are loaded one row ahead (20000 x 1001 fp32: 74 -> 57 us).
+  typedef Operand<IO, VEC, NJ, false> Act;
+  typedef Operand<RES, VEC, NJ, false> Res;
+  Act x1{a.x, nullptr, nullptr, a.ld_x, 0};
+  Res r1{a.residual, nullptr, nullptr, a.ld_residual, 0};
+  auto ahead = [&](int r) {
+    if constexpr (Act::kAhead) {
+      if (r < a.rows) {
+        x1.issue(0, r, col, okc, cols);
+        r1.issue(0, r, col, okc, cols);
+      } else {
+        x1.clear(0, okc, true);
+        r1.clear(0, okc, true);
+      }
+    }
+  };
+  const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
   int half = 0;
-  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += gridDim.x * pl.rpb, half ^= 1) {
+  ahead(blockIdx.x * pl.rpb + pos.slot);
+  for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, half ^= 1) {
     const int row = base + pos.slot;
     const bool rok = row < a.rows;
     float s[NJ][VEC];
     Cols<IO, VEC> xr[NJ];
     Cols<RES, VEC> rr[NJ];
+    if constexpr (Act::kAhead) {
+      x1.advance();
+      r1.advance();
+      ahead(row + step);
+    } else {
 #pragma unroll
-    for (int j = 0; j < NJ; j++) {
-      xr[j].zero();
-      rr[j].zero();
-      if (rok && okc[j]) {
-        xr[j].load((const IO*)a.x + (long long)row * a.ld_x + col[j]);
-        if (a.residual) rr[j].load((const RES*)a.residual + (long long)row * a.ld_residual + col[j]);
+      for (int j = 0; j < NJ; j++) {
+        xr[j].zero();
+        rr[j].zero();
+        if (rok && okc[j]) {
+          xr[j].load((const IO*)a.x + (long long)row * a.ld_x + col[j]);
+          if (a.residual)
+            rr[j].load((const RES*)a.residual + (long long)row * a.ld_residual + col[j]);
+        }
       }
     }
     float sq = 0.0f;
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       float xv[VEC], rv[VEC];
-      xr[j].get(xv);
-      rr[j].get(rv);
+      if constexpr (Act::kAhead) {
+        x1.get(0, j, true, row, col[j], cols, 7u, xv);
+        r1.get(0, j, true, row, col[j], cols, 7u, rv);
+      } else {
+        xr[j].get(xv);
+        rr[j].get(rv);
+      }
 #pragma unroll
       for (int i = 0; i < VEC; i++) {
         s[j][i] = __fadd_rn(rv[i], __fmul_rn(sc[j][i], xv[i]));
@@ -83,7 +113,8 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
       }
       if (a.x_q) {
         float xv[VEC];
-        xr[j].get(xv);
+        if constexpr (Act::kAhead) x1.get(0, j, true, row, col[j], cols, 7u, xv);
+        else xr[j].get(xv);
         store_ckpt8<VEC>(xv, ok, a.x_q + q, a.x_e + e);
       }
       if (a.out_q) {

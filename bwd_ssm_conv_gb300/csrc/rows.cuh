@@ -337,7 +337,8 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*part)[32], in
 // current one (cp.async, 8 columns at a time, RowPlan::slots rows in all).  It alone reads what it
 // copied, so no barrier is needed, and it may read a row twice, before and after the row's sum,
 // instead of holding it in registers.  Single columns (VEC = 1) are loaded one row ahead into
-// registers instead; rows too wide for the ring (VEC = 8 without RING) are read where they are used.
+// registers instead, up to 8 per thread; wider rows (and VEC = 8 without RING) are read where they
+// are used (2000 x 12345 bf16, 32 columns per thread held ahead: add_norm 489 us, not: 231).
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -378,8 +379,9 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   const uint8_t* e;
   int ld;
   uint32_t at;  // this thread's place in the first slot of the ring
+  static constexpr bool kAhead = VEC == 1 && NJ <= 8;
   // single columns of this row and the next, as loaded: nothing waits for the next row's
-  uint32_t cur[VEC == 1 ? NJ : 1], next[VEC == 1 ? NJ : 1];
+  uint32_t cur[kAhead ? NJ : 1], next[kAhead ? NJ : 1];
 
   __device__ __forceinline__ bool given() const { return t || q; }
   // Bytes that a block's threads need per slot of the ring.
@@ -388,14 +390,14 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   }
   // The row that was asked for last becomes the current one.
   __device__ __forceinline__ void advance() {
-    if constexpr (VEC == 1)
+    if constexpr (kAhead)
 #pragma unroll
       for (int j = 0; j < NJ; j++) cur[j] = next[j];
   }
   // Starts the copies of a row; col: the thread's chunks, `s` the byte offset of the ring slot.
   __device__ __forceinline__ void issue(uint32_t s, int row, const int (&col)[NJ],
                                         const bool (&okc)[NJ], int cols) {
-    if constexpr (VEC == 1) {
+    if constexpr (kAhead) {
       const int8_t* pq = q + (long long)row * cols;
       const IO* pt = (const IO*)t + (long long)row * ld;
 #pragma unroll
@@ -432,7 +434,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   // Zeros in the slot at s: for the chunks that the thread does not have, which are never copied to
   // (so once is enough), or for all of them, where there is no row to copy.
   __device__ __forceinline__ void clear(uint32_t s, const bool (&okc)[NJ], bool all) {
-    if constexpr (VEC == 1)
+    if constexpr (kAhead)
 #pragma unroll
       for (int j = 0; j < NJ; j++) next[j] = 0u;
     if constexpr (RING) {
@@ -461,9 +463,15 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   // A chunk's values (x is its scale byte); zeros for a chunk that the thread does not have.
   __device__ __forceinline__ void get(uint32_t s, int j, bool ok, int row, int col, int cols,
                                       uint32_t x, float (&v)[VEC]) const {
-    if constexpr (VEC == 1) {
+    if constexpr (kAhead) {
       v[0] = q ? (float)(int)cur[j] * block_step(x) :
              __uint_as_float(sizeof(IO) == 2 ? cur[j] << 16 : cur[j]);
+    } else if constexpr (VEC == 1) {
+      Cols<IO, 1> c;
+      c.zero();
+      if (ok && t) c.load((const IO*)t + (long long)row * ld + col);
+      c.get(v);
+      if (ok && q) v[0] = (float)q[(long long)row * cols + col] * block_step(x);
     } else if constexpr (!RING) {
       if (!ok || !given()) {
 #pragma unroll
