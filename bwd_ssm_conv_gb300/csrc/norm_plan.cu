@@ -67,8 +67,8 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
     } else {
       // Of 4, 3 and 2 chunks per thread (2 and 1 in the backward, which keeps more of each) the one
       // that leaves the fewest threads without a chunk: on 32768 rows of 1536 bf16 columns the
-      // forward takes 74 us with 3, 83 with 2 and 128 with 1, the backward 119, 108, 165.  Among
-      // equals the forward takes the one nearest to two warps per row (add_norm of bf16 rows and an
+      // forward takes 66 us with 3, 73 with 2 and 91 with 1, the backward 90 with 2 and 101 with 1.
+      // Among equals the forward takes the one nearest to two warps per row (add_norm of bf16 rows and an
       // fp32 stream, 2 and 4 chunks: 16384 x 512 17.9 and 20.3 us, 16384 x 1024 34.4 and 37.1; both
       // bf16, 8192 x 2048: 30.1 and 28.0), the backward the larger, whose fewer rows at a time leave
       // fewer column sums to add (8192 x 512 fp32, 2 and 1: 18.7 and 20.2 us with them).
