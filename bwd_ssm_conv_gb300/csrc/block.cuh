@@ -140,7 +140,7 @@ struct GatedNormFwd {
   void* out;
   int ld_y, ld_z, ld_out;
   float* rstd;
-  int8_t *y_q, *z_q, *out_q;
+  int8_t *y_q, *z_q, *out_q;  // y's and z's: both or neither
   uint8_t *y_e, *z_e, *out_e;
 };
 struct GatedNormBwd {

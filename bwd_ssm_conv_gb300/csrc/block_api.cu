@@ -188,17 +188,19 @@ int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y,
   const int norm_first = (desc->flags & SSM_NORM_FIRST) ? 1 : 0;
   ssm::GatedNormFwd a{(int)desc->rows, cols, group, norm_first, desc->eps, y, z, w, out, (int)ld_y,
                       (int)ld_z, (int)ld_out, rstd, y_q, z_q, out_q, y_e, z_e, out_e};
-  // Blocks of 32 columns that straddle groups belong to no group's threads: such checkpoints are
-  // saved by their own kernel, the inputs' before out is written.
+  // Blocks of 32 columns that straddle groups belong to no group's threads, and the norm's kernel
+  // keeps y and z together or not at all (a branch for each costs the pair 0.8 % of 32768 x 1536):
+  // such checkpoints are saved by their own kernel, the inputs' before out is written.
   const bool straddle = group != cols && group % SSM_CKPT8_BLOCK != 0;
-  if (straddle) {
-    a.y_q = a.z_q = a.out_q = nullptr;
+  if (straddle || !y_q != !z_q) {
+    a.y_q = a.z_q = nullptr;
     cudaError_t e = cudaSuccess;
     if (y_q) e = ssm::launch_ckpt8_save(y, ld_y, y_q, y_e, desc->rows, cols, io, sms, st);
     if (e == cudaSuccess && z_q)
       e = ssm::launch_ckpt8_save(z, ld_z, z_q, z_e, desc->rows, cols, io, sms, st);
     if (e != cudaSuccess) return SSM_ERR_CUDA;
   }
+  if (straddle) a.out_q = nullptr;
   cudaError_t e = ssm::launch_gated_norm_fwd(a, io, r.vec, sms, st);
   if (e == cudaSuccess && straddle && out_q)
     e = ssm::launch_ckpt8_save(out, ld_out, out_q, out_e, desc->rows, cols, io, sms, st);

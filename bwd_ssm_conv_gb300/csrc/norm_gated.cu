@@ -78,7 +78,7 @@ __global__ void __launch_bounds__(MAXT, MINB) gated_norm_fwd_kernel(const GatedN
       float zv[VEC];
       y.get(s, j, ok, row, col[j], a.cols, 7u, v[j]);
       z.get(s, j, ok, row, col[j], a.cols, 7u, zv);
-      if (a.y_q) {
+      if (a.y_q) {  // both checkpoints or neither (block_api.cu)
         const uint32_t ytop = y.top(s, j, v[j]), ztop = z.top(s, j, zv);
         const int blk = (int)((unsigned)col[j] / 32);
         store_ckpt8_top<VEC>(v[j], ytop, ok, a.y_q + qrow + col[j], a.y_e + erow + blk);

@@ -92,7 +92,8 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
                      size_t ws_bytes, void* stream);
 
 /* ---- gated RMSNorm (after the scan) --------------------------------------------------------
- * Forward.  Required: y, z, out.  Optional: w, rstd, checkpoints of y, z and out. */
+ * Forward.  Required: y, z, out.  Optional: w, rstd, checkpoints of y, z and out, each by itself (a
+ * pair of pointers, both or neither). */
 int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y, const void* z,
                        long long ld_z, const float* w, void* out, long long ld_out, float* rstd,
                        int8_t* y_q, uint8_t* y_e, int8_t* z_q, uint8_t* z_e, int8_t* out_q,

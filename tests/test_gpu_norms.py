@@ -159,6 +159,41 @@ def test_gated_norm(rows, cols, group, io, norm_first):
         assert bool(torch.isnan(wide[:, :cols]).all())
 
 
+def _gated_fwd_c(y, z, group, keep):
+    """ssm_gated_norm_fwd through the C ABI with the checkpoints named in ``keep`` only; buffers for
+    all three, filled with 99."""
+    rows, cols = y.shape
+    out = _nan((rows, cols), y.dtype)
+    kept = {n: (torch.full((rows, cols), 99, dtype=torch.int8, device="cuda"),
+                torch.full((rows, -(-cols // 32)), 99, dtype=torch.uint8, device="cuda"))
+            for n in ("y", "z", "out")}
+    pairs = [p.data_ptr() if n in keep else None for n in kept for p in kept[n]]
+    d = block.NormDesc(rows, cols, group, block._IO[y.dtype], 0, 0, EPS)
+    rc = block.lib().ssm_gated_norm_fwd(d, y.data_ptr(), 0, z.data_ptr(), 0, None, out.data_ptr(), 0,
+                                        None, *pairs, torch.cuda.current_stream().cuda_stream)
+    assert rc == 0
+    return out, kept
+
+
+@pytest.mark.parametrize("keep", [(), ("y",), ("z",), ("out",), ("y", "z"), ("z", "out")])
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+# eight columns at a time, blocks of 32 that straddle groups, single columns, rows without groups
+@pytest.mark.parametrize("rows,cols,group", [(9, 192, 64), (9, 144, 48), (5, 99, 33), (7, 264, 0),
+                                             (3, 1003, 0), (2, 8200, 0)])
+def test_gated_norm_keeps_each_checkpoint_by_itself(rows, cols, group, io, keep):
+    g = torch.Generator().manual_seed(31)
+    y, z = (_rand(g, rows, cols, dtype=DT[io]) for _ in range(2))
+    out, kept = _gated_fwd_c(y.cuda(), z.cuda(), group, keep)
+    close("out", out, ref.gated_norm(y, z, None, group, EPS, False)[0])
+    for name, of in (("y", y), ("z", z), ("out", out.cpu())):
+        q, e = (t.cpu() for t in kept[name])
+        if name in keep:
+            want_q, want_e = ref.quantise(of)
+            assert torch.equal(q, want_q) and torch.equal(e, want_e), name
+        else:
+            assert bool((q == 99).all()) and bool((e == 99).all()), name
+
+
 def test_zero_rows_and_bad_values_stay_in_their_rows():
     """An all-zero row gives zeros (eps keeps it finite); a row with an infinity or a NaN spoils
     its own outputs and its 8-bit block only."""
