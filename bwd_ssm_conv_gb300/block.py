@@ -5,6 +5,9 @@ As in ``binding``: argument marshalling only, every step of the computation runs
 library's CUDA kernels on PyTorch's current stream (or ``stream``), and a missing library raises.
 The marshalling itself is compiled (``csrc/block_binding.cpp``), since a token's call costs more on
 the host than on the GPU; ``lib()`` gives the C entry points themselves.
+A call on another ``stream`` behaves as under ``torch.cuda.stream(stream)``: its results and workspace
+come from that stream's memory.  The caller orders it after what makes its inputs, keeps them until it is
+done, and orders the use of its results after it.
 Activations are CUDA tensors [..., cols], float32 or bfloat16, whose last dimension is dense and
 whose rows lie at one stride (a slice of a wider tensor is fine); parameters are contiguous fp32.
 """

@@ -11,6 +11,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/cuda/EmptyTensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -196,26 +197,29 @@ int64_t int_attr(PyObject* o, const char* name) {
   if (r == -1 && PyErr_Occurred()) throw python_error();
   return r;
 }
-// The call's stream: the current one of t's device, or a torch.cuda.Stream.  Tensors made here for a
-// stream other than the current one are marked as used there, so that their memory is not given out
-// again before that stream is done.
+// The call's stream: the current one of t's device, or a torch.cuda.Stream, which is then current
+// while this object lives.  What the call allocates therefore comes from the memory of the stream that it
+// runs on: a block that was freed with work pending on the current stream is never handed to
+// another one.  Made before anything is allocated.
 struct On {
+  const c10::cuda::CUDAStream now;
+  c10::cuda::OptionalCUDAStreamGuard guard;
   void* raw;
-  std::optional<c10::Stream> other;
-  On(PyObject* stream, const Tensor& t) {
-    const c10::cuda::CUDAStream now = c10::cuda::getCurrentCUDAStream(t.device().index());
-    raw = now.stream();
+  On(PyObject* stream, const Tensor& t)
+      : now(c10::cuda::getCurrentCUDAStream(t.device().index())), raw(now.stream()) {
     if (stream == Py_None) return;
     raw = (void*)(uintptr_t)int_attr(stream, "cuda_stream");
     const c10::Stream s = c10::Stream::unpack3(
         int_attr(stream, "stream_id"), (c10::DeviceIndex)int_attr(stream, "device_index"),
         (c10::DeviceType)int_attr(stream, "device_type"));
-    if (s != now.unwrap()) other = s;
+    if (s != now.unwrap()) guard.reset_stream(s);
   }
+  // Results made for another stream are marked as used on the caller's current one too, so that
+  // freeing them with work pending there does not give their memory to the other stream's next call.
   void made(std::initializer_list<const Tensor*> ts) const {
-    if (!other) return;
+    if (!guard.current_stream()) return;
     for (const Tensor* t : ts)
-      if (t->defined()) t->record_stream(*other);
+      if (t->defined()) t->record_stream(now.unwrap());
   }
 };
 
@@ -300,6 +304,7 @@ SSM_FUNCTION(add_norm_fwd) {
   }
   const Rows rx(&x, "x"), rr(residual, "residual", shape, rdt);
   const float *ps = f32(scale, "scale", cols), *pw = f32(w, "w", cols);
+  const On on(a[12], x);
   Tensor o, res;
   Rows ro, rs;
   const bool given = a[11] != Py_None;
@@ -323,7 +328,6 @@ SSM_FUNCTION(add_norm_fwd) {
   const NewCkpt8 res8(yes(a[6]), x), x8(yes(a[7]), x), out8(yes(a[8]), x);
   const ssm_norm_desc d =
       norm_desc(rows_in(x, cols), cols, 0, io, io_code(rdt), 0, number(a[4]));
-  const On on(a[12], x);
   on.made({&rstd, &res8.q, &res8.e, &x8.q, &x8.e, &out8.q, &out8.e});
   if (!given) on.made({&o, &res});
   const int rc = call([&] {
@@ -365,6 +369,7 @@ SSM_FUNCTION(add_norm_bwd) {
   const Kept kx = kept(x8, "x", shape);
   const float *pr = f32(rstd, "rstd", rows), *ps = f32(scale, "scale", cols),
               *pw = f32(w, "w", cols);
+  const On on(a[12], d_out);
   Tensor g[4];  // d_res, d_x, d_w, d_scale
   Rows go, gx;
   const bool given = a[11] != Py_None;
@@ -385,8 +390,6 @@ SSM_FUNCTION(add_norm_bwd) {
   const ssm_norm_desc d = norm_desc(rows, cols, 0, io, io_code(rdt), 0, 1.0);
   const int sums = g[2].defined() + g[3].defined();
   const Workspace ws(sums ? ssm_norm_bwd_workspace_size(&d, sums) : 0, tensor(a[10], "ws"), d_out);
-  const On on(a[12], d_out);
-  on.made({&ws.mine});
   if (!given) on.made({&g[0], &g[1], &g[2], &g[3]});
   const int rc = call([&] {
     return ssm_add_norm_bwd(&d, rd.p, rd.ld, ru.p, ru.ld, rr.p, rr.ld, kr.q, kr.e, rx.p, rx.ld,
@@ -410,6 +413,7 @@ SSM_FUNCTION(gated_norm_fwd) {
   const int64_t cols = columns(y, "y"), group = integer(a[3]);
   const Rows ry(&y, "y"), rz(&z, "z", shape, dt);
   const float* pw = f32(w, "w", cols);
+  const On on(a[10], y);
   Tensor o, rstd;
   Rows ro(out, "out", shape, dt);
   if (out) o = *out;
@@ -423,7 +427,6 @@ SSM_FUNCTION(gated_norm_fwd) {
   const NewCkpt8 y8(save8, y), z8(save8, y), out8(yes(a[7]), y);
   const ssm_norm_desc d = norm_desc(rows_in(y, cols), cols, group, io, io,
                                     (unsigned)integer(a[5]), number(a[4]));
-  const On on(a[10], y);
   on.made({&rstd, &y8.q, &y8.e, &z8.q, &z8.e, &out8.q, &out8.e});
   if (!out) on.made({&o});
   const int rc = call([&] {
@@ -453,6 +456,7 @@ SSM_FUNCTION(gated_norm_bwd) {
   const Kept kz = kept(z8, "z", shape);
   const float *pr = f32(rstd, "rstd", rows * (group > 0 ? cols / group : 1)),
               *pw = f32(w, "w", cols);
+  const On on(a[9], d_out);
   Tensor g[3];  // d_y, d_z, d_w
   Rows gy, gz;
   const bool given = a[8] != Py_None;
@@ -471,8 +475,6 @@ SSM_FUNCTION(gated_norm_bwd) {
   const ssm_norm_desc d = norm_desc(rows, cols, group, io, io, (unsigned)integer(a[6]), 1.0);
   const Workspace ws(g[2].defined() ? ssm_norm_bwd_workspace_size(&d, 1) : 0, tensor(a[7], "ws"),
                      d_out);
-  const On on(a[9], d_out);
-  on.made({&ws.mine});
   if (!given) on.made({&g[0], &g[1], &g[2]});
   const int rc = call([&] {
     return ssm_gated_norm_bwd(&d, rd.p, rd.ld, ry.p, ry.ld, ky.q, ky.e, rz.p, rz.ld, kz.q, kz.e,
@@ -492,6 +494,7 @@ SSM_FUNCTION(ckpt8_save) {
   const int io = io_of(x, "x");
   const int64_t cols = columns(x, "x");
   const Rows rx(&x, "x");
+  const On on(a[2], x);
   NewCkpt8 made;
   Kept k;
   if (a[1] != Py_None) {
@@ -502,7 +505,6 @@ SSM_FUNCTION(ckpt8_save) {
     made = NewCkpt8(true, x);
     k = {made.pq(), made.pe()};
   }
-  const On on(a[2], x);
   on.made({&made.q, &made.e});
   const int rc = call([&] {
     return ssm_ckpt8_save(rx.p, rx.ld, k.q, k.e, rows_in(x, cols),
@@ -527,6 +529,7 @@ SSM_FUNCTION(ckpt8_load) {
   const IntArrayRef shape = c.q->sizes();
   const int64_t cols = columns(*c.q, "c");
   const Kept k = kept(c, "c", shape);
+  const On on(a[3], *c.q);
   Tensor o;
   if (out) {
     o = *out;
@@ -536,7 +539,6 @@ SSM_FUNCTION(ckpt8_load) {
   }
   const int io = io_of(o, "out");
   const Rows ro(&o, "out", shape, o.scalar_type());
-  const On on(a[3], *c.q);
   if (!out) on.made({&o});
   const int rc = call([&] {
     return ssm_ckpt8_load(k.q, k.e, ro.p, ro.ld, rows_in(*c.q, cols),
@@ -566,14 +568,13 @@ SSM_FUNCTION(ckpt8_wgrad) {
   at::DimVector shape(g.sizes().begin(), g.sizes().end());
   shape.back() = k;
   const Kept x = kept(x8, "x8", shape);
+  const On on(a[5], g);
   const Tensor o = out ? *out : make(want, at::kFloat, g);
   float* po = f32(&o, "out", m * k);
   TORCH_CHECK_VALUE(m <= 0x7fffffff && k <= 0x7fffffff, "g and x8 are too wide");
   const int aligned = !((((uintptr_t)rg.p | (uintptr_t)x.q) & 15) || ((rg.ld ? rg.ld : m) & 7));
   const Workspace ws(ssm_ckpt8_wgrad_workspace_size(tokens, (int)m, (int)k, io, aligned),
                      tensor(a[3], "ws"), g);
-  const On on(a[5], g);
-  on.made({&ws.mine});
   if (!out) on.made({&o});
   const int rc = call([&] {
     return ssm_ckpt8_wgrad(rg.p, rg.ld, x.q, x.e, po, tokens, (int)m, (int)k, io,
