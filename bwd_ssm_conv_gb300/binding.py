@@ -3,11 +3,16 @@
 Argument marshalling only: every step of the computation runs in the library's CUDA
 kernels.  Tensors must be CUDA tensors, contiguous, of the dtypes the header states
 (activations in the I/O dtype, parameters and states fp32).  Work is enqueued on PyTorch's
-current stream.  If the library is missing or cannot be loaded, every call raises.
+current stream, or on ``stream`` as under ``torch.cuda.stream(stream)``: results and workspace then
+come from that stream's memory, and the caller orders it after what makes the inputs, keeps them until
+it is done, and orders the use of the results after it.  If the library is missing or cannot be
+loaded, every call raises.
 """
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 from dataclasses import dataclass
 
@@ -111,6 +116,36 @@ def _stream(stream=None):
     return s.cuda_stream
 
 
+def _cuda_tensors(r):
+    if torch.is_tensor(r):
+        return [r]
+    if isinstance(r, dict):
+        r = tuple(r.values())
+    return [t for v in r for t in _cuda_tensors(v)] if isinstance(r, tuple) else []
+
+
+def _on_its_stream(fn):
+    """A call with ``stream`` runs with that stream current, so that what it allocates is ordered with
+    its work: a block that was freed with work pending on the caller's current stream goes to no other
+    stream.  Its results are marked as used on the current stream too, so that freeing them with work
+    pending there does not give their memory to the other stream's next call."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        now = torch.cuda.current_stream()
+        with torch.cuda.stream(stream):
+            r = fn(*args, **kw)
+        if stream != now:
+            for t in _cuda_tensors(r):
+                t.record_stream(now)
+        return r
+    return call
+
+
 def _workspace(nbytes, device, ws=None):
     if ws is not None:
         if ws.numel() * ws.element_size() < nbytes:
@@ -121,6 +156,7 @@ def _workspace(nbytes, device, ws=None):
 
 # ---- conv ---------------------------------------------------------------------------------
 
+@_on_its_stream
 def ssm_conv_fwd(sx, c, bias=None, silu=True, want_state=False, out=None, stream=None):
     """out[n_s][n_t][d] = act(sum_k sx[b][d][t+k] c[d][k] + bias[d]); sx is [n_s][d][K-1+n_t]."""
     n_s, d, w = sx.shape
@@ -142,6 +178,7 @@ def ssm_conv_workspace_size(n_s, d_inner, n_t, d_conv) -> int:
     return int(lib().ssm_conv_workspace_size(n_s, d_inner, n_t, d_conv))
 
 
+@_on_its_stream
 def ssm_conv_bwd(sx, c, dout, bias=None, silu=True, want_bias_grad=None, ws=None, out=None,
                  stream=None):
     """Returns (d_sx, d_c, d_bias); d_bias is None unless bias is given or want_bias_grad."""
@@ -209,6 +246,7 @@ def ssm_scan_workspace_size(shape: ScanShape, backward: bool) -> int:
     return int(lib().ssm_scan_workspace_size(ctypes.byref(d), 1 if backward else 0))
 
 
+@_on_its_stream
 def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, s0=None, ids=None, chunk=256,
                  softplus=False, check_finite=False, want_ckpt=True, state_rows=0, ws=None,
                  out=None, stream=None, a_log=False, chunked=False):
@@ -239,6 +277,7 @@ def ssm_scan_fwd(x, dt, A, B, C, D=None, z=None, dt_bias=None, s0=None, ids=None
     return y, st, ck
 
 
+@_on_its_stream
 def ssm_decode_step(x_new, conv_state, c, dt, A, B, C, state, bias=None, D=None, z=None,
                     dt_bias=None, ids=None, silu=True, softplus=False, check_finite=False,
                     ws=None, out=None, stream=None, a_log=False):
@@ -273,6 +312,7 @@ def ssm_decode_step(x_new, conv_state, c, dt, A, B, C, state, bias=None, D=None,
 GRAD_NAMES = ("d_s0", "d_x", "d_dt", "d_A", "d_B", "d_C", "d_D", "d_z", "d_dt_bias")
 
 
+@_on_its_stream
 def ssm_scan_bwd(x, dt, A, B, C, dy, D=None, z=None, dt_bias=None, s0=None, ids=None, ckpt=None,
                  d_state_out=None, chunk=256, softplus=False, check_finite=False, state_rows=0,
                  want_ds0=True, ws=None, out=None, stream=None, a_log=False, debug_flags=0):
@@ -331,6 +371,7 @@ def ssm_conv_scan_workspace_size(shape: ScanShape, d_conv: int, backward: bool) 
     return int(lib().ssm_conv_scan_workspace_size(ctypes.byref(d), d_conv, 1 if backward else 0))
 
 
+@_on_its_stream
 def ssm_conv_scan_fwd(sx, c, dt, A, B, C, bias=None, silu=True, D=None, z=None, dt_bias=None,
                       s0=None, ids=None, chunk=256, softplus=False, check_finite=False,
                       want_ckpt=True, state_rows=0, ws=None, out=None, stream=None, a_log=False):
@@ -364,6 +405,7 @@ CONV_SCAN_GRAD_NAMES = ("d_s0", "d_sx", "d_c", "d_bias", "d_dt", "d_A", "d_B", "
                         "d_z", "d_dt_bias")
 
 
+@_on_its_stream
 def ssm_conv_scan_bwd(sx, c, dt, A, B, C, dy, bias=None, silu=True, D=None, z=None,
                       dt_bias=None, s0=None, ids=None, ckpt=None, d_state_out=None, chunk=256,
                       softplus=False, check_finite=False, state_rows=0, want_ds0=True,

@@ -9,7 +9,7 @@ import gc
 import pytest
 import torch
 
-from bwd_ssm_conv_gb300 import block
+from bwd_ssm_conv_gb300 import binding, block
 
 pytestmark = pytest.mark.gpu
 ROWS, COLS = 1024, 2048  # results of 1 MiB and more: blocks of their own size in the allocator
@@ -48,14 +48,54 @@ def _block_calls():
     }
 
 
+def _scan_calls():
+    n, L, d, N, K = 2, 512, 512, 16, 4
+    sx = _rand(10, n, d, K - 1 + L)
+    c, bias = _rand(11, d, K), _rand(12, d)
+    x, z, dy = (_rand(13 + i, n, L, d, 1) for i in range(3))
+    dt = 0.1 * _rand(16, n, L, d).abs()
+    A, D = -_rand(17, d, N).abs() - 0.1, _rand(18, d)
+    B, C = (_rand(19 + i, n, L, 1, N) for i in range(2))
+    how = dict(D=D, z=z, chunk=64)
+    ckpt = binding.ssm_scan_fwd(x, dt, A, B, C, **how)[2]
+    fused = binding.ssm_conv_scan_fwd(sx, c, dt, A, B, C, bias=bias, **how)[2]
+    dout = dy.view(n, L, d)
+    tok = dict(x_new=_rand(21, 512, d, 1), c=c, dt=0.1 * _rand(22, 512, d).abs(), A=A,
+               B=_rand(23, 512, 1, N), C=_rand(24, 512, 1, N), D=D)
+
+    # decode's states are updated in place: fresh ones for every call of the tests, made beforehand
+    states = iter([(torch.zeros(512, d, K - 1, device="cuda"), torch.zeros(512, d, 1, N, device="cuda"))
+                   for _ in range(7)])
+
+    def decode(**k):
+        conv, state = next(states)
+        return binding.ssm_decode_step(conv_state=conv, state=state, **tok, **k)
+
+    def plain(f):  # without the workspace, which holds nothing defined
+        return lambda **k: {n: t for n, t in f(**k).items() if n != "_ws" and t is not None}
+
+    return {
+        "conv_fwd": lambda **k: binding.ssm_conv_fwd(sx, c, bias, want_state=True, **k),
+        "conv_bwd": lambda **k: binding.ssm_conv_bwd(sx, c, dout, bias, **k),
+        "scan_fwd": lambda **k: binding.ssm_scan_fwd(x, dt, A, B, C, **how, **k),
+        "scan_bwd": plain(lambda **k: binding.ssm_scan_bwd(x, dt, A, B, C, dy, ckpt=ckpt, **how, **k)),
+        "conv_scan_fwd": lambda **k: binding.ssm_conv_scan_fwd(sx, c, dt, A, B, C, bias=bias, **how,
+                                                               **k),
+        "conv_scan_bwd": plain(lambda **k: binding.ssm_conv_scan_bwd(
+            sx, c, dt, A, B, C, dy, bias=bias, ckpt=fused, **how, **k)),
+        "decode_step": decode,
+    }
+
+
 BLOCK = ("add_norm_fwd", "add_norm_bwd", "gated_norm_fwd", "gated_norm_bwd", "ckpt8_save",
          "ckpt8_load", "ckpt8_wgrad")
-CALLS = [("block", n) for n in BLOCK]
+SCAN = ("conv_fwd", "conv_bwd", "scan_fwd", "scan_bwd", "conv_scan_fwd", "conv_scan_bwd", "decode_step")
+CALLS = [("block", n) for n in BLOCK] + [("scan", n) for n in SCAN]
 
 
 @pytest.fixture(scope="module")
 def calls():
-    c = {"block": _block_calls()}
+    c = {"block": _block_calls(), "scan": _scan_calls()}
     torch.cuda.synchronize()
     return c
 
