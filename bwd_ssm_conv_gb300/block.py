@@ -8,6 +8,8 @@ the host than on the GPU; ``lib()`` gives the C entry points themselves.
 A call on another ``stream`` behaves as under ``torch.cuda.stream(stream)``: its results and workspace
 come from that stream's memory.  The caller orders it after what makes its inputs, keeps them until it is
 done, and orders the use of its results after it.
+Every tensor, and the stream, of a call belongs to the GPU of its first tensor, which need not be the
+current one.
 Activations are CUDA tensors [..., cols], float32 or bfloat16, whose last dimension is dense and
 whose rows lie at one stride (a slice of a wider tensor is fine); parameters are contiguous fp32.
 """

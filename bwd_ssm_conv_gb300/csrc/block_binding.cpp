@@ -51,6 +51,19 @@ int io_of(const Tensor& t, const char* name) {
   TORCH_CHECK_TYPE(io >= 0, name, " must be float32 or bfloat16, got ", t.scalar_type());
   return io;
 }
+// Every tensor of a call lies on the GPU of its first.
+struct Named {
+  const Tensor* t;  // nullptr: not given
+  const char* name;
+};
+Named some(const Tensor& t, const char* name) { return {t.defined() ? &t : nullptr, name}; }
+void together(Named first, std::initializer_list<Named> others) {
+  TORCH_CHECK_VALUE(first.t->is_cuda(), first.name, " must be a CUDA tensor");
+  const at::Device home = first.t->device();
+  for (const Named& o : others)
+    TORCH_CHECK_VALUE(!o.t || o.t->device() == home, o.name, " must be a CUDA tensor on ", home,
+                      ", as ", first.name, " is; got ", o.t->device());
+}
 int64_t columns(const Tensor& t, const char* name) {
   TORCH_CHECK_VALUE(t.dim() >= 1, name, " must have at least one dimension");
   return t.size(-1);
@@ -197,22 +210,33 @@ int64_t int_attr(PyObject* o, const char* name) {
   if (r == -1 && PyErr_Occurred()) throw python_error();
   return r;
 }
-// The call's stream: the current one of t's device, or a torch.cuda.Stream, which is then current
-// while this object lives.  What the call allocates therefore comes from the memory of the stream that it
-// runs on: a block that was freed with work pending on the current stream is never handed to
-// another one.  Made before anything is allocated.
+// The call's device, that of its first tensor t, and its stream: the current one there, or a
+// torch.cuda.Stream of it.  Both are current while this object lives.  What the call allocates
+// therefore comes from the memory of the stream that it runs on: a block that was freed with work
+// pending on the caller's stream is never handed to another one.  Made before anything is allocated.
 struct On {
+  std::optional<c10::Stream> given;
+  c10::cuda::CUDAGuard device;
   const c10::cuda::CUDAStream now;
   c10::cuda::OptionalCUDAStreamGuard guard;
   void* raw;
   On(PyObject* stream, const Tensor& t)
-      : now(c10::cuda::getCurrentCUDAStream(t.device().index())), raw(now.stream()) {
-    if (stream == Py_None) return;
+      : given(stream_of(stream, t.device())),
+        device(t.device()),
+        now(c10::cuda::getCurrentCUDAStream(t.device().index())),
+        raw(now.stream()) {
+    if (!given) return;
     raw = (void*)(uintptr_t)int_attr(stream, "cuda_stream");
+    if (*given != now.unwrap()) guard.reset_stream(*given);
+  }
+  static std::optional<c10::Stream> stream_of(PyObject* stream, at::Device home) {
+    if (stream == Py_None) return std::nullopt;
     const c10::Stream s = c10::Stream::unpack3(
         int_attr(stream, "stream_id"), (c10::DeviceIndex)int_attr(stream, "device_index"),
         (c10::DeviceType)int_attr(stream, "device_type"));
-    if (s != now.unwrap()) guard.reset_stream(s);
+    TORCH_CHECK_VALUE(s.device() == home, "stream must be one of ", home,
+                      ", where the tensors are; got one of ", s.device());
+    return s;
   }
   // Results made for another stream are marked as used on the caller's current one too, so that
   // freeing them with work pending there does not give their memory to the other stream's next call.
@@ -302,16 +326,20 @@ SSM_FUNCTION(add_norm_fwd) {
     TORCH_CHECK_TYPE(THPDtype_Check(a[5]), "res_dtype must be a torch.dtype");
     rdt = reinterpret_cast<THPDtype*>(a[5])->scalar_type;
   }
+  const bool given = a[11] != Py_None;
+  const Tensor *go = nullptr, *gr = nullptr;
+  if (given) {
+    outs_are(a[11], 2, "(out, res_out)");
+    go = tensor(PyTuple_GET_ITEM(a[11], 0), "out"), gr = tensor(PyTuple_GET_ITEM(a[11], 1), "res_out");
+  }
+  together({&x, "x"}, {{w, "w"}, {residual, "residual"}, {scale, "scale"}, {go, "out"},
+                       {gr, "res_out"}});
   const Rows rx(&x, "x"), rr(residual, "residual", shape, rdt);
   const float *ps = f32(scale, "scale", cols), *pw = f32(w, "w", cols);
   const On on(a[12], x);
   Tensor o, res;
   Rows ro, rs;
-  const bool given = a[11] != Py_None;
   if (given) {
-    outs_are(a[11], 2, "(out, res_out)");
-    const Tensor *go = tensor(PyTuple_GET_ITEM(a[11], 0), "out"),
-                 *gr = tensor(PyTuple_GET_ITEM(a[11], 1), "res_out");
     ro = Rows(go, "out", shape, x.scalar_type()), rs = Rows(gr, "res_out", shape, rdt);
     if (go) o = *go;
     if (gr) res = *gr;
@@ -363,6 +391,18 @@ SSM_FUNCTION(add_norm_bwd) {
     TORCH_CHECK_TYPE(THPDtype_Check(a[7]), "res_dtype must be a torch.dtype");
     rdt = reinterpret_cast<THPDtype*>(a[7])->scalar_type;
   }
+  Tensor g[4];  // d_res, d_x, d_w, d_scale
+  const bool given = a[11] != Py_None;
+  if (given) {
+    outs_are(a[11], 4, "d_res, d_x, d_w and d_scale");
+    for (int i = 0; i < 4; i++)
+      if (const Tensor* t = tensor(PyTuple_GET_ITEM(a[11], i), "out")) g[i] = *t;
+  }
+  const Tensor* given_ws = tensor(a[10], "ws");
+  together({&d_out, "d_out"},
+           {{res, "res"}, {res8.q, "res"}, {res8.e, "res"}, {rstd, "rstd"}, {w, "w"},
+            {up, "d_res_out"}, {scale, "scale"}, {x, "x"}, {x8.q, "x"}, {x8.e, "x"}, some(g[0], "d_res"),
+            some(g[1], "d_x"), some(g[2], "d_w"), some(g[3], "d_scale"), {given_ws, "ws"}});
   const Rows rd(&d_out, "d_out"), ru(up, "d_res_out", shape, rdt), rr(res, "res", shape, rdt);
   const Kept kr = kept(res8, "res", shape);
   const Rows rx(x, "x", shape, dt);
@@ -370,13 +410,8 @@ SSM_FUNCTION(add_norm_bwd) {
   const float *pr = f32(rstd, "rstd", rows), *ps = f32(scale, "scale", cols),
               *pw = f32(w, "w", cols);
   const On on(a[12], d_out);
-  Tensor g[4];  // d_res, d_x, d_w, d_scale
   Rows go, gx;
-  const bool given = a[11] != Py_None;
   if (given) {
-    outs_are(a[11], 4, "d_res, d_x, d_w and d_scale");
-    for (int i = 0; i < 4; i++)
-      if (const Tensor* t = tensor(PyTuple_GET_ITEM(a[11], i), "out")) g[i] = *t;
     if (g[0].defined()) go = Rows(&g[0], "d_res", shape, rdt);
     if (g[1].defined()) gx = Rows(&g[1], "d_x", shape, dt);
     if (g[2].defined()) f32(&g[2], "d_w", cols);
@@ -389,7 +424,7 @@ SSM_FUNCTION(add_norm_bwd) {
   }
   const ssm_norm_desc d = norm_desc(rows, cols, 0, io, io_code(rdt), 0, 1.0);
   const int sums = g[2].defined() + g[3].defined();
-  const Workspace ws(sums ? ssm_norm_bwd_workspace_size(&d, sums) : 0, tensor(a[10], "ws"), d_out);
+  const Workspace ws(sums ? ssm_norm_bwd_workspace_size(&d, sums) : 0, given_ws, d_out);
   if (!given) on.made({&g[0], &g[1], &g[2], &g[3]});
   const int rc = call([&] {
     return ssm_add_norm_bwd(&d, rd.p, rd.ld, ru.p, ru.ld, rr.p, rr.ld, kr.q, kr.e, rx.p, rx.ld,
@@ -411,6 +446,7 @@ SSM_FUNCTION(gated_norm_fwd) {
   const IntArrayRef shape = y.sizes();
   const ScalarType dt = y.scalar_type();
   const int64_t cols = columns(y, "y"), group = integer(a[3]);
+  together({&y, "y"}, {{&z, "z"}, {w, "w"}, {out, "out"}});
   const Rows ry(&y, "y"), rz(&z, "z", shape, dt);
   const float* pw = f32(w, "w", cols);
   const On on(a[10], y);
@@ -450,6 +486,17 @@ SSM_FUNCTION(gated_norm_bwd) {
   const IntArrayRef shape = d_out.sizes();
   const ScalarType dt = d_out.scalar_type();
   const int64_t cols = columns(d_out, "d_out"), rows = rows_in(d_out, cols), group = integer(a[5]);
+  Tensor g[3];  // d_y, d_z, d_w
+  const bool given = a[8] != Py_None;
+  if (given) {
+    outs_are(a[8], 3, "d_y, d_z and d_w");
+    for (int i = 0; i < 3; i++)
+      if (const Tensor* t = tensor(PyTuple_GET_ITEM(a[8], i), "out")) g[i] = *t;
+  }
+  const Tensor* given_ws = tensor(a[7], "ws");
+  together({&d_out, "d_out"},
+           {{y, "y"}, {y8.q, "y"}, {y8.e, "y"}, {z, "z"}, {z8.q, "z"}, {z8.e, "z"}, {rstd, "rstd"},
+            {w, "w"}, some(g[0], "d_y"), some(g[1], "d_z"), some(g[2], "d_w"), {given_ws, "ws"}});
   const Rows rd(&d_out, "d_out"), ry(y, "y", shape, dt);
   const Kept ky = kept(y8, "y", shape);
   const Rows rz(z, "z", shape, dt);
@@ -457,13 +504,8 @@ SSM_FUNCTION(gated_norm_bwd) {
   const float *pr = f32(rstd, "rstd", rows * (group > 0 ? cols / group : 1)),
               *pw = f32(w, "w", cols);
   const On on(a[9], d_out);
-  Tensor g[3];  // d_y, d_z, d_w
   Rows gy, gz;
-  const bool given = a[8] != Py_None;
   if (given) {
-    outs_are(a[8], 3, "d_y, d_z and d_w");
-    for (int i = 0; i < 3; i++)
-      if (const Tensor* t = tensor(PyTuple_GET_ITEM(a[8], i), "out")) g[i] = *t;
     if (g[0].defined()) gy = Rows(&g[0], "d_y", shape, dt);
     if (g[1].defined()) gz = Rows(&g[1], "d_z", shape, dt);
     if (g[2].defined()) f32(&g[2], "d_w", cols);
@@ -473,8 +515,7 @@ SSM_FUNCTION(gated_norm_bwd) {
     if (w) g[2] = make(w->sizes(), at::kFloat, d_out);
   }
   const ssm_norm_desc d = norm_desc(rows, cols, group, io, io, (unsigned)integer(a[6]), 1.0);
-  const Workspace ws(g[2].defined() ? ssm_norm_bwd_workspace_size(&d, 1) : 0, tensor(a[7], "ws"),
-                     d_out);
+  const Workspace ws(g[2].defined() ? ssm_norm_bwd_workspace_size(&d, 1) : 0, given_ws, d_out);
   if (!given) on.made({&g[0], &g[1], &g[2]});
   const int rc = call([&] {
     return ssm_gated_norm_bwd(&d, rd.p, rd.ld, ry.p, ry.ld, ky.q, ky.e, rz.p, rz.ld, kz.q, kz.e,
@@ -493,13 +534,14 @@ SSM_FUNCTION(ckpt8_save) {
   const Tensor& x = needed(a[0], "x");
   const int io = io_of(x, "x");
   const int64_t cols = columns(x, "x");
+  const Pair given(a[1], "out");
+  TORCH_CHECK_TYPE(given.q || a[1] == Py_None, "out must be a pair of tensors (q, e)");
+  together({&x, "x"}, {{given.q, "out"}, {given.e, "out"}});
   const Rows rx(&x, "x");
   const On on(a[2], x);
   NewCkpt8 made;
   Kept k;
-  if (a[1] != Py_None) {
-    const Pair given(a[1], "out");
-    TORCH_CHECK_TYPE(given.q, "out must be a pair of tensors (q, e)");
+  if (given.q) {
     k = kept(given, "out", x.sizes());
   } else {
     made = NewCkpt8(true, x);
@@ -511,7 +553,7 @@ SSM_FUNCTION(ckpt8_save) {
                           cols > 0x7fffffff ? 0x7fffffff : (int)cols, io, on.raw);
   });
   if (rc) return PyLong_FromLong(rc);
-  if (a[1] != Py_None) {
+  if (given.q) {
     Py_INCREF(a[1]);
     return a[1];
   }
@@ -526,6 +568,7 @@ SSM_FUNCTION(ckpt8_load) {
   const Pair c(a[0], "c");
   TORCH_CHECK_TYPE(c.q, "c must be a pair of tensors (q, e)");
   const Tensor* out = tensor(a[2], "out");
+  together({c.q, "c"}, {{c.e, "c"}, {out, "out"}});
   const IntArrayRef shape = c.q->sizes();
   const int64_t cols = columns(*c.q, "c");
   const Kept k = kept(c, "c", shape);
@@ -564,6 +607,8 @@ SSM_FUNCTION(ckpt8_wgrad) {
   const int64_t want[2] = {m, k};
   TORCH_CHECK_VALUE(!out || out->sizes() == IntArrayRef(want), "out must have shape ",
                     IntArrayRef(want), ", got ", out ? out->sizes() : IntArrayRef());
+  const Tensor* given_ws = tensor(a[3], "ws");
+  together({&g, "g"}, {{x8.q, "x8"}, {x8.e, "x8"}, {out, "out"}, {given_ws, "ws"}});
   const Rows rg(&g, "g");
   at::DimVector shape(g.sizes().begin(), g.sizes().end());
   shape.back() = k;
@@ -574,7 +619,7 @@ SSM_FUNCTION(ckpt8_wgrad) {
   TORCH_CHECK_VALUE(m <= 0x7fffffff && k <= 0x7fffffff, "g and x8 are too wide");
   const int aligned = !((((uintptr_t)rg.p | (uintptr_t)x.q) & 15) || ((rg.ld ? rg.ld : m) & 7));
   const Workspace ws(ssm_ckpt8_wgrad_workspace_size(tokens, (int)m, (int)k, io, aligned),
-                     tensor(a[3], "ws"), g);
+                     given_ws, g);
   if (!out) on.made({&o});
   const int rc = call([&] {
     return ssm_ckpt8_wgrad(rg.p, rg.ld, x.q, x.e, po, tokens, (int)m, (int)k, io,

@@ -221,3 +221,69 @@ def test_binding_names_the_argument_that_is_not_a_tensor():
         block.ssm_add_norm_fwd(t, res_dtype="float32")
     with pytest.raises(ValueError, match="pair"):
         block.ssm_ckpt8_load((c.q,))
+
+
+# ---- devices: tensors that only look like those of two GPUs, so that nothing can run ---------------
+
+def _fake(*shape, dtype=torch.float32, gpu=0):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        return torch.empty(*shape, dtype=dtype, device=f"cuda:{gpu}")
+
+
+def _fake8(rows, cols, gpu_q=0, gpu_e=0):
+    return block.Ckpt8(_fake(rows, cols, dtype=torch.int8, gpu=gpu_q),
+                       _fake(rows, -(-cols // 32), dtype=torch.uint8, gpu=gpu_e))
+
+
+def _device_calls():
+    """(call, its tensor arguments by the name that the error gives them)"""
+    def t():
+        return _fake(4, 64)
+
+    def v():
+        return _fake(64)
+    ws = _fake(1 << 16, dtype=torch.uint8)
+    return {
+        "add_norm_fwd": (lambda a: block.ssm_add_norm_fwd(
+            a["x"], a["w"], a["residual"], a["scale"], out=(a["out"], a["res_out"])),
+            dict(x=t(), w=v(), residual=t(), scale=v(), out=t(), res_out=t())),
+        "add_norm_bwd": (lambda a: block.ssm_add_norm_bwd(
+            a["d_out"], a["res"], a["rstd"], a["w"], a["d_res_out"], a["scale"], a["x"], ws=a["ws"],
+            out={n: a[n] for n in ("d_res", "d_x", "d_w", "d_scale")}),
+            dict(d_out=t(), res=t(), rstd=_fake(4), w=v(), d_res_out=t(), scale=v(), x=t(), ws=ws,
+                 d_res=t(), d_x=t(), d_w=v(), d_scale=v())),
+        "add_norm_bwd8": (lambda a: block.ssm_add_norm_bwd(
+            a["d_out"], a["res"], a["rstd"], scale=a["scale"], x=a["x"]),
+            dict(d_out=t(), res=_fake8(4, 64), rstd=_fake(4), scale=v(), x=_fake8(4, 64))),
+        "gated_norm_fwd": (lambda a: block.ssm_gated_norm_fwd(a["y"], a["z"], a["w"], out=a["out"]),
+                           dict(y=t(), z=t(), w=v(), out=t())),
+        "gated_norm_bwd": (lambda a: block.ssm_gated_norm_bwd(
+            a["d_out"], a["y"], a["z"], a["rstd"], a["w"], ws=a["ws"],
+            out={n: a[n] for n in ("d_y", "d_z", "d_w")}),
+            dict(d_out=t(), y=t(), z=t(), rstd=_fake(4), w=v(), ws=ws, d_y=t(), d_z=t(), d_w=v())),
+        "gated_norm_bwd8": (lambda a: block.ssm_gated_norm_bwd(a["d_out"], a["y"], a["z"], a["rstd"]),
+                            dict(d_out=t(), y=_fake8(4, 64), z=_fake8(4, 64), rstd=_fake(4))),
+        "ckpt8_save": (lambda a: block.ssm_ckpt8_save(a["x"], out=a["out"]),
+                       dict(x=t(), out=_fake8(4, 64))),
+        "ckpt8_load": (lambda a: block.ssm_ckpt8_load(a["c"], out=a["out"]),
+                       dict(c=_fake8(4, 64), out=t())),
+        "ckpt8_wgrad": (lambda a: block.ssm_ckpt8_wgrad(a["g"], a["x8"], ws=a["ws"], out=a["out"]),
+                        dict(g=t(), x8=_fake8(4, 64), ws=ws, out=_fake(64, 64))),
+    }
+
+
+@pytest.mark.parametrize("name", list(_device_calls()))
+def test_binding_refuses_tensors_of_two_gpus_by_name(name):
+    call, args = _device_calls()[name]
+    first = next(iter(args))
+    for n, t in args.items():
+        if isinstance(t, tuple):
+            others = [_fake8(4, 64, 0, 1)] + ([_fake8(4, 64, 1, 1)] if n != first else [])
+        else:
+            others = [_fake(*t.shape, dtype=t.dtype, gpu=1)]
+        for other in others:
+            # the first tensor's GPU is the call's: with that one elsewhere, the next is refused
+            wrong = n if n != first or isinstance(t, tuple) else "|".join(args)
+            with pytest.raises(ValueError, match=f"^({wrong}) must be a CUDA tensor on cuda"):
+                call({**args, n: other})

@@ -5,6 +5,7 @@ A tensor freed with work pending on its stream may be handed out again at once o
 orders the next user after that work; a call on another stream is not ordered after it, so nothing that
 it writes may lie there."""
 import gc
+from types import SimpleNamespace
 
 import pytest
 import torch
@@ -168,3 +169,14 @@ def test_results_freed_with_readers_pending_on_the_current_stream(calls, kind, n
     torch.cuda.synchronize()
     for p, q in zip(want, copies):
         assert torch.equal(p, q)
+
+
+@pytest.mark.parametrize("name", BLOCK)
+def test_a_stream_of_another_gpu_is_refused(calls, name):
+    """Found on the host, before anything is allocated or enqueued."""
+    other = SimpleNamespace(cuda_stream=0, stream_id=0, device_type=1,
+                            device_index=torch.cuda.current_device() + 1)
+    before = torch.cuda.memory_allocated()
+    with pytest.raises(ValueError, match="stream must be one of cuda"):
+        calls["block"][name](stream=other)
+    assert torch.cuda.memory_allocated() == before
