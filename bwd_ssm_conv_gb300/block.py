@@ -40,7 +40,7 @@ class NormDesc(ctypes.Structure):
 
 class Ckpt8(NamedTuple):
     """An activation held in 8 bits: q int8 [..., cols], e uint8 [..., ceil(cols / 32)]; the value
-    is q * 2^(e - 133), NaN where e is 255."""
+    is q * 2^(e - 133) for any e below 255 (zeros hold zeros), NaN where e is 255."""
     q: torch.Tensor
     e: torch.Tensor
 

@@ -182,10 +182,14 @@ __device__ __forceinline__ uint32_t block_exp(uint32_t top) {
   const uint32_t x = top >> 23;  // E + 127 of a normal number; 0 for zero and subnormals
   return x < 7u ? 7u : x;        // E >= -120; 255 stays
 }
-// 2^(6 - E) and 2^(E - 6) from e = E + 127 in 7 .. 254 (both normal numbers).
+// 2^(6 - E) from e = E + 127 in 7 .. 254, as a save makes it (a normal number).
 __device__ __forceinline__ float block_up(uint32_t e) { return __uint_as_float((260u - e) << 23); }
+// 2^(E - 6) = 2^(e - 133) from any e that a checkpoint may hold, by way of 2^(e - 127) (a subnormal
+// number for e = 0); below 7, where a save writes none but a buffer filled with zeros does, it is
+// subnormal.
 __device__ __forceinline__ float block_step(uint32_t e) {
-  return __uint_as_float(e == 255u ? 0x7fc00000u : (e - 6u) << 23);
+  const float f = __uint_as_float(max(e << 23, 0x00400000u)) * 0.015625f;
+  return e == 255u ? __uint_as_float(0x7fc00000u) : f;
 }
 // A value as a byte: v 2^(6 - E), within +-128, is rounded to the nearest even integer by adding
 // 1.5 2^23 (one rounding, the product being exact); the low byte is then the two's complement value.

@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
 #pragma unroll
     for (int j = 0; j < 128; j++) acc[j] = 0.0f;
     // A word is the scale bytes of 128 columns of a row; 255 marks NaN, 7 fills what is not there.
-    // They are stored as bf16: 2^(E-6) has the exponent field e - 6.
+    // The steps 2^(e - 133) are stored as bf16, which holds each of them (below 7 as subnormals).
     constexpr int W = L::blocks / 4, kBatch = kSegTokens * W / (32 * kSumWarps);
     const int blk0 = nq / 32;
     const bool words = a.nb % 4 == 0 && (uintptr_t)a.e % 4 == 0;
@@ -474,10 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
       for (int b = 0; b < kBatch; b++) {
         uint32_t h[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-          const uint32_t e = (v[b] >> (8 * u)) & 0xffu;
-          h[u] = e == 255u ? 0x7fc0u : (e - 6u) << 7;
-        }
+        for (int u = 0; u < 4; u++)
+          h[u] = __float_as_uint(block_step((v[b] >> (8 * u)) & 0xffu)) >> 16;
         dst[(tid - 128) + 32 * kSumWarps * b] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
       }
       __syncwarp();

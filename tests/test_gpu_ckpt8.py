@@ -50,6 +50,18 @@ def test_edges_of_the_format():
     _check(x.bfloat16(), x.bfloat16().cuda(), "bf16")
 
 
+@pytest.mark.parametrize("cols", [32, 33, 64])  # one column and eight at a time
+def test_every_scale_byte_reads_as_its_power_of_two(cols):
+    g = torch.Generator().manual_seed(21)
+    q = torch.randint(-127, 128, (256, cols), generator=g).to(torch.int8)
+    q[:, ::5] = 0
+    e = torch.arange(256)[:, None].expand(256, -(-cols // 32)).to(torch.uint8).contiguous()
+    want = ref.kept(q, e)
+    for dt in DT.values():  # both types hold q 2^(e - 133) exactly, as subnormals where e is small
+        got = block.ssm_ckpt8_load(block.Ckpt8(q.cuda(), e.cuda()), dt).cpu().double()
+        assert torch.allclose(got, want, rtol=0, atol=0, equal_nan=True)
+
+
 @pytest.mark.parametrize("lead,tail", [(8, 8), (1, 2)])
 def test_strided_rows(lead, tail):
     g = torch.Generator().manual_seed(2)
@@ -189,3 +201,28 @@ def test_wgrad_of_large_and_not_finite_gradients():
     fine = [i for i in range(24) if i not in (3, 4)]
     assert torch.allclose(got[fine].double(), want[fine], rtol=1e-5, atol=0)
     assert bool(torch.isinf(got[3]).all()) and bool(torch.isnan(got[4]).all())
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("tokens,m,k", [(70, 24, 96), (300, 136, 264), (65, 8, 33), (1500, 264, 72)])
+def test_wgrad_of_checkpoints_with_rows_of_zeros(tokens, m, k, io):
+    """Zeros for padding, scale bytes and all, add nothing: the same bits as zeros with any scale."""
+    gv, q, e = _exact_case(tokens, m, k, DT[io], seed=22)
+    q[tokens // 3:tokens // 2], e[tokens // 3:tokens // 2] = 0, 0
+    e[:, 0][q[:, :32].abs().sum(1) == 0] = 0
+    q[-1], e[-1] = 0, 5
+    want = gv.double().t() @ ref.kept(q, e)
+    got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda()))
+    assert torch.equal(got.cpu().double(), want)
+
+
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+def test_wgrad_of_the_smallest_scales(io):
+    """q 2^(e - 133) with e of 0 .. 4, subnormal steps, times 2^100: products are multiples of 2^-33
+    below 2^-22, sums of 64 of them below 2^-16, so that fp32 holds every partial sum exactly."""
+    g = torch.Generator().manual_seed(23)
+    gv = ((torch.randint(0, 2, (64, 40), generator=g) * 2 - 1) * 2.0 ** 100).to(DT[io])
+    q = torch.randint(-127, 128, (64, 96), generator=g).to(torch.int8)
+    e = torch.randint(0, 5, (64, 3), generator=g).to(torch.uint8)
+    got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda())).cpu().double()
+    assert torch.equal(got, gv.double().t() @ ref.kept(q, e))

@@ -215,6 +215,31 @@ def test_zero_rows_and_bad_values_stay_in_their_rows():
     assert bool((b.out[0] == 0).all())  # a closed gate: silu(-200) is -0
 
 
+@pytest.mark.parametrize("io", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [99, 264, 1003, 4608, 8193, 8200])  # every way a row is read
+def test_backwards_of_checkpoints_with_zeros_for_padding(cols, io):
+    """Rows and blocks of zeros, scale bytes and all, are zeros to the backwards too."""
+    g = torch.Generator().manual_seed(cols)
+    rows = 9
+    s, x, y, z, d = (_rand(g, rows, cols, dtype=DT[io]) for _ in range(5))
+    w, scale, rstd = 1.0 + 0.2 * _rand(g, cols), torch.rand(cols, generator=g), torch.rand(rows, generator=g) + 0.5
+    kept = []
+    for i, v in enumerate((s, x, y, z)):
+        q, e = ref.quantise(v)
+        q[2 + i:5], e[2 + i:5] = 0, 0
+        q[7, -(cols % 32 or 32):], e[7, -1] = 0, 5
+        kept.append((q, e))
+    s8, x8, y8, z8 = (block.Ckpt8(q.cuda(), e.cuda()) for q, e in kept)
+    s, x, y, z = (ref.kept(q, e) for q, e in kept)
+    got = block.ssm_add_norm_bwd(d.cuda(), s8, rstd.cuda(), w.cuda(), scale=scale.cuda(), x=x8)
+    want = ref.add_norm_bwd(d, s, rstd, None, scale, w, x)
+    for k, v in zip(("d_res", "d_x", "d_w", "d_scale"), want):
+        close(k, got[k], v, grad=True)
+    got = block.ssm_gated_norm_bwd(d.cuda(), y8, z8, rstd[:, None].cuda(), w.cuda())
+    for k, v in zip(("d_y", "d_z", "d_w"), ref.gated_norm_bwd(d, y, z, rstd[:, None], w, 0, False)):
+        close(k, got[k], v, grad=True)
+
+
 def test_outputs_in_place_of_inputs():
     g = torch.Generator().manual_seed(9)
     x, r, d = (_rand(g, 40, 200).cuda() for _ in range(3))
