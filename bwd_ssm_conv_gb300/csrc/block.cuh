@@ -176,7 +176,7 @@ struct Wgrad {
   const uint8_t* e;
   float* d_W;
   long long tokens;
-  int m, k, io, accumulate;
+  int m, k, io, accumulate, no_wait;
 };
 bool wgrad_aligned(const Wgrad& a);  // g's and q's rows are 16-byte aligned, widths permitting
 size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int sms);

@@ -291,14 +291,15 @@ int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_
                     size_t ws_bytes, void* stream) {
   int rc = wgrad_check(tokens, m, k, io);
   if (rc != SSM_OK) return rc;
-  if (!g || !q || !e || !d_W || (flags & ~(unsigned)SSM_WGRAD_ACCUMULATE))
+  if (!g || !q || !e || !d_W || (flags & ~(unsigned)(SSM_WGRAD_ACCUMULATE | SSM_DEBUG_NO_WAIT)))
     return SSM_ERR_INVALID_ARG;
   if (ld_g == 0) ld_g = m;
   if (ld_g < m || !aligned(g, io_size(io)) || !aligned(d_W, 4)) return SSM_ERR_INVALID_ARG;
   if (ld_g > kMaxWgrad / tokens) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
-  ssm::Wgrad a{g, ld_g, q, e, d_W, tokens, m, k, io, (flags & SSM_WGRAD_ACCUMULATE) ? 1 : 0};
+  ssm::Wgrad a{g, ld_g, q, e, d_W, tokens, m, k, io, (flags & SSM_WGRAD_ACCUMULATE) ? 1 : 0,
+               (flags & SSM_DEBUG_NO_WAIT) ? 1 : 0};
   if (!ws || !aligned(ws, 256) ||
       ws_bytes < ssm::wgrad_ws_bytes(tokens, m, k, io, ssm::wgrad_aligned(a), sms))
     return SSM_ERR_WORKSPACE;

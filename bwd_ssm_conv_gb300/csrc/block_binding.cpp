@@ -592,7 +592,7 @@ SSM_FUNCTION(ckpt8_load) {
   END_HANDLE_TH_ERRORS
 }
 
-// g, x8, accumulate, ws, out, stream
+// g, x8, flags, ws, out, stream
 SSM_FUNCTION(ckpt8_wgrad) {
   HANDLE_TH_ERRORS
   args_are(n, 6);
@@ -600,7 +600,8 @@ SSM_FUNCTION(ckpt8_wgrad) {
   const Pair x8(a[1], "x8");
   TORCH_CHECK_TYPE(x8.q, "x8 must be a pair of tensors (q, e)");
   const Tensor* out = tensor(a[4], "out");
-  const bool accumulate = yes(a[2]);
+  const unsigned flags = (unsigned)integer(a[2]);
+  const bool accumulate = flags & SSM_WGRAD_ACCUMULATE;
   const int io = io_of(g, "g");
   const int64_t m = columns(g, "g"), k = columns(*x8.q, "x8"), tokens = rows_in(g, m);
   TORCH_CHECK_VALUE(!accumulate || out, "accumulate needs the tensor to add to (out)");
@@ -622,8 +623,8 @@ SSM_FUNCTION(ckpt8_wgrad) {
                      given_ws, g);
   if (!out) on.made({&o});
   const int rc = call([&] {
-    return ssm_ckpt8_wgrad(rg.p, rg.ld, x.q, x.e, po, tokens, (int)m, (int)k, io,
-                           accumulate ? SSM_WGRAD_ACCUMULATE : 0, ws.p, ws.bytes, on.raw);
+    return ssm_ckpt8_wgrad(rg.p, rg.ld, x.q, x.e, po, tokens, (int)m, (int)k, io, flags, ws.p,
+                           ws.bytes, on.raw);
   });
   if (rc) return PyLong_FromLong(rc);
   return give(o);

@@ -79,7 +79,7 @@ struct TcArgs {
   float* out;  // d_W, or the splits' partial tiles
   long long tokens;
   int stages, per_term, per_split;  // in all, of one term of g, of one split
-  int m, k, nb, accumulate, vec_out, q_copied;
+  int m, k, nb, accumulate, vec_out, q_copied, no_wait;
   int* status;
 };
 
@@ -122,6 +122,15 @@ template <int CG> struct Mma {
           "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
           "[%0], %1;" ::"r"(smem_u32(bar)),
           "h"((uint16_t)3)
+          : "memory");
+  }
+  static __device__ __forceinline__ void commit_here(uint64_t* bar) {  // of this CTA only
+    if constexpr (CG == 1)
+      tc::mma_commit(bar);
+    else
+      asm volatile(
+          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+              smem_u32(bar))
           : "memory");
   }
   static __device__ __forceinline__ void alloc(uint32_t* dst) {
@@ -485,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     if (segs > 1) load_scales(1);
     bool ok = true;
     for (int seg = 0; seg < segs && ok; seg++) {
-      ok = mbar_wait(&seg_done[seg & 1], (seg >> 1) & 1);
+      ok = !a.no_wait && mbar_wait(&seg_done[seg & 1], (seg >> 1) & 1);
       __syncwarp();
       tmem_fence_after_sync();
       const uint32_t t = tacc + (seg & 1) * kTN;
@@ -534,6 +543,13 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
   }
   __syncwarp();
   __syncthreads();
+  if (warp == 1 && rank == 0 && bad) {
+    // Some wait has given up, perhaps with MMAs in flight: they read the shared memory and write the
+    // tensor memory of both CTAs, so they complete first.  g_here is the second CTA's; free here.
+    if (elect_one()) Mma<CG>::commit_here(&g_here[0]);
+    __syncwarp();
+    mbar_wait(&g_here[0], 0);
+  }
   sync_tile<CG>();  // the other CTA may still arrive on barriers here
   if (warp == 1) {
     tmem_fence_after_sync();
@@ -618,6 +634,7 @@ cudaError_t launch_wgrad_tc(const void* g, long long ld_g, int terms, const int8
   t.nb = (a.k + 31) / 32;
   t.accumulate = part ? 0 : a.accumulate;
   t.q_copied = q != a.q;
+  t.no_wait = a.no_wait;
   t.vec_out = a.k % 8 == 0 && (uintptr_t)t.out % 32 == 0;
   t.status = status;
   return cg == 1 ? launch<1>(t, splits, st) : launch<2>(t, splits, st);

@@ -49,6 +49,8 @@ extern "C" {
 enum {
   SSM_NORM_FIRST = 1u,      /* gated_norm: norm of y, then the gate */
   SSM_WGRAD_ACCUMULATE = 1u /* wgrad: add to d_W instead of overwriting it */
+  /* wgrad also takes ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take the
+     sums out give up at once, as if the bound of their wait had run out */
 };
 
 typedef struct {

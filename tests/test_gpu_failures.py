@@ -4,6 +4,9 @@
   block give up at once.  The persistent backward (resident blocks over (chain, chunk) units,
   each waiting for the adjoint that the unit of the next chunk publishes) must then record
   SSM_ERR_TIMEOUT, return promptly and leave the context usable.
+* The weight gradient's bounded waits: with SSM_DEBUG_NO_WAIT the warps that take the sums out of tensor
+  memory give up at once, with the products in flight; the call records SSM_ERR_TIMEOUT, waits for what
+  it has in flight and leaves the context usable.
 * SSM_CHECK_FINITE: an infinite input must be reported as SSM_ERR_NONFINITE by the forward and
   the backward; without the flag, or with finite inputs, the status stays SSM_OK.
 """
@@ -12,7 +15,7 @@ import time
 import pytest
 import torch
 
-from bwd_ssm_conv_gb300 import binding
+from bwd_ssm_conv_gb300 import binding, block
 from bwd_ssm_conv_gb300.workloads import random_scan_inputs
 from gpu_util import assert_close, gpu_bwd, gpu_fwd, oracle_bwd, tol
 
@@ -44,6 +47,37 @@ def test_flag_wait_gives_up_reports_timeout_and_leaves_the_context_usable():
     o = oracle_bwd(inp, 16)
     for k in ("d_x", "d_dt", "d_A", "d_B", "d_C", "d_D", "d_z", "d_s0"):
         assert_close(k, g[k], o[k], tol("bf16", grad=True))
+
+
+def _wgrad_case(tokens, m, k, io, seed=53):
+    """g and a checkpoint whose products and sums fp32 holds exactly, and their weight gradient."""
+    gen = torch.Generator().manual_seed(seed)
+    g = torch.randint(-2, 3, (tokens, m), generator=gen).to(io)
+    q = torch.randint(-4, 5, (tokens, k), generator=gen).to(torch.int8)
+    e = torch.full((tokens, -(-k // 32)), 133, dtype=torch.uint8)
+    return g.cuda(), block.Ckpt8(q.cuda(), e.cuda()), g.double().t() @ q.double()
+
+
+# one CTA per tile and pairs; one range of tokens and several; at most two segments of 1024 tokens per
+# range, so that no other wait of the kernel depends on the warps that gave up
+WGRAD = [(500, 100, 2048 * 16), (500, 200, 4096 * 16), (5000, 128, 320), (5000, 264, 320)]
+
+
+@pytest.mark.parametrize("tokens,m,k", WGRAD)
+@pytest.mark.parametrize("io", [torch.float32, torch.bfloat16])
+def test_wgrad_that_gives_up_reports_timeout_and_leaves_the_context_usable(tokens, m, k, io):
+    g, x8, want = _wgrad_case(tokens, m, k, io)
+    ws = torch.empty(block.ssm_ckpt8_wgrad_workspace_size(tokens, m, k, block._IO[io], aligned=False),
+                     dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    t0 = time.time()
+    block.ssm_ckpt8_wgrad(g, x8, ws=ws, debug_flags=binding.SSM_DEBUG_NO_WAIT)
+    status = binding.ssm_scan_status(ws)
+    assert status == binding.SSM_ERR_TIMEOUT, binding.ssm_status_string(status)
+    assert time.time() - t0 < 10.0
+    got = block.ssm_ckpt8_wgrad(g, x8, ws=ws)
+    assert binding.ssm_scan_status(ws) == binding.SSM_OK
+    assert torch.equal(got.cpu().double(), want)
 
 
 @pytest.mark.parametrize("shape,io", [
