@@ -207,7 +207,9 @@ def ssm_ckpt8_wgrad_workspace_size(tokens, m, k, io=SSM_BF16, aligned=True) -> i
 def ssm_ckpt8_wgrad(g, x8, accumulate=False, ws=None, out=None, stream=None, debug_flags=0):
     """The gradient d_W [m][k] (fp32) of a projection y = x W^T from g = dL/dy [..., m] and the
     8-bit checkpoint x8 of x [..., k]: d_W = sum over rows of g x^T.  ``accumulate`` adds it to
-    ``out``.  ``debug_flags``: SSM_DEBUG_NO_WAIT (tests of the error path only)."""
+    ``out``.  Where a bounded wait inside the kernel gave up, that part of d_W is NaN and the workspace's
+    status is SSM_ERR_TIMEOUT: pass ``ws`` (ssm_ckpt8_wgrad_workspace_size bytes) and read it with
+    ssm_scan_status(ws).  ``debug_flags``: SSM_DEBUG_NO_WAIT (tests of the error path only)."""
     flags = (SSM_WGRAD_ACCUMULATE if accumulate else 0) | debug_flags
     r = (_B or _calls()).ckpt8_wgrad(g, x8, flags, ws, out, stream)
     if type(r) is int:

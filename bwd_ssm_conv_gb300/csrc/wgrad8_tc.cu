@@ -512,8 +512,12 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     }
     if (!ok) atomicExch(&bad, 1);
     const int i = m0 + 32 * quad + lane;
-    if (ok && i < a.m) {
-      float* dst = a.out + ((long long)blockIdx.z * a.m + i) * a.k;
+    float* dst = a.out + ((long long)blockIdx.z * a.m + i) * a.k;
+    if (!ok && i < a.m) {  // what is missing reads as NaN, also where nobody looks at the status
+#pragma unroll 1
+      for (int j = n0 + 128 * half; j < n0 + 128 * (half + 1) && j < a.k; j++)
+        dst[j] = __uint_as_float(0x7fc00000u);
+    } else if (i < a.m) {
 #pragma unroll
       for (int b = 0; b < 128; b += 8) {
         const int j = n0 + 128 * half + b;

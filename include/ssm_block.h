@@ -129,7 +129,8 @@ int ssm_ckpt8_load(const int8_t* q, const uint8_t* e, void* out, long long ld_ou
  * contiguous; tokens up to 2^29.  It runs on the tensor cores, exactly: kept values and bf16 g are
  * bf16 numbers, fp32 g is split into three, products and sums are fp32.
  * Workspace: ssm_ckpt8_wgrad_workspace_size bytes (at least 256: its first word is a status word,
- * read with ssm_scan_status).  aligned: the rows of g (pointer and ld_g * element size) and q's
+ * read with ssm_scan_status).  Where a bounded wait gave up (SSM_ERR_TIMEOUT there), the tiles of d_W that
+ * it concerns are NaN.  aligned: the rows of g (pointer and ld_g * element size) and q's
  * pointer are 16-byte aligned; 0 asks for room for copies that are.  With bf16 g, m a multiple of 8
  * and k of 16 an aligned call needs no copies. */
 size_t ssm_ckpt8_wgrad_workspace_size(long long tokens, int m, int k, int io, int aligned);

@@ -80,6 +80,20 @@ def test_wgrad_that_gives_up_reports_timeout_and_leaves_the_context_usable(token
     assert torch.equal(got.cpu().double(), want)
 
 
+@pytest.mark.parametrize("tokens,m,k", WGRAD + [(300, 130, 33)])  # and rows stored value by value
+@pytest.mark.parametrize("accumulate", [False, True])
+def test_what_a_wgrad_that_gave_up_lacks_is_nan(tokens, m, k, accumulate):
+    """The call makes its own workspace, whose status nobody can read."""
+    g, x8, want = _wgrad_case(tokens, m, k, torch.bfloat16)
+    out = torch.zeros(m, k, device="cuda")
+    block.ssm_ckpt8_wgrad(g, x8, out=out, accumulate=accumulate,
+                          debug_flags=binding.SSM_DEBUG_NO_WAIT)
+    assert bool(torch.isnan(out).all())
+    out.zero_()
+    block.ssm_ckpt8_wgrad(g, x8, out=out, accumulate=accumulate)
+    assert torch.equal(out.cpu().double(), want)
+
+
 @pytest.mark.parametrize("shape,io", [
     ((2, 70, 64, 1, 16, 1), "bf16"),   # TMA-staged kernels
     ((2, 70, 24, 1, 16, 1), "f32"),    # general kernels
