@@ -225,6 +225,17 @@ __device__ __forceinline__ uint32_t two_bf16(uint32_t w, __nv_bfloat162 scale) {
   r = __hmul2(r, scale);
   return *reinterpret_cast<uint32_t*>(&r);
 }
+// The steps 2^(e - 133) of the scale bytes in bits 0 .. 7 and 16 .. 23 as bf16, which holds each of
+// them: as 2^(e - 127) (a subnormal number for e = 0, infinite for 255) times 2^-6, plus f - f for a NaN.
+__device__ __forceinline__ uint32_t two_steps(uint32_t e2) {
+  uint32_t f;
+  asm("max.u16x2 %0, %1, %2;" : "=r"(f) : "r"(e2 << 7), "r"(0x00400040u));
+  const uint32_t small = 0x3c803c80u;
+  const __nv_bfloat162 f2 = *reinterpret_cast<const __nv_bfloat162*>(&f);
+  const __nv_bfloat162 r =
+      __hfma2(f2, *reinterpret_cast<const __nv_bfloat162*>(&small), __hsub2(f2, f2));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 // Four columns of a word leave in the order 0, 2, 1, 3 (taking every other byte saves moving them):
 // place j of the tile holds column column_of(j), undone where the accumulator is stored.
 __device__ __forceinline__ constexpr int column_of(int j) {
@@ -455,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
 #pragma unroll
     for (int j = 0; j < 128; j++) acc[j] = 0.0f;
     // A word is the scale bytes of 128 columns of a row; 255 marks NaN, 7 fills what is not there.
-    // The steps 2^(e - 133) are stored as bf16, which holds each of them (below 7 as subnormals).
+    // The steps are stored as bf16.
     constexpr int W = L::blocks / 4, kBatch = kSegTokens * W / (32 * kSumWarps);
     const int blk0 = nq / 32;
     const bool words = a.nb % 4 == 0 && (uintptr_t)a.e % 4 == 0;
@@ -480,13 +491,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
         }
       }
 #pragma unroll
-      for (int b = 0; b < kBatch; b++) {
-        uint32_t h[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++)
-          h[u] = __float_as_uint(block_step((v[b] >> (8 * u)) & 0xffu)) >> 16;
-        dst[(tid - 128) + 32 * kSumWarps * b] = make_uint2(h[0] | h[1] << 16, h[2] | h[3] << 16);
-      }
+      for (int b = 0; b < kBatch; b++)
+        dst[(tid - 128) + 32 * kSumWarps * b] =
+            make_uint2(two_steps(__byte_perm(v[b], 0u, 0x4140)),
+                       two_steps(__byte_perm(v[b], 0u, 0x4342)));
       __syncwarp();
       if (lane == 0) mbar_arrive(&scaled[seg & 1]);
     };

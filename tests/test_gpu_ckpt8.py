@@ -226,3 +226,16 @@ def test_wgrad_of_the_smallest_scales(io):
     e = torch.randint(0, 5, (64, 3), generator=g).to(torch.uint8)
     got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda())).cpu().double()
     assert torch.equal(got, gv.double().t() @ ref.kept(q, e))
+
+
+def test_wgrad_of_every_scale_byte():
+    """One token: d_W is g times the kept values, in one product each, exact within fp32's normal
+    numbers (g = 2^60 for the small half of the scales)."""
+    g = torch.Generator().manual_seed(24)
+    for power, first in ((60, 0), (0, 128)):
+        q = torch.randint(-127, 128, (1, 128 * 32), generator=g).to(torch.int8)
+        e = torch.arange(first, first + 128)[None].to(torch.uint8)
+        gv = torch.full((1, 8), 2.0 ** power).bfloat16()
+        got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda())).cpu().double()
+        want = gv.double().t() @ ref.kept(q, e)
+        assert torch.allclose(got, want, rtol=0, atol=0, equal_nan=True)
