@@ -178,8 +178,8 @@ struct Wgrad {
   long long tokens;
   int m, k, io, accumulate, no_wait;
 };
-bool wgrad_aligned(const Wgrad& a);  // g's and q's rows are 16-byte aligned, widths permitting
 size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int sms);
+size_t wgrad_ws_bytes(const Wgrad& a, int sms);  // what this call needs: at most the above
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st);
 // The tensor-core kernel (wgrad8_tc.cu): g as `terms` bf16 planes [tokens] x ld_g, q with rows of ld_q
 // bytes.  part: the splits' tiles, [splits][m][k], or NULL with one split.

@@ -301,7 +301,7 @@ int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_
   ssm::Wgrad a{g, ld_g, q, e, d_W, tokens, m, k, io, (flags & SSM_WGRAD_ACCUMULATE) ? 1 : 0,
                (flags & SSM_DEBUG_NO_WAIT) ? 1 : 0};
   if (!ws || !aligned(ws, 256) ||
-      ws_bytes < ssm::wgrad_ws_bytes(tokens, m, k, io, ssm::wgrad_aligned(a), sms))
+      ws_bytes < ssm::wgrad_ws_bytes(a, sms))
     return SSM_ERR_WORKSPACE;
   return status_of(ssm::launch_wgrad(a, ws, sms, (cudaStream_t)stream));
 }

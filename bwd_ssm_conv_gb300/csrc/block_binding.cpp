@@ -618,7 +618,8 @@ SSM_FUNCTION(ckpt8_wgrad) {
   const Tensor o = out ? *out : make(want, at::kFloat, g);
   float* po = f32(&o, "out", m * k);
   TORCH_CHECK_VALUE(m <= 0x7fffffff && k <= 0x7fffffff, "g and x8 are too wide");
-  const int aligned = !((((uintptr_t)rg.p | (uintptr_t)x.q) & 15) || ((rg.ld ? rg.ld : m) & 7));
+  const uintptr_t row = (uintptr_t)(rg.ld ? rg.ld : m) * g.element_size();  // fp32 g may lie anywhere
+  const int aligned = !((uintptr_t)x.q & 15) && (io == SSM_F32 || !(((uintptr_t)rg.p | row) & 15));
   const Workspace ws(ssm_ckpt8_wgrad_workspace_size(tokens, (int)m, (int)k, io, aligned),
                      given_ws, g);
   if (!out) on.made({&o});

@@ -165,13 +165,13 @@ struct Plan {
   bool copy_g, copy_q;
   size_t g, q, part, bytes;
 };
-Plan plan_of(long long tokens, int m, int k, int io, bool aligned, int sms) {
+Plan plan_of(long long tokens, int m, int k, int io, bool aligned_g, bool aligned_q, int sms) {
   Plan p{};
   p.terms = io == SSM_F32 ? 3 : 1;
   p.m8 = (m + 7) / 8 * 8;
   p.k16 = (k + 15) / 16 * 16;
-  p.copy_g = io == SSM_F32 || p.m8 != m || !aligned;
-  p.copy_q = p.k16 != k || !aligned;
+  p.copy_g = io == SSM_F32 || p.m8 != m || !aligned_g;
+  p.copy_q = p.k16 != k || !aligned_q;
   p.splits = wgrad_tc_splits(tokens, p.terms, m, k, sms);
   p.g = kStatusBytes;
   p.q = p.g + (p.copy_g ? align_up((size_t)p.terms * tokens * p.m8 * 2, 256) : 0);
@@ -182,16 +182,21 @@ Plan plan_of(long long tokens, int m, int k, int io, bool aligned, int sms) {
 
 }  // namespace
 
-bool wgrad_aligned(const Wgrad& a) {
-  return a.ld_g % 8 == 0 && (uintptr_t)a.g % 16 == 0 && (uintptr_t)a.q % 16 == 0;
+// Each operand is copied for its own sake only: what is not 16-byte aligned costs a pass over itself, and
+// fp32 g, which is copied in any case, may lie anywhere.
+static Plan plan_of(const Wgrad& a, int sms) {
+  const size_t row = (size_t)a.ld_g * (a.io == SSM_F32 ? 4 : 2);
+  return plan_of(a.tokens, a.m, a.k, a.io, (uintptr_t)a.g % 16 == 0 && row % 16 == 0,
+                 (uintptr_t)a.q % 16 == 0, sms);
 }
 
 size_t wgrad_ws_bytes(long long tokens, int m, int k, int io, bool aligned, int sms) {
-  return plan_of(tokens, m, k, io, aligned, sms).bytes;
+  return plan_of(tokens, m, k, io, aligned, aligned, sms).bytes;
 }
+size_t wgrad_ws_bytes(const Wgrad& a, int sms) { return plan_of(a, sms).bytes; }
 
 cudaError_t launch_wgrad(const Wgrad& a, void* ws, int sms, cudaStream_t st) {
-  const Plan p = plan_of(a.tokens, a.m, a.k, a.io, wgrad_aligned(a), sms);
+  const Plan p = plan_of(a, sms);
   char* w = (char*)ws;
   int* status = (int*)ws;
   const void* g = a.g;

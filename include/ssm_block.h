@@ -130,9 +130,10 @@ int ssm_ckpt8_load(const int8_t* q, const uint8_t* e, void* out, long long ld_ou
  * bf16 numbers, fp32 g is split into three, products and sums are fp32.
  * Workspace: ssm_ckpt8_wgrad_workspace_size bytes (at least 256: its first word is a status word,
  * read with ssm_scan_status).  Where a bounded wait gave up (SSM_ERR_TIMEOUT there), the tiles of d_W that
- * it concerns are NaN.  aligned: the rows of g (pointer and ld_g * element size) and q's
- * pointer are 16-byte aligned; 0 asks for room for copies that are.  With bf16 g, m a multiple of 8
- * and k of 16 an aligned call needs no copies. */
+ * it concerns are NaN.  aligned: the rows of g (pointer and ld_g * element size; fp32 g may lie
+ * anywhere) and q's pointer are 16-byte aligned; 0 asks for room for copies that are.  Each of the two is
+ * copied only where it is not aligned itself; with bf16 g, m a multiple of 8 and k of 16 an aligned call
+ * needs no copies. */
 size_t ssm_ckpt8_wgrad_workspace_size(long long tokens, int m, int k, int io, int aligned);
 int ssm_ckpt8_wgrad(const void* g, long long ld_g, const int8_t* q, const uint8_t* e, float* d_W,
                     long long tokens, int m, int k, int io, unsigned flags, void* ws,

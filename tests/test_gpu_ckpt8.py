@@ -239,3 +239,39 @@ def test_wgrad_of_every_scale_byte():
         got = block.ssm_ckpt8_wgrad(gv.cuda(), block.Ckpt8(q.cuda(), e.cuda())).cpu().double()
         want = gv.double().t() @ ref.kept(q, e)
         assert torch.allclose(got, want, rtol=0, atol=0, equal_nan=True)
+
+
+def _off(t, elements):
+    """The same values on the GPU, ``elements`` past an aligned address."""
+    wide = torch.zeros(t.numel() + elements, dtype=t.dtype, device="cuda")
+    wide[elements:] = t.reshape(-1).cuda()
+    return wide[elements:].view(t.shape)
+
+
+# (type of g, m, k, row stride of g, offsets of g and q in elements, what the size query is told)
+ALIGNED = [("f32", 12, 512, 0, 0, 0, 1), ("f32", 12, 512, 516, 0, 0, 1), ("f32", 64, 512, 0, 3, 0, 1),
+           ("f32", 40, 48, 41, 1, 0, 1), ("bf16", 64, 512, 72, 0, 0, 1), ("bf16", 64, 512, 0, 8, 16, 1),
+           ("bf16", 64, 512, 68, 0, 0, 0), ("bf16", 64, 512, 0, 1, 0, 0), ("bf16", 64, 512, 0, 0, 5, 0),
+           ("f32", 64, 512, 0, 0, 8, 0), ("bf16", 20, 33, 0, 0, 0, 0)]
+
+
+@pytest.mark.parametrize("io,m,k,ld,off_g,off_q,aligned", ALIGNED)
+def test_wgrad_takes_the_workspace_that_the_header_asks_for(io, m, k, ld, off_g, off_q, aligned):
+    tokens = 300
+    gv, q, e = _exact_case(tokens, m, k, DT[io], seed=25)
+    rows = torch.zeros(tokens, ld or m, dtype=gv.dtype)
+    rows[:, :m] = gv
+    g, q8, e8 = _off(rows, off_g), _off(q, off_q), e.cuda()
+    L = block.lib()
+    n = L.ssm_ckpt8_wgrad_workspace_size(tokens, m, k, block._IO[gv.dtype], aligned)
+    ws = torch.full((n + 256,), 0x5a, dtype=torch.uint8, device="cuda")
+    out = torch.full((m, k), float("nan"), device="cuda")
+    rc = L.ssm_ckpt8_wgrad(g.data_ptr(), ld, q8.data_ptr(), e8.data_ptr(), out.data_ptr(), tokens, m, k,
+                           block._IO[gv.dtype], 0, ws.data_ptr(), n,
+                           torch.cuda.current_stream().cuda_stream)
+    assert rc == binding.SSM_OK
+    assert torch.equal(out.cpu().double(), gv.double().t() @ ref.kept(q, e))
+    assert bool((ws[n:] == 0x5a).all())
+    # and through the binding, which asks for as much
+    got = block.ssm_ckpt8_wgrad(g[:, :m], block.Ckpt8(q8, e8), ws=ws[:n])
+    assert torch.equal(got, out)
