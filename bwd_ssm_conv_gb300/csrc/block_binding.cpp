@@ -215,28 +215,23 @@ int64_t int_attr(PyObject* o, const char* name) {
 // therefore comes from the memory of the stream that it runs on: a block that was freed with work
 // pending on the caller's stream is never handed to another one.  Made before anything is allocated.
 struct On {
-  std::optional<c10::Stream> given;
-  c10::cuda::CUDAGuard device;
+  c10::cuda::OptionalCUDAGuard device;       // only where another device is current
+  c10::cuda::OptionalCUDAStreamGuard guard;  // only for another stream
   const c10::cuda::CUDAStream now;
-  c10::cuda::OptionalCUDAStreamGuard guard;
   void* raw;
   On(PyObject* stream, const Tensor& t)
-      : given(stream_of(stream, t.device())),
-        device(t.device()),
-        now(c10::cuda::getCurrentCUDAStream(t.device().index())),
-        raw(now.stream()) {
-    if (!given) return;
-    raw = (void*)(uintptr_t)int_attr(stream, "cuda_stream");
-    if (*given != now.unwrap()) guard.reset_stream(*given);
-  }
-  static std::optional<c10::Stream> stream_of(PyObject* stream, at::Device home) {
-    if (stream == Py_None) return std::nullopt;
-    const c10::Stream s = c10::Stream::unpack3(
-        int_attr(stream, "stream_id"), (c10::DeviceIndex)int_attr(stream, "device_index"),
-        (c10::DeviceType)int_attr(stream, "device_type"));
-    TORCH_CHECK_VALUE(s.device() == home, "stream must be one of ", home,
-                      ", where the tensors are; got one of ", s.device());
-    return s;
+      : now(c10::cuda::getCurrentCUDAStream(t.device().index())), raw(now.stream()) {
+    const at::Device home = t.device();
+    if (stream != Py_None) {
+      const c10::Stream s = c10::Stream::unpack3(
+          int_attr(stream, "stream_id"), (c10::DeviceIndex)int_attr(stream, "device_index"),
+          (c10::DeviceType)int_attr(stream, "device_type"));
+      TORCH_CHECK_VALUE(s.device() == home, "stream must be one of ", home,
+                        ", where the tensors are; got one of ", s.device());
+      raw = (void*)(uintptr_t)int_attr(stream, "cuda_stream");
+      if (s != now.unwrap()) guard.reset_stream(s);
+    }
+    if (c10::cuda::current_device() != home.index()) device.set_index(home.index());
   }
   // Results made for another stream are marked as used on the caller's current one too, so that
   // freeing them with work pending there does not give their memory to the other stream's next call.
