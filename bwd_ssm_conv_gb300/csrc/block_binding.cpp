@@ -3,9 +3,8 @@
 // No computation happens here.
 //
 // The host is all that bounds a call for a token or a small layer, so the marshalling is compiled:
-// add_norm of 8192 x 512 fp32, forward and backward (31 us of kernels), takes the host 15 us (three
-// launches and seven allocations) where the same checks in Python took 38, a token's call 3.3 where
-// it took 7.3.
+// add_norm's forward and backward of a small fp32 layer take the host 14 us (three launches and seven
+// allocations) where the same checks in Python took 38, a token's call 2.9 where it took 7.3.
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>

@@ -1,8 +1,9 @@
 // ckpt8.cu -- 8-bit activation checkpoints: saving an activation and reading it back.  Pure
 // streaming: a save reads the activation and writes 33/32 bytes per value, a load the reverse.
-// 16384 x 2048 bf16 (GB300): save 17.5 us and load 12.0 us for 102 MB each (the load finds part of the
-// checkpoint in L2), 5.8 and 8.5 TB/s beside 6.7 measured for a copy; 20.7 and 14.2 us while every
-// segment's row was found by a 64-bit division.
+// 16384 x 2048 bf16 (GB300): 18.5 and 18.8 us for 102 MB each, 5.5 TB/s of 6.7 measured for a copy, with
+// inputs and outputs beyond L2; a save and its load back to back 34, the load finding part of the
+// checkpoint in L2 (35 while every segment's row was found by a 64-bit division).  Single columns,
+// 16384 x 2047: 45 and 37 us.
 #include "block.cuh"
 #include "rows.cuh"
 

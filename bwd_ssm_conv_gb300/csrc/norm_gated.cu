@@ -3,18 +3,22 @@
 //                dv = rstd (w d_out - n mean(w d_out n)),  d_y = dv silu(z),  d_z = dv y silu'(z)
 //   norm first:  n = y rstd(y),  out = w n silu(z),  dn = w d_out silu(z)
 //                d_y = rstd (dn - n mean(dn n)),  d_z = w d_out n silu'(z)
-// A group is read once, copied ahead to shared memory (rows.cuh), and its one sum formed over its
-// threads.  The sigmoid is taken once per value in each direction.
+// A group is read once, copied to shared memory (rows.cuh; ahead, but for fp32 rows of four chunks per
+// thread, and with plain loads beyond 8192 columns, in the backward beyond 4096), and its one sum
+// formed over its threads.  The sigmoid is taken once per value in each direction.
 //
 // What bounds them (32768 rows of 1536 bf16 columns, checkpoints of y and z, GB300):
-//   forward   66 us, 406 MB: 6.2 TB/s of 6.7 measured for a copy, and 57 % of the issue slots.
+//   forward   67 us, 406 MB: 6.1 TB/s of 6.7 measured for a copy, and 57 % of the issue slots.
 //             Largest magnitudes of bf16 blocks taken two at a time, and one fused rounding per
 //             value, brought 94 -> 74 us; rows and strides in 32 bits 74 -> 67 us.
-//   backward  90 us, 406 MB at 4.5 TB/s: issue slots (58 % busy at 14 warps per SM, which wait for
+//   backward  93 us, 406 MB at 4.4 TB/s: issue slots (58 % busy at 14 warps per SM, which wait for
 //             their own results).  The rows read with plain loads took 191 us, the next row
 //             loaded ahead into registers (which spill) 252 us, copied ahead 134 us; fewer chunks per
 //             thread (norm_shape) and all blocks resident 108 us, 32-bit rows and strides 93 us,
-//             pairs of values per instruction 90 us.  One chunk per thread, for twice the warps: 101.
+//             pairs of values per instruction 90 us; 1 us goes to scale bytes below 7 (block_step).
+//             One chunk per thread, for twice the warps, takes 10 us more.
+// Beyond 4096 columns the backward spills 1.2 KB per thread (single columns 0.7 - 3.0 KB): bf16,
+// 4096 x 8192 139 us of 50, 2048 x 16384 271 of 50.
 #include "block.cuh"
 #include "rows.cuh"
 

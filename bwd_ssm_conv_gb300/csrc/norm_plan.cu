@@ -14,8 +14,9 @@ constexpr int kFewRows = 4;
 
 // out[c] = sum_b part[b][c]: a block sums 32 columns (blockIdx.x) of one of the sums (blockIdx.y),
 // 8 threads x 4 columns across and 128 slices of the rows, every slice in order, then the slices in
-// order.  Launched so that it may start while the kernel that writes `part` is still running; it
-// waits for that one's end here.
+// order.  Its launch is set up while the kernel that writes `part` runs (which gives no early signal, so
+// that this one starts at its end) and it waits here for that one's results: 2 - 3 us less per
+// backward than an ordinary launch (8192 x 512 fp32, forward and backward: 34.9 and 37.6 us).
 __global__ void __launch_bounds__(1024) column_sums_kernel(const float* part, int n, int cols,
                                                            float* out0, float* out1) {
   __shared__ float s[128][33];
@@ -66,12 +67,13 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
       nj = 2, s.variant = kVec2Wide;
     } else {
       // Of 4, 3 and 2 chunks per thread (2 and 1 in the backward, which keeps more of each) the one
-      // that leaves the fewest threads without a chunk: on 32768 rows of 1536 bf16 columns the
-      // forward takes 66 us with 3, 73 with 2 and 91 with 1, the backward 90 with 2 and 101 with 1.
+      // that leaves the fewest threads without a chunk: on 32768 rows of 1536 bf16 columns from and to
+      // 8 bits the forward takes 68 us with 3, 75 with 2, 86 with 4 and 92 with 1, the backward 96 with
+      // 2 and 106 with 1; add_norm's backward of 32768 x 768 65 with 1 and 72 with 2.
       // Among equals the forward takes the one nearest to two warps per row (add_norm of bf16 rows and an
-      // fp32 stream, 2 and 4 chunks: 16384 x 512 17.9 and 20.3 us, 16384 x 1024 34.4 and 37.1; both
-      // bf16, 8192 x 2048: 30.1 and 28.0), the backward the larger, whose fewer rows at a time leave
-      // fewer column sums to add (8192 x 512 fp32, 2 and 1: 18.7 and 20.2 us with them).
+      // fp32 stream, 2 and 4 chunks: 16384 x 512 20.5 and 22.6 us, 16384 x 1024 36.8 and 39.3; both
+      // bf16, 8192 x 2048: 32.2 and 30.4), the backward the larger, whose fewer rows at a time leave
+      // fewer column sums to add (8192 x 512 fp32, 2 and 1: 22.6 and 22.7 us with them).
       int best = -1, from64 = 0;
       nj = 2;
       for (int k = backward ? 2 : 4; k >= (backward ? 1 : 2); k--) {

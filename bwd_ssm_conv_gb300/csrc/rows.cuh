@@ -340,9 +340,11 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*part)[32], in
 // A thread's own chunks of the rows to come are copied to shared memory while it works on the
 // current one (cp.async, 8 columns at a time, RowPlan::slots rows in all).  It alone reads what it
 // copied, so no barrier is needed, and it may read a row twice, before and after the row's sum,
-// instead of holding it in registers.  Single columns (VEC = 1) are loaded one row ahead into
-// registers instead, up to 8 per thread; wider rows (and VEC = 8 without RING) are read where they
-// are used (2000 x 12345 bf16, 32 columns per thread held ahead: add_norm 489 us, not: 231).
+// instead of holding it in registers.  With one slot (ring_slots) nothing is ahead: a row is copied as
+// a whole and waited for.  Single columns (VEC = 1) are loaded one row ahead into registers instead, up
+// to 8 per thread (20000 x 1001 fp32, add_norm: forward 59 us, backward 123; read where they are used
+// 77 and 233); wider rows (and VEC = 8 without RING) are read where they are used (2000 x 12345 bf16
+// forward, 32 columns per thread held ahead: add_norm 491 us, gated_norm 412; not: 232 and 185).
 
 __device__ __forceinline__ uint32_t shared_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
@@ -549,7 +551,10 @@ inline RowPlan row_plan(long long rows, int group, int groups, int tpr, int bloc
   return p;
 }
 
-// Rows in shared memory: as many, up to 3, as leave room for per_sm_threads threads on an SM.
+// Rows in shared memory: as many, up to 3, as leave room for per_sm_threads threads on an SM.  One for
+// fp32 rows of more than one chunk per thread in add_norm's backward (its four operands take 128 KB
+// per row on an SM, those that a call does not have included) and of four in the gated forward; two
+// or three else.
 constexpr int kRingBytesPerSm = 208 * 1024;
 constexpr int kRingBytesMost = 224 * 1024;  // of one block
 inline int ring_slots(uint32_t slot_bytes, int threads, int per_sm_threads) {

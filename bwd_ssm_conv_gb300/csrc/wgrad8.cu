@@ -3,11 +3,10 @@
 //   before  operands that it cannot read as they are go to the workspace in a form that it can:
 //           fp32 g as three bf16 terms, rows that are not 16-byte aligned with their rows padded
 //   after   where the tokens are split over blocks, the splits' tiles are added in order
-// The copies read and write each value once.  8189 tokens x 64 x 512, fp32 g (GB300): 17.6 us, of
-// which the copy 2.1, the product 9.8 and the sum 3.0 by themselves; each is set up while the one
-// before it runs (one after the other, with the status word cleared by a copy of its own: 20.5).
-// 8192 x 2048 x 1024: 102 us, 1010 TFLOP/s of bf16 products for 337 of fp32 (a plain fp32 product:
-// 54).
+// The copies read and write each value once.  8189 tokens x 64 x 512, fp32 g (GB300): 16.7 us, a chain
+// of three kernels, each set up while the one before it runs (one after the other, with the status word
+// cleared by a copy of its own: 20.5).  8192 x 2048 x 1024: 94 us, 1100 TFLOP/s of bf16 products for
+// 367 of fp32 (a library fp32 product: 61).  Padding: 8192 x 1000 x 1008 in bf16 26 us, x 1001 50.
 #include "block.cuh"
 #include "rows.cuh"
 

@@ -37,8 +37,8 @@
 // product's 7e-7.  At the end they go to d_W or, where the tokens are split over blocks, to the
 // workspace; wgrad8.cu then adds the splits in order.
 //
-// Measured (GB300): g 16384 x 4096, X 16384 x 1024: 87 us, 1587 TFLOP/s (84 % of the measured bf16
-// peak on 128 of 152 SMs); MMAs alone 78 us.  g 32768 x 768, X 32768 x 1536: 53 us.
+// Measured (GB300): g 16384 x 4096, X 16384 x 1024: 88 us, 1565 TFLOP/s (82 % of the measured bf16
+// peak on 128 of 152 SMs); MMAs alone 78 us.  g 32768 x 768, X 32768 x 1536: 52 us.
 #include "block.cuh"
 #include "rows.cuh"
 #include "tma.cuh"

@@ -20,8 +20,8 @@
  * over the block, raised to -120 where it is less (or the block is zero),
  *   e = E + 127,   q = round-to-nearest-even(v * 2^(6 - E)) limited to -127 .. 127,
  * and the value kept is q * 2^(E - 6): exact in bf16 and in fp32.  The error of a kept value is
- * at most 2^(E - 7), i.e. max |v| / 128 of its block (2^(E - 6) where |v| > 127 2^(E-6)).  A block that holds
- * an infinity or a NaN is kept as e = 255, q = 0 and reads back as NaN throughout.  A save writes e of
+ * at most 2^(E - 7), i.e. max |v| / 128 of its block (2^(E - 6) where |v| > 127 2^(E-6)).  A block
+ * that holds an infinity or a NaN is kept as e = 255, q = 0 and reads back as NaN throughout.  A save writes e of
  * 7 .. 255; everything that reads a checkpoint takes any byte as q 2^(e - 133), so that one filled
  * with zeros holds zeros.
  *
@@ -30,8 +30,9 @@
  * anything is enqueued.  Outputs are overwritten.  Inputs and outputs must not overlap, except
  * that an output may be the same tensor (pointer and stride) as an input of its own type of the
  * norms' forward or backward, element for element (res_out = residual, d_x = d_out, ...).
- * Row statistics, sums over rows and products are fp32; a value is rounded to the I/O type once,
- * where it is stored.  Sums run in a fixed order: results are bitwise reproducible.
+ * Row statistics and sums over rows are fp32 (the weight gradient's as it says below); a value is
+ * rounded to the I/O type once, where it is stored.  Sums run in a fixed order: results are bitwise
+ * reproducible.
  */
 #ifndef SSM_BLOCK_GB300_H
 #define SSM_BLOCK_GB300_H
@@ -126,8 +127,10 @@ int ssm_ckpt8_load(const int8_t* q, const uint8_t* e, void* out, long long ld_ou
 /* Weight gradient of a projection from its input's checkpoint:
  *   d_W[i][j] (+)= sum_{t < tokens} g[t][i] * X[t][j],   i < m, j < k
  * g [tokens][m] (io), X = the ckpt8 (q [tokens][k], e [tokens][ceil(k / 32)]), d_W [m][k] fp32
- * contiguous; tokens up to 2^29.  It runs on the tensor cores, exactly: kept values and bf16 g are
- * bf16 numbers, fp32 g is split into three, products and sums are fp32.
+ * contiguous; tokens up to 2^29.  It runs on the tensor cores: kept values and bf16 g are bf16 numbers,
+ * fp32 g is split into three exactly, so that every product is exact.  Sums are fp32, truncated by
+ * the tensor cores within 1024 tokens (64 additions) and rounded to nearest between them: about
+ * (64 + tokens / 2048) 2^-23 of sum |g X| off at worst, (64 + 3 tokens / 2048) 2^-23 with fp32 g.
  * Workspace: ssm_ckpt8_wgrad_workspace_size bytes (at least 256: its first word is a status word,
  * read with ssm_scan_status).  Where a bounded wait gave up (SSM_ERR_TIMEOUT there), the tiles of d_W that
  * it concerns are NaN.  aligned: the rows of g (pointer and ld_g * element size; fp32 g may lie
