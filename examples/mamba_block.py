@@ -94,10 +94,12 @@ class Block:
 
     @staticmethod
     def _weight_grad(g, x):
-        """sum over rows of g x^T, from x's checkpoint or from x itself."""
+        """sum over rows of g x^T in fp32, from x's checkpoint or from x itself (a library product of
+        the activations' type with fp32 sums)."""
         if isinstance(x, ssm.Ckpt8):
             return ssm.ssm_ckpt8_wgrad(g, x)
-        return g.flatten(0, -2).float().t() @ x.flatten(0, -2).float()
+        g, x = g.flatten(0, -2), x.flatten(0, -2)
+        return g.t() @ x if g.dtype == torch.float32 else torch.mm(g.t(), x, out_dtype=torch.float32)
 
     def backward(self, d_out, d_stream, kept):
         """(d_h, d_residual, gradients by name); d_stream: the gradient that reaches the stream past

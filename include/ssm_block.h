@@ -21,9 +21,9 @@
  *   e = E + 127,   q = round-to-nearest-even(v * 2^(6 - E)) limited to -127 .. 127,
  * and the value kept is q * 2^(E - 6): exact in bf16 and in fp32.  The error of a kept value is
  * at most 2^(E - 7), i.e. max |v| / 128 of its block (2^(E - 6) where |v| > 127 2^(E-6)).  A block
- * that holds an infinity or a NaN is kept as e = 255, q = 0 and reads back as NaN throughout.  A save writes e of
- * 7 .. 255; everything that reads a checkpoint takes any byte as q 2^(e - 133), so that one filled
- * with zeros holds zeros.
+ * that holds an infinity or a NaN is kept as e = 255, q = 0 and reads back as NaN throughout.  A save
+ * writes e of 7 .. 255; everything that reads a checkpoint takes any byte below 255 as q 2^(e - 133),
+ * so that one filled with zeros holds zeros.
  *
  * Ownership, streams and errors are those of ssm.h: caller-owned device pointers, nothing
  * allocated or synchronised, work enqueued on `stream`, argument errors found on the host before
