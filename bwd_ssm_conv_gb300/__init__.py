@@ -11,7 +11,8 @@ from .binding import (  # noqa: F401
     ssm_status_string,
 )
 from .block import (  # noqa: F401
-    AddNorm, Ckpt8, GatedNorm, ssm_add_norm_bwd, ssm_add_norm_fwd, ssm_ckpt8_load,
+    AddLayerNorm, AddNorm, Ckpt8, GatedNorm, ssm_add_layer_norm_bwd, ssm_add_layer_norm_fwd,
+    ssm_add_norm_bwd, ssm_add_norm_fwd, ssm_ckpt8_load,
     ssm_ckpt8_save, ssm_ckpt8_wgrad, ssm_ckpt8_wgrad_workspace_size, ssm_gated_norm_bwd,
     ssm_gated_norm_fwd, ssm_norm_bwd_workspace_size,
 )

@@ -27,7 +27,8 @@ SSM_NORM_FIRST = 1        # gated_norm: norm of y, then the gate
 SSM_WGRAD_ACCUMULATE = 1  # wgrad: add to d_W
 SSM_MAX_NORM_COLS = 32768
 
-EXPORTED = ("ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
+EXPORTED = ("ssm_add_norm_fwd", "ssm_add_norm_bwd", "ssm_add_layer_norm_fwd",
+            "ssm_add_layer_norm_bwd", "ssm_gated_norm_fwd", "ssm_gated_norm_bwd",
             "ssm_norm_bwd_workspace_size", "ssm_ckpt8_save", "ssm_ckpt8_load",
             "ssm_ckpt8_wgrad_workspace_size", "ssm_ckpt8_wgrad")
 
@@ -48,6 +49,16 @@ class Ckpt8(NamedTuple):
 class AddNorm(NamedTuple):
     out: torch.Tensor
     res_out: torch.Tensor | None
+    rstd: torch.Tensor | None
+    res8: Ckpt8 | None
+    x8: Ckpt8 | None
+    out8: Ckpt8 | None
+
+
+class AddLayerNorm(NamedTuple):
+    out: torch.Tensor
+    res_out: torch.Tensor | None
+    mean: torch.Tensor | None
     rstd: torch.Tensor | None
     res8: Ckpt8 | None
     x8: Ckpt8 | None
@@ -77,6 +88,11 @@ def lib():
                                        [_vp] * 8)
         L.ssm_add_norm_bwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll] +
                                        [_vp] * 5 + [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _sz, _vp])
+        L.ssm_add_layer_norm_fwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp, _ll, _vp,
+                                              _ll] + [_vp] * 9)
+        L.ssm_add_layer_norm_bwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll] +
+                                             [_vp] * 6 + [_vp, _ll, _vp, _ll, _vp, _vp, _vp, _vp,
+                                                          _sz, _vp])
         L.ssm_gated_norm_fwd.argtypes = [d, _vp, _ll, _vp, _ll, _vp, _vp, _ll] + [_vp] * 8
         L.ssm_gated_norm_bwd.argtypes = ([d, _vp, _ll, _vp, _ll, _vp, _vp, _vp, _ll, _vp, _vp,
                                           _vp, _vp, _vp, _ll, _vp, _ll, _vp, _vp, _sz, _vp])
@@ -148,6 +164,37 @@ def ssm_add_norm_bwd(d_out, res, rstd, w=None, d_res_out=None, scale=None, x=Non
     if type(r) is int:
         _check("ssm_add_norm_bwd", r)
     return {"d_res": r[0], "d_x": r[1], "d_w": r[2], "d_scale": r[3]} if out is None else out
+
+
+# ---- residual add + layer norm ----------------------------------------------------------------
+
+def ssm_add_layer_norm_fwd(x, w=None, b=None, residual=None, scale=None, eps=1e-5, res_dtype=None,
+                           save8=False, save_x8=False, save_out8=False, want_res=True,
+                           want_stats=True, out=None, stream=None) -> AddLayerNorm:
+    """s = residual + scale * x; out = w * (s - mean) / sqrt(mean((s - mean)^2) + eps) + b, per row of
+    x [..., cols]; mean and 1 / sqrt(...) are returned with ``want_stats``.  The other arguments are
+    those of ssm_add_norm_fwd."""
+    r = (_B or _calls()).add_layer_norm_fwd(x, w, residual, scale, eps, res_dtype, save8, save_x8,
+                                            save_out8, want_res, want_stats, out, stream, b)
+    if type(r) is int:
+        _check("ssm_add_layer_norm_fwd", r)
+    return AddLayerNorm(*r)
+
+
+def ssm_add_layer_norm_bwd(d_out, res, mean, rstd, w=None, d_res_out=None, scale=None, x=None,
+                           res_dtype=None, want_dres=True, want_dx=True, want_db=True, ws=None,
+                           out=None, stream=None) -> dict:
+    """Backward of ssm_add_layer_norm_fwd; returns {"d_res", "d_x", "d_w", "d_b", "d_scale"} (None
+    where not wanted or not applicable).  ``mean`` and ``rstd`` are the forward's, the other
+    arguments those of ssm_add_norm_bwd."""
+    into = out if out is None else (out["d_res"], out["d_x"], out["d_w"], out["d_scale"],
+                                    out["d_b"])
+    r = (_B or _calls()).add_layer_norm_bwd(d_out, res, rstd, w, d_res_out, scale, x, res_dtype,
+                                            want_dres, want_dx, ws, into, stream, mean, want_db)
+    if type(r) is int:
+        _check("ssm_add_layer_norm_bwd", r)
+    return ({"d_res": r[0], "d_x": r[1], "d_w": r[2], "d_b": r[4], "d_scale": r[3]} if out is None
+            else out)
 
 
 # ---- gated RMSNorm ----------------------------------------------------------------------------

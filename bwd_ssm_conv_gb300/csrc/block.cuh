@@ -54,9 +54,9 @@ NormShape norm_shape(long long rows, int group, int groups, bool vec, int sms, b
 
 // A backward's column sums: each block's own over its rows, [nbx][cols], then their sum.
 size_t column_sums_bytes(long long rows, int group, int groups, int sms, int sums);
-// out0 and out1 (either may be NULL) from part [sums][n][cols], in that order.
+// out0, out1 and out2 (any may be NULL) from part [sums][n][cols], in that order.
 cudaError_t launch_column_sums(const float* part, int n, int cols, float* out0, float* out1,
-                               cudaStream_t st);
+                               float* out2, cudaStream_t st);
 
 inline size_t slots_bytes(const RowPlan& p, int vec, int nj) {
   return p.rpb > 1 ? sizeof(float) * (size_t)p.threads * vec * nj : 0;
@@ -90,7 +90,7 @@ __device__ __forceinline__ void store_partial(float (&v)[NJ][VEC], const RowPlan
     if (okc[j]) st_cols(part + (long long)blockIdx.x * cols + col[j], v[j]);
 }
 
-// ---- add_norm -----------------------------------------------------------------------------------
+// ---- add_norm, add_layer_norm (which also has b, mean and d_b) ----------------------------------
 struct AddNormFwd {
   int rows, cols;
   float eps;
@@ -104,6 +104,8 @@ struct AddNormFwd {
   int ld_x, ld_residual, ld_out, ld_res_out;
   int8_t *res_q, *x_q, *out_q;
   uint8_t *res_e, *x_e, *out_e;
+  const float* b;
+  float* mean;
 };
 struct AddNormBwd {
   int rows, cols;
@@ -123,12 +125,19 @@ struct AddNormBwd {
   float* d_w;
   float* d_scale;
   float* part;
+  const float* mean_in;
+  float* d_b;
 };
 // vec: widths, strides and pointers allow 8 columns at a time
 cudaError_t launch_add_norm_fwd(const AddNormFwd& a, int io, int res_io, bool vec, int sms,
                                 cudaStream_t st);
 cudaError_t launch_add_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
                                 cudaStream_t st);
+
+cudaError_t launch_add_layer_norm_fwd(const AddNormFwd& a, int io, int res_io, bool vec, int sms,
+                                      cudaStream_t st);
+cudaError_t launch_add_layer_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
+                                      cudaStream_t st);
 
 // ---- gated_norm ---------------------------------------------------------------------------------
 struct GatedNormFwd {

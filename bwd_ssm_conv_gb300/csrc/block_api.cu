@@ -78,11 +78,13 @@ int status_of(cudaError_t e) { return e == cudaSuccess ? SSM_OK : SSM_ERR_CUDA; 
 
 extern "C" {
 
-int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
-                     const void* residual, long long ld_residual, const float* scale,
-                     const float* w, void* out, long long ld_out, void* res_out,
-                     long long ld_res_out, float* rstd, int8_t* res_q, uint8_t* res_e, int8_t* x_q,
-                     uint8_t* x_e, int8_t* out_q, uint8_t* out_e, void* stream) {
+// Both norms in front of a block: with b and mean, which the RMSNorm has not, the layer norm.
+static int add_norm_fwd(bool layer, const ssm_norm_desc* desc, const void* x, long long ld_x,
+                        const void* residual, long long ld_residual, const float* scale,
+                        const float* w, const float* b, void* out, long long ld_out, void* res_out,
+                        long long ld_res_out, float* mean, float* rstd, int8_t* res_q,
+                        uint8_t* res_e, int8_t* x_q, uint8_t* x_e, int8_t* out_q, uint8_t* out_e,
+                        void* stream) {
   int group;
   int rc = norm_check(desc, true, &group);
   if (rc != SSM_OK) return rc;
@@ -98,20 +100,43 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
   r.kept(out_q, out_e);
   r.f32(scale);
   r.f32(w);
-  if (!r.ok || (rstd && !aligned(rstd, 4))) return SSM_ERR_INVALID_ARG;
+  r.f32(b);
+  if (!r.ok || (rstd && !aligned(rstd, 4)) || (mean && !aligned(mean, 4)))
+    return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_x, ld_residual, ld_out, ld_res_out})
     if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
   ssm::AddNormFwd a{(int)desc->rows, desc->cols, desc->eps, x, residual, scale, w, out, res_out,
                     rstd, (int)ld_x, (int)ld_residual, (int)ld_out, (int)ld_res_out, res_q, x_q,
-                    out_q, res_e, x_e, out_e};
-  return status_of(ssm::launch_add_norm_fwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
+                    out_q, res_e, x_e, out_e, b, mean};
+  auto launch = layer ? ssm::launch_add_layer_norm_fwd : ssm::launch_add_norm_fwd;
+  return status_of(launch(a, io, rio, r.vec, sms, (cudaStream_t)stream));
+}
+
+int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
+                     const void* residual, long long ld_residual, const float* scale,
+                     const float* w, void* out, long long ld_out, void* res_out,
+                     long long ld_res_out, float* rstd, int8_t* res_q, uint8_t* res_e, int8_t* x_q,
+                     uint8_t* x_e, int8_t* out_q, uint8_t* out_e, void* stream) {
+  return add_norm_fwd(false, desc, x, ld_x, residual, ld_residual, scale, w, nullptr, out, ld_out,
+                      res_out, ld_res_out, nullptr, rstd, res_q, res_e, x_q, x_e, out_q, out_e,
+                      stream);
+}
+
+int ssm_add_layer_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
+                           const void* residual, long long ld_residual, const float* scale,
+                           const float* w, const float* b, void* out, long long ld_out,
+                           void* res_out, long long ld_res_out, float* mean, float* rstd,
+                           int8_t* res_q, uint8_t* res_e, int8_t* x_q, uint8_t* x_e, int8_t* out_q,
+                           uint8_t* out_e, void* stream) {
+  return add_norm_fwd(true, desc, x, ld_x, residual, ld_residual, scale, w, b, out, ld_out, res_out,
+                      ld_res_out, mean, rstd, res_q, res_e, x_q, x_e, out_q, out_e, stream);
 }
 
 size_t ssm_norm_bwd_workspace_size(const ssm_norm_desc* desc, int sums) {
   int group;
-  if (sums < 0 || sums > 2) return 0;
+  if (sums < 0 || sums > 3) return 0;
   if (norm_check(desc, false, &group) != SSM_OK && norm_check(desc, true, &group) != SSM_OK)
     return 0;
   const int sms = num_sms();
@@ -119,17 +144,19 @@ size_t ssm_norm_bwd_workspace_size(const ssm_norm_desc* desc, int sums) {
   return 256 + ssm::column_sums_bytes(desc->rows, group, desc->cols / group, sms, sums);
 }
 
-int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_d_out,
-                     const void* d_res_out, long long ld_d_res_out, const void* res,
-                     long long ld_res, const int8_t* res_q, const uint8_t* res_e, const void* x,
-                     long long ld_x, const int8_t* x_q, const uint8_t* x_e, const float* rstd,
-                     const float* scale, const float* w, void* d_res, long long ld_d_res,
-                     void* d_x, long long ld_d_x, float* d_w, float* d_scale, void* ws,
-                     size_t ws_bytes, void* stream) {
+static int add_norm_bwd(bool layer, const ssm_norm_desc* desc, const void* d_out,
+                        long long ld_d_out, const void* d_res_out, long long ld_d_res_out,
+                        const void* res, long long ld_res, const int8_t* res_q,
+                        const uint8_t* res_e, const void* x, long long ld_x, const int8_t* x_q,
+                        const uint8_t* x_e, const float* mean, const float* rstd,
+                        const float* scale, const float* w, void* d_res, long long ld_d_res,
+                        void* d_x, long long ld_d_x, float* d_w, float* d_b, float* d_scale,
+                        void* ws, size_t ws_bytes, void* stream) {
   int group;
   int rc = norm_check(desc, true, &group);
   if (rc != SSM_OK) return rc;
-  if (!d_out || !rstd || (!d_res && !d_x && !d_w && !d_scale)) return SSM_ERR_INVALID_ARG;
+  if (!d_out || !rstd || (layer && !mean) || (!d_res && !d_x && !d_w && !d_b && !d_scale))
+    return SSM_ERR_INVALID_ARG;
   if ((res != nullptr) == (res_q != nullptr)) return SSM_ERR_INVALID_ARG;  // one of the two
   if (x && x_q) return SSM_ERR_INVALID_ARG;
   if (d_scale && (!scale || (!x && !x_q))) return SSM_ERR_INVALID_ARG;
@@ -145,21 +172,48 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
   r.kept(x_q, x_e);
   r.f32(scale);
   r.f32(w);
-  if (!r.ok || !aligned(rstd, 4) || (d_w && !aligned(d_w, 4)) || (d_scale && !aligned(d_scale, 4)))
-    return SSM_ERR_INVALID_ARG;
+  if (!r.ok) return SSM_ERR_INVALID_ARG;
+  for (const float* p : {mean, rstd, (const float*)d_w, (const float*)d_b, (const float*)d_scale})
+    if (p && !aligned(p, 4)) return SSM_ERR_INVALID_ARG;
   for (long long ld : {ld_d_out, ld_d_res_out, ld_res, ld_x, ld_d_res, ld_d_x})
     if (ld > kMaxStride) return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;
-  const int sums = (d_w ? 1 : 0) + (d_scale ? 1 : 0);
+  const int sums = (d_w ? 1 : 0) + (d_b ? 1 : 0) + (d_scale ? 1 : 0);
   if (sums && (!ws || !aligned(ws, 256) ||
                ws_bytes < 256 + ssm::column_sums_bytes(desc->rows, group, 1, sms, sums)))
     return SSM_ERR_WORKSPACE;
   ssm::AddNormBwd a{(int)desc->rows, desc->cols, d_out, d_res_out, res, x, (int)ld_d_out,
                     (int)ld_d_res_out, (int)ld_res, (int)ld_x, res_q, x_q, res_e, x_e, rstd, scale,
                     w, d_res, d_x, (int)ld_d_res, (int)ld_d_x, d_w, d_scale,
-                    sums ? (float*)((char*)ws + 256) : nullptr};
-  return status_of(ssm::launch_add_norm_bwd(a, io, rio, r.vec, sms, (cudaStream_t)stream));
+                    sums ? (float*)((char*)ws + 256) : nullptr, mean, d_b};
+  auto launch = layer ? ssm::launch_add_layer_norm_bwd : ssm::launch_add_norm_bwd;
+  return status_of(launch(a, io, rio, r.vec, sms, (cudaStream_t)stream));
+}
+
+int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_d_out,
+                     const void* d_res_out, long long ld_d_res_out, const void* res,
+                     long long ld_res, const int8_t* res_q, const uint8_t* res_e, const void* x,
+                     long long ld_x, const int8_t* x_q, const uint8_t* x_e, const float* rstd,
+                     const float* scale, const float* w, void* d_res, long long ld_d_res,
+                     void* d_x, long long ld_d_x, float* d_w, float* d_scale, void* ws,
+                     size_t ws_bytes, void* stream) {
+  return add_norm_bwd(false, desc, d_out, ld_d_out, d_res_out, ld_d_res_out, res, ld_res, res_q,
+                      res_e, x, ld_x, x_q, x_e, nullptr, rstd, scale, w, d_res, ld_d_res, d_x,
+                      ld_d_x, d_w, nullptr, d_scale, ws, ws_bytes, stream);
+}
+
+int ssm_add_layer_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_d_out,
+                           const void* d_res_out, long long ld_d_res_out, const void* res,
+                           long long ld_res, const int8_t* res_q, const uint8_t* res_e,
+                           const void* x, long long ld_x, const int8_t* x_q, const uint8_t* x_e,
+                           const float* mean, const float* rstd, const float* scale,
+                           const float* w, void* d_res, long long ld_d_res, void* d_x,
+                           long long ld_d_x, float* d_w, float* d_b, float* d_scale, void* ws,
+                           size_t ws_bytes, void* stream) {
+  return add_norm_bwd(true, desc, d_out, ld_d_out, d_res_out, ld_d_res_out, res, ld_res, res_q,
+                      res_e, x, ld_x, x_q, x_e, mean, rstd, scale, w, d_res, ld_d_res, d_x, ld_d_x,
+                      d_w, d_b, d_scale, ws, ws_bytes, stream);
 }
 
 int ssm_gated_norm_fwd(const ssm_norm_desc* desc, const void* y, long long ld_y, const void* z,

@@ -303,13 +303,11 @@ template <typename F> int call(F f) {
 // SSM_OK.
 #define SSM_FUNCTION(name) PyObject* name(PyObject*, PyObject* const* a, Py_ssize_t n)
 
-// x, w, residual, scale, eps, res_dtype, save8, save_x8, save_out8, want_res, want_rstd, out, stream
-SSM_FUNCTION(add_norm_fwd) {
-  HANDLE_TH_ERRORS
-  args_are(n, 13);
+// Both norms in front of a block; the layer norm has b besides, and a mean beside its rstd.
+PyObject* add_norm_fwd_of(bool layer, PyObject* const* a, PyObject* ob) {
   const Tensor& x = needed(a[0], "x");
   const Tensor *w = tensor(a[1], "w"), *residual = tensor(a[2], "residual"),
-               *scale = tensor(a[3], "scale");
+               *scale = tensor(a[3], "scale"), *b = layer ? tensor(ob, "b") : nullptr;
   const int io = io_of(x, "x");
   const IntArrayRef shape = x.sizes();
   const int64_t cols = columns(x, "x");
@@ -326,10 +324,10 @@ SSM_FUNCTION(add_norm_fwd) {
     outs_are(a[11], 2, "(out, res_out)");
     go = tensor(PyTuple_GET_ITEM(a[11], 0), "out"), gr = tensor(PyTuple_GET_ITEM(a[11], 1), "res_out");
   }
-  together({&x, "x"}, {{w, "w"}, {residual, "residual"}, {scale, "scale"}, {go, "out"},
+  together({&x, "x"}, {{w, "w"}, {b, "b"}, {residual, "residual"}, {scale, "scale"}, {go, "out"},
                        {gr, "res_out"}});
   const Rows rx(&x, "x"), rr(residual, "residual", shape, rdt);
-  const float *ps = f32(scale, "scale", cols), *pw = f32(w, "w", cols);
+  const float *ps = f32(scale, "scale", cols), *pw = f32(w, "w", cols), *pb = f32(b, "b", cols);
   const On on(a[12], x);
   Tensor o, res;
   Rows ro, rs;
@@ -345,33 +343,54 @@ SSM_FUNCTION(add_norm_fwd) {
       rs.p = res.data_ptr();
     }
   }
-  Tensor rstd;
-  if (yes(a[10])) rstd = make(shape.slice(0, shape.size() - 1), at::kFloat, x);
+  Tensor rstd, mean;
+  if (yes(a[10])) {
+    rstd = make(shape.slice(0, shape.size() - 1), at::kFloat, x);
+    if (layer) mean = make(shape.slice(0, shape.size() - 1), at::kFloat, x);
+  }
   const NewCkpt8 res8(yes(a[6]), x), x8(yes(a[7]), x), out8(yes(a[8]), x);
   const ssm_norm_desc d =
       norm_desc(rows_in(x, cols), cols, 0, io, io_code(rdt), 0, number(a[4]));
-  on.made({&rstd, &res8.q, &res8.e, &x8.q, &x8.e, &out8.q, &out8.e});
+  on.made({&rstd, &mean, &res8.q, &res8.e, &x8.q, &x8.e, &out8.q, &out8.e});
   if (!given) on.made({&o, &res});
   const int rc = call([&] {
+    if (layer)
+      return ssm_add_layer_norm_fwd(&d, rx.p, rx.ld, rr.p, rr.ld, ps, pw, pb, ro.p, ro.ld, rs.p,
+                                    rs.ld, ptr<float>(mean), ptr<float>(rstd), res8.pq(), res8.pe(),
+                                    x8.pq(), x8.pe(), out8.pq(), out8.pe(), on.raw);
     return ssm_add_norm_fwd(&d, rx.p, rx.ld, rr.p, rr.ld, ps, pw, ro.p, ro.ld, rs.p, rs.ld,
                             ptr<float>(rstd), res8.pq(), res8.pe(), x8.pq(), x8.pe(), out8.pq(),
                             out8.pe(), on.raw);
   });
   if (rc) return PyLong_FromLong(rc);
+  if (layer)
+    return pack({give(o), give(res), give(mean), give(rstd), give(res8), give(x8), give(out8)});
   return pack({give(o), give(res), give(rstd), give(res8), give(x8), give(out8)});
+}
+
+// x, w, residual, scale, eps, res_dtype, save8, save_x8, save_out8, want_res, want_rstd, out, stream
+SSM_FUNCTION(add_norm_fwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 13);
+  return add_norm_fwd_of(false, a, nullptr);
+  END_HANDLE_TH_ERRORS
+}
+// the same (want_rstd: of the mean too), then b
+SSM_FUNCTION(add_layer_norm_fwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 14);
+  return add_norm_fwd_of(true, a, a[13]);
   END_HANDLE_TH_ERRORS
 }
 
-// d_out, res, rstd, w, d_res_out, scale, x, res_dtype, want_dres, want_dx, ws, out, stream
-SSM_FUNCTION(add_norm_bwd) {
-  HANDLE_TH_ERRORS
-  args_are(n, 13);
+PyObject* add_norm_bwd_of(bool layer, PyObject* const* a, PyObject* omean, PyObject* want_db) {
   const Tensor& d_out = needed(a[0], "d_out");
   const Pair res8(a[1], "res"), x8(a[6], "x");
   const Tensor *res = res8.q ? nullptr : &needed(a[1], "res"),
                *x = x8.q ? nullptr : tensor(a[6], "x");
   const Tensor *rstd = tensor(a[2], "rstd"), *w = tensor(a[3], "w"),
-               *up = tensor(a[4], "d_res_out"), *scale = tensor(a[5], "scale");
+               *up = tensor(a[4], "d_res_out"), *scale = tensor(a[5], "scale"),
+               *mean = layer ? &needed(omean, "mean") : nullptr;
   const int io = io_of(d_out, "d_out");
   const IntArrayRef shape = d_out.sizes();
   const ScalarType dt = d_out.scalar_type();
@@ -385,23 +404,26 @@ SSM_FUNCTION(add_norm_bwd) {
     TORCH_CHECK_TYPE(THPDtype_Check(a[7]), "res_dtype must be a torch.dtype");
     rdt = reinterpret_cast<THPDtype*>(a[7])->scalar_type;
   }
-  Tensor g[4];  // d_res, d_x, d_w, d_scale
+  Tensor g[5];  // d_res, d_x, d_w, d_scale, d_b
+  const int outs = layer ? 5 : 4;
   const bool given = a[11] != Py_None;
   if (given) {
-    outs_are(a[11], 4, "d_res, d_x, d_w and d_scale");
-    for (int i = 0; i < 4; i++)
+    outs_are(a[11], outs, layer ? "d_res, d_x, d_w, d_scale and d_b" :
+                                  "d_res, d_x, d_w and d_scale");
+    for (int i = 0; i < outs; i++)
       if (const Tensor* t = tensor(PyTuple_GET_ITEM(a[11], i), "out")) g[i] = *t;
   }
   const Tensor* given_ws = tensor(a[10], "ws");
   together({&d_out, "d_out"},
-           {{res, "res"}, {res8.q, "res"}, {res8.e, "res"}, {rstd, "rstd"}, {w, "w"},
+           {{res, "res"}, {res8.q, "res"}, {res8.e, "res"}, {mean, "mean"}, {rstd, "rstd"}, {w, "w"},
             {up, "d_res_out"}, {scale, "scale"}, {x, "x"}, {x8.q, "x"}, {x8.e, "x"}, some(g[0], "d_res"),
-            some(g[1], "d_x"), some(g[2], "d_w"), some(g[3], "d_scale"), {given_ws, "ws"}});
+            some(g[1], "d_x"), some(g[2], "d_w"), some(g[3], "d_scale"), some(g[4], "d_b"),
+            {given_ws, "ws"}});
   const Rows rd(&d_out, "d_out"), ru(up, "d_res_out", shape, rdt), rr(res, "res", shape, rdt);
   const Kept kr = kept(res8, "res", shape);
   const Rows rx(x, "x", shape, dt);
   const Kept kx = kept(x8, "x", shape);
-  const float *pr = f32(rstd, "rstd", rows), *ps = f32(scale, "scale", cols),
+  const float *pm = f32(mean, "mean", rows), *pr = f32(rstd, "rstd", rows), *ps = f32(scale, "scale", cols),
               *pw = f32(w, "w", cols);
   const On on(a[12], d_out);
   Rows go, gx;
@@ -410,23 +432,45 @@ SSM_FUNCTION(add_norm_bwd) {
     if (g[1].defined()) gx = Rows(&g[1], "d_x", shape, dt);
     if (g[2].defined()) f32(&g[2], "d_w", cols);
     if (g[3].defined()) f32(&g[3], "d_scale", cols);
+    if (g[4].defined()) f32(&g[4], "d_b", cols);
   } else {
     if (yes(a[8])) g[0] = make(shape, rdt, d_out), go.p = g[0].data_ptr();
     if (yes(a[9])) g[1] = make(shape, dt, d_out), gx.p = g[1].data_ptr();
     if (w) g[2] = make(w->sizes(), at::kFloat, d_out);
     if (scale && (x || x8.q)) g[3] = make(scale->sizes(), at::kFloat, d_out);
+    if (layer && yes(want_db)) g[4] = make({cols}, at::kFloat, d_out);
   }
   const ssm_norm_desc d = norm_desc(rows, cols, 0, io, io_code(rdt), 0, 1.0);
-  const int sums = g[2].defined() + g[3].defined();
+  const int sums = g[2].defined() + g[3].defined() + g[4].defined();
   const Workspace ws(sums ? ssm_norm_bwd_workspace_size(&d, sums) : 0, given_ws, d_out);
-  if (!given) on.made({&g[0], &g[1], &g[2], &g[3]});
+  if (!given) on.made({&g[0], &g[1], &g[2], &g[3], &g[4]});
   const int rc = call([&] {
+    if (layer)
+      return ssm_add_layer_norm_bwd(&d, rd.p, rd.ld, ru.p, ru.ld, rr.p, rr.ld, kr.q, kr.e, rx.p,
+                                    rx.ld, kx.q, kx.e, pm, pr, ps, pw, go.p, go.ld, gx.p, gx.ld,
+                                    ptr<float>(g[2]), ptr<float>(g[4]), ptr<float>(g[3]), ws.p,
+                                    ws.bytes, on.raw);
     return ssm_add_norm_bwd(&d, rd.p, rd.ld, ru.p, ru.ld, rr.p, rr.ld, kr.q, kr.e, rx.p, rx.ld,
                             kx.q, kx.e, pr, ps, pw, go.p, go.ld, gx.p, gx.ld, ptr<float>(g[2]),
                             ptr<float>(g[3]), ws.p, ws.bytes, on.raw);
   });
   if (rc) return PyLong_FromLong(rc);
+  if (layer) return pack({give(g[0]), give(g[1]), give(g[2]), give(g[3]), give(g[4])});
   return pack({give(g[0]), give(g[1]), give(g[2]), give(g[3])});
+}
+
+// d_out, res, rstd, w, d_res_out, scale, x, res_dtype, want_dres, want_dx, ws, out, stream
+SSM_FUNCTION(add_norm_bwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 13);
+  return add_norm_bwd_of(false, a, nullptr, nullptr);
+  END_HANDLE_TH_ERRORS
+}
+// the same, then mean, want_db
+SSM_FUNCTION(add_layer_norm_bwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 15);
+  return add_norm_bwd_of(true, a, a[13], a[14]);
   END_HANDLE_TH_ERRORS
 }
 
@@ -642,6 +686,8 @@ PyObject* use_ckpt8(PyObject*, PyObject* type) {
   {#name, (PyCFunction)(void (*)(void))name, METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {SSM_METHOD(add_norm_fwd),
                          SSM_METHOD(add_norm_bwd),
+                         SSM_METHOD(add_layer_norm_fwd),
+                         SSM_METHOD(add_layer_norm_bwd),
                          SSM_METHOD(gated_norm_fwd),
                          SSM_METHOD(gated_norm_bwd),
                          SSM_METHOD(ckpt8_save),

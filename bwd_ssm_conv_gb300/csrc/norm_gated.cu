@@ -299,7 +299,7 @@ cudaError_t bwd_types(const GatedNormBwd& a, bool vec, int sms, cudaStream_t st)
   SSM_NORM_BWD_SWITCH(s.variant, SSM_LAUNCH)
 #undef SSM_LAUNCH
   if (e != cudaSuccess || !a.d_w) return e;
-  return launch_column_sums(a.part, s.plan.nbx, a.cols, a.d_w, nullptr, st);
+  return launch_column_sums(a.part, s.plan.nbx, a.cols, a.d_w, nullptr, nullptr, st);
 }
 
 }  // namespace

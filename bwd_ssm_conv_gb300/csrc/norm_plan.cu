@@ -18,10 +18,12 @@ constexpr int kFewRows = 4;
 // that this one starts at its end) and it waits here for that one's results: 2 - 3 us less per
 // backward than an ordinary launch (8192 x 512 fp32, forward and backward: 34.9 and 37.6 us).
 __global__ void __launch_bounds__(1024) column_sums_kernel(const float* part, int n, int cols,
-                                                           float* out0, float* out1) {
+                                                           float* out0, float* out1,
+                                                           float* out2) {
   __shared__ float s[128][33];
   const int tx = threadIdx.x & 7, ty = threadIdx.x >> 3, c = blockIdx.x * 32 + 4 * tx;
-  float* out = blockIdx.y == 0 && out0 ? out0 : out1;
+  int nth = blockIdx.y;  // of the outputs that are given
+  float* out = out0 && nth-- == 0 ? out0 : out1 && nth-- == 0 ? out1 : out2;
   part += (long long)blockIdx.y * n * cols;
   asm volatile("griddepcontrol.wait;" ::: "memory");
   float v[4] = {};
@@ -108,9 +110,9 @@ size_t column_sums_bytes(long long rows, int group, int groups, int sms, int sum
 }
 
 cudaError_t launch_column_sums(const float* part, int n, int cols, float* out0, float* out1,
-                               cudaStream_t st) {
+                               float* out2, cudaStream_t st) {
   cudaLaunchConfig_t c{};
-  c.gridDim = dim3((cols + 31) / 32, (out0 ? 1 : 0) + (out1 ? 1 : 0));
+  c.gridDim = dim3((cols + 31) / 32, (out0 ? 1 : 0) + (out1 ? 1 : 0) + (out2 ? 1 : 0));
   c.blockDim = dim3(1024);
   c.stream = st;
   cudaLaunchAttribute at{};
@@ -118,7 +120,7 @@ cudaError_t launch_column_sums(const float* part, int n, int cols, float* out0, 
   at.val.programmaticStreamSerializationAllowed = 1;
   c.attrs = &at;
   c.numAttrs = 1;
-  const cudaError_t e = cudaLaunchKernelEx(&c, column_sums_kernel, part, n, cols, out0, out1);
+  const cudaError_t e = cudaLaunchKernelEx(&c, column_sums_kernel, part, n, cols, out0, out1, out2);
   count_launches(1);
   return e;
 }

@@ -100,11 +100,12 @@ __device__ __forceinline__ void st_cols(float* p, const Cols<float, 8>& c) { st_
 __device__ __forceinline__ void st_cols(__nv_bfloat16* p, const Cols<__nv_bfloat16, 8>& c) {
   *reinterpret_cast<uint4*>(p) = c.a;
 }
-// fp32 parameters of VEC columns (1 where there are none), 16-byte aligned for VEC = 8.
+// fp32 parameters of VEC columns (`none` where there are none), 16-byte aligned for VEC = 8.
 template <int VEC>
-__device__ __forceinline__ void ld_param(const float* p, int col, bool ok, float (&v)[VEC]) {
+__device__ __forceinline__ void ld_param(const float* p, int col, bool ok, float (&v)[VEC],
+                                         float none = 1.0f) {
 #pragma unroll
-  for (int i = 0; i < VEC; i++) v[i] = 1.0f;
+  for (int i = 0; i < VEC; i++) v[i] = none;
   if (ok && p) {
     if constexpr (VEC == 1) {
       v[0] = __ldg(p + col);
@@ -334,6 +335,30 @@ __device__ __forceinline__ float row_sum(float v, int tpr, float (*part)[32], in
   float s = 0.0f;
   for (int w = 0; w < tpr >> 5; w++) s += part[half][w];
   return s;
+}
+
+// Two such sums at once, in place.
+__device__ __forceinline__ void row_sum2(float& v, float& u, int tpr, float (*part)[32],
+                                         float (*part2)[32], int half) {
+  if (tpr <= 32) {
+    for (int off = tpr >> 1; off > 0; off >>= 1) {
+      v += __shfl_xor_sync(0xffffffffu, v, off);
+      u += __shfl_xor_sync(0xffffffffu, u, off);
+    }
+    return;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    v += __shfl_xor_sync(0xffffffffu, v, off);
+    u += __shfl_xor_sync(0xffffffffu, u, off);
+  }
+  if ((threadIdx.x & 31) == 0) {
+    part[half][threadIdx.x >> 5] = v;
+    part2[half][threadIdx.x >> 5] = u;
+  }
+  __syncthreads();
+  v = u = 0.0f;
+  for (int w = 0; w < tpr >> 5; w++) v += part[half][w], u += part2[half][w];
 }
 
 // ---- rows ahead ---------------------------------------------------------------------------------

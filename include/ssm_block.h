@@ -4,6 +4,9 @@
  *
  *   add_norm    s   = residual + scale * x            (residual and scale optional)
  *               out = w * s * rstd,   rstd = 1 / sqrt(mean(s^2) + eps)
+ *   add_layer_norm
+ *               s   = residual + scale * x            (residual and scale optional)
+ *               out = w * (s - mean) * rstd + b,   rstd = 1 / sqrt(mean((s - mean)^2) + eps)
  *   gated_norm  per group of columns:
  *               v   = y * silu(z),  out = w * v * rstd(v)              (gate first, the default)
  *               out = w * y * rstd(y) * silu(z)                        (SSM_NORM_FIRST)
@@ -13,7 +16,7 @@
  * Layouts: row-major; a row is a token, `cols` channels each.  Activations may be strided by
  * row: `ld_*` is the row stride in elements (0 means cols; at least cols otherwise), so that a
  * tensor may be a slice of a wider one (the gate's half of an input projection).  Parameters w,
- * scale and their gradients are fp32 [cols]; rstd is fp32 [rows][cols / group].
+ * b, scale and their gradients are fp32 [cols]; mean and rstd are fp32 [rows][cols / group].
  *
  * 8-bit checkpoints ("ckpt8"): q int8 [rows][cols] and e uint8 [rows][ceil(cols / 32)], both
  * contiguous.  Block j of a row holds columns 32 j .. 32 j + 31.  With E = floor(log2(max |v|))
@@ -79,7 +82,7 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
                      uint8_t* x_e, int8_t* out_q, uint8_t* out_e, void* stream);
 
 /* Bytes of scratch the norms' backward needs for `sums` column sums (add_norm: 1, or 2 with
- * d_scale; gated_norm: 1) on the current device; 0 if the arguments are invalid. */
+ * d_scale; add_layer_norm: one for each of d_w, d_b and d_scale; gated_norm: 1) on the current device; 0 if the arguments are invalid. */
 size_t ssm_norm_bwd_workspace_size(const ssm_norm_desc* desc, int sums);
 
 /* Backward.  Required: d_out, rstd (the forward's), and s as either res (the forward's res_out)
@@ -95,6 +98,28 @@ int ssm_add_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_
                      const float* scale, const float* w, void* d_res, long long ld_d_res,
                      void* d_x, long long ld_d_x, float* d_w, float* d_scale, void* ws,
                      size_t ws_bytes, void* stream);
+
+/* ---- residual add + layer norm (before a block, or before the head) -------------------------
+ * As ssm_add_norm_fwd, with an optional b, and mean and rstd as two optional outputs. */
+int ssm_add_layer_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
+                           const void* residual, long long ld_residual, const float* scale,
+                           const float* w, const float* b, void* out, long long ld_out,
+                           void* res_out, long long ld_res_out, float* mean, float* rstd,
+                           int8_t* res_q, uint8_t* res_e, int8_t* x_q, uint8_t* x_e, int8_t* out_q,
+                           uint8_t* out_e, void* stream);
+
+/* As ssm_add_norm_bwd; mean and rstd (the forward's) are both required, d_b is optional.
+ *   n = (s - mean) rstd,  a = w d_out,  r = d_res_out + rstd (a - mean(a) - n mean(a n)),
+ *   d_res = r,  d_x = scale r,  d_w = sum_rows d_out n,  d_b = sum_rows d_out,
+ *   d_scale = sum_rows r x */
+int ssm_add_layer_norm_bwd(const ssm_norm_desc* desc, const void* d_out, long long ld_d_out,
+                           const void* d_res_out, long long ld_d_res_out, const void* res,
+                           long long ld_res, const int8_t* res_q, const uint8_t* res_e,
+                           const void* x, long long ld_x, const int8_t* x_q, const uint8_t* x_e,
+                           const float* mean, const float* rstd, const float* scale,
+                           const float* w, void* d_res, long long ld_d_res, void* d_x,
+                           long long ld_d_x, float* d_w, float* d_b, float* d_scale, void* ws,
+                           size_t ws_bytes, void* stream);
 
 /* ---- gated RMSNorm (after the scan) --------------------------------------------------------
  * Forward.  Required: y, z, out.  Optional: w, rstd, checkpoints of y, z and out, each by itself (a
