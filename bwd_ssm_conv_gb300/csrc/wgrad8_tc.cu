@@ -40,9 +40,8 @@
 // Measured (GB300): g 16384 x 4096, X 16384 x 1024: 88 us, 1565 TFLOP/s (82 % of the measured bf16
 // peak on 128 of 152 SMs); MMAs alone 78 us.  g 32768 x 768, X 32768 x 1536: 52 us.
 #include "block.cuh"
+#include "pair.cuh"
 #include "rows.cuh"
-#include "tma.cuh"
-#include "tmem.cuh"
 
 namespace ssm {
 
@@ -92,110 +91,6 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
   d |= (uint64_t)1 << 46;
   d |= (uint64_t)2 << 61;
   return d;
-}
-
-template <int CG> struct Mma {
-  // D fp32, A and B bf16, both MN-major, 128 CG x 256
-  static constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (1u << 15) | (1u << 16) |
-                                    ((uint32_t)(kTN >> 3) << 17) |
-                                    ((uint32_t)(kTM * CG >> 4) << 24);
-  static __device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, bool accumulate) {
-    if constexpr (CG == 1)
-      asm volatile(
-          "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-          "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-          "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
-          : "memory");
-    else
-      asm volatile(
-          "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-          "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d),
-          "l"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
-          : "memory");
-  }
-  // Arrives on `bar` (of both CTAs) once the MMAs issued before have completed.
-  static __device__ __forceinline__ void commit(uint64_t* bar) {
-    if constexpr (CG == 1)
-      tc::mma_commit(bar);
-    else
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
-          "[%0], %1;" ::"r"(smem_u32(bar)),
-          "h"((uint16_t)3)
-          : "memory");
-  }
-  static __device__ __forceinline__ void commit_here(uint64_t* bar) {  // of this CTA only
-    if constexpr (CG == 1)
-      tc::mma_commit(bar);
-    else
-      asm volatile(
-          "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-              smem_u32(bar))
-          : "memory");
-  }
-  static __device__ __forceinline__ void alloc(uint32_t* dst) {
-    if constexpr (CG == 1) {
-      tmem_alloc(dst, kTmCols);
-    } else {
-      asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                       smem_u32(dst)),
-                   "r"(kTmCols)
-                   : "memory");
-      asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
-    }
-  }
-  static __device__ __forceinline__ void dealloc(uint32_t t) {
-    if constexpr (CG == 1)
-      tmem_dealloc(t, kTmCols);
-    else
-      asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(t), "r"(kTmCols)
-                   : "memory");
-  }
-};
-
-__device__ __forceinline__ void mbar_arrive(uint64_t* bar) {
-  asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(smem_u32(bar))
-               : "memory");
-}
-// The first CTA's barrier at the same place, and an arrival there.
-template <int CG> __device__ __forceinline__ uint32_t bar_of_first(uint64_t* bar) {
-  uint32_t a = smem_u32(bar);
-  if constexpr (CG > 1) asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(a));
-  return a;
-}
-template <int CG> __device__ __forceinline__ void mbar_arrive_first(uint32_t bar) {
-  if constexpr (CG == 1)
-    asm volatile("{ .reg .b64 st; mbarrier.arrive.shared::cta.b64 st, [%0]; }" ::"r"(bar) : "memory");
-  else
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
-}
-// One lane of a converged warp, in a form that the compiler knows to be a single one.
-__device__ __forceinline__ bool elect_one() {
-  uint32_t p;
-  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(p));
-  return p != 0;
-}
-// Where an agent stands in the ring of stages: the slot, and the parity of its current use.
-template <int S> struct Ring {
-  int s = 0;
-  uint32_t phase = 0;
-  __device__ __forceinline__ void next() {
-    if (++s == S) s = 0, phase ^= 1;
-  }
-};
-// This kernel may start while the one before it in the call runs (wgrad8.cu): here its results are
-// complete, also for TMA.
-__device__ __forceinline__ void wait_for_copies() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  asm volatile("fence.proxy.async.global;" ::: "memory");
-}
-template <int CG> __device__ __forceinline__ void sync_tile() {  // every thread of the tile's CTAs
-  if constexpr (CG == 1) {
-    __syncthreads();
-  } else {
-    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
-  }
 }
 
 __device__ __forceinline__ uint4 lds128(uint32_t a) {
@@ -333,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
     prefetch_tmap(&a.q);
   }
   __syncwarp();
-  if (warp == 1) Mma<CG>::alloc(&tbase);
+  if (warp == 1) Mma<CG>::alloc(&tbase, kTmCols);
   tmem_fence_before_sync();
   __syncthreads();
   sync_tile<CG>();
@@ -387,6 +282,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
       // Only the address in a descriptor's low word changes: 16 tokens on, 2048 bytes (>> 4: 128).
       Ring<S> r;
       const uint64_t desc0 = desc_mn(smem_u32(smem));
+      constexpr uint32_t idesc = idesc_bf16(kTM * CG, kTN, true, true);
       int it = 0;
       for (int seg = 0; seg < segs; seg++) {
         const uint32_t d = tm + (seg & 1) * kTN;
@@ -400,10 +296,10 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
           tmem_fence_after_sync();
           if (ok && elect_one()) {
             const uint64_t da = desc0 + (uint32_t)(r.s * (L::stage >> 4)), db = da + (kBytesA >> 4);
-            Mma<CG>::mma(d, da, db, !first);
+            Mma<CG>::mma(idesc, d, da, db, !first);
 #pragma unroll
             for (int kk = 1; kk < kTT / 16; kk++)
-              Mma<CG>::mma(d, da + 128 * kk, db + 128 * kk, true);
+              Mma<CG>::mma(idesc, d, da + 128 * kk, db + 128 * kk, true);
             Mma<CG>::commit(&empty[r.s]);
           }
           __syncwarp();
@@ -565,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) wgrad8_tc_kernel(const __grid_con
   sync_tile<CG>();  // the other CTA may still arrive on barriers here
   if (warp == 1) {
     tmem_fence_after_sync();
-    Mma<CG>::dealloc(tm);
+    Mma<CG>::dealloc(tm, kTmCols);
   }
   if (tid == 0) {
     wait_for_copies();  // the kernel before clears the status; this one does not end ahead of it
