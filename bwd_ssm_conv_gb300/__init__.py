@@ -16,3 +16,7 @@ from .block import (  # noqa: F401
     ssm_ckpt8_save, ssm_ckpt8_wgrad, ssm_ckpt8_wgrad_workspace_size, ssm_gated_norm_bwd,
     ssm_gated_norm_fwd, ssm_norm_bwd_workspace_size,
 )
+from .head import (  # noqa: F401
+    HeadLoss, ssm_head_ce_bwd, ssm_head_ce_fwd, ssm_head_distill_bwd, ssm_head_distill_fwd,
+    ssm_head_workspace_size,
+)

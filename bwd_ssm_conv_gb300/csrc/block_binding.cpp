@@ -1,5 +1,5 @@
-// block_binding.cpp -- the Python module behind block.py: takes PyTorch tensors apart, checks what
-// the C ABI (ssm_block.h) cannot see, makes the results and calls the entry point on the stream.
+// block_binding.cpp -- the Python module behind block.py and head.py: takes PyTorch tensors apart, checks
+// what the C ABI (ssm_block.h, ssm_head.h) cannot see, makes the results and calls the entry point on the stream.
 // No computation happens here.
 //
 // The host is all that bounds a call for a token or a small layer, so the marshalling is compiled:
@@ -21,6 +21,7 @@
 
 #include "ssm.h"
 #include "ssm_block.h"
+#include "ssm_head.h"
 
 namespace {
 
@@ -670,6 +671,172 @@ SSM_FUNCTION(ckpt8_wgrad) {
   END_HANDLE_TH_ERRORS
 }
 
+// ---- the head and its loss ------------------------------------------------------------------------
+// A contiguous tensor of int64, of a shape.
+const int64_t* words(const Tensor& t, const char* name, IntArrayRef shape) {
+  TORCH_CHECK_TYPE(t.scalar_type() == at::kLong, name, " must be int64, got ", t.scalar_type());
+  TORCH_CHECK_VALUE(t.is_cuda() && t.is_contiguous() && t.sizes() == shape, name,
+                    " must be a contiguous CUDA tensor of shape ", shape, ", got ", t.sizes());
+  return t.const_data_ptr<int64_t>();
+}
+// What the four calls share: h [..., cols], w [vocab, cols], and what the rows should say, a target each
+// (target, ignore_index) or a teacher's entries (t_idx, t_logit, temperature).
+struct Head {
+  const Tensor &h, &w, &said;
+  const Tensor* t_logit;
+  ssm_head_desc d{};
+  Rows rh, rw;
+  const int64_t* idx;
+  const void* logit = nullptr;
+  IntArrayRef lead;  // the shape of a row's values
+  Head(bool distill, PyObject* const* a)
+      : h(needed(a[0], "h")), w(needed(a[1], "w")), said(needed(a[2], distill ? "t_idx" : "target")),
+        t_logit(distill ? &needed(a[3], "t_logit") : nullptr) {
+    d.io = io_of(h, "h");
+    const int64_t cols = columns(h, "h");
+    TORCH_CHECK_VALUE(w.dim() == 2, "w must have two dimensions (vocabulary, columns)");
+    lead = h.sizes().slice(0, h.sizes().size() - 1);
+    d.rows = rows_in(h, cols);
+    d.cols = in_int(cols), d.vocab = in_int(w.size(0));
+    if (distill) {
+      d.entries = in_int(columns(said, "t_idx"));
+      d.entry_io = io_of(*t_logit, "t_logit");
+      d.temperature = (float)number(a[4]);
+    } else {
+      d.ignore_index = integer(a[3]);
+    }
+  }
+  static int in_int(int64_t v) { return v > 0x7fffffff || v < 0 ? -1 : (int)v; }
+  // Once it is known that every tensor lies on one GPU.
+  void take(bool distill) {
+    const int64_t cols = h.size(-1), want_w[2] = {w.size(0), cols};
+    rh = Rows(&h, "h");
+    rw = Rows(&w, "w", want_w, h.scalar_type());
+    if (distill) {
+      at::DimVector shape(lead.begin(), lead.end());
+      shape.push_back(said.size(-1));
+      idx = words(said, "t_idx", shape);
+      TORCH_CHECK_VALUE(t_logit->is_contiguous() && t_logit->sizes() == IntArrayRef(shape),
+                        "t_logit must be contiguous and of t_idx's shape ", IntArrayRef(shape), ", got ",
+                        t_logit->sizes());
+      logit = t_logit->data_ptr();
+    } else {
+      idx = words(said, "target", lead);
+    }
+  }
+  // W's rows can be read as they lie
+  int aligned() const {
+    const uintptr_t row = (uintptr_t)(rw.ld ? rw.ld : d.cols) * w.element_size();
+    return !(((uintptr_t)rw.p | row) & 15);
+  }
+};
+
+// h, w, then target, ignore_index or t_idx, t_logit, temperature, then ws, out, stream, flags
+PyObject* head_fwd_of(bool distill, PyObject* const* a) {
+  Head x(distill, a);
+  PyObject* const* rest = a + (distill ? 5 : 4);
+  const Tensor* given_ws = tensor(rest[0], "ws");
+  const bool given = rest[1] != Py_None;
+  Tensor loss, lse;
+  if (given) {
+    outs_are(rest[1], 2, "(loss, lse)");
+    loss = needed(PyTuple_GET_ITEM(rest[1], 0), "loss");
+    if (const Tensor* t = tensor(PyTuple_GET_ITEM(rest[1], 1), "lse")) lse = *t;
+  }
+  x.d.flags = (unsigned)integer(rest[3]);
+  together({&x.h, "h"}, {{&x.w, "w"}, {&x.said, distill ? "t_idx" : "target"}, {x.t_logit, "t_logit"},
+                         {given_ws, "ws"}, some(loss, "loss"), some(lse, "lse")});
+  x.take(distill);
+  if (given) {
+    f32(&loss, "loss", x.d.rows);
+    if (lse.defined()) f32(&lse, "lse", x.d.rows);
+  }
+  const On on(rest[2], x.h);
+  if (!given) loss = make(x.lead, at::kFloat, x.h), lse = make(x.lead, at::kFloat, x.h);
+  const Workspace ws(ssm_head_workspace_size(&x.d, 0, x.aligned()), given_ws, x.h);
+  if (!given) on.made({&loss, &lse});
+  const int rc = call([&] {
+    if (distill)
+      return ssm_head_distill_fwd(&x.d, x.rh.p, x.rh.ld, x.rw.p, x.rw.ld, x.idx, x.logit,
+                                  ptr<float>(loss), ptr<float>(lse), ws.p, ws.bytes, on.raw);
+    return ssm_head_ce_fwd(&x.d, x.rh.p, x.rh.ld, x.rw.p, x.rw.ld, x.idx, ptr<float>(loss),
+                           ptr<float>(lse), ws.p, ws.bytes, on.raw);
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return pack({give(loss), give(lse)});
+}
+
+// h, w, then target, ignore_index or t_idx, t_logit, temperature, then lse, d_loss, want_dh, want_dw, ws,
+// out, stream, flags
+PyObject* head_bwd_of(bool distill, PyObject* const* a) {
+  Head x(distill, a);
+  PyObject* const* rest = a + (distill ? 5 : 4);
+  const Tensor &lse = needed(rest[0], "lse"), &up = needed(rest[1], "d_loss");
+  const Tensor* given_ws = tensor(rest[4], "ws");
+  const bool given = rest[5] != Py_None;
+  Tensor g[2];  // d_h, d_w
+  if (given) {
+    outs_are(rest[5], 2, "d_h and d_w");
+    for (int i = 0; i < 2; i++)
+      if (const Tensor* t = tensor(PyTuple_GET_ITEM(rest[5], i), "out")) g[i] = *t;
+  }
+  x.d.flags = (unsigned)integer(rest[7]);
+  together({&x.h, "h"}, {{&x.w, "w"}, {&x.said, distill ? "t_idx" : "target"}, {x.t_logit, "t_logit"},
+                         {&lse, "lse"}, {&up, "d_loss"}, {given_ws, "ws"}, some(g[0], "d_h"),
+                         some(g[1], "d_w")});
+  x.take(distill);
+  const float *pl = f32(&lse, "lse", x.d.rows), *pu = f32(&up, "d_loss", x.d.rows);
+  const ScalarType dt = x.h.scalar_type();
+  Rows gh;
+  if (g[0].defined()) gh = Rows(&g[0], "d_h", x.h.sizes(), dt);
+  if (g[1].defined()) {
+    Rows(&g[1], "d_w", x.w.sizes(), dt);
+    TORCH_CHECK_VALUE(g[1].is_contiguous(), "d_w must be contiguous");
+  }
+  const On on(rest[6], x.h);
+  if (!given) {
+    if (yes(rest[2])) g[0] = make(x.h.sizes(), dt, x.h), gh.p = g[0].data_ptr();
+    if (yes(rest[3])) g[1] = make(x.w.sizes(), dt, x.h);
+  }
+  const int grads = (g[0].defined() ? 1 : 0) | (g[1].defined() ? 2 : 0);
+  const Workspace ws(ssm_head_workspace_size(&x.d, grads, x.aligned()), given_ws, x.h);
+  if (!given) on.made({&g[0], &g[1]});
+  const int rc = call([&] {
+    if (distill)
+      return ssm_head_distill_bwd(&x.d, x.rh.p, x.rh.ld, x.rw.p, x.rw.ld, x.idx, x.logit, pl, pu, gh.p,
+                                  gh.ld, ptr(g[1]), ws.p, ws.bytes, on.raw);
+    return ssm_head_ce_bwd(&x.d, x.rh.p, x.rh.ld, x.rw.p, x.rw.ld, x.idx, pl, pu, gh.p, gh.ld,
+                           ptr(g[1]), ws.p, ws.bytes, on.raw);
+  });
+  if (rc) return PyLong_FromLong(rc);
+  return pack({give(g[0]), give(g[1])});
+}
+
+SSM_FUNCTION(head_ce_fwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 8);
+  return head_fwd_of(false, a);
+  END_HANDLE_TH_ERRORS
+}
+SSM_FUNCTION(head_distill_fwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 9);
+  return head_fwd_of(true, a);
+  END_HANDLE_TH_ERRORS
+}
+SSM_FUNCTION(head_ce_bwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 12);
+  return head_bwd_of(false, a);
+  END_HANDLE_TH_ERRORS
+}
+SSM_FUNCTION(head_distill_bwd) {
+  HANDLE_TH_ERRORS
+  args_are(n, 13);
+  return head_bwd_of(true, a);
+  END_HANDLE_TH_ERRORS
+}
+
 // The type of the checkpoints that the functions return (a pair of tensors).
 PyObject* use_ckpt8(PyObject*, PyObject* type) {
   if (!PyType_Check(type) || !PyType_IsSubtype((PyTypeObject*)type, &PyTuple_Type)) {
@@ -693,6 +860,10 @@ PyMethodDef methods[] = {SSM_METHOD(add_norm_fwd),
                          SSM_METHOD(ckpt8_save),
                          SSM_METHOD(ckpt8_load),
                          SSM_METHOD(ckpt8_wgrad),
+                         SSM_METHOD(head_ce_fwd),
+                         SSM_METHOD(head_ce_bwd),
+                         SSM_METHOD(head_distill_fwd),
+                         SSM_METHOD(head_distill_bwd),
                          {"use_ckpt8", use_ckpt8, METH_O, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module{PyModuleDef_HEAD_INIT, "_block", nullptr, -1, methods,

@@ -1,0 +1,666 @@
+// head_tc.cu -- the head's products on the tensor cores.  One kernel, three uses:
+//   kLogits  Z = h W^T, of which a tile leaves only what its row needs: the maximum, the sum of the
+//            exponentials below it, and the logits of the row's entries
+//   kGrad    Z again, turned into G = (softmax - p) d_loss, a piece of the vocabulary at a time
+//   kOut     d_h = G W (sums over the vocabulary), d_W = G^T h (sums over the rows)
+//
+// A pair of CTAs (tcgen05 cta_group::2) forms a 256 x 256 tile, 64 steps of the sum per stage: each CTA
+// holds 128 rows of A and 128 columns of B.  An operand is staged as it lies: [row][64 of the sum]
+// (K-major) or [64 of the sum][64 columns] slabs (MN-major), both from 64 x 64 boxes with the 128-byte
+// swizzle, so that neither G nor W nor h is ever transposed.  Pairs step over the tiles; two accumulators
+// in tensor memory alternate, so that a tile's results are taken out under the products of the next.
+//   warp 0      one thread copies the tiles by TMA (past the ends they read as 0)
+//   warp 1      one thread of the first CTA issues the MMAs; the second CTA's passes on that its copies
+//               have landed
+//   warps 4-11  take the results out: thread = row, 128 of its columns each
+// fp32 operands are three bf16 planes each, all six staged at once: six products per stage (of ranks
+// 0 0, 0 1, 1 0, 1 1, 0 2, 2 0; the rest is below 2^-24 of a product).  As the tensor cores truncate when
+// they add, these sums are taken out every 128 columns and added in registers.
+#include "head.cuh"
+#include "pair.cuh"
+
+namespace ssm {
+
+namespace {
+
+enum Use { kLogits, kGrad, kOut };
+
+constexpr int kThreads = 384;
+constexpr int kSumWarps = 8;
+constexpr uint32_t kSlab = 64 * 128;          // a box of 64 x 64 bf16
+constexpr uint32_t kOperand = 2 * kSlab;      // 128 rows or columns of a CTA
+constexpr uint32_t kTmCols = 2 * kHeadTile;
+constexpr int kRegsFew = 64, kRegsSum = 216;  // PLANES = 3: 128 x 64 + 256 x 216 <= 384 x 168
+
+template <int PLANES> struct Lay {
+  static constexpr int stages = PLANES == 1 ? 6 : 2;
+  static constexpr uint32_t stage = 2 * PLANES * kOperand;
+  static constexpr uint32_t smem = stages * stage + 1024;
+  // stages between two emptyings of the accumulator
+  static constexpr int segment = PLANES == 1 ? 1 << 30 : 2;
+};
+
+struct TcArgs {
+  CUtensorMap a, b;
+  HeadState* state;
+  int a_mn, b_mn;      // how the operands lie
+  int m_fixed;         // rows of the result; 0: the packed rows
+  int n;               // columns of the result
+  int k_fixed;         // length of the sum; 0: the packed rows
+  int splits, per_split;  // of the sum, in stages
+  int a_row0, b_row0;  // first row of a's (W's) in the tensor
+  int m_first;         // unit order: m fastest (else n)
+  int no_wait;
+  // kLogits, kGrad
+  float scale;         // log2(e) / tau
+  int v0, vocab;       // the word of column 0
+  int entries;
+  const int* src;
+  const int* idx;
+  const float* p;
+  float2* stats;
+  float* zt;
+  long long ld_stats;
+  const float *rl, *rg;
+  __nv_bfloat16* g;
+  long long ld_g, plane_g;
+  // kOut
+  float* part;
+  long long part_rows;
+  int ld_part, add;
+  void* out;
+  int io, ld_out, vec_out;
+};
+
+// Matrix descriptors: 128-byte swizzle.  K-major: rows of 128 bytes, 8 of them 1024 bytes apart; 16 of the
+// sum are 32 bytes.  MN-major: slabs of 64 columns, kSlab apart, rows of 128 bytes; 16 of the sum are
+// 2048 bytes.
+__device__ __forceinline__ uint64_t desc_of(uint32_t addr, bool mn) {
+  uint64_t d = (uint64_t)((addr & 0x3FFFFu) >> 4);
+  d |= (uint64_t)(mn ? kSlab >> 4 : 1u) << 16;
+  d |= (uint64_t)(1024u >> 4) << 32;
+  d |= (uint64_t)1 << 46;
+  d |= (uint64_t)2 << 61;
+  return d;
+}
+
+// A bounded wait that also ends where another part of the pair has given up.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, const int* bad) {
+  const uint32_t addr = smem_u32(bar);
+  for (uint32_t i = 0; i < kSpinLimit; i++) {
+    uint32_t done;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(done)
+        : "r"(addr), "r"(parity)
+        : "memory");
+    if (done) return true;
+    if (*reinterpret_cast<const volatile int*>(bad)) return false;
+  }
+  return false;
+}
+// Tells both CTAs.
+__device__ __forceinline__ void give_up(int* bad) {
+#pragma unroll
+  for (int cta = 0; cta < 2; cta++) {
+    uint32_t a = smem_u32(bad);
+    asm("mapa.shared::cluster.u32 %0, %0, %1;" : "+r"(a) : "r"(cta));
+    asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(a), "r"(1u) : "memory");
+  }
+}
+
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&v)[8]) {  // 32-byte aligned
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(v[0]),
+               "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+               : "memory");
+}
+
+// The smaller one, NaN if either is one.
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float r;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// v[i], i known to the thread only.
+__device__ __forceinline__ float pick(const float (&v)[32], int i) {
+  float r = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 32; j++) r = j == i ? v[j] : r;
+  return r;
+}
+
+// What becomes of a row's 128 columns, 32 at a time (chunk c).
+template <int USE, int PLANES> struct Taker {
+  const TcArgs& a;
+  const int row, col0;  // of the result: its row, and the first of its 128 columns
+  const bool row_ok;
+  // kLogits, kGrad
+  int e, next, src;  // the row's next entry, from this thread's first column on
+  float top = -INFINITY, sum = 0.0f, rl = 0.0f, rg = 0.0f;
+  // kOut
+  float* dst = nullptr;
+  float scale = 1.0f;
+
+  __device__ __forceinline__ Taker(const TcArgs& a, int row, int col0, int rows, int split)
+      : a(a), row(row), col0(col0), row_ok(row < rows) {
+    if constexpr (USE != kOut) {
+      // The first entry from this column on, by halving: the list is in order.
+      src = row_ok ? a.src[row] : -1;
+      e = 0, next = kNoEntry;
+      if (src >= 0) {
+        const int* list = a.idx + (long long)src * a.entries;
+        int n = a.entries;
+        while (n > 0) {
+          const int half = n >> 1;
+          if (list[e + half] < a.v0 + col0) e += half + 1, n -= half + 1;
+          else n = half;
+        }
+        if (e < a.entries) next = list[e];
+      }
+      if constexpr (USE == kGrad)
+        if (row_ok) rl = a.rl[row], rg = a.rg[row];
+    } else {
+      if (a.part) dst = a.part + ((long long)split * a.part_rows + row) * a.ld_part + col0;
+      else scale = a.state->scale;
+    }
+  }
+
+  __device__ __forceinline__ void chunk(int c, float (&v)[32]) {
+    if constexpr (USE == kLogits) {
+      const int word = a.v0 + col0 + 32 * c;
+      if (word + 32 > a.vocab) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (word + i >= a.vocab) v[i] = -INFINITY;
+      }
+      float m[4] = {v[0], v[1], v[2], v[3]};
+#pragma unroll
+      for (int i = 4; i < 32; i++) m[i & 3] = fmaxf(m[i & 3], v[i]);
+      const float above = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
+      const float at = above == -INFINITY ? 0.0f : above;
+      sum *= ex2((top - at) * a.scale);
+      top = above;
+      // The distance first: logits may be so large that a product's rounding is not small.
+      f2_t s[4] = {};
+      const f2_t off = f2_pack(-at, -at), scale = f2_pack(a.scale, a.scale);
+#pragma unroll
+      for (int i = 0; i < 16; i++)
+        s[i & 3] = f2_add(s[i & 3], f2_ex2(f2_mul(f2_add(f2_pack(v[2 * i], v[2 * i + 1]), off), scale)));
+      float s0, s1;
+      f2_unpack(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3])), s0, s1);
+      sum += s0 + s1;
+      while (next < word + 32) {
+        a.zt[(long long)src * a.entries + e] = pick(v, next - word);
+        advance();
+      }
+    } else if constexpr (USE == kGrad) {
+      const int word = a.v0 + col0 + 32 * c;
+#pragma unroll
+      for (int i = 0; i < 32; i++)  // at most 1, also where logits are so large that roundings are not small
+        v[i] = ex2(min_nan(fmaf(v[i], a.scale, -rl), 0.0f));
+      while (next < word + 32) {
+        const float p = a.p ? a.p[(long long)src * a.entries + e] : 1.0f;
+        const int at = next - word;
+#pragma unroll
+        for (int i = 0; i < 32; i++) v[i] -= i == at ? p : 0.0f;
+        advance();
+      }
+#pragma unroll
+      for (int i = 0; i < 32; i++) v[i] *= rg;
+      if (word + 32 > a.vocab) {
+#pragma unroll
+        for (int i = 0; i < 32; i++)
+          if (word + i >= a.vocab) v[i] = 0.0f;
+      }
+      if (!row_ok) return;
+      __nv_bfloat16* g = a.g + (long long)row * a.ld_g + col0 + 32 * c;
+#pragma unroll
+      for (int r = 0; r < PLANES; r++) {
+#pragma unroll
+        for (int b = 0; b < 2; b++) {
+          uint32_t w[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) {
+            const int j = 16 * b + 2 * i;
+            w[i] = bf16x2_rn(v[j], v[j + 1]);
+            if (r + 1 < PLANES) {
+              v[j] -= __uint_as_float(w[i] << 16);
+              v[j + 1] -= __uint_as_float(w[i] & 0xffff0000u);
+            }
+          }
+          st_global32(g + r * a.plane_g + 16 * b, w);
+        }
+      }
+    } else if (a.part) {
+      if (!row_ok) return;
+#pragma unroll
+      for (int b = 0; b < 4; b++) {
+        if (col0 + 32 * c + 8 * b >= a.ld_part) break;
+        float* to = dst + 32 * c + 8 * b;
+        float o[8];
+#pragma unroll
+        for (int i = 0; i < 8; i++) o[i] = v[8 * b + i];
+        if (a.add) {
+          Cols<float, 8> was;
+          was.load(to);
+#pragma unroll
+          for (int i = 0; i < 8; i++) o[i] += was.a[i];
+        }
+        st_cols(to, o);
+      }
+    } else {
+      if (!row_ok) return;
+#pragma unroll
+      for (int i = 0; i < 32; i++) v[i] *= scale;
+      const long long at = (long long)row * a.ld_out + col0 + 32 * c;
+      if (a.io == SSM_BF16) store((__nv_bfloat16*)a.out + at, c, v);
+      else store((float*)a.out + at, c, v);
+    }
+  }
+  __device__ __forceinline__ void advance() {
+    e++;
+    next = e < a.entries ? a.idx[(long long)src * a.entries + e] : kNoEntry;
+  }
+  template <typename T> __device__ __forceinline__ void store(T* to, int c, const float (&v)[32]) {
+#pragma unroll
+    for (int b = 0; b < 4; b++) {
+      const int col = col0 + 32 * c + 8 * b;
+      if (a.vec_out) {
+        if (col < a.n) {
+          float o[8];
+#pragma unroll
+          for (int i = 0; i < 8; i++) o[i] = v[8 * b + i];
+          st_cols(to + 8 * b, o);
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; i++)
+          if (col + i < a.n) st(to + 8 * b + i, v[8 * b + i]);
+      }
+    }
+  }
+  __device__ __forceinline__ void done() {
+    if constexpr (USE == kLogits)
+      if (row_ok)
+        a.stats[(long long)((a.v0 + col0) / (kHeadTile / 2)) * a.ld_stats + row] =
+            make_float2(top, sum);
+  }
+};
+
+// The units of a launch: tiles, and ranges of the sum.
+struct Units {
+  int m, n, rows, stages, per, total, m_first;
+  __device__ __forceinline__ Units(const TcArgs& a, int count) {
+    rows = a.m_fixed ? a.m_fixed : count;
+    m = (rows + kHeadTile - 1) / kHeadTile;
+    n = (a.n + kHeadTile - 1) / kHeadTile;
+    const int k = a.k_fixed ? a.k_fixed : count;
+    stages = (k + kHeadBlock - 1) / kHeadBlock;
+    per = a.per_split;
+    total = m * n * ((stages + per - 1) / per);
+    m_first = a.m_first;
+  }
+  __device__ __forceinline__ void of(int u, int& mt, int& nt, int& split, int& begin,
+                                     int& iters) const {
+    split = u / (m * n);
+    const int t = u - split * (m * n);
+    if (m_first) nt = t / m, mt = t - nt * m;
+    else mt = t / n, nt = t - mt * n;
+    begin = split * per;
+    iters = stages - begin < per ? stages - begin : per;
+  }
+};
+
+template <int USE, int PLANES>
+__global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
+  using L = Lay<PLANES>;
+  constexpr int S = L::stages;
+  extern __shared__ unsigned char raw[];
+  __shared__ uint64_t here[S], there[S], empty[S], ready[2], drained[2], last;
+  __shared__ uint32_t tbase;
+  __shared__ int bad;
+  unsigned char* smem =
+      reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+  const int tid = threadIdx.x, lane = tid & 31;
+  const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // known to the compiler as uniform
+  const int rank = blockIdx.x & 1, pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+  if (tid == 0) {
+    for (int i = 0; i < S; i++) {
+      mbar_init(&here[i], 1);
+      mbar_init(&there[i], 1);
+      mbar_init(&empty[i], 1);
+    }
+    for (int b = 0; b < 2; b++) {
+      mbar_init(&ready[b], 1);
+      mbar_init(&drained[b], 2 * kSumWarps);
+    }
+    mbar_init(&last, 1);
+    bad = 0;
+    fence_barrier_init();
+    prefetch_tmap(&a.a);
+    prefetch_tmap(&a.b);
+  }
+  __syncwarp();
+  if (warp == 1) Mma<2>::alloc(&tbase, kTmCols);
+  tmem_fence_before_sync();
+  __syncthreads();
+  sync_tile<2>();
+  tmem_fence_after_sync();
+  const uint32_t tm = tbase;
+  asm volatile("griddepcontrol.launch_dependents;");
+  wait_for_copies();
+  const int count = a.state->count > 0 ? a.state->count : 1;
+  const Units units(a, count);
+  int mt, nt, split, begin, iters;
+
+  if (warp < 4) {
+    if constexpr (PLANES > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
+    if (warp == 0) {
+      Ring<S> r;
+      int it = 0;
+      bool ok = true;
+      for (int u = pair; u < units.total && ok; u += pairs) {
+        units.of(u, mt, nt, split, begin, iters);
+        const int m0 = mt * kHeadTile + rank * (kHeadTile / 2), n0 = nt * kHeadTile + rank * (kHeadTile / 2);
+        for (int k = begin; k < begin + iters; k++, it++, r.next()) {
+          if (it >= S && !wait_for(&empty[r.s], r.phase ^ 1, &bad)) {
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            mbar_expect_tx(&here[r.s], L::stage);
+            unsigned char* to = smem + r.s * L::stage;
+#pragma unroll
+            for (int p = 0; p < PLANES; p++)
+#pragma unroll
+              for (int c = 0; c < 2; c++) {
+                tma_load_3d(to + p * kOperand + c * kSlab, &a.a, a.a_mn ? m0 + 64 * c : 64 * k,
+                            a.a_row0 + (a.a_mn ? 64 * k : m0 + 64 * c), p, &here[r.s]);
+                tma_load_3d(to + (PLANES + p) * kOperand + c * kSlab, &a.b,
+                            a.b_mn ? n0 + 64 * c : 64 * k,
+                            a.b_row0 + (a.b_mn ? 64 * k : n0 + 64 * c), p, &here[r.s]);
+              }
+          }
+          __syncwarp();
+        }
+      }
+      // the copies in flight land, and the first CTA's word that their slots are free arrives, before the
+      // block may end
+      for (int j = it > S ? it - S : 0; j < it; j++) {
+        if (!mbar_wait(&here[j % S], (j / S) & 1)) break;
+        if (ok) ok = wait_for(&empty[j % S], (j / S) & 1, &bad);
+      }
+      if (!ok) give_up(&bad);
+    } else if (warp == 1 && rank == 0) {
+      Ring<S> r;
+      const bool a_mn = a.a_mn, b_mn = a.b_mn;
+      const uint32_t idesc = idesc_bf16(kHeadTile, kHeadTile, a_mn, b_mn);
+      const uint64_t da0 = desc_of(smem_u32(smem), a_mn),
+                     db0 = desc_of(smem_u32(smem) + PLANES * kOperand, b_mn);
+      const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
+      int seg = 0;  // counted over the units
+      bool ok = true;
+      for (int u = pair; u < units.total && ok; u += pairs) {
+        units.of(u, mt, nt, split, begin, iters);
+        for (int it = 0; it < iters && ok; seg++) {
+          const uint32_t d = tm + (seg & 1) * kHeadTile;
+          const int end = iters - it < L::segment ? iters : it + L::segment;
+          if (seg >= 2) ok = wait_for(&drained[seg & 1], ((seg >> 1) - 1) & 1, &bad);
+          bool first = true;
+          for (; it < end && ok; it++, r.next()) {
+            ok = wait_for(&here[r.s], r.phase, &bad) && wait_for(&there[r.s], r.phase, &bad);
+            tmem_fence_after_sync();
+            if (ok && elect_one()) {
+              const uint64_t da = da0 + (uint32_t)(r.s * (L::stage >> 4)),
+                             db = db0 + (uint32_t)(r.s * (L::stage >> 4));
+              constexpr int kPairs = PLANES == 1 ? 1 : 6;
+              constexpr int pa[6] = {0, 0, 1, 1, 0, 2}, pb[6] = {0, 1, 0, 1, 2, 0};
+#pragma unroll
+              for (int x = 0; x < kPairs; x++)
+#pragma unroll
+                for (int kk = 0; kk < kHeadBlock / 16; kk++)
+                  Mma<2>::mma(idesc, d, da + (uint32_t)(pa[x] * (kOperand >> 4)) + sa * kk,
+                              db + (uint32_t)(pb[x] * (kOperand >> 4)) + sb * kk,
+                              !first || x > 0 || kk > 0);
+              Mma<2>::commit(&empty[r.s]);
+            }
+            __syncwarp();
+            first = false;
+          }
+          if (!ok) break;
+          if (elect_one()) Mma<2>::commit(&ready[seg & 1]);
+          __syncwarp();
+        }
+      }
+      if (!ok) give_up(&bad);
+    } else if (warp == 1) {
+      Ring<S> r;
+      const uint32_t first_there = bar_of_first<2>(there);
+      bool ok = true;
+      for (int u = pair; u < units.total && ok; u += pairs) {
+        units.of(u, mt, nt, split, begin, iters);
+        for (int it = 0; it < iters && ok; it++, r.next()) {
+          ok = wait_for(&here[r.s], r.phase, &bad);
+          if (ok && elect_one()) mbar_arrive_first<2>(first_there + 8 * r.s);
+          __syncwarp();
+        }
+      }
+      if (!ok) give_up(&bad);
+    }
+  } else {
+    if constexpr (PLANES > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
+    const int quad = warp & 3, half = (warp - 4) >> 2;
+    const uint32_t tacc = tm + ((uint32_t)(32 * quad) << 16) + 128 * half;
+    const uint32_t first_drained = bar_of_first<2>(drained);
+    int seg = 0;
+    bool ok = !a.no_wait;
+    for (int u = pair; u < units.total && ok; u += pairs) {
+      units.of(u, mt, nt, split, begin, iters);
+      // the rows that a sum over rows reads: zeros past the packed ones
+      const int rows = USE == kGrad ? (units.rows + 63) / 64 * 64 : units.rows;
+      Taker<USE, PLANES> taker(a, mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
+                               nt * kHeadTile + 128 * half, rows, split);
+      if constexpr (PLANES == 1) {
+        ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
+        __syncwarp();
+        tmem_fence_after_sync();
+        if (!ok) break;
+        const uint32_t t = tacc + (seg & 1) * kHeadTile;
+#pragma unroll 1
+        for (int c = 0; c < 4; c++) {
+          float v[32];
+          tmem_ld32(t + 32 * c, v);
+          if (c == 3) {
+            tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & 1));
+          }
+          taker.chunk(c, v);
+          __syncwarp();
+        }
+        seg++;
+      } else {
+        float acc[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; c++)
+#pragma unroll
+          for (int i = 0; i < 32; i++) acc[c][i] = 0.0f;
+        for (int it = 0; it < iters && ok; it += L::segment, seg++) {
+          ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
+          __syncwarp();
+          tmem_fence_after_sync();
+          if (!ok) break;
+          const uint32_t t = tacc + (seg & 1) * kHeadTile;
+#pragma unroll
+          for (int c = 0; c < 8; c++) {
+            float v[16];
+            tmem_ld16(t + 16 * c, v);
+#pragma unroll
+            for (int i = 0; i < 16; i++) acc[c >> 1][16 * (c & 1) + i] += v[i];
+          }
+          tmem_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & 1));
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int c = 0; c < 4; c++) {
+          taker.chunk(c, acc[c]);
+          __syncwarp();
+        }
+      }
+      taker.done();
+    }
+    if (!ok) give_up(&bad);
+  }
+  __syncwarp();
+  __syncthreads();
+  sync_tile<2>();  // what either CTA gave up is known to both
+  const bool gave_up = *reinterpret_cast<volatile int*>(&bad);
+  if (warp == 1 && rank == 0 && gave_up) {
+    // Perhaps with MMAs in flight: they read the shared memory and write the tensor memory of both CTAs,
+    // so they complete first.
+    if (elect_one()) Mma<2>::commit_here(&last);
+    __syncwarp();
+    mbar_wait(&last, 0);
+  }
+  sync_tile<2>();
+  if (warp == 1) {
+    tmem_fence_after_sync();
+    Mma<2>::dealloc(tm, kTmCols);
+  }
+  if (tid == 0 && gave_up) atomicExch(&a.state->status, SSM_ERR_TIMEOUT);
+}
+
+template <int USE, int PLANES> cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
+  auto kernel = head_tc_kernel<USE, PLANES>;
+  // asked for once per device (the first 64 remember it)
+  static std::atomic<unsigned long long> asked{0};
+  int dev = 0;
+  if (cudaError_t e = cudaGetDevice(&dev)) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+  if (!(asked.load(std::memory_order_relaxed) & bit)) {
+    if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             (int)Lay<PLANES>::smem))
+      return e;
+    asked.fetch_or(bit, std::memory_order_relaxed);
+  }
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(sms / 2 * 2);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = Lay<PLANES>::smem;
+  c.stream = st;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = 2;
+  at[1].val.clusterDim.y = at[1].val.clusterDim.z = 1;
+  c.attrs = at;
+  c.numAttrs = 2;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, t);
+  count_launches(1);
+  return e;
+}
+template <int USE> cudaError_t launch(const ssm_head_desc& d, const TcArgs& t, int sms, cudaStream_t st) {
+  return d.io == SSM_F32 ? launch<USE, 3>(t, sms, st) : launch<USE, 1>(t, sms, st);
+}
+
+bool encode(CUtensorMap* map, const HeadMatrix& x, int planes) {
+  return encode_tmap_3d(map, x.p, 2, x.cols, x.rows, planes, x.ld, planes > 1 ? x.plane : x.ld, 64,
+                        64, 1, 128);
+}
+int planes_of(const ssm_head_desc& d) { return d.io == SSM_F32 ? 3 : 1; }
+
+TcArgs logits_args(const ssm_head_desc& d, const HeadRows& r, const int* idx) {
+  TcArgs t{};
+  t.state = r.state;
+  t.k_fixed = d.cols;
+  t.splits = 1;
+  t.per_split = (d.cols + kHeadBlock - 1) / kHeadBlock;
+  t.m_first = 1;
+  t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
+  t.scale = d.entries ? kLog2e / d.temperature : kLog2e;
+  t.vocab = d.vocab;
+  t.entries = d.entries ? d.entries : 1;
+  t.src = r.src;
+  t.idx = idx;
+  return t;
+}
+
+}  // namespace
+
+cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
+                               const HeadRows& r, const int* idx, float2* stats, float* zt, int sms,
+                               cudaStream_t st) {
+  TcArgs t = logits_args(d, r, idx);
+  if (!encode(&t.a, h, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
+  t.n = d.vocab;
+  t.stats = stats;
+  t.ld_stats = h.rows;
+  t.zt = zt;
+  return launch<kLogits>(d, t, sms, st);
+}
+
+cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
+                             const HeadRows& r, const int* idx, const float* p, __nv_bfloat16* g,
+                             int v0, int n, int sms, cudaStream_t st) {
+  TcArgs t = logits_args(d, r, idx);
+  if (!encode(&t.a, h, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
+  t.n = n;
+  t.v0 = t.b_row0 = v0;
+  t.p = p;
+  t.rl = r.rl;
+  t.rg = r.rg;
+  t.g = g;
+  t.ld_g = n;
+  t.plane_g = h.rows * n;
+  return launch<kGrad>(d, t, sms, st);
+}
+
+cudaError_t launch_head_dh(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& w,
+                           const HeadRows& r, float* part, int splits, int per_split, int v0,
+                           bool add, int sms, cudaStream_t st) {
+  TcArgs t{};
+  if (!encode(&t.a, g, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
+  t.state = r.state;
+  t.b_mn = 1;
+  t.n = d.cols;
+  t.k_fixed = g.cols;
+  t.splits = splits;
+  t.per_split = per_split;
+  t.b_row0 = v0;
+  t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
+  t.part = part;
+  t.part_rows = g.rows;
+  t.ld_part = pad8(d.cols);
+  t.add = add;
+  return launch<kOut>(d, t, sms, st);
+}
+
+cudaError_t launch_head_dw(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
+                           const HeadRows& r, void* d_w, float* part, int splits, int per_split,
+                           int v0, int n, int sms, cudaStream_t st) {
+  TcArgs t{};
+  if (!encode(&t.a, g, planes_of(d)) || !encode(&t.b, h, planes_of(d))) return cudaErrorInvalidValue;
+  t.state = r.state;
+  t.a_mn = t.b_mn = 1;
+  t.m_fixed = n;
+  t.n = d.cols;
+  t.splits = splits;
+  t.per_split = per_split;
+  t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
+  t.part = part;
+  t.part_rows = g.cols;
+  t.ld_part = pad8(d.cols);
+  const size_t size = d.io == SSM_F32 ? 4 : 2;
+  t.out = (char*)d_w + (size_t)v0 * d.cols * size;
+  t.io = d.io;
+  t.ld_out = d.cols;
+  t.vec_out = d.cols % 8 == 0 && (uintptr_t)d_w % (8 * size) == 0;
+  return launch<kOut>(d, t, sms, st);
+}
+
+}  // namespace ssm

@@ -1,0 +1,89 @@
+/*
+ * ssm_head.h -- C ABI of the head and its loss (libssm_gb300.so): the logits z = h W^T over a vocabulary
+ * are formed in pieces, used and dropped, in the forward and again in the backward.
+ *
+ *   head_ce       loss = lse - z_target,               lse = log sum_v exp(z_v)
+ *   head_distill  from a teacher's logits t at `entries` words i of the vocabulary (its largest, say):
+ *                 p = softmax(t / tau) over the row's entries,  q = softmax(z / tau) over the vocabulary,
+ *                 lse = log sum_v exp(z_v / tau)
+ *                 loss = tau^2 sum_j p_j (log p_j - log q_{i_j})
+ *   backward      G = d loss / d z:  (softmax(z) - onehot(target)) d_loss,  tau (q - p) d_loss
+ *                 d_h = G W,  d_W = G^T h
+ *
+ * Layouts: h and d_h [rows][cols], W [vocab][cols] (io), rows `ld_*` elements apart (0 means cols; at
+ * least cols otherwise); d_W [vocab][cols] (io) contiguous; target int64 [rows]; t_idx int64 and t_logit
+ * (entry_io) [rows][entries], loss, lse and d_loss fp32 [rows], all contiguous.
+ *
+ * Rows without a loss: a target of ignore_index; a row without an entry.  Their loss, lse and gradient are
+ * 0 and h is not read there, whatever it holds; they cost no product.  An entry with t_idx below 0 is not
+ * there; one whose logit is -infinity has p = 0.  The same word twice adds up.  Any other target or entry
+ * outside the vocabulary is recorded as SSM_ERR_INVALID_ARG in the status word, and the row's loss, lse and
+ * d_h are NaN, without a part in d_W.
+ *
+ * Ownership, streams and errors are those of ssm.h: caller-owned device pointers, nothing allocated or
+ * synchronised, work enqueued on `stream`, argument errors found on the host before anything is
+ * enqueued.  Outputs are overwritten and overlap neither inputs nor each other.  The first word of the
+ * workspace is a status word, read with ssm_scan_status; where a bounded wait gave up (SSM_ERR_TIMEOUT
+ * there), every output of the call is NaN.  Sums run in a fixed order: results are bitwise reproducible.
+ *
+ * Arithmetic: products on the tensor cores with fp32 sums, fp32 operands as three bf16 terms each
+ * (six products, which leave out 2^-24 of a product and less).  The tensor cores truncate as they
+ * add: about 10^-8 of the sum for each 16 columns (bf16 operands); with fp32 operands the sums are taken out
+ * every 128 columns and added with rounding to nearest.  With bf16 operands G, divided by the largest
+ * |d_loss|, is rounded to bf16 between the products, which gives d_h and d_W an error of the size of their
+ * own rounding.
+ */
+#ifndef SSM_HEAD_GB300_H
+#define SSM_HEAD_GB300_H
+
+#include "ssm.h"
+
+#ifdef __cplusplus
+extern "C" {
+#endif
+
+#define SSM_MAX_HEAD_ENTRIES 128 /* teacher entries of a row (SSM_ERR_UNSUPPORTED beyond) */
+#define SSM_MAX_HEAD_COLS 65536
+#define SSM_MAX_HEAD_VOCAB (1 << 22)
+#define SSM_MAX_HEAD_ROWS (1 << 24)
+
+typedef struct {
+  long long rows; /* tokens, >= 1 */
+  int cols;       /* channels of h */
+  int vocab;
+  int io;         /* ssm_dtype of h, W and their gradients */
+  int entries;    /* head_distill: teacher entries of a row, >= 1; head_ce: 0 */
+  int entry_io;   /* head_distill: ssm_dtype of t_logit */
+  float temperature;      /* head_distill: tau > 0, finite */
+  long long ignore_index; /* head_ce: the target of a row without a loss */
+  unsigned flags; /* 0, or ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
+                     the sums out give up at once, as if the bound of their wait had run out */
+} ssm_head_desc;
+
+/* Bytes of scratch of a call on the current device (at least 256; 0 if the arguments are invalid).
+ * grads: 0 for the forward, else bits 1 (d_h wanted) and 2 (d_W wanted) of the backward.  aligned: W's rows
+ * (pointer and ld_w * element size) are 16-byte aligned; fp32 W may lie anywhere. */
+size_t ssm_head_workspace_size(const ssm_head_desc* desc, int grads, int aligned);
+
+/* Forward.  Required: everything but lse. */
+int ssm_head_ce_fwd(const ssm_head_desc* desc, const void* h, long long ld_h, const void* w,
+                    long long ld_w, const int64_t* target, float* loss, float* lse, void* ws,
+                    size_t ws_bytes, void* stream);
+int ssm_head_distill_fwd(const ssm_head_desc* desc, const void* h, long long ld_h, const void* w,
+                         long long ld_w, const int64_t* t_idx, const void* t_logit, float* loss,
+                         float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/* Backward.  lse: the forward's.  One of d_h and d_w may be NULL. */
+int ssm_head_ce_bwd(const ssm_head_desc* desc, const void* h, long long ld_h, const void* w,
+                    long long ld_w, const int64_t* target, const float* lse, const float* d_loss,
+                    void* d_h, long long ld_d_h, void* d_w, void* ws, size_t ws_bytes,
+                    void* stream);
+int ssm_head_distill_bwd(const ssm_head_desc* desc, const void* h, long long ld_h, const void* w,
+                         long long ld_w, const int64_t* t_idx, const void* t_logit,
+                         const float* lse, const float* d_loss, void* d_h, long long ld_d_h,
+                         void* d_w, void* ws, size_t ws_bytes, void* stream);
+
+#ifdef __cplusplus
+}
+#endif
+#endif

@@ -81,3 +81,81 @@ def layer_norm_bwd(d_out, s, mean, rstd, d_s, scale, w, x):
         out.append((r * x).sum(0))
         bound.append(A * (r * x).abs().sum(0) + (dr * x.abs()).sum(0))
     return out, bound
+
+
+# ---- the head -----------------------------------------------------------------------------------------
+
+def _product(io, a, b, n):
+    """The error of a sum of n products a b with magnitudes a_abs b_abs: bf16 terms have exact products and
+    the tensor cores truncate each of the n / 16 additions, and the 16 products in it, at 2^-23 of the
+    largest magnitude so far (two units: the terms' alignment and the sum's); fp32 terms add six such
+    products per 16, taken out every 128 and added in fp32, and leave out 2^-22 of each product."""
+    size = a.abs() @ b.abs()
+    steps = n / 16 + 4
+    if io == torch.float32:
+        return size * (2.0 ** -22 * (1 + 48 + 4) + U * (n / 128 + 1))
+    return size * 2.0 ** -22 * steps
+
+
+def _p_of(t_idx, t_logit, tau, vocab):
+    """(p [rows][vocab], rows with a loss, sum p log p)"""
+    there = (t_idx >= 0) & (t_logit > -float("inf"))
+    t = torch.where(there, t_logit.to(f64) / tau, torch.tensor(-float("inf"), dtype=f64))
+    some = there.any(1)
+    p = torch.zeros_like(t)
+    p[some] = torch.softmax(t[some], 1)
+    logs = torch.where(p > 0, p * torch.log(p.clamp(min=1e-300)), torch.zeros_like(p)).sum(1)
+    P = torch.zeros(t.shape[0], vocab, dtype=f64)
+    P.scatter_add_(1, t_idx.clamp(min=0), torch.where(there, p, torch.zeros_like(p)))
+    return P, some, logs
+
+
+def head(h, w, P, some, logs, tau=1.0):
+    """(loss, lse) and their bounds; the rows that are not in ``some`` are 0 whatever h holds."""
+    io, V = h.dtype, w.shape[0]
+    hh = torch.where(some[:, None], h.to(f64), torch.zeros(1, dtype=f64))
+    ww = w.to(f64)
+    z = hh @ ww.t() / tau
+    lse = torch.logsumexp(z, 1)
+    loss = tau * tau * (logs + lse * P.sum(1) - (P * z).sum(1))
+    dz = _product(io, hh, ww.t(), h.shape[1]) / tau + 2 * U * z.abs()
+    # 2^x is good to 2^-22 and its argument to one rounding; the sum's additions; its logarithm
+    dlse = dz.amax(1) + 2.0 ** -21 + (SUM + V // 4096) * U + 4 * U * (lse.abs() + z.abs().amax(1))
+    mean = P * (z.amax(1, keepdim=True) - z).abs()
+    dloss = tau * tau * (dlse + (P * dz).sum(1) + 80 * U * (mean.sum(1) + logs.abs() + lse.abs()))
+    zero = torch.zeros_like(lse)
+    return ((torch.where(some, loss, zero), torch.where(some, lse, zero)),
+            (torch.where(some, dloss, zero), torch.where(some, dlse, zero)))
+
+
+def head_bwd(h, w, P, some, lse, d_loss, tau=1.0):
+    """(d_h, d_w) and their bounds; lse as the backward gets it."""
+    io = h.dtype
+    hh = torch.where(some[:, None], h.to(f64), torch.zeros(1, dtype=f64))
+    ww = w.to(f64)
+    z = hh @ ww.t() / tau
+    lse = lse.to(f64)[:, None]
+    q = torch.exp(z - lse)
+    up = torch.where(some, d_loss.to(f64), torch.zeros(1, dtype=f64))[:, None] * tau
+    G = (q - P) * up
+    # of q: its argument (an error e of it is a factor exp(e) <= 1 + 2 e here), 2^x
+    de = _product(io, hh, ww.t(), h.shape[1]) / tau + 4 * U * (z.abs() + lse.abs())
+    dG = (q * (2 * de + 2.0 ** -21) + 2.0 ** -21 * P + 8 * U * (q + P)) * up.abs()
+    # between the products: bf16, or three terms of it; d_loss over the largest and back
+    dG = dG + G.abs() * ((2.0 ** -8 if io == torch.bfloat16 else 2.0 ** -22) + 6 * U)
+    # 2^x below the smallest normal number 2^-126 is 0, and a G (over the largest |d_loss| tau) as small
+    # is a subnormal number, whose digits end at a fixed place: off by 2^-126 at most in either case
+    dG = dG + 2.0 ** -126 * (up.abs() + up.abs().max())
+    T, V = G.shape
+    d_h, d_w = G @ ww, G.t() @ hh
+    dd_h = dG @ ww.abs() + _product(io, G.abs() + dG, ww, V) + 16 * U * (G.abs() @ ww.abs())
+    dd_w = dG.t() @ hh.abs() + _product(io, (G.abs() + dG).t(), hh, T) + 16 * U * (G.abs().t() @ hh.abs())
+    return (d_h, d_w), (dd_h, dd_w)
+
+
+def ce_rows(target, vocab, ignore=-100):
+    """(P, some, logs) of class targets."""
+    some = target != ignore
+    P = torch.zeros(target.numel(), vocab, dtype=f64)
+    P[some, target[some]] = 1.0
+    return P, some, torch.zeros(target.numel(), dtype=f64)
