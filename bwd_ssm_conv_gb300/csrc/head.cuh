@@ -45,30 +45,23 @@ inline long long pad_rows(long long rows) { return (rows + 63) / 64 * 64; }
 // p, sum p log p in known[row], and in valid[row] whether the row has a loss (1), or is bad (2).
 cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, const void* t_logit,
                                 int* idx, float* p, float* known, uint8_t* valid, cudaStream_t st);
-// Which rows count: from `valid`, or from the targets (whose words go to idx).
-cudaError_t launch_head_begin(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
-                              const float* d_loss, int* idx, const HeadRows& r, bool first,
-                              cudaStream_t st);
-// Packs h's rows (and rl, rg, given lse).
-cudaError_t launch_head_pack(const ssm_head_desc& d, const void* h, long long ld_h,
-                             const float* lse, const float* d_loss, const HeadRows& r, int sms,
-                             cudaStream_t st);
-// W with padded rows, fp32 as three planes.
-cudaError_t launch_head_copy_w(const ssm_head_desc& d, const void* w, long long ld_w,
-                               __nv_bfloat16* out, int sms, cudaStream_t st);
+// Which rows count, from `valid` or from the targets (whose words go to idx), their h packed (and, given
+// lse, rl and rg); W with padded rows, fp32 as three planes, to w_out where that is given.
+cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
+                             const void* h, long long ld_h, const float* lse, const float* d_loss,
+                             const void* w, long long ld_w, int* idx, const HeadRows& r,
+                             __nv_bfloat16* w_out, int sms, cudaStream_t st);
 // Loss and lse from the tiles' sums; zt: the entries' logits [rows][entries or 1].
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
                              const float* zt, const float* p, const float* known,
                              const HeadRows& r, float* loss, float* lse, cudaStream_t st);
-// d_h from the splits' sums [splits][padded rows][padded cols].  Where a wait of the call gave up, d_h and
-// d_w are filled with NaN.
-cudaError_t launch_head_finish(const ssm_head_desc& d, const float* part, int splits,
-                               const HeadRows& r, void* d_h, long long ld_d_h, void* d_w, int sms,
+// What the gradients' sums lack: d_h from the splits' sums [splits][padded rows][padded cols], and
+// rows v0 .. v0 + n of d_W from theirs [splits][piece][padded cols], either where given.  `last`: of the
+// call; where a wait of it gave up, d_h and all of d_w are filled with NaN.
+cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const float* h_part,
+                               int h_splits, void* d_h, long long ld_d_h, const float* w_part,
+                               int w_per, int piece, void* d_w, int v0, int n, bool last, int sms,
                                cudaStream_t st);
-// Rows v0 .. v0 + n of d_W from the splits' sums [splits][n_part][padded cols].
-cudaError_t launch_head_sum_w(const ssm_head_desc& d, const float* part, int per_split, int n_part,
-                              const HeadRows& r, void* d_w, int v0, int n, int sms,
-                              cudaStream_t st);
 
 // ---- head_tc.cu -----------------------------------------------------------------------------------
 struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart
@@ -76,21 +69,30 @@ struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart
   long long rows, ld, plane;
   int cols;
 };
+// How a product is cut: columns of a tile (256 or 128), splits of the sum and their stages.
+struct HeadCut {
+  int tile_n, splits, per;
+};
 // The sums of the vocabulary's tiles, stats [2 tiles][padded rows], and the entries' logits.
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const int* idx, float2* stats, float* zt, int sms,
-                               cudaStream_t st);
+                               const HeadRows& r, const int* idx, int tile_n, float2* stats,
+                               float* zt, int sms, cudaStream_t st);
 // G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [planes][padded rows][n].
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                             const HeadRows& r, const int* idx, const float* p, __nv_bfloat16* g,
-                             int v0, int n, int sms, cudaStream_t st);
-// part [splits][padded rows][padded cols] (+)= G W over a piece, its words split over `splits`.
-cudaError_t launch_head_dh(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& w,
-                           const HeadRows& r, float* part, int splits, int per_split, int v0,
-                           bool add, int sms, cudaStream_t st);
-// Rows v0 .. v0 + n of d_W = G^T h, or with part the splits' sums.
-cudaError_t launch_head_dw(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
-                           const HeadRows& r, void* d_w, float* part, int splits, int per_split,
-                           int v0, int n, int sms, cudaStream_t st);
+                             const HeadRows& r, const int* idx, const float* p, int tile_n,
+                             __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st);
+// The two products with G of the words v0 .. v0 + n, in one launch:
+//   h_part [splits][padded rows][padded cols] (+)= G W, the piece's words split,
+//   rows v0 .. v0 + n of d_W = G^T h, or with w_part [splits][piece][padded cols] the splits' sums.
+struct HeadOut {
+  HeadCut h, w;
+  bool h_first;  // the units of d_h before those of d_W
+  float* h_part;
+  float* w_part;
+  void* d_w;
+};
+cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
+                            const HeadMatrix& w, const HeadRows& r, const HeadOut& o, int v0, int n,
+                            bool add, int sms, cudaStream_t st);
 
 }  // namespace ssm

@@ -28,24 +28,79 @@ int num_sms() {
   return sms;
 }
 
-// Splits of a sum of `stages` stages over `tiles` tiles' pairs of CTAs: the number that the slowest pair
-// needs least time with, in stages (half a microsecond and less), where a split costs its tiles' way to
-// memory and back besides.
-struct Split {
-  int splits, per;
+// ---- how the products are cut ---------------------------------------------------------------------
+// Costs are in stages, the time of a 256 x 256 tile's step over 64 of the sum.
+constexpr int kUnitCost = 3;             // what a unit costs by itself
+constexpr double kStageBytes = 1.5e6;    // what memory moves in a stage's time
+double tile_cost(int tile_n, int io) { return tile_n == kHeadTile ? 1.0 : io == SSM_F32 ? 0.55 : 0.65; }
+
+// Units of one or two kinds are dealt out to the pairs of CTAs in turn, the first kind first: the time of
+// the pair with the most to do.
+double dealt(long long n0, double c0, long long n1, double c1, long long pairs) {
+  double most = 0.0;
+  const auto of = [&](long long p) {  // pair p's units: those u with u % pairs == p
+    const long long a = p < n0 ? (n0 - 1 - p) / pairs + 1 : 0,
+                    b = p < n0 + n1 ? (n0 + n1 - 1 - p) / pairs + 1 : 0;
+    const double time = (double)a * c0 + (double)(b - a) * c1;
+    if (time > most) most = time;
+  };
+  of(0);
+  of(n0 % pairs);
+  if (n0 % pairs) of(n0 % pairs - 1);
+  const long long end = (n0 + n1) % pairs;
+  of(end ? end - 1 : pairs - 1);
+  return most;
+}
+
+// The tile's columns for Z: 128 where fewer tiles of 256 than pairs leave some of those idle.
+int logits_tile(long long rows, int cols, int words, int io, int sms) {
+  const long long pairs = sms / 2 > 0 ? sms / 2 : 1, m = (rows + kHeadTile - 1) / kHeadTile;
+  const int stages = (cols + kHeadBlock - 1) / kHeadBlock;
+  const auto time = [&](int tile) {
+    return dealt(m * ((words + tile - 1) / tile), stages * tile_cost(tile, io) + kUnitCost, 0, 0.0,
+                 pairs);
+  };
+  return time(128) < time(256) ? 128 : 256;
+}
+
+struct Cuts {
+  HeadCut h, w;
+  bool h_first;
 };
-Split split_of(long long tiles, int stages, double part_bytes, int sms) {
-  const long long pairs = sms / 2 > 0 ? sms / 2 : 1;
-  constexpr double kStageBytes = 1.5e6;  // that memory moves in a stage's time
-  constexpr int kUnit = 3;               // stages that a unit costs by itself
-  Split best{1, stages};
-  double least = 0.0;
-  for (int s = 1; s <= 64 && s <= stages; s++) {
-    const int per = (stages + s - 1) / s;
-    if ((stages + per - 1) / per != s) continue;
-    const double time = (double)((tiles * s + pairs - 1) / pairs) * (per + kUnit) +
-                        (s > 1 ? 2.0 * s * part_bytes / kStageBytes : 0.0);
-    if (s == 1 || time < least) least = time, best = {s, per};
+// The two products with G: pairs of numbers of splits, and both widths, as far as more units than a few for
+// each pair of CTAs could help.
+Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool several, int sms) {
+  const long long pairs = sms / 2 > 0 ? sms / 2 : 1, padded = pad_rows(rows);
+  const int st_h = piece / kHeadBlock, st_w = (int)(padded / kHeadBlock);
+  const long long m_h = (rows + kHeadTile - 1) / kHeadTile, m_w = piece / kHeadTile;
+  const double mb_h = 4.0 * padded * pad8(cols), mb_w = 4.0 * piece * pad8(cols);
+  const auto per_of = [](int stages, int splits) { return (stages + splits - 1) / splits; };
+  Cuts best{};
+  double least = -1.0;
+  static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
+  const long long enough = 5 * pairs;
+  for (int tile : {256, 128}) {
+    const long long n = (cols + tile - 1) / tile;
+    if (tile == 128 && m_w * n > enough && m_h * n > enough) break;
+    for (int sw : kSplits) {
+      if (sw > 1 && (!(grads & 2) || sw > st_w || m_w * n * sw > enough)) break;
+      const int pw = per_of(st_w, sw);
+      if (per_of(st_w, pw) != sw) continue;
+      for (int sh : kSplits) {
+        if (sh > 1 && (!(grads & 1) || sh > st_h || m_h * n * sh > enough)) break;
+        const int ph = per_of(st_h, sh);
+        if (per_of(st_h, ph) != sh) continue;
+        const long long nw = grads & 2 ? m_w * n * sw : 0, nh = grads & 1 ? m_h * n * sh : 0;
+        const double cw = pw * tile_cost(tile, io) + kUnitCost, ch = ph * tile_cost(tile, io) + kUnitCost;
+        const bool h_first = ch > cw;
+        double time = h_first ? dealt(nh, ch, nw, cw, pairs) : dealt(nw, cw, nh, ch, pairs);
+        // the splits' sums: written and read, those of d_h once for each piece and under its products
+        if (grads & 1) time += sh * mb_h * (several ? 1.0 : 2.0) / kStageBytes;
+        if (sw > 1) time += 2.0 * sw * mb_w / kStageBytes;
+        if (least < 0.0 || time < least)
+          least = time, best = {{tile, sh, ph}, {tile, sw, pw}, h_first};
+      }
+    }
   }
   return best;
 }
@@ -53,15 +108,14 @@ Split split_of(long long tiles, int stages, double part_bytes, int sms) {
 // The workspace, by bytes from its start.
 struct Plan {
   size_t pos, src, idx, p, known, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
-  int planes, tiles, piece, pieces;
-  Split s_h, s_w;
+  int planes, tile_z, tiles, piece, pieces;
+  Cuts cuts;
 };
 Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   Plan p{};
   const long long T = d.rows, Tp = pad_rows(T), n_e = d.entries ? d.entries : 1;
   const int Dp = pad8(d.cols);
   p.planes = d.io == SSM_F32 ? 3 : 1;
-  p.tiles = (d.vocab + kHeadTile - 1) / kHeadTile;
   size_t at = 256;
   const auto take = [&](size_t n) {
     const size_t was = at;
@@ -79,28 +133,26 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   p.h = take((size_t)2 * p.planes * Tp * Dp);
   if (copy_w) p.w = take((size_t)2 * p.planes * d.vocab * Dp);
   if (!grads) {
+    p.tile_z = logits_tile(T, d.cols, d.vocab, d.io, sms);
+    p.tiles = (d.vocab + p.tile_z - 1) / p.tile_z;
     p.stats = take((size_t)8 * 2 * p.tiles * Tp);
     p.zt = take(4 * T * n_e);
   } else {
     p.rl = take(4 * Tp);
     p.rg = take(4 * Tp);
     // pieces of the vocabulary, alike
+    const int tiles = (d.vocab + kHeadTile - 1) / kHeadTile;
     long long most = kMaxPiece / (2 * p.planes * Tp) / kHeadTile;
     if (most < 1) most = 1;
-    p.pieces = (int)((p.tiles + most - 1) / most);
-    p.piece = (p.tiles + p.pieces - 1) / p.pieces * kHeadTile;
+    p.pieces = (int)((tiles + most - 1) / most);
+    p.piece = (tiles + p.pieces - 1) / p.pieces * kHeadTile;
     p.pieces = (d.vocab + p.piece - 1) / p.piece;
     p.g = take((size_t)2 * p.planes * Tp * p.piece);
-    const long long rows = (T + kHeadTile - 1) / kHeadTile,
-                    cols = (d.cols + kHeadTile - 1) / kHeadTile;
-    if (grads & 1) {
-      p.s_h = split_of(rows * cols, p.piece / kHeadBlock, 4.0 * Tp * Dp, sms);
-      p.dh = take((size_t)4 * p.s_h.splits * Tp * Dp);
-    }
-    if (grads & 2) {
-      p.s_w = split_of(p.piece / kHeadTile * cols, (int)(Tp / kHeadBlock), 4.0 * p.piece * Dp, sms);
-      if (p.s_w.splits > 1) p.dw = take((size_t)4 * p.s_w.splits * p.piece * Dp);
-    }
+    p.tile_z = logits_tile(T, d.cols, p.piece, d.io, sms);
+    p.cuts = cuts_of(T, d.cols, p.piece, d.io, grads, p.pieces > 1, sms);
+    if (grads & 1) p.dh = take((size_t)4 * p.cuts.h.splits * Tp * Dp);
+    if ((grads & 2) && p.cuts.w.splits > 1)
+      p.dw = take((size_t)4 * p.cuts.w.splits * p.piece * Dp);
   }
   p.bytes = at;
   return p;
@@ -185,37 +237,32 @@ int run(Call c, bool distill, bool backward) {
 #define SSM_DO(call) \
   if ((call) != cudaSuccess) return SSM_ERR_CUDA
   if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, idx, prob, known, valid, st));
-  SSM_DO(launch_head_begin(d, c.target, valid, backward ? c.d_loss : nullptr, idx, r, !distill, st));
-  SSM_DO(launch_head_pack(d, c.h, c.ld_h, backward ? c.lse : nullptr, c.d_loss, r, sms, st));
+  __nv_bfloat16* w_out = copy_w ? (__nv_bfloat16*)(ws + p.w) : nullptr;
+  SSM_DO(launch_head_rows(d, c.target, valid, c.h, c.ld_h, backward ? c.lse : nullptr,
+                          backward ? c.d_loss : nullptr, c.w, c.ld_w, idx, r, w_out, sms, st));
   const HeadMatrix h{r.h, Tp, Dp, Tp * Dp, d.cols};
-  HeadMatrix w{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
-  if (copy_w) {
-    __nv_bfloat16* to = (__nv_bfloat16*)(ws + p.w);
-    SSM_DO(launch_head_copy_w(d, c.w, c.ld_w, to, sms, st));
-    w = {to, d.vocab, Dp, (long long)d.vocab * Dp, d.cols};
-  }
+  const HeadMatrix w = copy_w ? HeadMatrix{w_out, d.vocab, Dp, (long long)d.vocab * Dp, d.cols} :
+                                HeadMatrix{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
   if (!backward) {
     float2* stats = (float2*)(ws + p.stats);
     float* zt = (float*)(ws + p.zt);
-    SSM_DO(launch_head_logits(d, h, w, r, idx, stats, zt, sms, st));
+    SSM_DO(launch_head_logits(d, h, w, r, idx, p.tile_z, stats, zt, sms, st));
     SSM_DO(launch_head_loss(d, stats, 2 * p.tiles, zt, prob, known, r, c.loss, c.lse_out, st));
     return SSM_OK;
   }
   __nv_bfloat16* gp = (__nv_bfloat16*)(ws + p.g);
-  float *dh = (float*)(ws + p.dh), *dw = p.dw ? (float*)(ws + p.dw) : nullptr;
   const HeadMatrix g{gp, Tp, p.piece, Tp * p.piece, p.piece};
+  const HeadOut out{p.cuts.h, p.cuts.w, p.cuts.h_first, c.d_h ? (float*)(ws + p.dh) : nullptr,
+                    p.dw ? (float*)(ws + p.dw) : nullptr, c.d_w};
   for (int i = 0; i < p.pieces; i++) {
     const int v0 = i * p.piece, n = d.vocab - v0 < p.piece ? d.vocab - v0 : p.piece;
-    SSM_DO(launch_head_grad(d, h, w, r, idx, prob, gp, v0, p.piece, sms, st));
-    if (c.d_w) {
-      SSM_DO(launch_head_dw(d, g, h, r, c.d_w, dw, p.s_w.splits, p.s_w.per, v0, n, sms, st));
-      if (dw)
-        SSM_DO(launch_head_sum_w(d, dw, p.s_w.per, p.piece, r, c.d_w, v0, n, sms, st));
-    }
-    if (c.d_h)
-      SSM_DO(launch_head_dh(d, g, w, r, dh, p.s_h.splits, p.s_h.per, v0, i > 0, sms, st));
+    const bool last = i == p.pieces - 1;
+    SSM_DO(launch_head_grad(d, h, w, r, idx, prob, p.tile_z, gp, v0, p.piece, sms, st));
+    SSM_DO(launch_head_out(d, g, h, w, r, out, v0, n, i > 0, sms, st));
+    if (last || out.w_part)
+      SSM_DO(launch_head_finish(d, r, out.h_part, p.cuts.h.splits, last ? c.d_h : nullptr, c.ld_d_h,
+                                out.w_part, p.cuts.w.per, p.piece, c.d_w, v0, n, last, sms, st));
   }
-  SSM_DO(launch_head_finish(d, dh, p.s_h.splits, r, c.d_h, c.ld_d_h, c.d_w, sms, st));
 #undef SSM_DO
   return SSM_OK;
 }

@@ -92,91 +92,6 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
   }
 }
 
-// ---- which rows count -----------------------------------------------------------------------------
-// One block steps over the rows, 4 per thread, and numbers those that have a loss; in the backward it
-// also finds the largest |d_loss| of theirs.
-constexpr int kBeginThreads = 1024, kBeginRows = 4;
-__global__ void __launch_bounds__(kBeginThreads) head_begin_kernel(const int64_t* target,
-                                                                   const uint8_t* valid,
-                                                                   long long rows, int vocab,
-                                                                   long long ignore, float tau,
-                                                                   const float* d_loss, int* idx,
-                                                                   HeadRows r) {
-  __shared__ int sums[2][32];
-  __shared__ float tops[32];
-  early_launch();
-  wait_for_before();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int total = 0, half = 0;
-  bool bad = false;
-  float top = 0.0f;
-  for (long long base = 0; base < rows; base += kBeginThreads * kBeginRows, half ^= 1) {
-    const long long t0 = base + (long long)threadIdx.x * kBeginRows;
-    int pos[kBeginRows], n = 0;
-#pragma unroll
-    for (int i = 0; i < kBeginRows; i++) {
-      pos[i] = kIgnored;
-      if (t0 + i >= rows) continue;
-      if (target) {
-        const int64_t y = target[t0 + i];
-        const bool in = y >= 0 && y < vocab;
-        if (y != ignore) pos[i] = in ? 0 : kBadRow;
-        idx[t0 + i] = pos[i] == 0 ? (int)y : kNoEntry;
-      } else {
-        const int v = valid[t0 + i];
-        pos[i] = v == 1 ? 0 : v == 2 ? kBadRow : kIgnored;
-      }
-      n += pos[i] == 0;
-      bad = bad || pos[i] == kBadRow;
-      if (pos[i] == 0 && d_loss) {
-        const float g = fabsf(d_loss[t0 + i]);
-        if (g < INFINITY) top = fmaxf(top, g);
-      }
-    }
-    int before = n;  // within the warp, then the block
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, before, off);
-      if (lane >= off) before += o;
-    }
-    if (lane == 31) sums[half][warp] = before;
-    before -= n;
-    __syncthreads();
-    int all = sums[half][lane], upto = all;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int o = __shfl_up_sync(0xffffffffu, upto, off);
-      if (lane >= off) upto += o;
-    }
-    before += __shfl_sync(0xffffffffu, upto - all, warp) + total;
-    total += __shfl_sync(0xffffffffu, upto, 31);
-#pragma unroll
-    for (int i = 0; i < kBeginRows; i++)
-      if (t0 + i < rows) {
-        if (pos[i] == 0) {
-          pos[i] = before++;
-          r.src[pos[i]] = (int)(t0 + i);
-        }
-        r.pos[t0 + i] = pos[i];
-      }
-  }
-  const int padded = ((total > 0 ? total : 1) + 63) / 64 * 64;
-  for (int i = total + threadIdx.x; i < padded; i += kBeginThreads) r.src[i] = -1;
-  top = warp_max(top);
-  if (lane == 0) tops[warp] = top;
-  bad = __syncthreads_or(bad);
-  if (warp == 0) {
-    top = warp_max(tops[lane]);
-    if (lane == 0) {
-      r.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
-      r.state->count = total;
-      if (!(top > 0.0f)) top = 1.0f;
-      r.state->g_top = top;
-      r.state->scale = top * tau;
-    }
-  }
-}
-
 // ---- rows as the products read them ---------------------------------------------------------------
 // A value as PLANES bf16 terms, each rounded from what the ones before leave: three hold all 24 bits.
 // What is not finite stays so in the first.
@@ -220,53 +135,136 @@ __device__ __forceinline__ void copy8(const IO* x, int left, __nv_bfloat16* out,
   }
 }
 
-// A warp per packed row, or per row of zeros past them.
-template <typename IO, int PLANES, bool VEC>
-__global__ void __launch_bounds__(kThreads) head_pack_kernel(const IO* h, long long ld_h, int cols,
-                                                             int padded_cols, long long plane,
-                                                             const float* lse, const float* d_loss,
-                                                             HeadRows r) {
+// ---- which rows count, and their copies --------------------------------------------------------------
+// A block takes `per_block` rows.  It looks at every row, which costs less than a launch of its own for a
+// count (8192 rows: 2 us), so that it knows where its own go, and packs them, a warp per row; the last
+// one also the rows of zeros past them.  The blocks behind copy W.
+struct RowsArgs {
+  const int64_t* target;
+  const uint8_t* valid;
+  long long rows, ignore;
+  int vocab, cols, padded_cols, per_block, row_blocks;
+  float tau;
+  const void* h;
+  long long ld_h;
+  const float* lse;
+  const float* d_loss;
+  const void* w;
+  long long ld_w;
+  __nv_bfloat16* w_out;
+  int* idx;
+  HeadRows r;
+};
+enum RowKind { kCounts, kNone, kBad };
+__device__ __forceinline__ int kind_of(const RowsArgs& a, long long row) {
+  if (a.target) {
+    const int64_t y = a.target[row];
+    return y == a.ignore ? kNone : y >= 0 && y < a.vocab ? kCounts : kBad;
+  }
+  const int v = a.valid[row];
+  return v == 1 ? kCounts : v == 2 ? kBad : kNone;
+}
+
+template <typename IO, int PLANES, bool VEC_H, bool VEC_W>
+__global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ int ints[3][kWarps];
+  __shared__ float tops[kWarps];
   early_launch();
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const HeadRows& r = a.r;
+  if ((int)blockIdx.x >= a.row_blocks) {
+    const int chunks = a.padded_cols / 8, copiers = gridDim.x - a.row_blocks;
+    const long long n = (long long)a.vocab * chunks, plane = (long long)a.vocab * a.padded_cols;
+    for (long long i = (blockIdx.x - a.row_blocks) * (long long)kThreads + threadIdx.x; i < n;
+         i += (long long)copiers * kThreads) {
+      const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
+      copy8<IO, PLANES, VEC_W>((const IO*)a.w + row * a.ld_w + c, a.cols - c,
+                               a.w_out + (long long)row * a.padded_cols + c, plane);
+    }
+    wait_for_before();  // this one does not end ahead of the kernel before
+    return;
+  }
   wait_for_before();
-  const int count = r.state->count, lane = threadIdx.x & 31;
-  const int rows = ((count > 0 ? count : 1) + 63) / 64 * 64;
-  const int step = gridDim.x * (kThreads / 32);
-  for (int row = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); row < rows; row += step) {
-    __nv_bfloat16* out = r.h + (long long)row * padded_cols;
-    const int from = row < count ? r.src[row] : -1;
+  const long long first = (long long)blockIdx.x * a.per_block;
+  int all = 0, before = 0, bad = 0;
+  float top = 0.0f;
+#pragma unroll 8
+  for (long long t = threadIdx.x; t < a.rows; t += kThreads) {
+    const int kind = kind_of(a, t);
+    all += kind == kCounts;
+    before += kind == kCounts && t < first;
+    bad |= kind == kBad;
+    if (a.d_loss) {
+      const float g = fabsf(a.d_loss[t]);
+      if (kind == kCounts && g < INFINITY) top = fmaxf(top, g);
+    }
+  }
+  all = __reduce_add_sync(0xffffffffu, all);
+  before = __reduce_add_sync(0xffffffffu, before);
+  top = warp_max(top);
+  bad = __any_sync(0xffffffffu, bad);
+  if (lane == 0) ints[0][warp] = all, ints[1][warp] = before, ints[2][warp] = bad, tops[warp] = top;
+  __syncthreads();
+  all = before = bad = 0, top = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kWarps; w++) {
+    all += ints[0][w], before += ints[1][w], bad |= ints[2][w];
+    top = fmaxf(top, tops[w]);
+  }
+  if (!(top > 0.0f)) top = 1.0f;
+  if (blockIdx.x == 0 && threadIdx.x == 0) {
+    r.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
+    r.state->count = all;
+    r.state->g_top = top;
+    r.state->scale = top * a.tau;
+  }
+  // its own rows' places, kThreads of them at a time
+  const int mine = before;
+  for (int base = 0; base < a.per_block; base += kThreads) {
+    const long long t = first + base + threadIdx.x;
+    const bool own = base + (int)threadIdx.x < a.per_block && t < a.rows;
+    const int kind = own ? kind_of(a, t) : kNone;
+    const unsigned votes = __ballot_sync(0xffffffffu, kind == kCounts);
+    __syncthreads();  // the counts before may still be read
+    if (lane == 0) ints[0][warp] = __popc(votes);
+    __syncthreads();
+    int at = before + __popc(votes & ((1u << lane) - 1u));
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+      if (w < warp) at += ints[0][w];
+      before += ints[0][w];
+    }
+    if (own) {
+      r.pos[t] = kind == kCounts ? at : kind == kBad ? kBadRow : kIgnored;
+      if (kind == kCounts) r.src[at] = (int)t;
+      if (a.target) a.idx[t] = kind == kCounts ? (int)a.target[t] : kNoEntry;
+    }
+  }
+  __syncthreads();
+  const bool last = (int)blockIdx.x == a.row_blocks - 1;
+  const int padded = ((all > 0 ? all : 1) + 63) / 64 * 64, end = last ? padded : before;
+  const long long plane = (a.rows + 63) / 64 * 64 * a.padded_cols;
+  for (int row = mine + warp; row < end; row += kWarps) {
+    __nv_bfloat16* out = r.h + (long long)row * a.padded_cols;
+    const int from = row < before ? r.src[row] : -1;
     if (from < 0) {
-      for (int c = 8 * lane; c < padded_cols; c += 256)
+      if (lane == 0) r.src[row] = -1;
+      for (int c = 8 * lane; c < a.padded_cols; c += 256)
 #pragma unroll
         for (int p = 0; p < PLANES; p++)
           *reinterpret_cast<uint4*>(out + p * plane + c) = make_uint4(0u, 0u, 0u, 0u);
     } else {
-      const IO* x = h + from * ld_h;
+      const IO* x = (const IO*)a.h + from * a.ld_h;
 #pragma unroll 4
-      for (int c = 8 * lane; c < padded_cols; c += 256)
-        copy8<IO, PLANES, VEC>(x + c, cols - c, out + c, plane);
+      for (int c = 8 * lane; c < a.padded_cols; c += 256)
+        copy8<IO, PLANES, VEC_H>(x + c, a.cols - c, out + c, plane);
     }
-    if (lse && lane == 0) {
-      r.rl[row] = from < 0 ? 0.0f : lse[from] * kLog2e;
-      r.rg[row] = from < 0 ? 0.0f : d_loss[from] / r.state->g_top;
+    if (a.lse && lane == 0) {
+      r.rl[row] = from < 0 ? 0.0f : a.lse[from] * kLog2e;
+      r.rg[row] = from < 0 ? 0.0f : a.d_loss[from] / top;
     }
   }
-}
-
-// A thread copies 8 columns of a row of W at a time.
-template <typename IO, int PLANES, bool VEC>
-__global__ void __launch_bounds__(kThreads) head_copy_w_kernel(const IO* w, long long ld_w, int rows,
-                                                               int cols, int padded_cols,
-                                                               __nv_bfloat16* out) {
-  early_launch();
-  const int chunks = padded_cols / 8;
-  const long long n = (long long)rows * chunks, plane = (long long)rows * padded_cols;
-  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
-       i += (long long)gridDim.x * kThreads) {
-    const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
-    copy8<IO, PLANES, VEC>(w + row * ld_w + c, cols - c, out + (long long)row * padded_cols + c,
-                           plane);
-  }
-  wait_for_before();  // this one does not end ahead of the kernel before
 }
 
 // ---- loss -------------------------------------------------------------------------------------------
@@ -355,52 +353,58 @@ __device__ __forceinline__ void put8(IO* out, int left, const float (&v)[8]) {
   }
 }
 
-template <typename IO, bool VEC>
-__global__ void __launch_bounds__(kThreads) head_finish_kernel(const float* part, int splits,
-                                                               long long step, long long rows,
-                                                               int cols, int padded_cols, HeadRows r,
-                                                               IO* d_h, long long ld, IO* d_w,
-                                                               long long n_w) {
+struct FinishArgs {
+  HeadRows r;
+  const float* h_part;
+  int h_splits;
+  long long h_step, rows;
+  void* d_h;
+  long long ld_h;
+  const float* w_part;
+  int w_per, words;
+  long long w_step;
+  void* d_w;        // the first of the words
+  void* all_w;      // the whole of d_W where this is the call's last kernel
+  long long n_w;
+  int cols, padded_cols, last;
+};
+// A thread takes 8 columns of a row at a time, first of d_h's rows, then of d_W's.
+template <typename IO, bool VEC_H, bool VEC_W>
+__global__ void __launch_bounds__(kThreads) head_finish_kernel(const FinishArgs a) {
   early_launch();
   wait_for_before();
-  const bool lost = r.state->status == SSM_ERR_TIMEOUT;
-  const float scale = r.state->scale;
-  const int chunks = padded_cols / 8;
-  const long long n = rows * chunks, stride = (long long)gridDim.x * kThreads,
-                  mine = blockIdx.x * (long long)kThreads + threadIdx.x;
-  if (d_h)
-    for (long long i = mine; i < n; i += stride) {
+  const HeadState state = *a.r.state;
+  const bool lost = a.last && state.status == SSM_ERR_TIMEOUT;
+  const int chunks = a.padded_cols / 8;
+  const long long n_h = a.d_h ? a.rows * chunks : 0,
+                  n = n_h + (a.w_part ? (long long)a.words * chunks : 0),
+                  stride = (long long)gridDim.x * kThreads,
+                  first = blockIdx.x * (long long)kThreads + threadIdx.x;
+  const int stages = ((state.count > 0 ? state.count : 1) + kHeadBlock - 1) / kHeadBlock;
+  for (long long i = first; i < n; i += stride) {
+    float v[8];
+    if (i < n_h) {
       const long long row = i / chunks;
-      const int c = (int)(i - row * chunks) * 8, at = r.pos[row];
-      float v[8];
-      if (at >= 0) sum8(part + (long long)at * padded_cols + c, splits, step, scale, v);
+      const int c = (int)(i - row * chunks) * 8, at = a.r.pos[row];
+      if (at >= 0)
+        sum8(a.h_part + (long long)at * a.padded_cols + c, a.h_splits, a.h_step, state.scale, v);
       if (at < 0 || lost)
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = at == kIgnored && !lost ? 0.0f : nan_();
-      put8<IO, VEC>(d_h + row * ld + c, cols - c, v);
+      put8<IO, VEC_H>((IO*)a.d_h + row * a.ld_h + c, a.cols - c, v);
+    } else {
+      const long long row = (i - n_h) / chunks;
+      const int c = (int)(i - n_h - row * chunks) * 8;
+      const int splits = (stages + a.w_per - 1) / a.w_per;  // those that had rows
+      sum8(a.w_part + row * a.padded_cols + c, splits, a.w_step, state.scale, v);
+      if (lost)
+#pragma unroll
+        for (int j = 0; j < 8; j++) v[j] = nan_();
+      put8<IO, VEC_W>((IO*)a.d_w + row * a.cols + c, a.cols - c, v);
     }
-  if (lost && d_w)
-    for (long long i = mine; i < n_w; i += stride) st(d_w + i, nan_());
-}
-
-template <typename IO, bool VEC>
-__global__ void __launch_bounds__(kThreads) head_sum_w_kernel(const float* part, int per_split,
-                                                              long long step, int rows, int cols,
-                                                              int padded_cols, HeadRows r, IO* d_w) {
-  early_launch();
-  wait_for_before();
-  const float scale = r.state->scale;
-  const int stages = ((r.state->count > 0 ? r.state->count : 1) + kHeadBlock - 1) / kHeadBlock;
-  const int splits = (stages + per_split - 1) / per_split;  // those that had rows
-  const int chunks = padded_cols / 8;
-  const long long n = (long long)rows * chunks;
-  for (long long i = blockIdx.x * (long long)kThreads + threadIdx.x; i < n;
-       i += (long long)gridDim.x * kThreads) {
-    const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
-    float v[8];
-    sum8(part + (long long)row * padded_cols + c, splits, step, scale, v);
-    put8<IO, VEC>(d_w + (long long)row * cols + c, cols - c, v);
   }
+  if (lost && a.all_w)
+    for (long long i = first; i < a.n_w; i += stride) st((IO*)a.all_w + i, nan_());
 }
 
 // A launch that is set up while the kernel before it runs.
@@ -444,44 +448,34 @@ cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, co
   return cudaGetLastError();
 }
 
-cudaError_t launch_head_begin(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
-                              const float* d_loss, int* idx, const HeadRows& r, bool first,
-                              cudaStream_t st) {
-  const float tau = d.entries ? d.temperature : 1.0f;
-  if (!first)
-    return go(head_begin_kernel, 1, kBeginThreads, st, target, valid, d.rows, d.vocab,
-              d.ignore_index, tau, d_loss, idx, r);
-  head_begin_kernel<<<1, kBeginThreads, 0, st>>>(target, valid, d.rows, d.vocab, d.ignore_index, tau,
-                                                 d_loss, idx, r);
+cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
+                             const void* h, long long ld_h, const float* lse, const float* d_loss,
+                             const void* w, long long ld_w, int* idx, const HeadRows& r,
+                             __nv_bfloat16* w_out, int sms, cudaStream_t st) {
+  RowsArgs a{target, valid, d.rows, d.ignore_index, d.vocab, d.cols, pad8(d.cols)};
+  const long long per = (d.rows + 511) / 512;  // at most 512 blocks, as each looks at every row
+  a.per_block = per < kThreads / 32 ? kThreads / 32 : (int)per;
+  a.row_blocks = (int)((d.rows + a.per_block - 1) / a.per_block);
+  a.tau = d.entries ? d.temperature : 1.0f;
+  a.h = h, a.ld_h = ld_h, a.lse = lse, a.d_loss = d_loss;
+  a.w = w, a.ld_w = ld_w, a.w_out = w_out;
+  a.idx = idx, a.r = r;
+  const long long chunks = (long long)d.vocab * (a.padded_cols / 8);
+  const long long copiers = w_out ? at_most((chunks + kThreads - 1) / kThreads, sms) : 0;
+  const bool vec_h = vec_rows(h, ld_h, d.cols, d.io), vec_w = vec_rows(w, ld_w, d.cols, d.io);
+  void (*kernel)(RowsArgs);
+  if (d.io == SSM_F32)
+    kernel = vec_h ? (vec_w ? head_rows_kernel<float, 3, true, true> :
+                              head_rows_kernel<float, 3, true, false>) :
+                     (vec_w ? head_rows_kernel<float, 3, false, true> :
+                              head_rows_kernel<float, 3, false, false>);
+  else  // W that can be copied in chunks is not copied
+    kernel = vec_h ? head_rows_kernel<__nv_bfloat16, 1, true, false> :
+                     head_rows_kernel<__nv_bfloat16, 1, false, false>;
+  if (valid) return go(kernel, a.row_blocks + copiers, kThreads, st, a);
+  kernel<<<(unsigned)(a.row_blocks + copiers), kThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
-}
-
-cudaError_t launch_head_pack(const ssm_head_desc& d, const void* h, long long ld_h,
-                             const float* lse, const float* d_loss, const HeadRows& r, int sms,
-                             cudaStream_t st) {
-  const long long rows = pad_rows(d.rows), blocks = at_most(rows / (kThreads / 32), sms);
-  const int padded = pad8(d.cols);
-  const bool vec = vec_rows(h, ld_h, d.cols, d.io);
-  if (d.io == SSM_F32)
-    return go(vec ? head_pack_kernel<float, 3, true> : head_pack_kernel<float, 3, false>, blocks,
-              kThreads, st, (const float*)h, ld_h, d.cols, padded, rows * padded, lse, d_loss, r);
-  return go(vec ? head_pack_kernel<__nv_bfloat16, 1, true> : head_pack_kernel<__nv_bfloat16, 1, false>,
-            blocks, kThreads, st, (const __nv_bfloat16*)h, ld_h, d.cols, padded, rows * padded, lse,
-            d_loss, r);
-}
-
-cudaError_t launch_head_copy_w(const ssm_head_desc& d, const void* w, long long ld_w,
-                               __nv_bfloat16* out, int sms, cudaStream_t st) {
-  const int padded = pad8(d.cols);
-  const long long blocks = at_most(((long long)d.vocab * (padded / 8) + kThreads - 1) / kThreads, sms);
-  const bool vec = vec_rows(w, ld_w, d.cols, d.io);
-  if (d.io == SSM_F32)
-    return go(vec ? head_copy_w_kernel<float, 3, true> : head_copy_w_kernel<float, 3, false>, blocks,
-              kThreads, st, (const float*)w, ld_w, d.vocab, d.cols, padded, out);
-  return go(vec ? head_copy_w_kernel<__nv_bfloat16, 1, true> :
-                  head_copy_w_kernel<__nv_bfloat16, 1, false>,
-            blocks, kThreads, st, (const __nv_bfloat16*)w, ld_w, d.vocab, d.cols, padded, out);
 }
 
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
@@ -492,36 +486,29 @@ cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_
             known, d.rows, d.entries ? d.entries : 1, kLog2e / tau, tau, r, loss, lse);
 }
 
-cudaError_t launch_head_finish(const ssm_head_desc& d, const float* part, int splits,
-                               const HeadRows& r, void* d_h, long long ld_d_h, void* d_w, int sms,
+cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const float* h_part,
+                               int h_splits, void* d_h, long long ld_d_h, const float* w_part,
+                               int w_per, int piece, void* d_w, int v0, int n, bool last, int sms,
                                cudaStream_t st) {
-  const int padded = pad8(d.cols);
-  const long long step = pad_rows(d.rows) * padded, n_w = (long long)d.vocab * d.cols;
-  const long long blocks = at_most(d_h ? (d.rows * (padded / 8) + kThreads - 1) / kThreads : sms, sms);
-  const bool vec = vec_rows(d_h, ld_d_h, d.cols, d.io);
-  if (d.io == SSM_F32)
-    return go(vec ? head_finish_kernel<float, true> : head_finish_kernel<float, false>, blocks,
-              kThreads, st, part, splits, step, d.rows, d.cols, padded, r, (float*)d_h, ld_d_h,
-              (float*)d_w, n_w);
-  return go(vec ? head_finish_kernel<__nv_bfloat16, true> : head_finish_kernel<__nv_bfloat16, false>,
-            blocks, kThreads, st, part, splits, step, d.rows, d.cols, padded, r,
-            (__nv_bfloat16*)d_h, ld_d_h, (__nv_bfloat16*)d_w, n_w);
-}
-
-cudaError_t launch_head_sum_w(const ssm_head_desc& d, const float* part, int per_split, int n_part,
-                              const HeadRows& r, void* d_w, int v0, int n, int sms,
-                              cudaStream_t st) {
-  const int padded = pad8(d.cols);
-  const long long step = (long long)n_part * padded,
-                  blocks = at_most(((long long)n * (padded / 8) + kThreads - 1) / kThreads, sms);
-  const long long at = (long long)v0 * d.cols;
-  const bool vec = vec_rows(d_w, d.cols, d.cols, d.io);
-  if (d.io == SSM_F32)
-    return go(vec ? head_sum_w_kernel<float, true> : head_sum_w_kernel<float, false>, blocks, kThreads,
-              st, part, per_split, step, n, d.cols, padded, r, (float*)d_w + at);
-  return go(vec ? head_sum_w_kernel<__nv_bfloat16, true> : head_sum_w_kernel<__nv_bfloat16, false>,
-            blocks, kThreads, st, part, per_split, step, n, d.cols, padded, r,
-            (__nv_bfloat16*)d_w + at);
+  FinishArgs a{r};
+  const size_t size = d.io == SSM_F32 ? 4 : 2;
+  a.cols = d.cols, a.padded_cols = pad8(d.cols), a.last = last;
+  a.h_part = h_part, a.h_splits = h_splits, a.h_step = pad_rows(d.rows) * a.padded_cols;
+  a.rows = d.rows, a.d_h = d_h, a.ld_h = ld_d_h;
+  a.w_part = w_part, a.w_per = w_per, a.words = n, a.w_step = (long long)piece * a.padded_cols;
+  a.d_w = (char*)d_w + (size_t)v0 * d.cols * size;
+  a.all_w = d_w, a.n_w = (long long)d.vocab * d.cols;
+  const long long work = ((d_h ? d.rows : 0) + (w_part ? n : 0)) * (a.padded_cols / 8);
+  const long long blocks = at_most(work ? (work + kThreads - 1) / kThreads : sms, sms);
+  const bool vec_h = vec_rows(d_h, ld_d_h, d.cols, d.io), vec_w = vec_rows(d_w, d.cols, d.cols, d.io);
+  void (*kernel)(FinishArgs);
+#define SSM_PICK(IO)                                                                             \
+  vec_h ? (vec_w ? head_finish_kernel<IO, true, true> : head_finish_kernel<IO, true, false>) :   \
+          (vec_w ? head_finish_kernel<IO, false, true> : head_finish_kernel<IO, false, false>)
+  if (d.io == SSM_F32) kernel = SSM_PICK(float);
+  else kernel = SSM_PICK(__nv_bfloat16);
+#undef SSM_PICK
+  return go(kernel, blocks, kThreads, st, a);
 }
 
 }  // namespace ssm

@@ -40,16 +40,28 @@ template <int PLANES> struct Lay {
   static constexpr int segment = PLANES == 1 ? 1 << 30 : 2;
 };
 
-struct TcArgs {
+// A product of a launch.
+struct Job {
   CUtensorMap a, b;
-  HeadState* state;
   int a_mn, b_mn;      // how the operands lie
   int m_fixed;         // rows of the result; 0: the packed rows
-  int n;               // columns of the result
+  int n, tile_n;       // columns of the result, and of a tile (256 or 128)
   int k_fixed;         // length of the sum; 0: the packed rows
-  int splits, per_split;  // of the sum, in stages
-  int a_row0, b_row0;  // first row of a's (W's) in the tensor
+  int per_split;       // stages of a split of the sum
+  int b_row0;          // first row of b's in the tensor
   int m_first;         // unit order: m fastest (else n)
+  // kOut: the splits' sums or, where there is one split, the result
+  float* part;
+  long long part_rows;
+  int ld_part, add;
+  void* out;
+  int ld_out, vec_out;
+};
+
+struct TcArgs {
+  Job job[2];
+  int jobs;
+  HeadState* state;
   int no_wait;
   // kLogits, kGrad
   float scale;         // log2(e) / tau
@@ -64,12 +76,7 @@ struct TcArgs {
   const float *rl, *rg;
   __nv_bfloat16* g;
   long long ld_g, plane_g;
-  // kOut
-  float* part;
-  long long part_rows;
-  int ld_part, add;
-  void* out;
-  int io, ld_out, vec_out;
+  int io;
 };
 
 // Matrix descriptors: 128-byte swizzle.  K-major: rows of 128 bytes, 8 of them 1024 bytes apart; 16 of the
@@ -131,10 +138,11 @@ __device__ __forceinline__ float pick(const float (&v)[32], int i) {
   return r;
 }
 
-// What becomes of a row's 128 columns, 32 at a time (chunk c).
+// What becomes of a row's columns of a tile's half, 32 at a time (chunk c).
 template <int USE, int PLANES> struct Taker {
   const TcArgs& a;
-  const int row, col0;  // of the result: its row, and the first of its 128 columns
+  const Job& job;
+  const int row, col0;  // of the result: its row, and the first of its columns
   const bool row_ok;
   // kLogits, kGrad
   int e, next, src;  // the row's next entry, from this thread's first column on
@@ -143,8 +151,9 @@ template <int USE, int PLANES> struct Taker {
   float* dst = nullptr;
   float scale = 1.0f;
 
-  __device__ __forceinline__ Taker(const TcArgs& a, int row, int col0, int rows, int split)
-      : a(a), row(row), col0(col0), row_ok(row < rows) {
+  __device__ __forceinline__ Taker(const TcArgs& a, const Job& job, int row, int col0, int rows,
+                                   int split)
+      : a(a), job(job), row(row), col0(col0), row_ok(row < rows) {
     if constexpr (USE != kOut) {
       // The first entry from this column on, by halving: the list is in order.
       src = row_ok ? a.src[row] : -1;
@@ -162,7 +171,7 @@ template <int USE, int PLANES> struct Taker {
       if constexpr (USE == kGrad)
         if (row_ok) rl = a.rl[row], rg = a.rg[row];
     } else {
-      if (a.part) dst = a.part + ((long long)split * a.part_rows + row) * a.ld_part + col0;
+      if (job.part) dst = job.part + ((long long)split * job.part_rows + row) * job.ld_part + col0;
       else scale = a.state->scale;
     }
   }
@@ -233,16 +242,16 @@ template <int USE, int PLANES> struct Taker {
           st_global32(g + r * a.plane_g + 16 * b, w);
         }
       }
-    } else if (a.part) {
+    } else if (job.part) {
       if (!row_ok) return;
 #pragma unroll
       for (int b = 0; b < 4; b++) {
-        if (col0 + 32 * c + 8 * b >= a.ld_part) break;
+        if (col0 + 32 * c + 8 * b >= job.ld_part) break;
         float* to = dst + 32 * c + 8 * b;
         float o[8];
 #pragma unroll
         for (int i = 0; i < 8; i++) o[i] = v[8 * b + i];
-        if (a.add) {
+        if (job.add) {
           Cols<float, 8> was;
           was.load(to);
 #pragma unroll
@@ -254,9 +263,9 @@ template <int USE, int PLANES> struct Taker {
       if (!row_ok) return;
 #pragma unroll
       for (int i = 0; i < 32; i++) v[i] *= scale;
-      const long long at = (long long)row * a.ld_out + col0 + 32 * c;
-      if (a.io == SSM_BF16) store((__nv_bfloat16*)a.out + at, c, v);
-      else store((float*)a.out + at, c, v);
+      const long long at = (long long)row * job.ld_out + col0 + 32 * c;
+      if (a.io == SSM_BF16) store((__nv_bfloat16*)job.out + at, c, v);
+      else store((float*)job.out + at, c, v);
     }
   }
   __device__ __forceinline__ void advance() {
@@ -267,8 +276,8 @@ template <int USE, int PLANES> struct Taker {
 #pragma unroll
     for (int b = 0; b < 4; b++) {
       const int col = col0 + 32 * c + 8 * b;
-      if (a.vec_out) {
-        if (col < a.n) {
+      if (job.vec_out) {
+        if (col < job.n) {
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; i++) o[i] = v[8 * b + i];
@@ -277,39 +286,54 @@ template <int USE, int PLANES> struct Taker {
       } else {
 #pragma unroll
         for (int i = 0; i < 8; i++)
-          if (col + i < a.n) st(to + 8 * b + i, v[8 * b + i]);
+          if (col + i < job.n) st(to + 8 * b + i, v[8 * b + i]);
       }
     }
   }
   __device__ __forceinline__ void done() {
     if constexpr (USE == kLogits)
       if (row_ok)
-        a.stats[(long long)((a.v0 + col0) / (kHeadTile / 2)) * a.ld_stats + row] =
+        a.stats[(long long)((a.v0 + col0) / (job.tile_n / 2)) * a.ld_stats + row] =
             make_float2(top, sum);
   }
 };
 
-// The units of a launch: tiles, and ranges of the sum.
+// The units of a launch: each product's tiles, and ranges of its sum; the first product's come first.
+struct Unit {
+  int job, mt, nt, split, begin, iters, tile_n;
+};
 struct Units {
-  int m, n, rows, stages, per, total, m_first;
+  int m[2], n[2], stages[2], rows[2], total[2];
   __device__ __forceinline__ Units(const TcArgs& a, int count) {
-    rows = a.m_fixed ? a.m_fixed : count;
-    m = (rows + kHeadTile - 1) / kHeadTile;
-    n = (a.n + kHeadTile - 1) / kHeadTile;
-    const int k = a.k_fixed ? a.k_fixed : count;
-    stages = (k + kHeadBlock - 1) / kHeadBlock;
-    per = a.per_split;
-    total = m * n * ((stages + per - 1) / per);
-    m_first = a.m_first;
+#pragma unroll
+    for (int j = 0; j < 2; j++) {
+      total[j] = 0;
+      if (j >= a.jobs) continue;
+      const Job& b = a.job[j];
+      rows[j] = b.m_fixed ? b.m_fixed : count;
+      m[j] = (rows[j] + kHeadTile - 1) / kHeadTile;
+      n[j] = (b.n + b.tile_n - 1) / b.tile_n;
+      const int k = b.k_fixed ? b.k_fixed : count;
+      stages[j] = (k + kHeadBlock - 1) / kHeadBlock;
+      total[j] = m[j] * n[j] * ((stages[j] + b.per_split - 1) / b.per_split);
+    }
   }
-  __device__ __forceinline__ void of(int u, int& mt, int& nt, int& split, int& begin,
-                                     int& iters) const {
-    split = u / (m * n);
-    const int t = u - split * (m * n);
-    if (m_first) nt = t / m, mt = t - nt * m;
-    else mt = t / n, nt = t - mt * n;
-    begin = split * per;
-    iters = stages - begin < per ? stages - begin : per;
+  __device__ __forceinline__ int all() const { return total[0] + total[1]; }
+  __device__ __forceinline__ Unit of(const TcArgs& a, int u) const {
+    Unit x;
+    x.job = u >= total[0];
+    const Job& b = a.job[x.job];
+    if (x.job) u -= total[0];
+    const int mj = x.job ? m[1] : m[0], nj = x.job ? n[1] : n[0],
+              sj = x.job ? stages[1] : stages[0];
+    x.split = u / (mj * nj);
+    const int t = u - x.split * (mj * nj);
+    if (b.m_first) x.nt = t / mj, x.mt = t - x.nt * mj;
+    else x.mt = t / nj, x.nt = t - x.mt * nj;
+    x.begin = x.split * b.per_split;
+    x.iters = sj - x.begin < b.per_split ? sj - x.begin : b.per_split;
+    x.tile_n = b.tile_n;
+    return x;
   }
 };
 
@@ -339,8 +363,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
     mbar_init(&last, 1);
     bad = 0;
     fence_barrier_init();
-    prefetch_tmap(&a.a);
-    prefetch_tmap(&a.b);
+    for (int j = 0; j < a.jobs; j++) {
+      prefetch_tmap(&a.job[j].a);
+      prefetch_tmap(&a.job[j].b);
+    }
   }
   __syncwarp();
   if (warp == 1) Mma<2>::alloc(&tbase, kTmCols);
@@ -353,7 +379,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
   wait_for_copies();
   const int count = a.state->count > 0 ? a.state->count : 1;
   const Units units(a, count);
-  int mt, nt, split, begin, iters;
+  const int n_units = units.all();
 
   if (warp < 4) {
     if constexpr (PLANES > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
@@ -361,26 +387,31 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       Ring<S> r;
       int it = 0;
       bool ok = true;
-      for (int u = pair; u < units.total && ok; u += pairs) {
-        units.of(u, mt, nt, split, begin, iters);
-        const int m0 = mt * kHeadTile + rank * (kHeadTile / 2), n0 = nt * kHeadTile + rank * (kHeadTile / 2);
-        for (int k = begin; k < begin + iters; k++, it++, r.next()) {
+      for (int u = pair; u < n_units && ok; u += pairs) {
+        const Unit x = units.of(a, u);
+        const Job& b = a.job[x.job];
+        const int half = x.tile_n / 2;  // columns of B here
+        const int m0 = x.mt * kHeadTile + rank * (kHeadTile / 2), n0 = x.nt * x.tile_n + rank * half;
+        const bool a_mn = b.a_mn, b_mn = b.b_mn;
+        const uint32_t bytes = PLANES * (kOperand + (half >> 6) * kSlab);
+        for (int k = x.begin; k < x.begin + x.iters; k++, it++, r.next()) {
           if (it >= S && !wait_for(&empty[r.s], r.phase ^ 1, &bad)) {
             ok = false;
             break;
           }
           if (elect_one()) {
-            mbar_expect_tx(&here[r.s], L::stage);
+            mbar_expect_tx(&here[r.s], bytes);
             unsigned char* to = smem + r.s * L::stage;
 #pragma unroll
             for (int p = 0; p < PLANES; p++)
 #pragma unroll
               for (int c = 0; c < 2; c++) {
-                tma_load_3d(to + p * kOperand + c * kSlab, &a.a, a.a_mn ? m0 + 64 * c : 64 * k,
-                            a.a_row0 + (a.a_mn ? 64 * k : m0 + 64 * c), p, &here[r.s]);
-                tma_load_3d(to + (PLANES + p) * kOperand + c * kSlab, &a.b,
-                            a.b_mn ? n0 + 64 * c : 64 * k,
-                            a.b_row0 + (a.b_mn ? 64 * k : n0 + 64 * c), p, &here[r.s]);
+                tma_load_3d(to + p * kOperand + c * kSlab, &b.a, a_mn ? m0 + 64 * c : 64 * k,
+                            a_mn ? 64 * k : m0 + 64 * c, p, &here[r.s]);
+                if (64 * c < half)
+                  tma_load_3d(to + (PLANES + p) * kOperand + c * kSlab, &b.b,
+                              b_mn ? n0 + 64 * c : 64 * k,
+                              b.b_row0 + (b_mn ? 64 * k : n0 + 64 * c), p, &here[r.s]);
               }
           }
           __syncwarp();
@@ -395,15 +426,16 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       if (!ok) give_up(&bad);
     } else if (warp == 1 && rank == 0) {
       Ring<S> r;
-      const bool a_mn = a.a_mn, b_mn = a.b_mn;
-      const uint32_t idesc = idesc_bf16(kHeadTile, kHeadTile, a_mn, b_mn);
-      const uint64_t da0 = desc_of(smem_u32(smem), a_mn),
-                     db0 = desc_of(smem_u32(smem) + PLANES * kOperand, b_mn);
-      const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
       int seg = 0;  // counted over the units
       bool ok = true;
-      for (int u = pair; u < units.total && ok; u += pairs) {
-        units.of(u, mt, nt, split, begin, iters);
+      for (int u = pair; u < n_units && ok; u += pairs) {
+        const Unit x = units.of(a, u);
+        const int iters = x.iters;
+        const bool a_mn = a.job[x.job].a_mn, b_mn = a.job[x.job].b_mn;
+        const uint32_t idesc = idesc_bf16(kHeadTile, x.tile_n, a_mn, b_mn);
+        const uint64_t da0 = desc_of(smem_u32(smem), a_mn),
+                       db0 = desc_of(smem_u32(smem) + PLANES * kOperand, b_mn);
+        const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
         for (int it = 0; it < iters && ok; seg++) {
           const uint32_t d = tm + (seg & 1) * kHeadTile;
           const int end = iters - it < L::segment ? iters : it + L::segment;
@@ -418,12 +450,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
               constexpr int kPairs = PLANES == 1 ? 1 : 6;
               constexpr int pa[6] = {0, 0, 1, 1, 0, 2}, pb[6] = {0, 1, 0, 1, 2, 0};
 #pragma unroll
-              for (int x = 0; x < kPairs; x++)
+              for (int t = 0; t < kPairs; t++)
 #pragma unroll
                 for (int kk = 0; kk < kHeadBlock / 16; kk++)
-                  Mma<2>::mma(idesc, d, da + (uint32_t)(pa[x] * (kOperand >> 4)) + sa * kk,
-                              db + (uint32_t)(pb[x] * (kOperand >> 4)) + sb * kk,
-                              !first || x > 0 || kk > 0);
+                  Mma<2>::mma(idesc, d, da + (uint32_t)(pa[t] * (kOperand >> 4)) + sa * kk,
+                              db + (uint32_t)(pb[t] * (kOperand >> 4)) + sb * kk,
+                              !first || t > 0 || kk > 0);
               Mma<2>::commit(&empty[r.s]);
             }
             __syncwarp();
@@ -439,8 +471,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       Ring<S> r;
       const uint32_t first_there = bar_of_first<2>(there);
       bool ok = true;
-      for (int u = pair; u < units.total && ok; u += pairs) {
-        units.of(u, mt, nt, split, begin, iters);
+      for (int u = pair; u < n_units && ok; u += pairs) {
+        const int iters = units.of(a, u).iters;
         for (int it = 0; it < iters && ok; it++, r.next()) {
           ok = wait_for(&here[r.s], r.phase, &bad);
           if (ok && elect_one()) mbar_arrive_first<2>(first_there + 8 * r.s);
@@ -452,16 +484,20 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
   } else {
     if constexpr (PLANES > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
     const int quad = warp & 3, half = (warp - 4) >> 2;
-    const uint32_t tacc = tm + ((uint32_t)(32 * quad) << 16) + 128 * half;
+    const uint32_t lanes = tm + ((uint32_t)(32 * quad) << 16);
     const uint32_t first_drained = bar_of_first<2>(drained);
     int seg = 0;
     bool ok = !a.no_wait;
-    for (int u = pair; u < units.total && ok; u += pairs) {
-      units.of(u, mt, nt, split, begin, iters);
+    for (int u = pair; u < n_units && ok; u += pairs) {
+      const Unit x = units.of(a, u);
+      const int iters = x.iters, width = x.tile_n / 2, chunks = width / 32;
+      const uint32_t tacc = lanes + width * half;
       // the rows that a sum over rows reads: zeros past the packed ones
-      const int rows = USE == kGrad ? (units.rows + 63) / 64 * 64 : units.rows;
-      Taker<USE, PLANES> taker(a, mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
-                               nt * kHeadTile + 128 * half, rows, split);
+      const int rows_here = x.job ? units.rows[1] : units.rows[0];
+      const int rows = USE == kGrad ? (rows_here + 63) / 64 * 64 : rows_here;
+      Taker<USE, PLANES> taker(a, a.job[x.job],
+                               x.mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
+                               x.nt * x.tile_n + width * half, rows, x.split);
       if constexpr (PLANES == 1) {
         ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
         __syncwarp();
@@ -469,10 +505,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         if (!ok) break;
         const uint32_t t = tacc + (seg & 1) * kHeadTile;
 #pragma unroll 1
-        for (int c = 0; c < 4; c++) {
+        for (int c = 0; c < chunks; c++) {
           float v[32];
           tmem_ld32(t + 32 * c, v);
-          if (c == 3) {
+          if (c == chunks - 1) {
             tmem_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & 1));
@@ -495,6 +531,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           const uint32_t t = tacc + (seg & 1) * kHeadTile;
 #pragma unroll
           for (int c = 0; c < 8; c++) {
+            if (c >= 2 * chunks) break;
             float v[16];
             tmem_ld16(t + 16 * c, v);
 #pragma unroll
@@ -507,6 +544,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         if (!ok) break;
 #pragma unroll
         for (int c = 0; c < 4; c++) {
+          if (c >= chunks) break;
           taker.chunk(c, acc[c]);
           __syncwarp();
         }
@@ -574,30 +612,38 @@ bool encode(CUtensorMap* map, const HeadMatrix& x, int planes) {
 }
 int planes_of(const ssm_head_desc& d) { return d.io == SSM_F32 ? 3 : 1; }
 
-TcArgs logits_args(const ssm_head_desc& d, const HeadRows& r, const int* idx) {
+TcArgs args_of(const ssm_head_desc& d, const HeadRows& r) {
   TcArgs t{};
+  t.jobs = 1;
   t.state = r.state;
-  t.k_fixed = d.cols;
-  t.splits = 1;
-  t.per_split = (d.cols + kHeadBlock - 1) / kHeadBlock;
-  t.m_first = 1;
   t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
   t.scale = d.entries ? kLog2e / d.temperature : kLog2e;
   t.vocab = d.vocab;
   t.entries = d.entries ? d.entries : 1;
   t.src = r.src;
-  t.idx = idx;
+  t.io = d.io;
   return t;
+}
+// Z of the words from v0 on.
+bool logits_job(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w, int v0, int n,
+                int tile_n, Job& j) {
+  j.n = n;
+  j.tile_n = tile_n;
+  j.k_fixed = d.cols;
+  j.per_split = (d.cols + kHeadBlock - 1) / kHeadBlock;
+  j.b_row0 = v0;
+  j.m_first = 1;
+  return encode(&j.a, h, planes_of(d)) && encode(&j.b, w, planes_of(d));
 }
 
 }  // namespace
 
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const int* idx, float2* stats, float* zt, int sms,
-                               cudaStream_t st) {
-  TcArgs t = logits_args(d, r, idx);
-  if (!encode(&t.a, h, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
-  t.n = d.vocab;
+                               const HeadRows& r, const int* idx, int tile_n, float2* stats,
+                               float* zt, int sms, cudaStream_t st) {
+  TcArgs t = args_of(d, r);
+  if (!logits_job(d, h, w, 0, d.vocab, tile_n, t.job[0])) return cudaErrorInvalidValue;
+  t.idx = idx;
   t.stats = stats;
   t.ld_stats = h.rows;
   t.zt = zt;
@@ -605,12 +651,12 @@ cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, cons
 }
 
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                             const HeadRows& r, const int* idx, const float* p, __nv_bfloat16* g,
-                             int v0, int n, int sms, cudaStream_t st) {
-  TcArgs t = logits_args(d, r, idx);
-  if (!encode(&t.a, h, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
-  t.n = n;
-  t.v0 = t.b_row0 = v0;
+                             const HeadRows& r, const int* idx, const float* p, int tile_n,
+                             __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st) {
+  TcArgs t = args_of(d, r);
+  if (!logits_job(d, h, w, v0, n, tile_n, t.job[0])) return cudaErrorInvalidValue;
+  t.v0 = v0;
+  t.idx = idx;
   t.p = p;
   t.rl = r.rl;
   t.rg = r.rg;
@@ -620,46 +666,46 @@ cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const 
   return launch<kGrad>(d, t, sms, st);
 }
 
-cudaError_t launch_head_dh(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& w,
-                           const HeadRows& r, float* part, int splits, int per_split, int v0,
-                           bool add, int sms, cudaStream_t st) {
-  TcArgs t{};
-  if (!encode(&t.a, g, planes_of(d)) || !encode(&t.b, w, planes_of(d))) return cudaErrorInvalidValue;
-  t.state = r.state;
-  t.b_mn = 1;
-  t.n = d.cols;
-  t.k_fixed = g.cols;
-  t.splits = splits;
-  t.per_split = per_split;
-  t.b_row0 = v0;
-  t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
-  t.part = part;
-  t.part_rows = g.rows;
-  t.ld_part = pad8(d.cols);
-  t.add = add;
-  return launch<kOut>(d, t, sms, st);
-}
-
-cudaError_t launch_head_dw(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
-                           const HeadRows& r, void* d_w, float* part, int splits, int per_split,
-                           int v0, int n, int sms, cudaStream_t st) {
-  TcArgs t{};
-  if (!encode(&t.a, g, planes_of(d)) || !encode(&t.b, h, planes_of(d))) return cudaErrorInvalidValue;
-  t.state = r.state;
-  t.a_mn = t.b_mn = 1;
-  t.m_fixed = n;
-  t.n = d.cols;
-  t.splits = splits;
-  t.per_split = per_split;
-  t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
-  t.part = part;
-  t.part_rows = g.cols;
-  t.ld_part = pad8(d.cols);
+cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
+                            const HeadMatrix& w, const HeadRows& r, const HeadOut& o, int v0, int n,
+                            bool add, int sms, cudaStream_t st) {
+  TcArgs t = args_of(d, r);
+  t.jobs = 0;
+  const int planes = planes_of(d), padded = pad8(d.cols);
   const size_t size = d.io == SSM_F32 ? 4 : 2;
-  t.out = (char*)d_w + (size_t)v0 * d.cols * size;
-  t.io = d.io;
-  t.ld_out = d.cols;
-  t.vec_out = d.cols % 8 == 0 && (uintptr_t)d_w % (8 * size) == 0;
+  if (o.d_w) {
+    Job& j = t.job[t.jobs++];
+    if (!encode(&j.a, g, planes) || !encode(&j.b, h, planes)) return cudaErrorInvalidValue;
+    j.a_mn = j.b_mn = 1;
+    j.m_fixed = n;
+    j.n = d.cols;
+    j.tile_n = o.w.tile_n;
+    j.per_split = o.w.per;
+    j.part = o.w_part;
+    j.part_rows = g.cols;
+    j.ld_part = padded;
+    j.out = (char*)o.d_w + (size_t)v0 * d.cols * size;
+    j.ld_out = d.cols;
+    j.vec_out = d.cols % 8 == 0 && (uintptr_t)o.d_w % (8 * size) == 0;
+  }
+  if (o.h_part) {
+    Job& j = t.job[t.jobs++];
+    if (!encode(&j.a, g, planes) || !encode(&j.b, w, planes)) return cudaErrorInvalidValue;
+    j.b_mn = 1;
+    j.n = d.cols;
+    j.tile_n = o.h.tile_n;
+    j.k_fixed = g.cols;
+    j.per_split = o.h.per;
+    j.b_row0 = v0;
+    j.part = o.h_part;
+    j.part_rows = g.rows;
+    j.ld_part = padded;
+    j.add = add;
+  }
+  if (t.jobs == 2 && o.h_first) {
+    const Job j = t.job[0];
+    t.job[0] = t.job[1], t.job[1] = j;
+  }
   return launch<kOut>(d, t, sms, st);
 }
 
