@@ -54,7 +54,8 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
 // Loss and lse from the tiles' sums; zt: the entries' logits [rows][entries or 1].
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
                              const float* zt, const float* p, const float* known,
-                             const HeadRows& r, float* loss, float* lse, cudaStream_t st);
+                             const HeadRows& r, float* loss, float* lse, int sms,
+                             cudaStream_t st);
 // What the gradients' sums lack: d_h from the splits' sums [splits][padded rows][padded cols], and
 // rows v0 .. v0 + n of d_W from theirs [splits][piece][padded cols], either where given.  `last`: of the
 // call; where a wait of it gave up, d_h and all of d_w are filled with NaN.
@@ -62,6 +63,16 @@ cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const 
                                int h_splits, void* d_h, long long ld_d_h, const float* w_part,
                                int w_per, int piece, void* d_w, int v0, int n, bool last, int sms,
                                cudaStream_t st);
+
+// ---- head_few.cu ----------------------------------------------------------------------------------
+// A forward of few rows, unpacked (pos[row] is row): what head_rows and head_logits do together, with
+// stats [blocks][padded rows].
+constexpr size_t kFewSmem = 72 * 1024;  // of a block
+bool head_few(long long rows, int cols);
+int head_few_blocks(long long rows, int sms);
+cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
+                            const void* h, long long ld_h, const void* w, long long ld_w, int* idx,
+                            const HeadRows& r, float2* stats, float* zt, int sms, cudaStream_t st);
 
 // ---- head_tc.cu -----------------------------------------------------------------------------------
 struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart

@@ -11,7 +11,9 @@ namespace {
 using namespace ssm;
 
 constexpr long long kMaxTotal = 1LL << 40;  // elements between a tensor's first and last row
-constexpr long long kMaxPiece = 256LL << 20;  // bytes of G at a time (a tile's columns at least)
+// Bytes of G at a time (a tile's columns at least).  Fewer and larger pieces leave fewer ends of launches with
+// idle SMs: 16384 x 1024 over 32768 words 2.97 ms at 96 MiB, 2.76 at 256, 2.64 at 512, 2.66 at 1024.
+constexpr long long kMaxPiece = 512LL << 20;
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 size_t io_size(int io) { return io == SSM_BF16 ? 2 : (io == SSM_F32 ? 4 : 0); }
@@ -29,9 +31,9 @@ int num_sms() {
 }
 
 // ---- how the products are cut ---------------------------------------------------------------------
-// Costs are in stages, the time of a 256 x 256 tile's step over 64 of the sum.
-constexpr int kUnitCost = 3;             // what a unit costs by itself
-constexpr double kStageBytes = 1.5e6;    // what memory moves in a stage's time
+// Costs are in stages, the time of a 256 x 256 tile's step over 64 of the sum (six products for fp32).
+double unit_cost(int io) { return io == SSM_F32 ? 0.7 : 3.0; }           // of a unit by itself
+double stage_bytes(int io) { return io == SSM_F32 ? 9.0e6 : 1.5e6; }     // that memory moves meanwhile
 double tile_cost(int tile_n, int io) { return tile_n == kHeadTile ? 1.0 : io == SSM_F32 ? 0.55 : 0.65; }
 
 // Units of one or two kinds are dealt out to the pairs of CTAs in turn, the first kind first: the time of
@@ -57,7 +59,7 @@ int logits_tile(long long rows, int cols, int words, int io, int sms) {
   const long long pairs = sms / 2 > 0 ? sms / 2 : 1, m = (rows + kHeadTile - 1) / kHeadTile;
   const int stages = (cols + kHeadBlock - 1) / kHeadBlock;
   const auto time = [&](int tile) {
-    return dealt(m * ((words + tile - 1) / tile), stages * tile_cost(tile, io) + kUnitCost, 0, 0.0,
+    return dealt(m * ((words + tile - 1) / tile), stages * tile_cost(tile, io) + unit_cost(io), 0, 0.0,
                  pairs);
   };
   return time(128) < time(256) ? 128 : 256;
@@ -91,12 +93,13 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
         const int ph = per_of(st_h, sh);
         if (per_of(st_h, ph) != sh) continue;
         const long long nw = grads & 2 ? m_w * n * sw : 0, nh = grads & 1 ? m_h * n * sh : 0;
-        const double cw = pw * tile_cost(tile, io) + kUnitCost, ch = ph * tile_cost(tile, io) + kUnitCost;
+        const double cw = pw * tile_cost(tile, io) + unit_cost(io),
+                     ch = ph * tile_cost(tile, io) + unit_cost(io);
         const bool h_first = ch > cw;
         double time = h_first ? dealt(nh, ch, nw, cw, pairs) : dealt(nw, cw, nh, ch, pairs);
         // the splits' sums: written and read, those of d_h once for each piece and under its products
-        if (grads & 1) time += sh * mb_h * (several ? 1.0 : 2.0) / kStageBytes;
-        if (sw > 1) time += 2.0 * sw * mb_w / kStageBytes;
+        if (grads & 1) time += sh * mb_h * (several ? 1.0 : 2.0) / stage_bytes(io);
+        if (sw > 1) time += 2.0 * sw * mb_w / stage_bytes(io);
         if (least < 0.0 || time < least)
           least = time, best = {{tile, sh, ph}, {tile, sw, pw}, h_first};
       }
@@ -108,7 +111,7 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
 // The workspace, by bytes from its start.
 struct Plan {
   size_t pos, src, idx, p, known, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
-  int planes, tile_z, tiles, piece, pieces;
+  int planes, tile_z, n_stats, piece, pieces;
   Cuts cuts;
 };
 Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
@@ -130,12 +133,19 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.known = take(4 * T);
     p.valid = take(T);
   }
+  if (!grads && head_few(T, d.cols)) {
+    p.n_stats = head_few_blocks(T, sms);
+    p.stats = take((size_t)8 * p.n_stats * Tp);
+    p.zt = take(4 * T * n_e);
+    p.bytes = at;
+    return p;
+  }
   p.h = take((size_t)2 * p.planes * Tp * Dp);
   if (copy_w) p.w = take((size_t)2 * p.planes * d.vocab * Dp);
   if (!grads) {
     p.tile_z = logits_tile(T, d.cols, d.vocab, d.io, sms);
-    p.tiles = (d.vocab + p.tile_z - 1) / p.tile_z;
-    p.stats = take((size_t)8 * 2 * p.tiles * Tp);
+    p.n_stats = 2 * ((d.vocab + p.tile_z - 1) / p.tile_z);
+    p.stats = take((size_t)8 * p.n_stats * Tp);
     p.zt = take(4 * T * n_e);
   } else {
     p.rl = take(4 * Tp);
@@ -237,6 +247,13 @@ int run(Call c, bool distill, bool backward) {
 #define SSM_DO(call) \
   if ((call) != cudaSuccess) return SSM_ERR_CUDA
   if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, idx, prob, known, valid, st));
+  float2* stats = (float2*)(ws + p.stats);
+  float* zt = (float*)(ws + p.zt);
+  if (!backward && head_few(d.rows, d.cols)) {
+    SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, idx, r, stats, zt, sms, st));
+    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, prob, known, r, c.loss, c.lse_out, sms, st));
+    return SSM_OK;
+  }
   __nv_bfloat16* w_out = copy_w ? (__nv_bfloat16*)(ws + p.w) : nullptr;
   SSM_DO(launch_head_rows(d, c.target, valid, c.h, c.ld_h, backward ? c.lse : nullptr,
                           backward ? c.d_loss : nullptr, c.w, c.ld_w, idx, r, w_out, sms, st));
@@ -244,10 +261,8 @@ int run(Call c, bool distill, bool backward) {
   const HeadMatrix w = copy_w ? HeadMatrix{w_out, d.vocab, Dp, (long long)d.vocab * Dp, d.cols} :
                                 HeadMatrix{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
   if (!backward) {
-    float2* stats = (float2*)(ws + p.stats);
-    float* zt = (float*)(ws + p.zt);
     SSM_DO(launch_head_logits(d, h, w, r, idx, p.tile_z, stats, zt, sms, st));
-    SSM_DO(launch_head_loss(d, stats, 2 * p.tiles, zt, prob, known, r, c.loss, c.lse_out, st));
+    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, prob, known, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }
   __nv_bfloat16* gp = (__nv_bfloat16*)(ws + p.g);

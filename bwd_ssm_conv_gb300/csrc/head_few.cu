@@ -1,0 +1,282 @@
+// head_few.cu -- the forward for a few rows (at most 8, as tokens come): Z = h W^T with every row of W read
+// once, by plain fp32 arithmetic.  W's bytes bound it; a tensor-core tile would be all but empty, and its
+// rows would have to be packed first.
+//
+// h lies in shared memory as fp32.  A warp takes 4 words at a time, a lane every 32nd chunk of 8 columns
+// of each, which leaves 4 to 32 sums of words and rows to add over the lanes: at each step the
+// lanes keep half of them and give the other half away, until each has one, the logit of one word and row.
+// A lane keeps the maximum and the sum of the exponentials of what comes its way.
+// The logits of the rows' own words (or entries) are computed by themselves, a warp each.
+#include "head.cuh"
+
+namespace ssm {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int blocks_per_sm(int R) { return R <= 2 ? 3 : 2; }  // as its registers leave room for
+constexpr int kWarps = kThreads / 32;
+constexpr int kWords = 4;  // whose loads are in flight together
+
+struct FewArgs {
+  const void* h;
+  long long ld_h;
+  const void* w;
+  long long ld_w;
+  const int64_t* target;
+  const uint8_t* valid;
+  int* idx;
+  HeadState* state;
+  int* pos;
+  float2* stats;  // [blocks][ld_stats]
+  float* zt;
+  long long ignore, ld_stats;
+  int rows, cols, vocab, entries;
+  float scale;
+};
+
+// 8 columns, or what is left of them, as fp32.
+template <typename IO, bool VEC> struct Chunk {
+  Cols<IO, VEC ? 8 : 1> c[VEC ? 1 : 8];
+  __device__ __forceinline__ void load(const IO* p, int left) {
+    if constexpr (VEC) {
+      c[0].load(p);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        c[i].zero();
+        if (i < left) c[i].load(p + i);
+      }
+    }
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    if constexpr (VEC) {
+      c[0].get(v);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; i++) {
+        float x[1];
+        c[i].get(x);
+        v[i] = x[0];
+      }
+    }
+  }
+};
+
+// sum[j] (+)= over this lane's chunks of words[j]; R rows each, h [R][padded] in shared memory.
+template <typename IO, bool VEC, int R, int N>
+__device__ __forceinline__ void dots(const FewArgs& a, const float* h, int padded, const int (&words)[N],
+                                     float (&sum)[N][R]) {
+  const int lane = threadIdx.x & 31;
+  const IO* p[N];
+#pragma unroll
+  for (int j = 0; j < N; j++) {
+    p[j] = (const IO*)a.w + words[j] * a.ld_w;
+#pragma unroll
+    for (int r = 0; r < R; r++) sum[j][r] = 0.0f;
+  }
+#pragma unroll 2
+  for (int c = 8 * lane; c < padded; c += 256) {
+    Chunk<IO, VEC> x[N];
+#pragma unroll
+    for (int j = 0; j < N; j++) x[j].load(p[j] + c, a.cols - c);
+    float v[N][8];
+#pragma unroll
+    for (int j = 0; j < N; j++) x[j].get(v[j]);
+#pragma unroll
+    for (int r = 0; r < R; r++) {
+      const float4 h0 = *reinterpret_cast<const float4*>(h + r * padded + c),
+                   h1 = *reinterpret_cast<const float4*>(h + r * padded + c + 4);
+      const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+      for (int j = 0; j < N; j++)
+#pragma unroll
+        for (int i = 0; i < 8; i++) sum[j][r] = fmaf(v[j][i], hv[i], sum[j][r]);
+    }
+  }
+}
+
+template <typename IO, bool VEC, int R>
+__global__ void __launch_bounds__(kThreads, blocks_per_sm(R)) head_few_kernel(const FewArgs a) {
+  extern __shared__ __align__(16) float h[];  // [R][padded], then the warps' sums
+  __shared__ int kind[8];
+  asm volatile("griddepcontrol.launch_dependents;");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int padded = (a.cols + 7) / 8 * 8;
+  // A warp's words lie together, as many as the others' or one more.  The first of them are on their way
+  // while the rows are looked at.
+  const long long warps = (long long)gridDim.x * kWarps, me = (long long)blockIdx.x * kWarps + warp;
+  const int from = (int)(me * a.vocab / warps), to = (int)((me + 1) * a.vocab / warps);
+  for (int w = from; w < to && w < from + 2 * kWords; w++)
+    for (int c = lane * (128 / (int)sizeof(IO)); c < a.cols; c += 32 * (128 / (int)sizeof(IO)))
+      asm volatile("prefetch.global.L2 [%0];" ::"l"((const IO*)a.w + w * a.ld_w + c));
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (threadIdx.x < 8) {  // which rows count: each block sees for itself
+    const int t = threadIdx.x;
+    int pos = kIgnored, word = kNoEntry;
+    if (t < a.rows) {
+      if (a.target) {
+        const int64_t y = a.target[t];
+        if (y != a.ignore) {
+          pos = y >= 0 && y < a.vocab ? t : kBadRow;
+          if (pos == t) word = (int)y;
+        }
+      } else {
+        pos = a.valid[t] == 1 ? t : a.valid[t] == 2 ? kBadRow : kIgnored;
+      }
+      if (blockIdx.x == 0) {
+        a.pos[t] = pos;
+        if (a.target) a.idx[t] = word;
+      }
+    }
+    kind[t] = pos;
+    const bool bad = __any_sync(0xffu, pos == kBadRow);
+    if (blockIdx.x == 0 && t == 0) a.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * padded; i += kThreads) {
+    const int r = i / padded, c = i - r * padded;
+    h[i] = r < a.rows && kind[r] >= 0 && c < a.cols ? ld((const IO*)a.h + r * a.ld_h + c) : 0.0f;
+  }
+  __syncthreads();
+
+  // the entries' logits, from the last warp on: first, as a word more would take longer at the end
+  for (long long i = warps - 1 - me; i < a.rows * a.entries; i += warps) {
+    const int row = (int)(i / a.entries);
+    const int word = kind[row] < 0 ? kNoEntry : a.target ? (int)a.target[row] : a.idx[i];
+    if (word == kNoEntry) continue;
+    const int words[1] = {word};
+    float d[1][1];
+    dots<IO, VEC, 1, 1>(a, h + row * padded, padded, words, d);
+    float v = d[0][0];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0) a.zt[i] = v;
+  }
+
+  constexpr int W = 4;               // words of a warp at a time
+  constexpr int N = W * R;           // sums: number j * R + r is word j's of row r
+  constexpr int kSame = 32 / N;      // lanes that end with the same one
+  const int mine = lane / kSame;
+  float top = -INFINITY, total = 0.0f;
+  for (int w0 = from; w0 < to; w0 += W) {
+    float s[N];
+#pragma unroll
+    for (int j = 0; j < W; j += kWords) {
+      int words[kWords];
+      float d[kWords][R];
+#pragma unroll
+      for (int i = 0; i < kWords; i++) words[i] = min(w0 + j + i, to - 1);
+      dots<IO, VEC, R, kWords>(a, h, padded, words, d);
+#pragma unroll
+      for (int i = 0; i < kWords; i++)
+#pragma unroll
+        for (int r = 0; r < R; r++) s[(j + i) * R + r] = d[i][r];
+    }
+#pragma unroll
+    for (int off = 16, n = N / 2; off > 0; off >>= 1, n >>= 1) {
+      if (n == 0) s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
+#pragma unroll
+      for (int i = 0; i < n; i++) {
+        const bool up = lane & off;
+        const float give = up ? s[i] : s[i + n], keep = up ? s[i + n] : s[i];
+        s[i] = keep + __shfl_xor_sync(0xffffffffu, give, off);
+      }
+    }
+    if (w0 + mine / R < to && lane % kSame == 0) {
+      const float above = fmaxf(top, s[0]), base = above == -INFINITY ? 0.0f : above;
+      total = total * ex2((top - base) * a.scale) + ex2((s[0] - base) * a.scale);
+      top = above;
+    }
+  }
+  // over the lanes of a row, then the warps
+#pragma unroll
+  for (int off = 16; off >= R * kSame; off >>= 1) {
+    const float t = __shfl_xor_sync(0xffffffffu, top, off), u = __shfl_xor_sync(0xffffffffu, total, off);
+    const float above = fmaxf(top, t), base = above == -INFINITY ? 0.0f : above;
+    total = total * ex2((top - base) * a.scale) + u * ex2((t - base) * a.scale);
+    top = above;
+  }
+  float2* sums = reinterpret_cast<float2*>(h + R * padded);
+  if (mine < R && lane % kSame == 0) sums[warp * R + mine] = make_float2(top, total);
+  __syncthreads();
+  if (threadIdx.x < R && (int)threadIdx.x < a.rows) {
+    top = -INFINITY, total = 0.0f;
+    for (int w = 0; w < kWarps; w++) {
+      const float2 v = sums[w * R + threadIdx.x];
+      const float above = fmaxf(top, v.x), base = above == -INFINITY ? 0.0f : above;
+      total = total * ex2((top - base) * a.scale) + v.y * ex2((v.x - base) * a.scale);
+      top = above;
+    }
+    a.stats[blockIdx.x * a.ld_stats + threadIdx.x] = make_float2(top, total);
+  }
+}
+
+int rows_of(long long rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8; }
+size_t smem_of(int R, int cols) { return sizeof(float) * R * pad8(cols) + sizeof(float2) * kWarps * R; }
+
+template <typename IO, bool VEC, int R>
+cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
+  auto kernel = head_few_kernel<IO, VEC, R>;
+  const size_t smem = smem_of(R, a.cols);
+  if (smem > 40 * 1024) {
+    // asked for once per device (the first 64 remember it)
+    static std::atomic<unsigned long long> asked{0};
+    int dev = 0;
+    if (cudaError_t e = cudaGetDevice(&dev)) return e;
+    const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
+    if (!(asked.load(std::memory_order_relaxed) & bit)) {
+      if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)kFewSmem))
+        return e;
+      asked.fetch_or(bit, std::memory_order_relaxed);
+    }
+  }
+  cudaLaunchConfig_t c{};
+  c.gridDim = dim3(blocks);
+  c.blockDim = dim3(kThreads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = first ? 0 : 1;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&c, kernel, a);
+  count_launches(1);
+  return e;
+}
+template <typename IO, bool VEC>
+cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
+  switch (rows_of(a.rows)) {
+    case 1: return launch<IO, VEC, 1>(a, blocks, first, st);
+    case 2: return launch<IO, VEC, 2>(a, blocks, first, st);
+    case 4: return launch<IO, VEC, 4>(a, blocks, first, st);
+    default: return launch<IO, VEC, 8>(a, blocks, first, st);
+  }
+}
+
+}  // namespace
+
+bool head_few(long long rows, int cols) {
+  return rows <= 8 && smem_of(rows_of(rows), cols) <= kFewSmem;
+}
+int head_few_blocks(long long rows, int sms) { return blocks_per_sm(rows_of(rows)) * sms; }
+
+cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
+                            const void* h, long long ld_h, const void* w, long long ld_w, int* idx,
+                            const HeadRows& r, float2* stats, float* zt, int sms, cudaStream_t st) {
+  FewArgs a{h, ld_h, w, ld_w, target, valid, idx, r.state, r.pos, stats, zt, d.ignore_index,
+            pad_rows(d.rows), (int)d.rows, d.cols, d.vocab, d.entries ? d.entries : 1,
+            d.entries ? kLog2e / d.temperature : kLog2e};
+  const size_t size = d.io == SSM_F32 ? 4 : 2;
+  const bool vec = d.cols % 8 == 0 && ld_w % 8 == 0 && (uintptr_t)w % (8 * size) == 0;
+  const int blocks = head_few_blocks(d.rows, sms);
+  const bool first = valid == nullptr;
+  if (d.io == SSM_F32)
+    return vec ? launch<float, true>(a, blocks, first, st) : launch<float, false>(a, blocks, first, st);
+  return vec ? launch<__nv_bfloat16, true>(a, blocks, first, st) :
+               launch<__nv_bfloat16, false>(a, blocks, first, st);
+}
+
+}  // namespace ssm

@@ -137,8 +137,9 @@ __device__ __forceinline__ void copy8(const IO* x, int left, __nv_bfloat16* out,
 
 // ---- which rows count, and their copies --------------------------------------------------------------
 // A block takes `per_block` rows.  It looks at every row, which costs less than a launch of its own for a
-// count (8192 rows: 2 us), so that it knows where its own go, and packs them, a warp per row; the last
-// one also the rows of zeros past them.  The blocks behind copy W.
+// count, so that it knows where its own go, and packs them, a warp per row; the last one also the rows
+// of zeros past them.  The blocks behind copy W.
+constexpr int kRowThreads = 512;
 struct RowsArgs {
   const int64_t* target;
   const uint8_t* valid;
@@ -156,18 +157,15 @@ struct RowsArgs {
   HeadRows r;
 };
 enum RowKind { kCounts, kNone, kBad };
-__device__ __forceinline__ int kind_of(const RowsArgs& a, long long row) {
-  if (a.target) {
-    const int64_t y = a.target[row];
-    return y == a.ignore ? kNone : y >= 0 && y < a.vocab ? kCounts : kBad;
-  }
-  const int v = a.valid[row];
-  return v == 1 ? kCounts : v == 2 ? kBad : kNone;
+// said: a row's target, or what `valid` holds of it.
+__device__ __forceinline__ int kind_of(const RowsArgs& a, int64_t said) {
+  if (a.target) return said == a.ignore ? kNone : said >= 0 && said < a.vocab ? kCounts : kBad;
+  return said == 1 ? kCounts : said == 2 ? kBad : kNone;
 }
 
 template <typename IO, int PLANES, bool VEC_H, bool VEC_W>
-__global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
-  constexpr int kWarps = kThreads / 32;
+__global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a) {
+  constexpr int kWarps = kRowThreads / 32;
   __shared__ int ints[3][kWarps];
   __shared__ float tops[kWarps];
   early_launch();
@@ -176,8 +174,8 @@ __global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
   if ((int)blockIdx.x >= a.row_blocks) {
     const int chunks = a.padded_cols / 8, copiers = gridDim.x - a.row_blocks;
     const long long n = (long long)a.vocab * chunks, plane = (long long)a.vocab * a.padded_cols;
-    for (long long i = (blockIdx.x - a.row_blocks) * (long long)kThreads + threadIdx.x; i < n;
-         i += (long long)copiers * kThreads) {
+    for (long long i = (blockIdx.x - a.row_blocks) * (long long)kRowThreads + threadIdx.x;
+         i < n; i += (long long)copiers * kRowThreads) {
       const int row = (int)(i / chunks), c = (int)(i - (long long)row * chunks) * 8;
       copy8<IO, PLANES, VEC_W>((const IO*)a.w + row * a.ld_w + c, a.cols - c,
                                a.w_out + (long long)row * a.padded_cols + c, plane);
@@ -189,15 +187,24 @@ __global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
   const long long first = (long long)blockIdx.x * a.per_block;
   int all = 0, before = 0, bad = 0;
   float top = 0.0f;
-#pragma unroll 8
-  for (long long t = threadIdx.x; t < a.rows; t += kThreads) {
-    const int kind = kind_of(a, t);
-    all += kind == kCounts;
-    before += kind == kCounts && t < first;
-    bad |= kind == kBad;
-    if (a.d_loss) {
-      const float g = fabsf(a.d_loss[t]);
-      if (kind == kCounts && g < INFINITY) top = fmaxf(top, g);
+  constexpr int kBatch = 8;  // rows of a thread whose loads are in flight together
+  for (long long t0 = threadIdx.x; t0 < a.rows; t0 += kBatch * kRowThreads) {
+    int64_t said[kBatch];
+    float g[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const long long t = t0 + i * kRowThreads < a.rows ? t0 + i * kRowThreads : t0;
+      said[i] = a.target ? a.target[t] : a.valid[t];
+      g[i] = a.d_loss ? fabsf(a.d_loss[t]) : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; i++) {
+      const long long t = t0 + i * kRowThreads;
+      const int kind = t < a.rows ? kind_of(a, said[i]) : kNone;
+      all += kind == kCounts;
+      before += kind == kCounts && t < first;
+      bad |= kind == kBad;
+      if (kind == kCounts && g[i] < INFINITY) top = fmaxf(top, g[i]);
     }
   }
   all = __reduce_add_sync(0xffffffffu, all);
@@ -219,12 +226,13 @@ __global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
     r.state->g_top = top;
     r.state->scale = top * a.tau;
   }
-  // its own rows' places, kThreads of them at a time
+  // its own rows' places, kRowThreads of them at a time
   const int mine = before;
-  for (int base = 0; base < a.per_block; base += kThreads) {
+  for (int base = 0; base < a.per_block; base += kRowThreads) {
     const long long t = first + base + threadIdx.x;
     const bool own = base + (int)threadIdx.x < a.per_block && t < a.rows;
-    const int kind = own ? kind_of(a, t) : kNone;
+    const int64_t said = own ? (a.target ? a.target[t] : a.valid[t]) : 0;
+    const int kind = own ? kind_of(a, said) : kNone;
     const unsigned votes = __ballot_sync(0xffffffffu, kind == kCounts);
     __syncthreads();  // the counts before may still be read
     if (lane == 0) ints[0][warp] = __popc(votes);
@@ -238,7 +246,7 @@ __global__ void __launch_bounds__(kThreads) head_rows_kernel(const RowsArgs a) {
     if (own) {
       r.pos[t] = kind == kCounts ? at : kind == kBad ? kBadRow : kIgnored;
       if (kind == kCounts) r.src[at] = (int)t;
-      if (a.target) a.idx[t] = kind == kCounts ? (int)a.target[t] : kNoEntry;
+      if (a.target) a.idx[t] = kind == kCounts ? (int)said : kNoEntry;
     }
   }
   __syncthreads();
@@ -275,49 +283,58 @@ __device__ __forceinline__ Sum join(const Sum& a, const Sum& b, float scale) {
   const float top = fmaxf(a.top, b.top), at = top == -INFINITY ? 0.0f : top;
   return {top, a.sum * ex2((a.top - at) * scale) + b.sum * ex2((b.top - at) * scale)};
 }
-// A block joins 32 rows' sums: 32 slices of the tiles, each in order, then the slices in a tree.
+// A block of 1024 threads joins X rows' sums: 1024 / X slices of the tiles, each in order, then the slices,
+// a few per lane of a row's warp in order, then a tree.  X is 32, or 4 where that many rows do not fill the
+// SMs and the chain of loads is what counts.
+template <int X>
 __global__ void __launch_bounds__(1024) head_loss_kernel(const float2* stats, int n_stats,
                                                          long long ld, const float* zt,
                                                          const float* p, const float* known,
                                                          long long rows, int entries, float scale,
                                                          float tau, HeadRows r, float* loss,
                                                          float* lse) {
-  __shared__ float2 part[32][33];
+  constexpr int Y = 1024 / X;
+  __shared__ float2 part[Y][X + 1];
   early_launch();
   wait_for_before();
-  const int x = threadIdx.x & 31, y = threadIdx.x >> 5;
-  const long long first = (long long)blockIdx.x * 32;
+  const int x = threadIdx.x % X, y = threadIdx.x / X;
+  const long long first = (long long)blockIdx.x * X;
   const int pos = first + x < rows ? r.pos[first + x] : kIgnored;
   Sum s{-INFINITY, 0.0f};
   if (pos >= 0)
 #pragma unroll 4
-    for (int i = y; i < n_stats; i += 32) {
+    for (int i = y; i < n_stats; i += Y) {
       const float2 v = stats[i * ld + pos];
       s = join(s, {v.x, v.y}, scale);
     }
   part[y][x] = make_float2(s.top, s.sum);
   __syncthreads();
-  const long long row = first + y;  // a warp per row from here
-  if (row >= rows) return;
-  const float2 v = part[x][y];
-  s = {v.x, v.y};
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const long long row = first + warp;  // a warp per row from here
+  if (warp >= X || row >= rows) return;
+  s = {-INFINITY, 0.0f};
+#pragma unroll
+  for (int i = lane; i < Y; i += 32) {
+    const float2 v = part[i][warp];
+    s = join(s, {v.x, v.y}, scale);
+  }
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     // the same order in both lanes
     const Sum o{__shfl_xor_sync(0xffffffffu, s.top, off), __shfl_xor_sync(0xffffffffu, s.sum, off)};
-    s = x & off ? join(o, s, scale) : join(s, o, scale);
+    s = lane & off ? join(o, s, scale) : join(s, o, scale);
   }
   const int at = r.pos[row];
   // loss from distances to the largest logit: a loss near 0 keeps its digits
   const float log_sum = logf(s.sum);
   float l = 0.0f;
   if (at >= 0)
-    for (int j = x; j < entries; j += 32) {
+    for (int j = lane; j < entries; j += 32) {
       const float pj = p ? p[row * entries + j] : 1.0f;
       if (!(pj == 0.0f)) l += pj * ((s.top - zt[row * entries + j]) / tau + log_sum);
     }
   l = warp_sum(l);
-  if (x != 0) return;
+  if (lane != 0) return;
   float whole = s.top / tau + log_sum;
   if (known && at >= 0) l = (l + known[row]) * (tau * tau);
   if (at < 0) l = whole = 0.0f;
@@ -453,15 +470,15 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
                              const void* w, long long ld_w, int* idx, const HeadRows& r,
                              __nv_bfloat16* w_out, int sms, cudaStream_t st) {
   RowsArgs a{target, valid, d.rows, d.ignore_index, d.vocab, d.cols, pad8(d.cols)};
-  const long long per = (d.rows + 511) / 512;  // at most 512 blocks, as each looks at every row
-  a.per_block = per < kThreads / 32 ? kThreads / 32 : (int)per;
+  const long long per = (d.rows + 255) / 256;  // at most 256 blocks, as each looks at every row
+  a.per_block = per < kRowThreads / 32 ? kRowThreads / 32 : (int)per;
   a.row_blocks = (int)((d.rows + a.per_block - 1) / a.per_block);
   a.tau = d.entries ? d.temperature : 1.0f;
   a.h = h, a.ld_h = ld_h, a.lse = lse, a.d_loss = d_loss;
   a.w = w, a.ld_w = ld_w, a.w_out = w_out;
   a.idx = idx, a.r = r;
   const long long chunks = (long long)d.vocab * (a.padded_cols / 8);
-  const long long copiers = w_out ? at_most((chunks + kThreads - 1) / kThreads, sms) : 0;
+  const long long copiers = w_out ? at_most((chunks + kRowThreads - 1) / kRowThreads, sms) : 0;
   const bool vec_h = vec_rows(h, ld_h, d.cols, d.io), vec_w = vec_rows(w, ld_w, d.cols, d.io);
   void (*kernel)(RowsArgs);
   if (d.io == SSM_F32)
@@ -472,18 +489,21 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
   else  // W that can be copied in chunks is not copied
     kernel = vec_h ? head_rows_kernel<__nv_bfloat16, 1, true, false> :
                      head_rows_kernel<__nv_bfloat16, 1, false, false>;
-  if (valid) return go(kernel, a.row_blocks + copiers, kThreads, st, a);
-  kernel<<<(unsigned)(a.row_blocks + copiers), kThreads, 0, st>>>(a);
+  if (valid) return go(kernel, a.row_blocks + copiers, kRowThreads, st, a);
+  kernel<<<(unsigned)(a.row_blocks + copiers), kRowThreads, 0, st>>>(a);
   count_launches(1);
   return cudaGetLastError();
 }
 
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
                              const float* zt, const float* p, const float* known,
-                             const HeadRows& r, float* loss, float* lse, cudaStream_t st) {
+                             const HeadRows& r, float* loss, float* lse, int sms,
+                             cudaStream_t st) {
   const float tau = d.entries ? d.temperature : 1.0f;
-  return go(head_loss_kernel, (d.rows + 31) / 32, 1024, st, stats, n_stats, pad_rows(d.rows), zt, p,
-            known, d.rows, d.entries ? d.entries : 1, kLog2e / tau, tau, r, loss, lse);
+  const int x = d.rows > 4 * sms ? 32 : 4;
+  return go(x == 32 ? head_loss_kernel<32> : head_loss_kernel<4>, (d.rows + x - 1) / x, 1024, st, stats,
+            n_stats, pad_rows(d.rows), zt, p, known, d.rows, d.entries ? d.entries : 1, kLog2e / tau,
+            tau, r, loss, lse);
 }
 
 cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const float* h_part,

@@ -120,9 +120,29 @@ def test_distill(T, D, V, k, tau, io, entry_io):
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("D,V", [(8, 3), (72, 700), (515, 1001), (1030, 40), (2048, 300)])
+@pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
+def test_a_few_rows(T, D, V, io):
+    """Up to 8 rows the forward is a kernel of its own; rows that do not count among them."""
+    i = _inputs(T, D, V, io, seed=T * D + V, ignored=0.0)
+    if T > 2:
+        i["target"][T // 2] = -100
+        i["h"][T // 2] = float("nan")
+    _check(*_ce(i), i, _ce_rows(i))
+    k = min(V, 20)
+    i["t_idx"], i["t_logit"] = _entries(T, V, k, seed=T)
+    i["h"] = torch.nan_to_num(i["h"])
+    _check(*_distill(i, 1.5), i, ref._p_of(i["t_idx"], i["t_logit"], 1.5, V), 1.5)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("lead,tail", [(0, 8), (8, 0), (3, 2), (1, 8)])  # aligned slices, and not
 def test_strided_and_misaligned_rows(lead, tail, io):
-    T, D, V = 70, 136, 270
+    for T in (70, 3):  # 3: a few rows
+        _strided(T, 136, 270, io, lead, tail)
+
+
+def _strided(T, D, V, io, lead, tail):
     i = _inputs(T, D, V, io, seed=4)
 
     def strided(t):
