@@ -12,6 +12,9 @@ namespace {
 template <bool LAYER, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormFwd a,
                                                                   const RowPlan pl) {
+  // The layer norm's rows of up to 8192 columns are copied ahead to shared memory (rows.cuh).
+  constexpr bool kRing = LAYER && VEC == 8 && MAXT <= 256;
+  extern __shared__ __align__(16) unsigned char ring[];
   __shared__ float part[2][32];
   const RowPos pos = row_pos(pl);
   const int cols = a.cols, nb = (cols + 31) / 32;
@@ -29,34 +32,48 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
     if constexpr (LAYER) ld_param<VEC>(a.b, col[j], okc[j], bias[j], 0.0f);
   }
   // Single columns are loaded one row ahead (rows.cuh).
-  typedef Operand<IO, VEC, NJ, false> Act;
-  typedef Operand<RES, VEC, NJ, false> Res;
-  Act x1{a.x, nullptr, nullptr, a.ld_x, 0};
-  Res r1{a.residual, nullptr, nullptr, a.ld_residual, 0};
-  auto ahead = [&](int r) {
-    if constexpr (Act::kAhead) {
+  typedef Operand<IO, VEC, NJ, kRing> Act;
+  typedef Operand<RES, VEC, NJ, kRing> Res;
+  const uint32_t at = shared_addr(ring) + 16 * threadIdx.x, act = Act::slot_bytes(blockDim.x),
+                 bytes = act + Res::slot_bytes(blockDim.x);
+  Act x1{a.x, nullptr, nullptr, a.ld_x, at};
+  Res r1{a.residual, nullptr, nullptr, a.ld_residual, at + act};
+  auto ahead = [&](int r, int slot) {
+    if constexpr (Act::kAhead || kRing) {
       if (r < a.rows) {
-        x1.issue(0, r, col, okc, cols);
-        r1.issue(0, r, col, okc, cols);
+        x1.issue(slot * bytes, r, col, okc, cols);
+        r1.issue(slot * bytes, r, col, okc, cols);
       } else {
-        x1.clear(0, okc, true);
-        r1.clear(0, okc, true);
+        x1.clear(slot * bytes, okc, true);
+        r1.clear(slot * bytes, okc, true);
       }
+      if constexpr (kRing) cp_async_commit();
     }
   };
   const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
-  int half = 0;
-  ahead(blockIdx.x * pl.rpb + pos.slot);
+  const int more = kRing ? pl.slots - 1 : 1;  // rows ahead
+  int half = 0, slot = 0;
+  if constexpr (kRing)
+    for (int i = 0; i < pl.slots; i++) {
+      x1.clear(i * bytes, okc, false);
+      r1.clear(i * bytes, okc, false);
+    }
+  for (int i = 0; i < more; i++) ahead(blockIdx.x * pl.rpb + pos.slot + i * step, i);
   for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, half ^= 1) {
     const int row = base + pos.slot;
     const bool rok = row < a.rows;
     float s[NJ][VEC];
     Cols<IO, VEC> xr[NJ];
     Cols<RES, VEC> rr[NJ];
-    if constexpr (Act::kAhead) {
+    const uint32_t here = slot * bytes;  // this row's place in the ring
+    if constexpr (kRing) {
+      ahead(row + more * step, slot == 0 ? more : slot - 1);
+      cp_async_wait(more);
+      slot = slot == more ? 0 : slot + 1;
+    } else if constexpr (Act::kAhead) {
       x1.advance();
       r1.advance();
-      ahead(row + step);
+      ahead(row + step, 0);
     } else {
 #pragma unroll
       for (int j = 0; j < NJ; j++) {
@@ -73,9 +90,9 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
 #pragma unroll
     for (int j = 0; j < NJ; j++) {
       float xv[VEC], rv[VEC];
-      if constexpr (Act::kAhead) {
-        x1.get(0, j, true, row, col[j], cols, 7u, xv);
-        r1.get(0, j, true, row, col[j], cols, 7u, rv);
+      if constexpr (Act::kAhead || kRing) {
+        x1.get(here, j, true, row, col[j], cols, 7u, xv);
+        r1.get(here, j, true, row, col[j], cols, 7u, rv);
       } else {
         xr[j].get(xv);
         rr[j].get(rv);
@@ -129,7 +146,7 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
       }
       if (a.x_q) {
         float xv[VEC];
-        if constexpr (Act::kAhead) x1.get(0, j, true, row, col[j], cols, 7u, xv);
+        if constexpr (Act::kAhead || kRing) x1.get(here, j, true, row, col[j], cols, 7u, xv);
         else xr[j].get(xv);
         store_ckpt8<VEC>(xv, ok, a.x_q + q, a.x_e + e);
       }
@@ -142,19 +159,25 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
 }
 
 template <bool LAYER, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
-void fwd_launch(const AddNormFwd& a, const RowPlan& pl, cudaStream_t st) {
-  add_norm_fwd_kernel<LAYER, IO, RES, VEC, NJ, MAXT, MINB>
-      <<<dim3(pl.nbx, pl.nby), pl.threads, 0, st>>>(a, pl);
+cudaError_t fwd_launch(const AddNormFwd& a, RowPlan pl, int per_sm, cudaStream_t st) {
+  constexpr bool kRing = LAYER && VEC == 8 && MAXT <= 256;
+  const uint32_t slot = Operand<IO, VEC, NJ, kRing>::slot_bytes(pl.threads) +
+                        Operand<RES, VEC, NJ, kRing>::slot_bytes(pl.threads);
+  pl.slots = ring_slots(slot, pl.threads, per_sm);
+  return launch_rows<add_norm_fwd_kernel<LAYER, IO, RES, VEC, NJ, MAXT, MINB>>(
+      a, pl, (size_t)pl.slots * slot, st);
 }
 template <bool LAYER, typename IO, typename RES>
 cudaError_t fwd_types(const AddNormFwd& a, bool vec, int sms, cudaStream_t st) {
   const NormShape s = norm_shape(a.rows, a.cols, 1, vec, sms, false);
   const RowPlan& p = s.plan;
-#define SSM_LAUNCH(VEC, NJ, MAXT, MINB) fwd_launch<LAYER, IO, RES, VEC, NJ, MAXT, MINB>(a, p, st)
+  cudaError_t e;
+#define SSM_LAUNCH(VEC, NJ, MAXT, MINB) \
+  e = fwd_launch<LAYER, IO, RES, VEC, NJ, MAXT, MINB>(a, p, norm_threads_per_sm(s.variant, false), st)
   SSM_NORM_FWD_SWITCH(s.variant, SSM_LAUNCH)
 #undef SSM_LAUNCH
   count_launches(1);
-  return cudaGetLastError();
+  return e;
 }
 
 template <bool LAYER>
