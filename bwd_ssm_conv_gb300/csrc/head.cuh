@@ -57,7 +57,8 @@ cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_
                              const HeadRows& r, float* loss, float* lse, int sms,
                              cudaStream_t st);
 // What the gradients' sums lack: d_h from the splits' sums [splits][padded rows][padded cols], and
-// rows v0 .. v0 + n of d_W from theirs [splits][piece][padded cols], either where given.  `last`: of the
+// rows v0 .. v0 + n of d_W from theirs [splits][piece][padded cols], either where given (d_h without its sums:
+// only the rows that were not written).  `last`: of the
 // call; where a wait of it gave up, d_h and all of d_w are filled with NaN.
 cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const float* h_part,
                                int h_splits, void* d_h, long long ld_d_h, const float* w_part,
@@ -93,7 +94,8 @@ cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const 
                              const HeadRows& r, const int* idx, const float* p, int tile_n,
                              __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st);
 // The two products with G of the words v0 .. v0 + n, in one launch:
-//   h_part [splits][padded rows][padded cols] (+)= G W, the piece's words split,
+//   h_part [splits][padded rows][padded cols] (+)= G W, the piece's words split, or without it rows src[]
+//   of d_h (with one split and one piece),
 //   rows v0 .. v0 + n of d_W = G^T h, or with w_part [splits][piece][padded cols] the splits' sums.
 struct HeadOut {
   HeadCut h, w;
@@ -101,6 +103,8 @@ struct HeadOut {
   float* h_part;
   float* w_part;
   void* d_w;
+  void* d_h;
+  long long ld_d_h;
 };
 cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const HeadMatrix& h,
                             const HeadMatrix& w, const HeadRows& r, const HeadOut& o, int v0, int n,

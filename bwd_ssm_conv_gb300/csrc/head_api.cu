@@ -98,7 +98,8 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
         const bool h_first = ch > cw;
         double time = h_first ? dealt(nh, ch, nw, cw, pairs) : dealt(nw, cw, nh, ch, pairs);
         // the splits' sums: written and read, those of d_h once for each piece and under its products
-        if (grads & 1) time += sh * mb_h * (several ? 1.0 : 2.0) / stage_bytes(io);
+        if ((grads & 1) && (several || sh > 1))
+          time += sh * mb_h * (several ? 1.0 : 2.0) / stage_bytes(io);
         if (sw > 1) time += 2.0 * sw * mb_w / stage_bytes(io);
         if (least < 0.0 || time < least)
           least = time, best = {{tile, sh, ph}, {tile, sw, pw}, h_first};
@@ -160,7 +161,8 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.g = take((size_t)2 * p.planes * Tp * p.piece);
     p.tile_z = logits_tile(T, d.cols, p.piece, d.io, sms);
     p.cuts = cuts_of(T, d.cols, p.piece, d.io, grads, p.pieces > 1, sms);
-    if (grads & 1) p.dh = take((size_t)4 * p.cuts.h.splits * Tp * Dp);
+    if ((grads & 1) && (p.pieces > 1 || p.cuts.h.splits > 1))
+      p.dh = take((size_t)4 * p.cuts.h.splits * Tp * Dp);
     if ((grads & 2) && p.cuts.w.splits > 1)
       p.dw = take((size_t)4 * p.cuts.w.splits * p.piece * Dp);
   }
@@ -267,8 +269,8 @@ int run(Call c, bool distill, bool backward) {
   }
   __nv_bfloat16* gp = (__nv_bfloat16*)(ws + p.g);
   const HeadMatrix g{gp, Tp, p.piece, Tp * p.piece, p.piece};
-  const HeadOut out{p.cuts.h, p.cuts.w, p.cuts.h_first, c.d_h ? (float*)(ws + p.dh) : nullptr,
-                    p.dw ? (float*)(ws + p.dw) : nullptr, c.d_w};
+  const HeadOut out{p.cuts.h, p.cuts.w, p.cuts.h_first, p.dh ? (float*)(ws + p.dh) : nullptr,
+                    p.dw ? (float*)(ws + p.dw) : nullptr, c.d_w, p.dh ? nullptr : c.d_h, c.ld_d_h};
   for (int i = 0; i < p.pieces; i++) {
     const int v0 = i * p.piece, n = d.vocab - v0 < p.piece ? d.vocab - v0 : p.piece;
     const bool last = i == p.pieces - 1;

@@ -403,8 +403,10 @@ __global__ void __launch_bounds__(kThreads) head_finish_kernel(const FinishArgs 
     if (i < n_h) {
       const long long row = i / chunks;
       const int c = (int)(i - row * chunks) * 8, at = a.r.pos[row];
-      if (at >= 0)
+      if (at >= 0 && !lost) {
+        if (!a.h_part) continue;
         sum8(a.h_part + (long long)at * a.padded_cols + c, a.h_splits, a.h_step, state.scale, v);
+      }
       if (at < 0 || lost)
 #pragma unroll
         for (int j = 0; j < 8; j++) v[j] = at == kIgnored && !lost ? 0.0f : nan_();

@@ -13,9 +13,11 @@
 //   warp 1      one thread of the first CTA issues the MMAs; the second CTA's passes on that its copies
 //               have landed
 //   warps 4-11  take the results out: thread = row, 128 of its columns each
-// fp32 operands are three bf16 planes each, all six staged at once: six products per stage (of ranks
-// 0 0, 0 1, 1 0, 1 1, 0 2, 2 0; the rest is below 2^-24 of a product).  As the tensor cores truncate when
-// they add, these sums are taken out every 128 columns and added in registers.
+// fp32 operands are three bf16 planes each, staged one after the other (0, 2, 1) in slots of their own:
+// six products per step over 64 of the sum (of planes 0 0, 2 0, 0 2, 0 1, 1 0, 1 1; the rest is below 2^-24
+// of a product), whose slots come free in between, so that a slot's next copy has more than a step's time
+// (with all six planes in one of two slots, a tile of 128 columns waited for copies 40 % of its time).  As the
+// tensor cores truncate when they add, these sums are taken out every 128 columns and added in registers.
 #include "head.cuh"
 #include "pair.cuh"
 
@@ -32,15 +34,13 @@ constexpr uint32_t kOperand = 2 * kSlab;      // 128 rows or columns of a CTA
 constexpr uint32_t kTmCols = 2 * kHeadTile;
 constexpr int kRegsFew = 64, kRegsSum = 216;  // PLANES = 3: 128 x 64 + 256 x 216 <= 384 x 168
 
-template <int PLANES> struct Lay {
-  static constexpr int stages = PLANES == 1 ? 6 : 2;
-  static constexpr uint32_t stage = 2 * PLANES * kOperand;
-  // then 32 x 32 values of each warp that takes results out, rows 33 apart (Taker::store)
-  static constexpr uint32_t at_turn = stages * stage;
-  static constexpr uint32_t smem = at_turn + kSumWarps * 32 * 33 * 4 + 1024;
-  // stages between two emptyings of the accumulator
-  static constexpr int segment = PLANES == 1 ? 1 << 30 : 2;
-};
+// Shared memory of a CTA: slots of A's and B's part of a stage (one plane of it), then 32 x 32 values of
+// each warp that takes results out, rows 33 apart (Taker::store).
+constexpr int kSlots = 6;
+constexpr uint32_t kSlot = 2 * kOperand, kAtTurn = kSlots * kSlot;
+constexpr uint32_t kSmem = kAtTurn + kSumWarps * 32 * 33 * 4 + 1024;
+// Stages between two emptyings of the accumulator.
+template <int PLANES> constexpr int kSegment = PLANES == 1 ? 1 << 30 : 2;
 
 // A product of a launch.
 struct Job {
@@ -57,7 +57,9 @@ struct Job {
   long long part_rows;
   int ld_part, add;
   void* out;
-  int ld_out, vec_out;
+  long long ld_out;
+  int vec_out;
+  const int* to_row;   // out's row of each of the result's; NULL: the same
 };
 
 struct TcArgs {
@@ -132,12 +134,16 @@ __device__ __forceinline__ float min_nan(float a, float b) {
   return r;
 }
 
-// v[i], i known to the thread only.
+// v[i], i known to the thread only: halving.
 __device__ __forceinline__ float pick(const float (&v)[32], int i) {
-  float r = 0.0f;
+  float s[16];
 #pragma unroll
-  for (int j = 0; j < 32; j++) r = j == i ? v[j] : r;
-  return r;
+  for (int j = 0; j < 16; j++) s[j] = i & 16 ? v[j + 16] : v[j];
+#pragma unroll
+  for (int n = 8; n > 0; n >>= 1)
+#pragma unroll
+    for (int j = 0; j < n; j++) s[j] = i & n ? s[j + n] : s[j];
+  return s[0];
 }
 
 // What becomes of a row's columns of a tile's half, 32 at a time (chunk c).
@@ -145,7 +151,6 @@ template <int USE, int PLANES> struct Taker {
   const TcArgs& a;
   const Job& job;
   const int row, col0;  // of the result: its row, and the first of its columns
-  const int rows;
   const bool row_ok;
   float* turn;  // this warp's
   // kLogits, kGrad
@@ -157,7 +162,7 @@ template <int USE, int PLANES> struct Taker {
 
   __device__ __forceinline__ Taker(const TcArgs& a, const Job& job, int row, int col0, int rows,
                                    int split, float* turn)
-      : a(a), job(job), row(row), col0(col0), rows(rows), row_ok(row < rows), turn(turn) {
+      : a(a), job(job), row(row), col0(col0), row_ok(row < rows), turn(turn) {
     if constexpr (USE != kOut) {
       // The first entry from this column on, by halving: the list is in order.
       src = row_ok ? a.src[row] : -1;
@@ -213,15 +218,18 @@ template <int USE, int PLANES> struct Taker {
 #pragma unroll
       for (int i = 0; i < 32; i++)  // at most 1, also where logits are so large that roundings are not small
         v[i] = ex2(min_nan(fmaf(v[i], a.scale, -rl), 0.0f));
-      while (next < word + 32) {
-        const float p = a.p ? a.p[(long long)src * a.entries + e] : 1.0f;
-        const int at = next - word;
+      if constexpr (PLANES > 1)
+        while (next < word + 32) {
+          const float p = prob();
+          const int at = next - word;
 #pragma unroll
-        for (int i = 0; i < 32; i++) v[i] -= i == at ? p : 0.0f;
-        advance();
-      }
+          for (int i = 0; i < 32; i++) v[i] -= i == at ? p : 0.0f;
+          advance();
+        }
+      const f2_t rg2 = f2_pack(rg, rg);
 #pragma unroll
-      for (int i = 0; i < 32; i++) v[i] *= rg;
+      for (int i = 0; i < 32; i += 2)
+        f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), rg2), v[i], v[i + 1]);
       if (word + 32 > a.vocab) {
 #pragma unroll
         for (int i = 0; i < 32; i++)
@@ -246,6 +254,13 @@ template <int USE, int PLANES> struct Taker {
           st_global32(g + r * a.plane_g + 16 * b, w);
         }
       }
+      if constexpr (PLANES == 1)  // cheaper than a subtraction from each: over what was stored for the word
+        while (next < word + 32) {
+          const int at = next - word;
+          float p = 0.0f;
+          for (; next == word + at; advance()) p += prob();
+          g[at] = __float2bfloat16_rn(pick(v, at) - p * rg);
+        }
     } else if (job.part) {
       if (!row_ok) return;
 #pragma unroll
@@ -270,6 +285,9 @@ template <int USE, int PLANES> struct Taker {
       else store((float*)job.out, c, v);
     }
   }
+  __device__ __forceinline__ float prob() const {
+    return a.p ? a.p[(long long)src * a.entries + e] : 1.0f;
+  }
   __device__ __forceinline__ void advance() {
     e++;
     next = e < a.entries ? a.idx[(long long)src * a.entries + e] : kNoEntry;
@@ -278,26 +296,27 @@ template <int USE, int PLANES> struct Taker {
   // single values down a column 10007 x 515 fp32 took 76 us in all.
   template <typename T> __device__ __forceinline__ void store(T* out, int c, const float (&v)[32]) {
     const int first = col0 + 32 * c;
+    const int mine = row_ok ? (job.to_row ? job.to_row[row] : row) : -1;
     if (job.vec_out) {
-      T* to = out + (long long)row * job.ld_out + first;
+      T* to = out + mine * job.ld_out + first;
 #pragma unroll
       for (int b = 0; b < 4; b++)
-        if (row_ok && first + 8 * b < job.n) {
+        if (mine >= 0 && first + 8 * b < job.n) {
           float o[8];
 #pragma unroll
           for (int i = 0; i < 8; i++) o[i] = v[8 * b + i];
           st_cols(to + 8 * b, o);
         }
     } else {
-      const int lane = threadIdx.x & 31, row0 = row - lane;
+      const int lane = threadIdx.x & 31;
 #pragma unroll
       for (int i = 0; i < 32; i++) turn[33 * lane + i] = v[i];
       __syncwarp();
-      T* to = out + (long long)row0 * job.ld_out + first + lane;
-      if (first + lane < job.n)
 #pragma unroll 8
-        for (int i = 0; i < 32; i++)
-          if (row0 + i < rows) st(to + (long long)i * job.ld_out, turn[33 * i + lane]);
+      for (int i = 0; i < 32; i++) {
+        const int at = __shfl_sync(0xffffffffu, mine, i);
+        if (at >= 0 && first + lane < job.n) st(out + at * job.ld_out + first + lane, turn[33 * i + lane]);
+      }
       __syncwarp();
     }
   }
@@ -350,8 +369,7 @@ struct Units {
 
 template <int USE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
-  using L = Lay<PLANES>;
-  constexpr int S = L::stages;
+  constexpr int S = kSlots, kSeg = kSegment<PLANES>;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t here[S], there[S], empty[S], ready[2], drained[2], last;
   __shared__ uint32_t tbase;
@@ -404,28 +422,27 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         const int half = x.tile_n / 2;  // columns of B here
         const int m0 = x.mt * kHeadTile + rank * (kHeadTile / 2), n0 = x.nt * x.tile_n + rank * half;
         const bool a_mn = b.a_mn, b_mn = b.b_mn;
-        const uint32_t bytes = PLANES * (kOperand + (half >> 6) * kSlab);
-        for (int k = x.begin; k < x.begin + x.iters; k++, it++, r.next()) {
-          if (it >= S && !wait_for(&empty[r.s], r.phase ^ 1, &bad)) {
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            mbar_expect_tx(&here[r.s], bytes);
-            unsigned char* to = smem + r.s * L::stage;
+        const uint32_t bytes = kOperand + (half >> 6) * kSlab;
+        for (int k = x.begin; k < x.begin + x.iters && ok; k++) {
 #pragma unroll
-            for (int p = 0; p < PLANES; p++)
+          for (int i = 0; i < PLANES; i++, it++, r.next()) {
+            const int p = i == 0 ? 0 : 3 - i;  // 0, 2, 1
+            if (it >= S) ok = ok && wait_for(&empty[r.s], r.phase ^ 1, &bad);
+            if (!ok) break;
+            if (elect_one()) {
+              mbar_expect_tx(&here[r.s], bytes);
+              unsigned char* to = smem + r.s * kSlot;
 #pragma unroll
               for (int c = 0; c < 2; c++) {
-                tma_load_3d(to + p * kOperand + c * kSlab, &b.a, a_mn ? m0 + 64 * c : 64 * k,
+                tma_load_3d(to + c * kSlab, &b.a, a_mn ? m0 + 64 * c : 64 * k,
                             a_mn ? 64 * k : m0 + 64 * c, p, &here[r.s]);
                 if (64 * c < half)
-                  tma_load_3d(to + (PLANES + p) * kOperand + c * kSlab, &b.b,
-                              b_mn ? n0 + 64 * c : 64 * k,
+                  tma_load_3d(to + kOperand + c * kSlab, &b.b, b_mn ? n0 + 64 * c : 64 * k,
                               b.b_row0 + (b_mn ? 64 * k : n0 + 64 * c), p, &here[r.s]);
               }
+            }
+            __syncwarp();
           }
-          __syncwarp();
         }
       }
       // the copies in flight land, and the first CTA's word that their slots are free arrives, before the
@@ -445,32 +462,45 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         const bool a_mn = a.job[x.job].a_mn, b_mn = a.job[x.job].b_mn;
         const uint32_t idesc = idesc_bf16(kHeadTile, x.tile_n, a_mn, b_mn);
         const uint64_t da0 = desc_of(smem_u32(smem), a_mn),
-                       db0 = desc_of(smem_u32(smem) + PLANES * kOperand, b_mn);
+                       db0 = desc_of(smem_u32(smem) + kOperand, b_mn);
         const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
         for (int it = 0; it < iters && ok; seg++) {
           const uint32_t d = tm + (seg & 1) * kHeadTile;
-          const int end = iters - it < L::segment ? iters : it + L::segment;
+          const int end = iters - it < kSeg ? iters : it + kSeg;
           if (seg >= 2) ok = wait_for(&drained[seg & 1], ((seg >> 1) - 1) & 1, &bad);
           bool first = true;
-          for (; it < end && ok; it++, r.next()) {
-            ok = wait_for(&here[r.s], r.phase, &bad) && wait_for(&there[r.s], r.phase, &bad);
-            tmem_fence_after_sync();
-            if (ok && elect_one()) {
-              const uint64_t da = da0 + (uint32_t)(r.s * (L::stage >> 4)),
-                             db = db0 + (uint32_t)(r.s * (L::stage >> 4));
-              constexpr int kPairs = PLANES == 1 ? 1 : 6;
-              constexpr int pa[6] = {0, 0, 1, 1, 0, 2}, pb[6] = {0, 1, 0, 1, 2, 0};
+          // the product of slot i's A and slot j's B
+          const auto mul = [&](int i, int j, bool add) {
+            const uint64_t da = da0 + (uint32_t)(i * (kSlot >> 4)), db = db0 + (uint32_t)(j * (kSlot >> 4));
 #pragma unroll
-              for (int t = 0; t < kPairs; t++)
+            for (int kk = 0; kk < kHeadBlock / 16; kk++)
+              Mma<2>::mma(idesc, d, da + sa * kk, db + sb * kk, add || kk > 0);
+          };
+          for (; it < end && ok; it++, first = false) {
+            int slot[PLANES];
 #pragma unroll
-                for (int kk = 0; kk < kHeadBlock / 16; kk++)
-                  Mma<2>::mma(idesc, d, da + (uint32_t)(pa[t] * (kOperand >> 4)) + sa * kk,
-                              db + (uint32_t)(pb[t] * (kOperand >> 4)) + sb * kk,
-                              !first || t > 0 || kk > 0);
-              Mma<2>::commit(&empty[r.s]);
+            for (int i = 0; i < PLANES && ok; i++, r.next()) {
+              slot[i] = r.s;
+              ok = wait_for(&here[r.s], r.phase, &bad) && wait_for(&there[r.s], r.phase, &bad);
+              tmem_fence_after_sync();
+              if (ok && elect_one()) {
+                if (i == 0) {
+                  mul(slot[0], slot[0], !first);
+                  if (PLANES == 1) Mma<2>::commit(&empty[slot[0]]);
+                } else if (i == 1) {  // plane 2
+                  mul(slot[i], slot[0], true);
+                  mul(slot[0], slot[i], true);
+                  Mma<2>::commit(&empty[slot[i]]);
+                } else {  // plane 1
+                  mul(slot[0], slot[i], true);
+                  mul(slot[i], slot[0], true);
+                  Mma<2>::commit(&empty[slot[0]]);
+                  mul(slot[i], slot[i], true);
+                  Mma<2>::commit(&empty[slot[i]]);
+                }
+              }
+              __syncwarp();
             }
-            __syncwarp();
-            first = false;
           }
           if (!ok) break;
           if (elect_one()) Mma<2>::commit(&ready[seg & 1]);
@@ -483,8 +513,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       const uint32_t first_there = bar_of_first<2>(there);
       bool ok = true;
       for (int u = pair; u < n_units && ok; u += pairs) {
-        const int iters = units.of(a, u).iters;
-        for (int it = 0; it < iters && ok; it++, r.next()) {
+        const int slots = units.of(a, u).iters * PLANES;
+        for (int it = 0; it < slots && ok; it++, r.next()) {
           ok = wait_for(&here[r.s], r.phase, &bad);
           if (ok && elect_one()) mbar_arrive_first<2>(first_there + 8 * r.s);
           __syncwarp();
@@ -496,7 +526,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
     if constexpr (PLANES > 1) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegsSum));
     const int quad = warp & 3, half = (warp - 4) >> 2;
     const uint32_t lanes = tm + ((uint32_t)(32 * quad) << 16);
-    float* turn = reinterpret_cast<float*>(smem + L::at_turn) + (warp - 4) * 32 * 33;
+    float* turn = reinterpret_cast<float*>(smem + kAtTurn) + (warp - 4) * 32 * 33;
     const uint32_t first_drained = bar_of_first<2>(drained);
     int seg = 0;
     bool ok = !a.no_wait;
@@ -535,7 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         for (int c = 0; c < 4; c++)
 #pragma unroll
           for (int i = 0; i < 32; i++) acc[c][i] = 0.0f;
-        for (int it = 0; it < iters && ok; it += L::segment, seg++) {
+        for (int it = 0; it < iters && ok; it += kSeg, seg++) {
           ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
           __syncwarp();
           tmem_fence_after_sync();
@@ -593,14 +623,14 @@ template <int USE, int PLANES> cudaError_t launch(const TcArgs& t, int sms, cuda
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(asked.load(std::memory_order_relaxed) & bit)) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)Lay<PLANES>::smem))
+                                             (int)kSmem))
       return e;
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(sms / 2 * 2);
   c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = Lay<PLANES>::smem;
+  c.dynamicSmemBytes = kSmem;
   c.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -700,7 +730,7 @@ cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const H
     j.ld_out = d.cols;
     j.vec_out = d.cols % 8 == 0 && (uintptr_t)o.d_w % (8 * size) == 0;
   }
-  if (o.h_part) {
+  if (o.h_part || o.d_h) {
     Job& j = t.job[t.jobs++];
     if (!encode(&j.a, g, planes) || !encode(&j.b, w, planes)) return cudaErrorInvalidValue;
     j.b_mn = 1;
@@ -713,6 +743,10 @@ cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const H
     j.part_rows = g.rows;
     j.ld_part = padded;
     j.add = add;
+    j.out = o.d_h;
+    j.ld_out = o.ld_d_h;
+    j.vec_out = d.cols % 8 == 0 && o.ld_d_h % 8 == 0 && (uintptr_t)o.d_h % (8 * size) == 0;
+    j.to_row = r.src;
   }
   if (t.jobs == 2 && o.h_first) {
     const Job j = t.job[0];
