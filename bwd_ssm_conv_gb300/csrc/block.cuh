@@ -138,6 +138,8 @@ cudaError_t launch_add_layer_norm_fwd(const AddNormFwd& a, int io, int res_io, b
                                       cudaStream_t st);
 cudaError_t launch_add_layer_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
                                       cudaStream_t st);
+cudaError_t add_layer_norm_bwd_f32(const AddNormBwd& a, bool vec, int sms, cudaStream_t st);
+cudaError_t add_layer_norm_bwd_mixed(const AddNormBwd& a, bool vec, int sms, cudaStream_t st);
 
 // ---- gated_norm ---------------------------------------------------------------------------------
 struct GatedNormFwd {

@@ -37,14 +37,29 @@ struct HeadRows {  // of a call, on the device
   __nv_bfloat16* h;  // [planes][padded rows][padded cols]
 };
 
+// What the rows say, by rows of the call: their words in order ([rows][entries], ended by kNoEntry where
+// there are fewer; one target) and, of a teacher, p, sum p log p, and for each of kHeadParts equal parts
+// of the vocabulary how many of the row's words lie before it.
+constexpr int kHeadParts = 64;
+struct HeadLists {
+  int* idx;
+  float* p;
+  float* known;
+  uint8_t* table;
+};
+inline int head_part_shift(int vocab) {  // a part's words, as a power of two
+  int shift = 0;
+  while (((vocab - 1) >> shift) >= kHeadParts) shift++;
+  return shift;
+}
+
 inline int pad8(int n) { return (n + 7) / 8 * 8; }
 inline long long pad_rows(long long rows) { return (rows + 63) / 64 * 64; }
 
 // ---- head_rows.cu ---------------------------------------------------------------------------------
-// Teacher entries: each row's in order of the vocabulary (idx, ended by kNoEntry where there are fewer), with
-// p, sum p log p in known[row], and in valid[row] whether the row has a loss (1), or is bad (2).
+// A teacher's entries as lists, and in valid[row] whether the row has a loss (1), or is bad (2).
 cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, const void* t_logit,
-                                int* idx, float* p, float* known, uint8_t* valid, cudaStream_t st);
+                                const HeadLists& lists, uint8_t* valid, cudaStream_t st);
 // Which rows count, from `valid` or from the targets (whose words go to idx), their h packed (and, given
 // lse, rl and rg); W with padded rows, fp32 as three planes, to w_out where that is given.
 cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
@@ -53,8 +68,8 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
                              __nv_bfloat16* w_out, int sms, cudaStream_t st);
 // Loss and lse from the tiles' sums; zt: the entries' logits [rows][entries or 1].
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
-                             const float* zt, const float* p, const float* known,
-                             const HeadRows& r, float* loss, float* lse, int sms,
+                             const float* zt, const HeadLists& lists, const HeadRows& r,
+                             float* loss, float* lse, int sms,
                              cudaStream_t st);
 // What the gradients' sums lack: d_h from the splits' sums [splits][padded rows][padded cols], and
 // rows v0 .. v0 + n of d_W from theirs [splits][piece][padded cols], either where given (d_h without its sums:
@@ -70,7 +85,7 @@ cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const 
 // stats [blocks][padded rows].
 constexpr size_t kFewSmem = 72 * 1024;  // of a block
 bool head_few(long long rows, int cols);
-int head_few_blocks(long long rows, int sms);
+int head_few_blocks(int sms);
 cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
                             const void* h, long long ld_h, const void* w, long long ld_w, int* idx,
                             const HeadRows& r, float2* stats, float* zt, int sms, cudaStream_t st);
@@ -87,11 +102,11 @@ struct HeadCut {
 };
 // The sums of the vocabulary's tiles, stats [2 tiles][padded rows], and the entries' logits.
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const int* idx, int tile_n, float2* stats,
+                               const HeadRows& r, const HeadLists& lists, int tile_n, float2* stats,
                                float* zt, int sms, cudaStream_t st);
 // G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [planes][padded rows][n].
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                             const HeadRows& r, const int* idx, const float* p, int tile_n,
+                             const HeadRows& r, const HeadLists& lists, int tile_n,
                              __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st);
 // The two products with G of the words v0 .. v0 + n, in one launch:
 //   h_part [splits][padded rows][padded cols] (+)= G W, the piece's words split, or without it rows src[]

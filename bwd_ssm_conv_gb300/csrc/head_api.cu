@@ -111,7 +111,7 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
 
 // The workspace, by bytes from its start.
 struct Plan {
-  size_t pos, src, idx, p, known, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
+  size_t pos, src, idx, p, known, table, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
   int planes, tile_z, n_stats, piece, pieces;
   Cuts cuts;
 };
@@ -132,10 +132,11 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   if (d.entries) {
     p.p = take(4 * T * n_e);
     p.known = take(4 * T);
+    p.table = take(kHeadParts * T);
     p.valid = take(T);
   }
   if (!grads && head_few(T, d.cols)) {
-    p.n_stats = head_few_blocks(T, sms);
+    p.n_stats = head_few_blocks(sms);
     p.stats = take((size_t)8 * p.n_stats * Tp);
     p.zt = take(4 * T * n_e);
     p.bytes = at;
@@ -240,31 +241,34 @@ int run(Call c, bool distill, bool backward) {
   char* ws = (char*)c.ws;
   const long long Tp = pad_rows(d.rows);
   const int Dp = pad8(d.cols);
-  int* idx = (int*)(ws + p.idx);
-  float* prob = d.entries ? (float*)(ws + p.p) : nullptr;
-  float* known = d.entries ? (float*)(ws + p.known) : nullptr;
+  HeadLists lists{(int*)(ws + p.idx)};
+  if (d.entries) {
+    lists.p = (float*)(ws + p.p);
+    lists.known = (float*)(ws + p.known);
+    lists.table = (uint8_t*)(ws + p.table);
+  }
   uint8_t* valid = d.entries ? (uint8_t*)(ws + p.valid) : nullptr;
   HeadRows r{(HeadState*)ws, (int*)(ws + p.pos), (int*)(ws + p.src), (float*)(ws + p.rl),
              (float*)(ws + p.rg), (__nv_bfloat16*)(ws + p.h)};
 #define SSM_DO(call) \
   if ((call) != cudaSuccess) return SSM_ERR_CUDA
-  if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, idx, prob, known, valid, st));
+  if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, lists, valid, st));
   float2* stats = (float2*)(ws + p.stats);
   float* zt = (float*)(ws + p.zt);
   if (!backward && head_few(d.rows, d.cols)) {
-    SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, idx, r, stats, zt, sms, st));
-    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, prob, known, r, c.loss, c.lse_out, sms, st));
+    SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, lists.idx, r, stats, zt, sms, st));
+    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }
   __nv_bfloat16* w_out = copy_w ? (__nv_bfloat16*)(ws + p.w) : nullptr;
   SSM_DO(launch_head_rows(d, c.target, valid, c.h, c.ld_h, backward ? c.lse : nullptr,
-                          backward ? c.d_loss : nullptr, c.w, c.ld_w, idx, r, w_out, sms, st));
+                          backward ? c.d_loss : nullptr, c.w, c.ld_w, lists.idx, r, w_out, sms, st));
   const HeadMatrix h{r.h, Tp, Dp, Tp * Dp, d.cols};
   const HeadMatrix w = copy_w ? HeadMatrix{w_out, d.vocab, Dp, (long long)d.vocab * Dp, d.cols} :
                                 HeadMatrix{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
   if (!backward) {
-    SSM_DO(launch_head_logits(d, h, w, r, idx, p.tile_z, stats, zt, sms, st));
-    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, prob, known, r, c.loss, c.lse_out, sms, st));
+    SSM_DO(launch_head_logits(d, h, w, r, lists, p.tile_z, stats, zt, sms, st));
+    SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }
   __nv_bfloat16* gp = (__nv_bfloat16*)(ws + p.g);
@@ -274,7 +278,7 @@ int run(Call c, bool distill, bool backward) {
   for (int i = 0; i < p.pieces; i++) {
     const int v0 = i * p.piece, n = d.vocab - v0 < p.piece ? d.vocab - v0 : p.piece;
     const bool last = i == p.pieces - 1;
-    SSM_DO(launch_head_grad(d, h, w, r, idx, prob, p.tile_z, gp, v0, p.piece, sms, st));
+    SSM_DO(launch_head_grad(d, h, w, r, lists, p.tile_z, gp, v0, p.piece, sms, st));
     SSM_DO(launch_head_out(d, g, h, w, r, out, v0, n, i > 0, sms, st));
     if (last || out.w_part)
       SSM_DO(launch_head_finish(d, r, out.h_part, p.cuts.h.splits, last ? c.d_h : nullptr, c.ld_d_h,

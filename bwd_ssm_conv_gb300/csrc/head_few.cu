@@ -1,10 +1,12 @@
-// head_few.cu -- the forward for a few rows (at most 8, as tokens come): Z = h W^T with every row of W read
+// head_few.cu -- the forward for one or two rows (tokens as they come): Z = h W^T with every row of W read
 // once, by plain fp32 arithmetic.  W's bytes bound it; a tensor-core tile would be all but empty, and its
-// rows would have to be packed first.
+// rows would have to be packed first.  768 columns, 32768 words in bf16, in a graph with the kernel that
+// joins the sums (GB300): one row 16.1 us, two 19.6, for 7.4 of reading; four by this kernel 24.4, by the
+// tensor cores 24.
 //
 // h lies in shared memory as fp32.  A warp takes 4 words at a time, a lane every 32nd chunk of 8 columns
-// of each, which leaves 4 to 32 sums of words and rows to add over the lanes: at each step the
-// lanes keep half of them and give the other half away, until each has one, the logit of one word and row.
+// of each, which leaves 4 or 8 sums of words and rows to add over the lanes: at each step the lanes keep
+// half of them and give the other half away, until each has one, the logit of one word and row.
 // A lane keeps the maximum and the sum of the exponentials of what comes its way.
 // The logits of the rows' own words (or entries) are computed by themselves, a warp each.
 #include "head.cuh"
@@ -14,7 +16,7 @@ namespace ssm {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int blocks_per_sm(int R) { return R <= 2 ? 3 : 2; }  // as its registers leave room for
+constexpr int kBlocksPerSm = 2;  // as the registers leave room for
 constexpr int kWarps = kThreads / 32;
 constexpr int kWords = 4;  // whose loads are in flight together
 
@@ -38,15 +40,17 @@ struct FewArgs {
 // 8 columns, or what is left of them, as fp32.
 template <typename IO, bool VEC> struct Chunk {
   Cols<IO, VEC ? 8 : 1> c[VEC ? 1 : 8];
-  __device__ __forceinline__ void load(const IO* p, int left) {
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (int i = 0; i < (VEC ? 1 : 8); i++) c[i].zero();
+  }
+  __device__ __forceinline__ void load(const IO* p, int left) {  // the rest stays as it is
     if constexpr (VEC) {
       c[0].load(p);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; i++) {
-        c[i].zero();
+      for (int i = 0; i < 8; i++)
         if (i < left) c[i].load(p + i);
-      }
     }
   }
   __device__ __forceinline__ void get(float (&v)[8]) const {
@@ -75,43 +79,51 @@ __device__ __forceinline__ void dots(const FewArgs& a, const float* h, int padde
 #pragma unroll
     for (int r = 0; r < R; r++) sum[j][r] = 0.0f;
   }
-#pragma unroll 2
-  for (int c = 8 * lane; c < padded; c += 256) {
-    Chunk<IO, VEC> x[N];
+  // U chunks of each word in flight together, those past the row's end as zeros
+  constexpr int U = R == 1 && sizeof(IO) == 2 ? 3 : 2;
+  for (int c0 = 0; c0 < padded; c0 += 256 * U) {
+    Chunk<IO, VEC> x[U][N];
 #pragma unroll
-    for (int j = 0; j < N; j++) x[j].load(p[j] + c, a.cols - c);
-    float v[N][8];
+    for (int u = 0; u < U; u++) {
+      const int c = c0 + 256 * u + 8 * lane;
 #pragma unroll
-    for (int j = 0; j < N; j++) x[j].get(v[j]);
+      for (int j = 0; j < N; j++) {
+        x[u][j].zero();
+        if (c < padded) x[u][j].load(p[j] + c, a.cols - c);
+      }
+    }
 #pragma unroll
-    for (int r = 0; r < R; r++) {
-      const float4 h0 = *reinterpret_cast<const float4*>(h + r * padded + c),
-                   h1 = *reinterpret_cast<const float4*>(h + r * padded + c + 4);
-      const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+    for (int u = 0; u < U; u++) {
+      const int c = min(c0 + 256 * u + 8 * lane, padded - 8);
+      float v[N][8];
 #pragma unroll
-      for (int j = 0; j < N; j++)
+      for (int j = 0; j < N; j++) x[u][j].get(v[j]);
 #pragma unroll
-        for (int i = 0; i < 8; i++) sum[j][r] = fmaf(v[j][i], hv[i], sum[j][r]);
+      for (int r = 0; r < R; r++) {
+        const float4 h0 = *reinterpret_cast<const float4*>(h + r * padded + c),
+                     h1 = *reinterpret_cast<const float4*>(h + r * padded + c + 4);
+        const float hv[8] = {h0.x, h0.y, h0.z, h0.w, h1.x, h1.y, h1.z, h1.w};
+#pragma unroll
+        for (int j = 0; j < N; j++)
+#pragma unroll
+          for (int i = 0; i < 8; i++) sum[j][r] = fmaf(v[j][i], hv[i], sum[j][r]);
+      }
     }
   }
 }
 
 template <typename IO, bool VEC, int R>
-__global__ void __launch_bounds__(kThreads, blocks_per_sm(R)) head_few_kernel(const FewArgs a) {
+__global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const FewArgs a) {
   extern __shared__ __align__(16) float h[];  // [R][padded], then the warps' sums
-  __shared__ int kind[8];
+  __shared__ int kind[R];
   asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = (a.cols + 7) / 8 * 8;
-  // A warp's words lie together, as many as the others' or one more.  The first of them are on their way
-  // while the rows are looked at.
+  // A warp's words lie together, as many as the others' or one more.
   const long long warps = (long long)gridDim.x * kWarps, me = (long long)blockIdx.x * kWarps + warp;
   const int from = (int)(me * a.vocab / warps), to = (int)((me + 1) * a.vocab / warps);
-  for (int w = from; w < to && w < from + 2 * kWords; w++)
-    for (int c = lane * (128 / (int)sizeof(IO)); c < a.cols; c += 32 * (128 / (int)sizeof(IO)))
-      asm volatile("prefetch.global.L2 [%0];" ::"l"((const IO*)a.w + w * a.ld_w + c));
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (threadIdx.x < 8) {  // which rows count: each block sees for itself
+  if (threadIdx.x < R) {  // which rows count: each block sees for itself
     const int t = threadIdx.x;
     int pos = kIgnored, word = kNoEntry;
     if (t < a.rows) {
@@ -130,7 +142,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(R)) head_few_kernel(co
       }
     }
     kind[t] = pos;
-    const bool bad = __any_sync(0xffu, pos == kBadRow);
+    const bool bad = __any_sync((1u << R) - 1u, pos == kBadRow);
     if (blockIdx.x == 0 && t == 0) a.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
   }
   __syncthreads();
@@ -212,7 +224,7 @@ __global__ void __launch_bounds__(kThreads, blocks_per_sm(R)) head_few_kernel(co
   }
 }
 
-int rows_of(long long rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8; }
+int rows_of(long long rows) { return rows <= 1 ? 1 : 2; }
 size_t smem_of(int R, int cols) { return sizeof(float) * R * pad8(cols) + sizeof(float2) * kWarps * R; }
 
 template <typename IO, bool VEC, int R>
@@ -248,20 +260,16 @@ cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
 }
 template <typename IO, bool VEC>
 cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
-  switch (rows_of(a.rows)) {
-    case 1: return launch<IO, VEC, 1>(a, blocks, first, st);
-    case 2: return launch<IO, VEC, 2>(a, blocks, first, st);
-    case 4: return launch<IO, VEC, 4>(a, blocks, first, st);
-    default: return launch<IO, VEC, 8>(a, blocks, first, st);
-  }
+  return a.rows <= 1 ? launch<IO, VEC, 1>(a, blocks, first, st) :
+                       launch<IO, VEC, 2>(a, blocks, first, st);
 }
 
 }  // namespace
 
 bool head_few(long long rows, int cols) {
-  return rows <= 8 && smem_of(rows_of(rows), cols) <= kFewSmem;
+  return rows <= 2 && smem_of(rows_of(rows), cols) <= kFewSmem;
 }
-int head_few_blocks(long long rows, int sms) { return blocks_per_sm(rows_of(rows)) * sms; }
+int head_few_blocks(int sms) { return kBlocksPerSm * sms; }
 
 cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
                             const void* h, long long ld_h, const void* w, long long ld_w, int* idx,
@@ -271,7 +279,7 @@ cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const
             d.entries ? kLog2e / d.temperature : kLog2e};
   const size_t size = d.io == SSM_F32 ? 4 : 2;
   const bool vec = d.cols % 8 == 0 && ld_w % 8 == 0 && (uintptr_t)w % (8 * size) == 0;
-  const int blocks = head_few_blocks(d.rows, sms);
+  const int blocks = head_few_blocks(sms);
   const bool first = valid == nullptr;
   if (d.io == SSM_F32)
     return vec ? launch<float, true>(a, blocks, first, st) : launch<float, false>(a, blocks, first, st);

@@ -27,38 +27,58 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ float nan_() { return __uint_as_float(0x7fc00000u); }
 
 // ---- a teacher's entries ------------------------------------------------------------------------
-// A warp per row.  An entry's place is the number of entries before it, counted.
+// A warp per row.  An entry's place in the order is the number of smaller keys, counted: a key is the word
+// and, behind it, the entry's number, so that no two are alike.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t_idx, const T* t_logit,
                                                                 long long rows, int k, int vocab,
-                                                                float tau, int* idx, float* p,
-                                                                float* known, uint8_t* valid) {
-  constexpr int N = SSM_MAX_HEAD_ENTRIES / 32;
-  __shared__ int keys[kThreads / 32][SSM_MAX_HEAD_ENTRIES];
+                                                                float tau, int shift,
+                                                                HeadLists lists, uint8_t* valid) {
+  constexpr int N = SSM_MAX_HEAD_ENTRIES / 32, kBits = 7, kNone = SSM_MAX_HEAD_VOCAB << kBits;
+  static_assert(SSM_MAX_HEAD_ENTRIES == 1 << kBits, "an entry's number in its key");
+  __shared__ int4 keys[kThreads / 32][SSM_MAX_HEAD_ENTRIES / 4];
+  __shared__ int parts[kThreads / 32][kHeadParts];
   early_launch();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const long long row = (long long)blockIdx.x * (kThreads / 32) + warp;
   if (row >= rows) return;
-  int* key = keys[warp];
+  int* key = reinterpret_cast<int*>(keys[warp]);
+  int* part = parts[warp];
+  part[2 * lane] = part[2 * lane + 1] = 0;
   float t[N];
-  bool here[N], bad = false, odd = false;
+  int word[N], mine[N], place[N];
+  bool bad = false, odd = false;
   float top = -INFINITY;
 #pragma unroll
   for (int j = 0; j < N; j++) {
     const int i = lane + 32 * j;
-    here[j] = false;
+    word[j] = -1;
     t[j] = -INFINITY;
+    place[j] = 0;
+    mine[j] = 0x7fffffff;
     if (i < k) {
-      const int64_t word = t_idx[row * k + i];
-      here[j] = word >= 0 && word < vocab;
-      bad = bad || word >= vocab;
-      if (here[j]) t[j] = ld(t_logit + row * k + i) / tau;
-      key[i] = here[j] ? (int)word : kNoEntry;
+      const int64_t w = t_idx[row * k + i];
+      bad = bad || w >= vocab;
+      if (w >= 0 && w < vocab) word[j] = (int)w;
+      const float x = ld(t_logit + row * k + i) / tau;
+      if (word[j] >= 0) t[j] = x;
+      mine[j] = word[j] >= 0 ? word[j] << kBits | i : kNone + i;
       odd = odd || t[j] != t[j];
       top = fmaxf(top, t[j]);
     }
+    key[i] = mine[j];
   }
   __syncwarp();
+  // sorted, and counted by parts of the vocabulary
+#pragma unroll
+  for (int j = 0; j < N; j++)
+    if (word[j] >= 0) atomicAdd(&part[word[j] >> shift], 1);
+  for (int o = 0; o < (k + 3) / 4; o++) {
+    const int4 x = keys[warp][o];
+#pragma unroll
+    for (int j = 0; j < N; j++)
+      place[j] += (x.x < mine[j]) + (x.y < mine[j]) + (x.z < mine[j]) + (x.w < mine[j]);
+  }
   top = warp_max(top);
   bad = __any_sync(0xffffffffu, bad);
   odd = __any_sync(0xffffffffu, odd);  // a NaN is a loss of NaN, not an entry that is not there
@@ -66,7 +86,7 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
   float e[N], sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    e[j] = here[j] && some ? expf(t[j] - top) : 0.0f;
+    e[j] = word[j] >= 0 && some ? expf(t[j] - top) : 0.0f;
     sum += e[j];
   }
   sum = warp_sum(sum);
@@ -76,18 +96,25 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
   for (int j = 0; j < N; j++) {
     e[j] = some ? e[j] / sum : 0.0f;
     if (!(e[j] == 0.0f)) kn += e[j] * (t[j] - top - log_sum);
-    const int i = lane + 32 * j;
-    if (i < k) {
-      const int mine = key[i];
-      int place = 0;
-      for (int o = 0; o < k; o++) place += key[o] < mine || (key[o] == mine && o < i);
-      idx[row * k + place] = mine;
-      p[row * k + place] = e[j];
+    if (lane + 32 * j < k) {
+      lists.idx[row * k + place[j]] = word[j] >= 0 ? word[j] : kNoEntry;
+      lists.p[row * k + place[j]] = e[j];
     }
   }
   kn = warp_sum(kn);
+  __syncwarp();
+  const int a = part[2 * lane], b = part[2 * lane + 1];
+  int before = a + b;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int o = __shfl_up_sync(0xffffffffu, before, off);
+    if (lane >= off) before += o;
+  }
+  before -= a + b;
+  reinterpret_cast<uchar2*>(lists.table + row * kHeadParts)[lane] =
+      make_uchar2((unsigned char)before, (unsigned char)(before + a));
   if (lane == 0) {
-    known[row] = kn;
+    lists.known[row] = kn;
     valid[row] = bad ? 2 : some ? 1 : 0;
   }
 }
@@ -349,7 +376,7 @@ __device__ __forceinline__ void sum8(const float* part, int splits, long long st
                                      float (&v)[8]) {
 #pragma unroll
   for (int i = 0; i < 8; i++) v[i] = 0.0f;
-#pragma unroll 4
+#pragma unroll 8
   for (int s = 0; s < splits; s++) {
     Cols<float, 8> c;
     c.load(part + s * step);
@@ -393,7 +420,8 @@ __global__ void __launch_bounds__(kThreads) head_finish_kernel(const FinishArgs 
   const HeadState state = *a.r.state;
   const bool lost = a.last && state.status == SSM_ERR_TIMEOUT;
   const int chunks = a.padded_cols / 8;
-  const long long n_h = a.d_h ? a.rows * chunks : 0,
+  // without sums of d_h only rows without a loss are left to do, if there are any
+  const long long n_h = a.d_h && (a.h_part || lost || state.count < a.rows) ? a.rows * chunks : 0,
                   n = n_h + (a.w_part ? (long long)a.words * chunks : 0),
                   stride = (long long)gridDim.x * kThreads,
                   first = blockIdx.x * (long long)kThreads + threadIdx.x;
@@ -454,15 +482,16 @@ bool vec_rows(const void* p, long long ld, int cols, int io) {
 }  // namespace
 
 cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, const void* t_logit,
-                                int* idx, float* p, float* known, uint8_t* valid, cudaStream_t st) {
+                                const HeadLists& lists, uint8_t* valid, cudaStream_t st) {
   const unsigned blocks = (unsigned)((d.rows + kThreads / 32 - 1) / (kThreads / 32));
+  const int shift = head_part_shift(d.vocab);
   if (d.entry_io == SSM_F32)
     head_entries_kernel<<<blocks, kThreads, 0, st>>>(t_idx, (const float*)t_logit, d.rows, d.entries,
-                                                     d.vocab, d.temperature, idx, p, known, valid);
+                                                     d.vocab, d.temperature, shift, lists, valid);
   else
     head_entries_kernel<<<blocks, kThreads, 0, st>>>(t_idx, (const __nv_bfloat16*)t_logit, d.rows,
-                                                     d.entries, d.vocab, d.temperature, idx, p,
-                                                     known, valid);
+                                                     d.entries, d.vocab, d.temperature, shift, lists,
+                                                     valid);
   count_launches(1);
   return cudaGetLastError();
 }
@@ -498,13 +527,13 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
 }
 
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
-                             const float* zt, const float* p, const float* known,
-                             const HeadRows& r, float* loss, float* lse, int sms,
+                             const float* zt, const HeadLists& lists, const HeadRows& r,
+                             float* loss, float* lse, int sms,
                              cudaStream_t st) {
   const float tau = d.entries ? d.temperature : 1.0f;
   const int x = d.rows > 4 * sms ? 32 : 4;
   return go(x == 32 ? head_loss_kernel<32> : head_loss_kernel<4>, (d.rows + x - 1) / x, 1024, st, stats,
-            n_stats, pad_rows(d.rows), zt, p, known, d.rows, d.entries ? d.entries : 1, kLog2e / tau,
+            n_stats, pad_rows(d.rows), zt, lists.p, lists.known, d.rows, d.entries ? d.entries : 1, kLog2e / tau,
             tau, r, loss, lse);
 }
 

@@ -9,7 +9,8 @@ namespace ssm {
 
 namespace {
 
-template <bool LAYER, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
+// KEPT: there may be checkpoints to write.
+template <bool LAYER, bool KEPT, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormFwd a,
                                                                   const RowPlan pl) {
   // The layer norm's rows of up to 8192 columns are copied ahead to shared memory (rows.cuh).
@@ -32,8 +33,8 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
     if constexpr (LAYER) ld_param<VEC>(a.b, col[j], okc[j], bias[j], 0.0f);
   }
   // Single columns are loaded one row ahead (rows.cuh).
-  typedef Operand<IO, VEC, NJ, kRing> Act;
-  typedef Operand<RES, VEC, NJ, kRing> Res;
+  typedef Operand<IO, VEC, NJ, kRing, false> Act;
+  typedef Operand<RES, VEC, NJ, kRing, false> Res;
   const uint32_t at = shared_addr(ring) + 16 * threadIdx.x, act = Act::slot_bytes(blockDim.x),
                  bytes = act + Res::slot_bytes(blockDim.x);
   Act x1{a.x, nullptr, nullptr, a.ld_x, at};
@@ -139,18 +140,18 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
       }
       const long long q = (long long)row * cols + col[j],
                       e = (long long)row * nb + (int)((unsigned)col[j] / 32);
-      if (a.res_q) {
+      if (KEPT && a.res_q) {
         float kept[VEC];
         stored.get(kept);
         store_ckpt8<VEC>(kept, ok, a.res_q + q, a.res_e + e);
       }
-      if (a.x_q) {
+      if (KEPT && a.x_q) {
         float xv[VEC];
         if constexpr (Act::kAhead || kRing) x1.get(here, j, true, row, col[j], cols, 7u, xv);
         else xr[j].get(xv);
         store_ckpt8<VEC>(xv, ok, a.x_q + q, a.x_e + e);
       }
-      if (a.out_q) {
+      if (KEPT && a.out_q) {
         oc.get(o);
         store_ckpt8<VEC>(o, ok, a.out_q + q, a.out_e + e);
       }
@@ -164,8 +165,12 @@ cudaError_t fwd_launch(const AddNormFwd& a, RowPlan pl, int per_sm, cudaStream_t
   const uint32_t slot = Operand<IO, VEC, NJ, kRing>::slot_bytes(pl.threads) +
                         Operand<RES, VEC, NJ, kRing>::slot_bytes(pl.threads);
   pl.slots = ring_slots(slot, pl.threads, per_sm);
-  return launch_rows<add_norm_fwd_kernel<LAYER, IO, RES, VEC, NJ, MAXT, MINB>>(
-      a, pl, (size_t)pl.slots * slot, st);
+  const size_t smem = (size_t)pl.slots * slot;
+  if constexpr (LAYER && VEC == 1)
+    if (!a.res_q && !a.x_q && !a.out_q)
+      return launch_rows<add_norm_fwd_kernel<LAYER, false, IO, RES, VEC, NJ, MAXT, MINB>>(a, pl, smem,
+                                                                                        st);
+  return launch_rows<add_norm_fwd_kernel<LAYER, true, IO, RES, VEC, NJ, MAXT, MINB>>(a, pl, smem, st);
 }
 template <bool LAYER, typename IO, typename RES>
 cudaError_t fwd_types(const AddNormFwd& a, bool vec, int sms, cudaStream_t st) {

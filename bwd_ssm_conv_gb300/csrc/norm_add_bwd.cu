@@ -18,7 +18,9 @@ namespace ssm {
 
 cudaError_t launch_add_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
                                 cudaStream_t st) {
-  return launch_add_norm_bwd_of<false>(a, io, res_io, vec, sms, st);
+  if (io == SSM_F32) return bwd_types<false, float, float>(a, vec, sms, st);
+  if (res_io == SSM_F32) return bwd_types<false, __nv_bfloat16, float>(a, vec, sms, st);
+  return bwd_types<false, __nv_bfloat16, __nv_bfloat16>(a, vec, sms, st);
 }
 
 }  // namespace ssm

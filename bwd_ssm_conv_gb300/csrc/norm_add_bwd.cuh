@@ -9,7 +9,8 @@ namespace ssm {
 
 namespace {
 
-template <bool LAYER, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
+// KEPT: s or x may be checkpoints.
+template <bool LAYER, bool KEPT, typename IO, typename RES, int VEC, int NJ, int MAXT, int MINB>
 __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormBwd a,
                                                                   const RowPlan pl) {
   extern __shared__ __align__(16) unsigned char ring[];  // at the end: the slots' column sums
@@ -22,6 +23,8 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
   int col[NJ];
   float w[NJ][VEC], dw[NJ][VEC], ds[NJ][VEC];
   float db[LAYER ? NJ : 1][VEC];
+  constexpr bool kHoldScale = LAYER && VEC == 1 && NJ <= 4;
+  float hold[kHoldScale ? NJ : 1];
 #pragma unroll
   for (int j = 0; j < NJ; j++) {
     col[j] = (pos.lane + j * pl.tpr) * VEC;
@@ -32,9 +35,14 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
     if constexpr (LAYER)
 #pragma unroll
       for (int i = 0; i < VEC; i++) db[j][i] = 0.0f;
+    if constexpr (kHoldScale) {
+      float one[1];
+      ld_param<1>(a.scale, col[j], okc[j], one);
+      hold[j] = one[0];
+    }
   }
-  typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256)> Act;
-  typedef Operand<RES, VEC, NJ, (VEC == 8 && MAXT <= 256)> Res;
+  typedef Operand<IO, VEC, NJ, (VEC == 8 && MAXT <= 256), KEPT> Act;
+  typedef Operand<RES, VEC, NJ, (VEC == 8 && MAXT <= 256), KEPT> Res;
   const uint32_t act = Act::slot_bytes(blockDim.x), res = Res::slot_bytes(blockDim.x);
   const uint32_t at = shared_addr(ring) + 16 * threadIdx.x, bytes = 2 * act + 2 * res;
   const bool want_ds = a.d_scale != nullptr;
@@ -141,10 +149,14 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_bwd_kernel(const AddNormB
       if (ok) {
         if (a.d_res) st_cols((RES*)a.d_res + (long long)row * a.ld_d_res + col[j], r);
         if (a.d_x) {
-          float sc[VEC];
-          ld_param<VEC>(a.scale, col[j], true, sc);
+          if constexpr (kHoldScale) {
+            r[0] *= hold[j];
+          } else {
+            float sc[VEC];
+            ld_param<VEC>(a.scale, col[j], true, sc);
 #pragma unroll
-          for (int i = 0; i < VEC; i++) r[i] *= sc[i];
+            for (int i = 0; i < VEC; i++) r[i] *= sc[i];
+          }
           st_cols((IO*)a.d_x + (long long)row * a.ld_d_x + col[j], r);
         }
       }
@@ -171,8 +183,12 @@ cudaError_t bwd_launch(const AddNormBwd& a, RowPlan pl, int per_sm, cudaStream_t
                              Operand<RES, VEC, NJ, kRing>::slot_bytes(pl.threads));
   pl.slots = VEC == 1 ? 2 : ring_slots(slot, pl.threads, per_sm);
   const size_t ring = (size_t)pl.slots * slot, sums = slots_bytes(pl, VEC, NJ);
-  return launch_rows<add_norm_bwd_kernel<LAYER, IO, RES, VEC, NJ, MAXT, MINB>>(
-      a, pl, ring > sums ? ring : sums, st);
+  const size_t smem = ring > sums ? ring : sums;
+  if constexpr (LAYER && VEC == 1)
+    if (!a.res_q && !a.x_q)
+      return launch_rows<add_norm_bwd_kernel<LAYER, false, IO, RES, VEC, NJ, MAXT, MINB>>(a, pl, smem,
+                                                                                        st);
+  return launch_rows<add_norm_bwd_kernel<LAYER, true, IO, RES, VEC, NJ, MAXT, MINB>>(a, pl, smem, st);
 }
 
 template <bool LAYER, typename IO, typename RES>
@@ -188,14 +204,6 @@ cudaError_t bwd_types(const AddNormBwd& a, bool vec, int sms, cudaStream_t st) {
   return launch_column_sums(a.part, s.plan.nbx, a.cols, a.d_w, a.d_b, a.d_scale, st);
 }
 
-
-template <bool LAYER>
-cudaError_t launch_add_norm_bwd_of(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
-                                   cudaStream_t st) {
-  if (io == SSM_F32) return bwd_types<LAYER, float, float>(a, vec, sms, st);
-  if (res_io == SSM_F32) return bwd_types<LAYER, __nv_bfloat16, float>(a, vec, sms, st);
-  return bwd_types<LAYER, __nv_bfloat16, __nv_bfloat16>(a, vec, sms, st);
-}
 
 }  // namespace
 

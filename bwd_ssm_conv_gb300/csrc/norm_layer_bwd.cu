@@ -3,13 +3,16 @@
 //   d_residual = r,  d_x = scale r,  d_w = sum_rows d_out n,  d_b = sum_rows d_out,
 //   d_scale = sum_rows r x
 // A row is read once and its two sums are formed together over its threads.
+// Each pair of types in a file of its own, as they take the compiler a minute each.
 #include "norm_add_bwd.cuh"
 
 namespace ssm {
 
 cudaError_t launch_add_layer_norm_bwd(const AddNormBwd& a, int io, int res_io, bool vec, int sms,
                                       cudaStream_t st) {
-  return launch_add_norm_bwd_of<true>(a, io, res_io, vec, sms, st);
+  if (io == SSM_F32) return add_layer_norm_bwd_f32(a, vec, sms, st);
+  if (res_io == SSM_F32) return add_layer_norm_bwd_mixed(a, vec, sms, st);
+  return bwd_types<true, __nv_bfloat16, __nv_bfloat16>(a, vec, sms, st);
 }
 
 }  // namespace ssm

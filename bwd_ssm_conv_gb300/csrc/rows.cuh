@@ -402,8 +402,9 @@ __device__ __forceinline__ uint4 ld_shared16(uint32_t a) {
   return v;
 }
 
-// One operand, a tensor t or (q given) its checkpoint, and a thread's NJ chunks of its rows.
-template <typename IO, int VEC, int NJ, bool RING> struct Operand {
+// One operand, a tensor t or (q given) its checkpoint, and a thread's NJ chunks of its rows.  Without KEPT
+// there is no checkpoint, and nothing asks for one: for single columns that is a third of the instructions.
+template <typename IO, int VEC, int NJ, bool RING, bool KEPT = true> struct Operand {
   static constexpr int kUnits = RING ? (int)sizeof(IO) / 2 : 0;  // 16 bytes per chunk and row
   const void* t;
   const int8_t* q;
@@ -414,7 +415,8 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   // single columns of this row and the next, as loaded: nothing waits for the next row's
   uint32_t cur[kAhead ? NJ : 1], next[kAhead ? NJ : 1];
 
-  __device__ __forceinline__ bool given() const { return t || q; }
+  __device__ __forceinline__ bool kept() const { return KEPT && q; }
+  __device__ __forceinline__ bool given() const { return t || kept(); }
   // Bytes that a block's threads need per slot of the ring.
   static __host__ __device__ constexpr uint32_t slot_bytes(int threads) {
     return 16u * kUnits * NJ * threads;
@@ -435,14 +437,14 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
       for (int j = 0; j < NJ; j++) {
         next[j] = 0u;
         if (!okc[j] || !given()) continue;
-        if (q) next[j] = (uint32_t)(int)pq[col[j]];
+        if (kept()) next[j] = (uint32_t)(int)pq[col[j]];
         else if constexpr (sizeof(IO) == 2) next[j] = reinterpret_cast<const uint16_t*>(pt)[col[j]];
         else next[j] = reinterpret_cast<const uint32_t*>(pt)[col[j]];
       }
     }
     if constexpr (RING) {
       const uint32_t unit = 16 * blockDim.x;
-      if (q) {
+      if (kept()) {
         const int8_t* p = q + (long long)row * cols;
 #pragma unroll
         for (int j = 0; j < NJ; j++)
@@ -482,7 +484,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   }
   // The scale byte of a chunk (a checkpoint's; 7 otherwise).
   __device__ __forceinline__ uint32_t scale(bool ok, int row, int col, int nb) const {
-    return q && ok ? e[(long long)row * nb + (int)((unsigned)col / 32)] : 7u;
+    return kept() && ok ? e[(long long)row * nb + (int)((unsigned)col / 32)] : 7u;
   }
   // The largest magnitude's bits of the block that a tensor's chunk lies in; v holds its values.
   __device__ __forceinline__ uint32_t top(uint32_t s, int j, const float (&v)[VEC]) const {
@@ -495,19 +497,19 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
   __device__ __forceinline__ void get(uint32_t s, int j, bool ok, int row, int col, int cols,
                                       uint32_t x, float (&v)[VEC]) const {
     if constexpr (kAhead) {
-      v[0] = q ? (float)(int)cur[j] * block_step(x) :
+      v[0] = kept() ? (float)(int)cur[j] * block_step(x) :
              __uint_as_float(sizeof(IO) == 2 ? cur[j] << 16 : cur[j]);
     } else if constexpr (VEC == 1) {
       Cols<IO, 1> c;
       c.zero();
       if (ok && t) c.load((const IO*)t + (long long)row * ld + col);
       c.get(v);
-      if (ok && q) v[0] = (float)q[(long long)row * cols + col] * block_step(x);
+      if (ok && kept()) v[0] = (float)q[(long long)row * cols + col] * block_step(x);
     } else if constexpr (!RING) {
       if (!ok || !given()) {
 #pragma unroll
         for (int i = 0; i < VEC; i++) v[i] = 0.0f;
-      } else if (q) {
+      } else if (kept()) {
         Kept<8> k;
         k.q = *reinterpret_cast<const uint2*>(q + (long long)row * cols + col);
         k.e = (uint8_t)x;
@@ -520,7 +522,7 @@ template <typename IO, int VEC, int NJ, bool RING> struct Operand {
     } else {
       const uint32_t unit = 16 * blockDim.x, a = at + s + j * kUnits * unit;
       const uint4 w = ld_shared16(a);
-      if (q) {
+      if (kept()) {
         Kept<8> k;
         k.q = make_uint2(w.x, w.y);
         k.e = (uint8_t)x;
