@@ -33,7 +33,7 @@ struct HeadRows {  // of a call, on the device
   HeadState* state;
   int* pos;  // [rows]
   int* src;  // [padded rows], -1 past the packed ones
-  float *rl, *rg;  // backward, [padded rows]: lse log2(e), d_loss / g_top
+  float *rl, *rg;  // backward, [padded rows]: lse, d_loss / g_top
   __nv_bfloat16* h;  // [planes][padded rows][padded cols]
 };
 

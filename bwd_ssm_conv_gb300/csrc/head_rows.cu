@@ -296,7 +296,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
         copy8<IO, PLANES, VEC_H>(x + c, a.cols - c, out + c, plane);
     }
     if (a.lse && lane == 0) {
-      r.rl[row] = from < 0 ? 0.0f : a.lse[from] * kLog2e;
+      r.rl[row] = from < 0 ? 0.0f : a.lse[from];
       r.rg[row] = from < 0 ? 0.0f : a.d_loss[from] / top;
     }
   }

@@ -13,11 +13,11 @@
 //   warp 1      one thread of the first CTA issues the MMAs; the second CTA's passes on that its copies
 //               have landed
 //   warps 4-11  take the results out: thread = row, 128 of its columns each
-// fp32 operands are three bf16 planes each, staged one after the other (0, 2, 1) in slots of their own:
-// six products per step over 64 of the sum (of planes 0 0, 2 0, 0 2, 0 1, 1 0, 1 1; the rest is below 2^-24
-// of a product), whose slots come free in between, so that a slot's next copy has more than a step's time
-// (with all six planes in one of two slots, a tile of 128 columns waited for copies 40 % of its time).  As the
-// tensor cores truncate when they add, these sums are taken out every 128 columns and added in registers.
+// fp32 operands are three bf16 planes each, staged one after the other (1, 0, 2) in slots of their own:
+// six products per step over 64 of the sum (of planes 1 1, 1 0, 0 1, 2 0, 0 2, 0 0; the rest is below 2^-24
+// of a product), whose slots come free in between, so that a slot's next copy has more than a step's time.
+// The tensor cores truncate when they add, by the size of the sum: small products come before the large one,
+// and the sums are taken out every 64 columns and added in registers.
 #include "head.cuh"
 #include "pair.cuh"
 
@@ -39,8 +39,14 @@ constexpr int kRegsFew = 64, kRegsSum = 216;  // PLANES = 3: 128 x 64 + 256 x 21
 constexpr int kSlots = 6;
 constexpr uint32_t kSlot = 2 * kOperand, kAtTurn = kSlots * kSlot;
 constexpr uint32_t kSmem = kAtTurn + kSumWarps * 32 * 33 * 4 + 1024;
-// Stages between two emptyings of the accumulator.
-template <int PLANES> constexpr int kSegment = PLANES == 1 ? 1 << 30 : 2;
+// Stages between two emptyings of the accumulator: as the tensor cores truncate when they add, by the size
+// of the sum.  Errors of lse and of d_W against 64 bits (plain fp32: 2e-7, 6.6e-7 and up):
+//   fp32, 1021 x 515 over 10007 words: every 2 stages 3.2e-7 and 6.4e-7, every stage 0.7e-7 and 3.5e-7, for
+//     5 % of the time
+//   bf16, lse alone (G is rounded to bf16): all at once 768 columns 5.8e-7, 1024 7.4e-7, 2048 1.5e-6; every 12
+//     stages 4.8e-7 to 5.8e-7, which slows 1024 columns down
+template <int USE, int PLANES>
+constexpr int kSegment = PLANES > 1 ? 1 : USE == kLogits ? 16 : 1 << 30;
 
 // A product of a launch.
 struct Job {
@@ -69,6 +75,7 @@ struct TcArgs {
   int no_wait;
   // kLogits, kGrad
   float scale;         // log2(e) / tau
+  float inv_tau, inv_tau_rest;
   int v0, vocab;       // the word of column 0
   int entries;
   const int* src;
@@ -170,7 +177,7 @@ template <int USE, int PLANES> struct Taker {
       e = 0, next = kNoEntry;
       if (src >= 0 && a.v0 + col0 < a.vocab) find(a.v0 + col0);
       if constexpr (USE == kGrad)
-        if (row_ok) rl = a.rl[row], rg = a.rg[row];
+        if (row_ok) rl = PLANES == 1 ? a.rl[row] * kLog2e : a.rl[row], rg = a.rg[row];
     } else {
       if (job.part) dst = job.part + ((long long)split * job.part_rows + row) * job.ld_part + col0;
       else scale = a.state->scale;
@@ -229,9 +236,15 @@ template <int USE, int PLANES> struct Taker {
       }
     } else if constexpr (USE == kGrad) {
       const int word = a.v0 + col0 + 32 * c;
+      // At most 1, also where logits are so large that roundings are not small.  With fp32 operands the
+      // distance z / tau - lse is formed first (1 / tau in two terms): a product rounded at lse log2(e) would
+      // be the largest error of G.
 #pragma unroll
-      for (int i = 0; i < 32; i++)  // at most 1, also where logits are so large that roundings are not small
-        v[i] = ex2(min_nan(fmaf(v[i], a.scale, -rl), 0.0f));
+      for (int i = 0; i < 32; i++) {
+        const float x = PLANES == 1 ? fmaf(v[i], a.scale, -rl) :
+                                      fmaf(v[i], a.inv_tau, fmaf(v[i], a.inv_tau_rest, -rl)) * kLog2e;
+        v[i] = ex2(min_nan(x, 0.0f));
+      }
       if constexpr (PLANES > 1)
         while (next < word + 32) {
           const float p = prob();
@@ -383,7 +396,7 @@ struct Units {
 
 template <int USE, int PLANES>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
-  constexpr int S = kSlots, kSeg = kSegment<PLANES>;
+  constexpr int S = kSlots, kSeg = kSegment<USE, PLANES>;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t here[S], there[S], empty[S], ready[2], drained[2], last;
   __shared__ uint32_t tbase;
@@ -440,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         for (int k = x.begin; k < x.begin + x.iters && ok; k++) {
 #pragma unroll
           for (int i = 0; i < PLANES; i++, it++, r.next()) {
-            const int p = i == 0 ? 0 : 3 - i;  // 0, 2, 1
+            const int p = PLANES == 1 ? 0 : i == 0 ? 1 : i == 1 ? 0 : 2;
             if (it >= S) ok = ok && wait_for(&empty[r.s], r.phase ^ 1, &bad);
             if (!ok) break;
             if (elect_one()) {
@@ -498,19 +511,21 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
               ok = wait_for(&here[r.s], r.phase, &bad) && wait_for(&there[r.s], r.phase, &bad);
               tmem_fence_after_sync();
               if (ok && elect_one()) {
-                if (i == 0) {
+                if (PLANES == 1) {
                   mul(slot[0], slot[0], !first);
-                  if (PLANES == 1) Mma<2>::commit(&empty[slot[0]]);
-                } else if (i == 1) {  // plane 2
-                  mul(slot[i], slot[0], true);
-                  mul(slot[0], slot[i], true);
-                  Mma<2>::commit(&empty[slot[i]]);
-                } else {  // plane 1
+                  Mma<2>::commit(&empty[slot[0]]);
+                } else if (i == 0) {  // plane 1
+                  mul(slot[0], slot[0], !first);
+                } else if (i == 1) {  // plane 0
                   mul(slot[0], slot[i], true);
                   mul(slot[i], slot[0], true);
                   Mma<2>::commit(&empty[slot[0]]);
-                  mul(slot[i], slot[i], true);
+                } else {  // plane 2, then the leading product
+                  mul(slot[i], slot[1], true);
+                  mul(slot[1], slot[i], true);
                   Mma<2>::commit(&empty[slot[i]]);
+                  mul(slot[1], slot[1], true);
+                  Mma<2>::commit(&empty[slot[1]]);
                 }
               }
               __syncwarp();
@@ -554,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       Taker<USE, PLANES> taker(a, a.job[x.job],
                                x.mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
                                x.nt * x.tile_n + width * half, rows, x.split, turn);
-      if constexpr (PLANES == 1) {
+      if (PLANES == 1 && iters <= kSeg) {
         ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
         __syncwarp();
         tmem_fence_after_sync();
@@ -573,7 +588,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           __syncwarp();
         }
         seg++;
-      } else {
+      } else if constexpr (kSeg < 1 << 30) {
         float acc[4][32];
 #pragma unroll
         for (int c = 0; c < 4; c++)
@@ -586,12 +601,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           if (!ok) break;
           const uint32_t t = tacc + (seg & 1) * kHeadTile;
 #pragma unroll
-          for (int c = 0; c < 8; c++) {
-            if (c >= 2 * chunks) break;
-            float v[16];
-            tmem_ld16(t + 16 * c, v);
+          for (int c = 0; c < 4; c++) {
+            if (c >= chunks) break;
+            float v[32];
+            tmem_ld32(t + 32 * c, v);
 #pragma unroll
-            for (int i = 0; i < 16; i++) acc[c >> 1][16 * (c & 1) + i] += v[i];
+            for (int i = 0; i < 32; i++) acc[c][i] += v[i];
           }
           tmem_fence_before_sync();
           __syncwarp();
@@ -674,6 +689,9 @@ TcArgs args_of(const ssm_head_desc& d, const HeadRows& r, const HeadLists& lists
   t.state = r.state;
   t.no_wait = (d.flags & SSM_DEBUG_NO_WAIT) != 0;
   t.scale = d.entries ? kLog2e / d.temperature : kLog2e;
+  const double inv = d.entries ? 1.0 / d.temperature : 1.0;
+  t.inv_tau = (float)inv;
+  t.inv_tau_rest = (float)(inv - t.inv_tau);
   t.vocab = d.vocab;
   t.entries = d.entries ? d.entries : 1;
   t.src = r.src;
