@@ -12,8 +12,13 @@ first norm's backward), u and v (for the projections' weight gradients), y and z
 norm's backward).  The norms write these checkpoints in the pass that computes them; the backward
 calls read them without unpacking them to memory first.
 
+``Head`` ends a language model of such blocks: the last layer norm with the residual add
+(ssm_add_layer_norm_fwd), the head and the loss, cross entropy against the next token (ssm_head_ce_fwd) or
+distillation from a teacher's top logits (ssm_head_distill_fwd), whose logits are never kept.
+
 ``python examples/mamba_block.py`` trains a small model of such blocks for some steps with and
-without the checkpoints and prints the losses, the memory kept and the time per step.
+without the checkpoints and prints the losses, the memory kept and the time per step, then the same as a
+language model over a vocabulary.
 """
 from __future__ import annotations
 
@@ -151,6 +156,44 @@ class Block:
         return v.out @ p["W_out"].to(self.io).t(), a.res_out
 
 
+class Head:
+    """The end of a language model: the last norm and the head's weights, one row per word (the embedding
+    may be the same); parameters in fp32."""
+
+    def __init__(self, d_model, vocab, seed: int, io=torch.bfloat16, device="cuda"):
+        g = torch.Generator().manual_seed(seed)
+        self.io = io
+        self.p = dict(w=torch.ones(d_model, device=device), b=torch.zeros(d_model, device=device),
+                      W=(d_model ** -0.5 * torch.randn(vocab, d_model, generator=g)).to(device))
+
+    def embed(self, tokens):
+        return self.p["W"].to(self.io)[tokens]
+
+    def forward(self, h, residual, target, teacher=None, temperature=1.0):
+        """The loss of each row of h [...][d_model] and what backward needs.  target [...]: the next
+        tokens, -100 where there is none; or teacher: (t_idx, t_logit) of each row."""
+        a = ssm.ssm_add_layer_norm_fwd(h, self.p["w"], self.p["b"], residual, res_dtype=torch.float32)
+        W = self.p["W"].to(self.io)
+        if teacher is None:
+            r = ssm.ssm_head_ce_fwd(a.out, W, target)
+        else:
+            r = ssm.ssm_head_distill_fwd(a.out, W, *teacher, temperature=temperature)
+        return r.loss, dict(norm=a, W=W, lse=r.lse, target=target, teacher=teacher,
+                            temperature=temperature)
+
+    def backward(self, d_loss, kept):
+        """(d_h, d_residual, gradients by name) of sum(d_loss * loss)."""
+        a, k = kept["norm"], kept
+        if k["teacher"] is None:
+            b = ssm.ssm_head_ce_bwd(a.out, k["W"], k["target"], k["lse"], d_loss)
+        else:
+            b = ssm.ssm_head_distill_bwd(a.out, k["W"], *k["teacher"], k["lse"], d_loss,
+                                         temperature=k["temperature"])
+        n = ssm.ssm_add_layer_norm_bwd(b["d_h"], a.res_out, a.mean, a.rstd, self.p["w"],
+                                       res_dtype=torch.float32)
+        return n["d_x"], n["d_res"], dict(w=n["d_w"], b=n["d_b"], W=b["d_w"].float())
+
+
 def kept_bytes(kept):
     """Bytes of the activations that a block keeps for its backward."""
     total = 0
@@ -180,6 +223,43 @@ def train_step(blocks, h, target, save8, lr=0.0):
     return float(loss), n_bytes
 
 
+def lm_step(blocks, head, tokens, save8=True, lr=0.0, teacher=None, temperature=1.0):
+    """One step of a language model on tokens [n_s][L], each to be told from those before it; the mean
+    loss.  The embedding is the head's weights."""
+    target = torch.full_like(tokens, -100)  # the last token of a sequence has no next one
+    target[:, :-1] = tokens[:, 1:]
+    kept, stream, x = [], None, head.embed(tokens)
+    for b in blocks:
+        x, stream, k = b.forward(x, stream, save8)
+        kept.append(k)
+    loss, last = head.forward(x, stream, target, teacher, temperature)
+    rows = tokens.numel() if teacher is not None else tokens.shape[0] * (tokens.shape[1] - 1)
+    d_x, d_stream, g_head = head.backward(torch.full_like(loss, 1.0 / rows), last)
+    for b, k in zip(reversed(blocks), reversed(kept)):
+        d_x, d_stream, g = b.backward(d_x, d_stream, k)
+        for name, v in g.items():
+            b.p[name] -= lr * v
+        b.p["A"].clamp_(max=-0.01)
+    # the first block's h is the embedding
+    g_head["W"].index_add_(0, tokens.flatten(), d_x.float().flatten(0, 1))
+    for name, v in g_head.items():
+        head.p[name] -= lr * v
+    return float(loss.sum() / rows)
+
+
+def score(blocks, head, tokens):
+    """The log-probability of each token of tokens [n_s][L] after the first, a token at a time."""
+    n, L = tokens.shape
+    caches, out = [b.new_cache(n) for b in blocks], []
+    for t in range(L - 1):
+        x, stream = head.embed(tokens[:, t]), None
+        for b, c in zip(blocks, caches):
+            x, stream = b.decode(x, stream, c)
+        loss, _ = head.forward(x, stream, tokens[:, t + 1].contiguous())
+        out.append(-loss)
+    return torch.stack(out, 1)
+
+
 def main():
     shape = Shape(d_model=768, n_head=24, head_dim=64, d_state=128)
     g = torch.Generator(device="cuda").manual_seed(0)
@@ -196,6 +276,19 @@ def main():
         torch.cuda.synchronize()
         print(f"save8={save8}: loss {losses[0]:.4f} -> {losses[-1]:.4f}, "
               f"{n / 2 ** 20:.0f} MiB kept, {start.elapsed_time(end) / 5:.2f} ms per step")
+
+    blocks, head = [Block(shape, seed=i) for i in range(4)], Head(shape.d_model, 32768, seed=9)
+    tokens = torch.randint(32768, (8, 1024), generator=g, device="cuda")
+    losses = [lm_step(blocks, head, tokens, lr=1e-2) for _ in range(10)]
+    start, end = torch.cuda.Event(True), torch.cuda.Event(True)
+    start.record()
+    for _ in range(5):
+        lm_step(blocks, head, tokens)
+    end.record()
+    torch.cuda.synchronize()
+    print(f"language model over 32768 words: loss {losses[0]:.4f} -> {losses[-1]:.4f}, "
+          f"{start.elapsed_time(end) / 5:.2f} ms per step, log-probability a token at a time "
+          f"{score(blocks, head, tokens[:1, :16]).mean():.4f}")
 
 
 if __name__ == "__main__":
