@@ -34,19 +34,21 @@ constexpr uint32_t kOperand = 2 * kSlab;      // 128 rows or columns of a CTA
 constexpr uint32_t kTmCols = 2 * kHeadTile;
 constexpr int kRegsFew = 64, kRegsSum = 216;  // PLANES = 3: 128 x 64 + 256 x 216 <= 384 x 168
 
-// Shared memory of a CTA: slots of A's and B's part of a stage (one plane of it), then 32 x 32 values of
-// each warp that takes results out, rows 33 apart (Taker::store).
+// Shared memory of a CTA: slots of A's and B's part of a stage (one plane of it), then, only where results
+// are stored at any width, 32 x 32 values of each warp that takes them out, rows 33 apart (Taker::store).
+// Without those a block of the small kernels before and behind fits beside it, so that either starts under the
+// other's end.
 constexpr int kSlots = 6;
 constexpr uint32_t kSlot = 2 * kOperand, kAtTurn = kSlots * kSlot;
-constexpr uint32_t kSmem = kAtTurn + kSumWarps * 32 * 33 * 4 + 1024;
+constexpr uint32_t kTurn = kSumWarps * 32 * 33 * 4, kSmem = kAtTurn + 1024;
+
 // Stages between two emptyings of the accumulator: as the tensor cores truncate when they add, by the size
 // of the sum.  Errors of lse and of d_W against 64 bits (plain fp32: 2e-7, 6.6e-7 and up):
 //   fp32, 1021 x 515 over 10007 words: every 2 stages 3.2e-7 and 6.4e-7, every stage 0.7e-7 and 3.5e-7, for
 //     5 % of the time
 //   bf16, lse alone (G is rounded to bf16): all at once 768 columns 5.8e-7, 1024 7.4e-7, 2048 1.5e-6; every 12
 //     stages 4.8e-7 to 5.8e-7, which slows 1024 columns down
-template <int USE, int PLANES>
-constexpr int kSegment = PLANES > 1 ? 1 : USE == kLogits ? 16 : 1 << 30;
+template <int PLANES> constexpr int kSegment = PLANES > 1 ? 1 : 16;
 
 // A product of a launch.
 struct Job {
@@ -394,9 +396,10 @@ struct Units {
   }
 };
 
-template <int USE, int PLANES>
+// SEG: sums are taken out in between (without it the kernel has half the registers).
+template <int USE, int PLANES, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
-  constexpr int S = kSlots, kSeg = kSegment<USE, PLANES>;
+  constexpr int S = kSlots, kSeg = SEG ? kSegment<PLANES> : 1 << 30;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t here[S], there[S], empty[S], ready[2], drained[2], last;
   __shared__ uint32_t tbase;
@@ -569,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       Taker<USE, PLANES> taker(a, a.job[x.job],
                                x.mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
                                x.nt * x.tile_n + width * half, rows, x.split, turn);
-      if (PLANES == 1 && iters <= kSeg) {
+      if constexpr (!SEG) {
         ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
         __syncwarp();
         tmem_fence_after_sync();
@@ -588,7 +591,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           __syncwarp();
         }
         seg++;
-      } else if constexpr (kSeg < 1 << 30) {
+      } else {
         float acc[4][32];
 #pragma unroll
         for (int c = 0; c < 4; c++)
@@ -643,8 +646,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
   if (tid == 0 && gave_up) atomicExch(&a.state->status, SSM_ERR_TIMEOUT);
 }
 
-template <int USE, int PLANES> cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
-  auto kernel = head_tc_kernel<USE, PLANES>;
+template <int USE, int PLANES, bool SEG>
+cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
+  auto kernel = head_tc_kernel<USE, PLANES, SEG>;
+  bool turn = false;
+  for (int j = 0; j < t.jobs; j++)
+    turn = turn || (USE == kOut && !t.job[j].part && !t.job[j].vec_out);
   // asked for once per device (the first 64 remember it)
   static std::atomic<unsigned long long> asked{0};
   int dev = 0;
@@ -652,14 +659,14 @@ template <int USE, int PLANES> cudaError_t launch(const TcArgs& t, int sms, cuda
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0;
   if (!(asked.load(std::memory_order_relaxed) & bit)) {
     if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             (int)kSmem))
+                                             (int)(kSmem + kTurn)))
       return e;
     asked.fetch_or(bit, std::memory_order_relaxed);
   }
   cudaLaunchConfig_t c{};
   c.gridDim = dim3(sms / 2 * 2);
   c.blockDim = dim3(kThreads);
-  c.dynamicSmemBytes = kSmem;
+  c.dynamicSmemBytes = kSmem + (turn ? kTurn : 0);
   c.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -674,7 +681,10 @@ template <int USE, int PLANES> cudaError_t launch(const TcArgs& t, int sms, cuda
   return e;
 }
 template <int USE> cudaError_t launch(const ssm_head_desc& d, const TcArgs& t, int sms, cudaStream_t st) {
-  return d.io == SSM_F32 ? launch<USE, 3>(t, sms, st) : launch<USE, 1>(t, sms, st);
+  if (d.io == SSM_F32) return launch<USE, 3, true>(t, sms, st);
+  if constexpr (USE == kLogits)
+    if (t.job[0].per_split > kSegment<1>) return launch<USE, 1, true>(t, sms, st);
+  return launch<USE, 1, false>(t, sms, st);
 }
 
 bool encode(CUtensorMap* map, const HeadMatrix& x, int planes) {
