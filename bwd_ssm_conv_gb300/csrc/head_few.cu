@@ -67,34 +67,27 @@ template <typename IO, bool VEC> struct Chunk {
   }
 };
 
-// sum[j] (+)= over this lane's chunks of words[j]; R rows each, h [R][padded] in shared memory.
-template <typename IO, bool VEC, int R, int N>
-__device__ __forceinline__ void dots(const FewArgs& a, const float* h, int padded, const int (&words)[N],
-                                     float (&sum)[N][R]) {
-  const int lane = threadIdx.x & 31;
-  const IO* p[N];
+// This lane's chunks of N words, U of them at a time, those past the row's end as zeros.
+template <typename IO, bool VEC, int R, int N> struct Words {
+  static constexpr int U = R == 1 && sizeof(IO) == 2 ? 3 : 2;
+  Chunk<IO, VEC> x[U][N];
+  __device__ __forceinline__ void load(const FewArgs& a, int padded, const int (&words)[N], int c0) {
 #pragma unroll
-  for (int j = 0; j < N; j++) {
-    p[j] = (const IO*)a.w + words[j] * a.ld_w;
+    for (int j = 0; j < N; j++) {
+      const IO* p = (const IO*)a.w + words[j] * a.ld_w;
 #pragma unroll
-    for (int r = 0; r < R; r++) sum[j][r] = 0.0f;
-  }
-  // U chunks of each word in flight together, those past the row's end as zeros
-  constexpr int U = R == 1 && sizeof(IO) == 2 ? 3 : 2;
-  for (int c0 = 0; c0 < padded; c0 += 256 * U) {
-    Chunk<IO, VEC> x[U][N];
-#pragma unroll
-    for (int u = 0; u < U; u++) {
-      const int c = c0 + 256 * u + 8 * lane;
-#pragma unroll
-      for (int j = 0; j < N; j++) {
+      for (int u = 0; u < U; u++) {
+        const int c = c0 + 256 * u + 8 * (threadIdx.x & 31);
         x[u][j].zero();
-        if (c < padded) x[u][j].load(p[j] + c, a.cols - c);
+        if (c < padded) x[u][j].load(p + c, a.cols - c);
       }
     }
+  }
+  // sum[j][r] += over them of words j and row r of h [R][padded] in shared memory
+  __device__ __forceinline__ void add(const float* h, int padded, int c0, float (&sum)[N][R]) const {
 #pragma unroll
     for (int u = 0; u < U; u++) {
-      const int c = min(c0 + 256 * u + 8 * lane, padded - 8);
+      const int c = min(c0 + 256 * u + 8 * (int)(threadIdx.x & 31), padded - 8);
       float v[N][8];
 #pragma unroll
       for (int j = 0; j < N; j++) x[u][j].get(v[j]);
@@ -110,7 +103,7 @@ __device__ __forceinline__ void dots(const FewArgs& a, const float* h, int padde
       }
     }
   }
-}
+};
 
 template <typename IO, bool VEC, int R>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const FewArgs a) {
@@ -122,6 +115,12 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
   // A warp's words lie together, as many as the others' or one more.
   const long long warps = (long long)gridDim.x * kWarps, me = (long long)blockIdx.x * kWarps + warp;
   const int from = (int)(me * a.vocab / warps), to = (int)((me + 1) * a.vocab / warps);
+  // its first ones are on their way while the rows are looked at: W is nobody's result in this call
+  Words<IO, VEC, R, kWords> batch;
+  int words[kWords];
+#pragma unroll
+  for (int i = 0; i < kWords; i++) words[i] = max(min(from + i, to - 1), 0);
+  batch.load(a, padded, words, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (threadIdx.x < R) {  // which rows count: each block sees for itself
     const int t = threadIdx.x;
@@ -152,38 +151,22 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
   }
   __syncthreads();
 
-  // the entries' logits, from the last warp on: first, as a word more would take longer at the end
-  for (long long i = warps - 1 - me; i < a.rows * a.entries; i += warps) {
-    const int row = (int)(i / a.entries);
-    const int word = kind[row] < 0 ? kNoEntry : a.target ? (int)a.target[row] : a.idx[i];
-    if (word == kNoEntry) continue;
-    const int words[1] = {word};
-    float d[1][1];
-    dots<IO, VEC, 1, 1>(a, h + row * padded, padded, words, d);
-    float v = d[0][0];
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    if (lane == 0) a.zt[i] = v;
-  }
-
-  constexpr int W = 4;               // words of a warp at a time
-  constexpr int N = W * R;           // sums: number j * R + r is word j's of row r
-  constexpr int kSame = 32 / N;      // lanes that end with the same one
+  constexpr int W = kWords;      // words of a warp at a time
+  constexpr int N = W * R;       // sums: number j * R + r is word j's of row r
+  constexpr int kSame = 32 / N;  // lanes that end with the same one
   const int mine = lane / kSame;
   float top = -INFINITY, total = 0.0f;
   for (int w0 = from; w0 < to; w0 += W) {
-    float s[N];
+    float d[W][R] = {}, s[N];
+    for (int c0 = 0; c0 < padded; c0 += 256 * batch.U) {
+      if (w0 > from || c0 > 0) batch.load(a, padded, words, c0);
+      batch.add(h, padded, c0, d);
+    }
 #pragma unroll
-    for (int j = 0; j < W; j += kWords) {
-      int words[kWords];
-      float d[kWords][R];
+    for (int i = 0; i < W; i++) {
+      words[i] = min(w0 + W + i, to - 1);
 #pragma unroll
-      for (int i = 0; i < kWords; i++) words[i] = min(w0 + j + i, to - 1);
-      dots<IO, VEC, R, kWords>(a, h, padded, words, d);
-#pragma unroll
-      for (int i = 0; i < kWords; i++)
-#pragma unroll
-        for (int r = 0; r < R; r++) s[(j + i) * R + r] = d[i][r];
+      for (int r = 0; r < R; r++) s[i * R + r] = d[i][r];
     }
 #pragma unroll
     for (int off = 16, n = N / 2; off > 0; off >>= 1, n >>= 1) {
@@ -208,6 +191,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
     const float above = fmaxf(top, t), base = above == -INFINITY ? 0.0f : above;
     total = total * ex2((top - base) * a.scale) + u * ex2((t - base) * a.scale);
     top = above;
+  }
+  // the entries' logits, from the last warp on, which has the fewest words
+  for (long long i = warps - 1 - me; i < a.rows * a.entries; i += warps) {
+    const int row = (int)(i / a.entries);
+    const int word = kind[row] < 0 ? kNoEntry : a.target ? (int)a.target[row] : a.idx[i];
+    if (word == kNoEntry) continue;
+    const int one[1] = {word};
+    Words<IO, VEC, 1, 1> x;
+    float d[1][1] = {};
+    for (int c0 = 0; c0 < padded; c0 += 256 * x.U) {
+      x.load(a, padded, one, c0);
+      x.add(h + row * padded, padded, c0, d);
+    }
+    float v = d[0][0];
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    if (lane == 0) a.zt[i] = v;
   }
   float2* sums = reinterpret_cast<float2*>(h + R * padded);
   if (mine < R && lane % kSame == 0) sums[warp * R + mine] = make_float2(top, total);
