@@ -11,6 +11,7 @@ namespace {
 using namespace ssm;
 
 constexpr long long kMaxTotal = 1LL << 40;  // elements between a tensor's first and last row
+constexpr long long kMaxLogits = 1LL << 40;  // rows times words: tiles are counted in 32 bits
 // Bytes of G at a time (a tile's columns at least).  Fewer and larger pieces leave fewer ends of launches with
 // idle SMs: 16384 x 1024 over 32768 words 2.97 ms at 96 MiB, 2.76 at 256, 2.64 at 512, 2.66 at 1024.
 constexpr long long kMaxPiece = 512LL << 20;
@@ -115,7 +116,7 @@ struct Plan {
   int planes, tile_z, n_stats, piece, pieces;
   Cuts cuts;
 };
-Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
+Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   Plan p{};
   const long long T = d.rows, Tp = pad_rows(T), n_e = d.entries ? d.entries : 1;
   const int Dp = pad8(d.cols);
@@ -171,6 +172,28 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   return p;
 }
 
+// The plan of sizes, which a call needs twice (workspace and launches) and a training loop again and again:
+// the thread's last few are kept (deciding on the cuts takes the host several us).
+Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
+  struct Known {
+    long long rows;
+    int cols, vocab, io, entries, grads, copy_w, sms;
+    Plan plan;
+  };
+  constexpr int kPlans = 8;
+  static thread_local Known known[kPlans];
+  static thread_local int next = 0;
+  for (const Known& k : known)
+    if (k.sms == sms && k.rows == d.rows && k.cols == d.cols && k.vocab == d.vocab && k.io == d.io &&
+        k.entries == d.entries && k.grads == grads && k.copy_w == (int)copy_w)
+      return k.plan;
+  Known& k = known[next];
+  next = (next + 1) % kPlans;
+  k = {d.rows, d.cols, d.vocab, d.io, d.entries, grads, (int)copy_w, sms,
+       make_plan(d, grads, copy_w, sms)};
+  return k.plan;
+}
+
 int check(const ssm_head_desc* d, bool distill) {
   if (!d || d->rows <= 0 || d->cols <= 0 || d->vocab <= 0 || !io_size(d->io))
     return SSM_ERR_INVALID_ARG;
@@ -178,12 +201,15 @@ int check(const ssm_head_desc* d, bool distill) {
   if (distill) {
     if (d->entries <= 0 || !io_size(d->entry_io)) return SSM_ERR_INVALID_ARG;
     if (!(d->temperature > 0.0f) || isinf(d->temperature)) return SSM_ERR_INVALID_ARG;
-    if (d->entries > SSM_MAX_HEAD_ENTRIES) return SSM_ERR_UNSUPPORTED;
+    if (d->entries > SSM_MAX_HEAD_ENTRIES || d->temperature < 1.0f / SSM_MAX_HEAD_TEMPERATURE ||
+        d->temperature > SSM_MAX_HEAD_TEMPERATURE)
+      return SSM_ERR_UNSUPPORTED;
   } else if (d->entries) {
     return SSM_ERR_INVALID_ARG;
   }
   if (d->rows > SSM_MAX_HEAD_ROWS || d->cols > SSM_MAX_HEAD_COLS || d->vocab > SSM_MAX_HEAD_VOCAB)
     return SSM_ERR_UNSUPPORTED;
+  if (d->rows > kMaxLogits / d->vocab) return SSM_ERR_UNSUPPORTED;
   return SSM_OK;
 }
 

@@ -100,7 +100,7 @@ def ssm_head_ce_bwd(h, w, target, lse, d_loss, ignore_index=-100, want_dh=True, 
 
 def ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=1.0, ws=None, out=None, stream=None,
                          debug_flags=0) -> HeadLoss:
-    """Per row of h [..., cols]: tau^2 KL(p || q), with tau the ``temperature``, p the softmax of a
+    """Per row of h [..., cols]: tau^2 KL(p || q), with tau the ``temperature`` (1e-6 .. 1e6), p the softmax of a
     teacher's logits t_logit / tau over its entries (t_idx int64, both [..., entries], 1 .. 128 of
     them; an index below 0: no entry) and q that of h w^T / tau over the whole vocabulary; and lse of
     the latter, for the backward.  Rows without an entry have loss and lse 0, cost no product and are

@@ -45,7 +45,8 @@ extern "C" {
 #define SSM_MAX_HEAD_ENTRIES 128 /* teacher entries of a row (SSM_ERR_UNSUPPORTED beyond) */
 #define SSM_MAX_HEAD_COLS 65536
 #define SSM_MAX_HEAD_VOCAB (1 << 22)
-#define SSM_MAX_HEAD_ROWS (1 << 24)
+#define SSM_MAX_HEAD_ROWS (1 << 24)    /* and rows * vocab up to 2^40 */
+#define SSM_MAX_HEAD_TEMPERATURE 1e6f  /* and 1e-6 at least (SSM_ERR_UNSUPPORTED beyond) */
 
 typedef struct {
   long long rows; /* tokens, >= 1 */
@@ -57,10 +58,15 @@ typedef struct {
   float temperature;      /* head_distill: tau > 0, finite */
   long long ignore_index; /* head_ce: the target of a row without a loss */
   unsigned flags; /* 0, or ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
-                     the sums out give up at once, as if the bound of their wait had run out */
+                     the sums out give up at once, as if the bound of their wait had run out (a forward of
+                     one or two rows waits for nothing) */
 } ssm_head_desc;
 
-/* Bytes of scratch of a call on the current device (at least 256; 0 if the arguments are invalid).
+/* Bytes of scratch of a call on the current device (at least 256; 0 if the arguments are invalid): a copy of
+ * h (three times its bf16 size with fp32), one of W with fp32 or rows that are not aligned, and
+ *   forward   rows * vocab / 16 bytes of sums (twice that for tiles of 128 words; next to none for 1 or 2 rows)
+ *   backward  a piece of G, 512 MiB at most (or 256 words of it), and fp32 sums of d_h and perhaps of d_W,
+ *             up to 64 of them where there are few rows.
  * grads: 0 for the forward, else bits 1 (d_h wanted) and 2 (d_W wanted) of the backward.  aligned: W's rows
  * (pointer and ld_w * element size) are 16-byte aligned; fp32 W may lie anywhere. */
 size_t ssm_head_workspace_size(const ssm_head_desc* desc, int grads, int aligned);

@@ -209,6 +209,7 @@ def test_every_declared_function_of_the_head_is_bound(H):
     (dict(rows=0), INV), (dict(rows=-1), INV), (dict(cols=0), INV), (dict(vocab=0), INV),
     (dict(vocab=-5), INV), (dict(io=2), INV), (dict(flags=1), INV), (dict(rows=(1 << 24) + 1), UNS),
     (dict(cols=65537), UNS), (dict(vocab=(1 << 22) + 1), UNS),
+    (dict(rows=1 << 24, vocab=(1 << 16) + 1), UNS),
 ])
 def test_head_refuses_bad_descriptors(H, kw, code):
     for name, (call, _, _) in _calls(H, **kw).items():
@@ -221,7 +222,8 @@ def test_head_refuses_bad_entries_and_temperatures(H):
     for kw, code in ((dict(entries=0), INV), (dict(entries=-1), INV), (dict(entries=129), UNS),
                      (dict(entry_io=3), INV), (dict(temperature=0.0), INV),
                      (dict(temperature=-1.0), INV), (dict(temperature=math.inf), INV),
-                     (dict(temperature=math.nan), INV)):
+                     (dict(temperature=math.nan), INV), (dict(temperature=9e-7), UNS),
+                     (dict(temperature=1.1e6), UNS)):
         for name in ("distill_fwd", "distill_bwd"):
             assert _calls(H, **kw)[name][0]() == code, (name, kw)
     for name in ("ce_fwd", "ce_bwd"):
