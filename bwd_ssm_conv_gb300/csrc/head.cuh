@@ -84,7 +84,7 @@ cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const 
 // A forward of few rows, unpacked (pos[row] is row): what head_rows and head_logits do together, with
 // stats [blocks][padded rows].
 constexpr size_t kFewSmem = 72 * 1024;  // of a block
-bool head_few(long long rows, int cols);
+bool head_few(long long rows, int cols, int io);
 int head_few_blocks(int sms);
 cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
                             const void* h, long long ld_h, const void* w, long long ld_w, int* idx,

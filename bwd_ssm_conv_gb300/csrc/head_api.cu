@@ -136,7 +136,7 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.table = take(kHeadParts * T);
     p.valid = take(T);
   }
-  if (!grads && head_few(T, d.cols)) {
+  if (!grads && head_few(T, d.cols, d.io)) {
     p.n_stats = head_few_blocks(sms);
     p.stats = take((size_t)8 * p.n_stats * Tp);
     p.zt = take(4 * T * n_e);
@@ -281,7 +281,7 @@ int run(Call c, bool distill, bool backward) {
   if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, lists, valid, st));
   float2* stats = (float2*)(ws + p.stats);
   float* zt = (float*)(ws + p.zt);
-  if (!backward && head_few(d.rows, d.cols)) {
+  if (!backward && head_few(d.rows, d.cols, d.io)) {
     SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, lists.idx, r, stats, zt, sms, st));
     SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;

@@ -1,11 +1,13 @@
-// head_few.cu -- the forward for one or two rows (tokens as they come): Z = h W^T with every row of W read
-// once, by plain fp32 arithmetic.  W's bytes bound it; a tensor-core tile would be all but empty, and its
-// rows would have to be packed first.  768 columns, 32768 words in bf16, in a graph with the kernel that
-// joins the sums (GB300): one row 16.1 us, two 19.6, for 7.4 of reading; four by this kernel 24.4, by the
-// tensor cores 24.
+// head_few.cu -- the forward for a few rows (tokens as they come): Z = h W^T with every row of W read once,
+// by plain fp32 arithmetic.  W's bytes bound it; a tensor-core tile would be all but empty, its rows would
+// have to be packed first, and fp32 W split into planes.  768 columns, 32768 words, in a graph with the kernel
+// that joins the sums (GB300), here and by the tensor cores:
+//   bf16  1 row 16.1 us, 2 20.0, 4 25.3; tensor cores 23.7 for any number up to 256; reading W 7.4
+//   fp32  1 row 23.6 us, 2 25.4, 4 29.8, 8 41.3; tensor cores 87.5; reading W 14.9
+// so that up to 2 rows come here, 8 in fp32.
 //
 // h lies in shared memory as fp32.  A warp takes 4 words at a time, a lane every 32nd chunk of 8 columns
-// of each, which leaves 4 or 8 sums of words and rows to add over the lanes: at each step the lanes keep
+// of each, which leaves 4 to 32 sums of words and rows to add over the lanes: at each step the lanes keep
 // half of them and give the other half away, until each has one, the logit of one word and row.
 // A lane keeps the maximum and the sum of the exponentials of what comes its way.
 // The logits of the rows' own words (or entries) are computed by themselves, a warp each.
@@ -224,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
   }
 }
 
-int rows_of(long long rows) { return rows <= 1 ? 1 : 2; }
+int rows_of(long long rows) { return rows <= 1 ? 1 : rows <= 2 ? 2 : rows <= 4 ? 4 : 8; }
 size_t smem_of(int R, int cols) { return sizeof(float) * R * pad8(cols) + sizeof(float2) * kWarps * R; }
 
 template <typename IO, bool VEC, int R>
@@ -260,14 +262,18 @@ cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
 }
 template <typename IO, bool VEC>
 cudaError_t launch(const FewArgs& a, int blocks, bool first, cudaStream_t st) {
-  return a.rows <= 1 ? launch<IO, VEC, 1>(a, blocks, first, st) :
-                       launch<IO, VEC, 2>(a, blocks, first, st);
+  switch (rows_of(a.rows)) {
+    case 1: return launch<IO, VEC, 1>(a, blocks, first, st);
+    case 2: return launch<IO, VEC, 2>(a, blocks, first, st);
+    case 4: return launch<float, VEC, 4>(a, blocks, first, st);  // fp32 only (head_few)
+    default: return launch<float, VEC, 8>(a, blocks, first, st);
+  }
 }
 
 }  // namespace
 
-bool head_few(long long rows, int cols) {
-  return rows <= 2 && smem_of(rows_of(rows), cols) <= kFewSmem;
+bool head_few(long long rows, int cols, int io) {
+  return rows <= (io == SSM_F32 ? 8 : 2) && smem_of(rows_of(rows), cols) <= kFewSmem;
 }
 int head_few_blocks(int sms) { return kBlocksPerSm * sms; }
 
