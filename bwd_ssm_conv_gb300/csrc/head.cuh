@@ -81,14 +81,21 @@ cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const 
                                cudaStream_t st);
 
 // ---- head_few.cu ----------------------------------------------------------------------------------
-// A forward of few rows, unpacked (pos[row] is row): what head_rows and head_logits do together, with
-// stats [blocks][padded rows].
+// A few rows, unpacked (pos[row] is row).  The forward: what head_rows and head_logits do together, with
+// stats [blocks][padded rows].  The backward: d_w, and d_h by way of its sums h_part [blocks][rows][padded cols]
+// (either NULL: not wanted).
 constexpr size_t kFewSmem = 72 * 1024;  // of a block
-bool head_few(long long rows, int cols, int io);
+bool head_few(long long rows, int cols, int io, bool backward);
 int head_few_blocks(int sms);
 cudaError_t launch_head_few(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
-                            const void* h, long long ld_h, const void* w, long long ld_w, int* idx,
-                            const HeadRows& r, float2* stats, float* zt, int sms, cudaStream_t st);
+                            const void* h, long long ld_h, const void* w, long long ld_w,
+                            const HeadLists& lists, const HeadRows& r, float2* stats, float* zt, int sms,
+                            cudaStream_t st);
+cudaError_t launch_head_few_bwd(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
+                                const void* h, long long ld_h, const void* w, long long ld_w,
+                                const HeadLists& lists, const HeadRows& r, const float* lse,
+                                const float* d_loss, float* h_part, void* d_h, long long ld_d_h,
+                                void* d_w, int sms, cudaStream_t st);
 
 // ---- head_tc.cu -----------------------------------------------------------------------------------
 struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart

@@ -114,6 +114,7 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
 struct Plan {
   size_t pos, src, idx, p, known, table, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
   int planes, tile_z, n_stats, piece, pieces;
+  bool few;
   Cuts cuts;
 };
 Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
@@ -136,7 +137,13 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.table = take(kHeadParts * T);
     p.valid = take(T);
   }
-  if (!grads && head_few(T, d.cols, d.io)) {
+  p.few = head_few(T, d.cols, d.io, grads != 0);
+  if (p.few && grads) {
+    if (grads & 1) p.dh = take((size_t)4 * head_few_blocks(sms) * T * Dp);
+    p.bytes = at;
+    return p;
+  }
+  if (p.few) {
     p.n_stats = head_few_blocks(sms);
     p.stats = take((size_t)8 * p.n_stats * Tp);
     p.zt = take(4 * T * n_e);
@@ -281,8 +288,14 @@ int run(Call c, bool distill, bool backward) {
   if (distill) SSM_DO(launch_head_entries(d, c.t_idx, c.t_logit, lists, valid, st));
   float2* stats = (float2*)(ws + p.stats);
   float* zt = (float*)(ws + p.zt);
-  if (!backward && head_few(d.rows, d.cols, d.io)) {
-    SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, lists.idx, r, stats, zt, sms, st));
+  if (p.few && backward) {
+    float* h_part = c.d_h ? (float*)(ws + p.dh) : nullptr;
+    SSM_DO(launch_head_few_bwd(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, lists, r, c.lse, c.d_loss,
+                               h_part, c.d_h, c.ld_d_h, c.d_w, sms, st));
+    return SSM_OK;
+  }
+  if (p.few) {
+    SSM_DO(launch_head_few(d, c.target, valid, c.h, c.ld_h, c.w, c.ld_w, lists, r, stats, zt, sms, st));
     SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }

@@ -31,8 +31,8 @@
  * add, about 10^-8 of the sum for each 16 columns: sums are taken out every 64 columns with fp32 operands,
  * those of the logits every 1024 with bf16 ones, and added with rounding to nearest.  With bf16 operands G,
  * divided by the largest |d_loss|, is rounded to bf16 between the products, which gives d_h and d_W an error
- * of the size of their own rounding.  A few rows' logits (up to 2, 8 in
- * fp32) are fp32 arithmetic throughout.
+ * of the size of their own rounding.  A few rows (bf16: 2 in the forward, 4 in
+ * the backward; fp32: 8) are fp32 arithmetic throughout, G too.
  */
 #ifndef SSM_HEAD_GB300_H
 #define SSM_HEAD_GB300_H
@@ -59,15 +59,15 @@ typedef struct {
   float temperature;      /* head_distill: tau > 0, finite */
   long long ignore_index; /* head_ce: the target of a row without a loss */
   unsigned flags; /* 0, or ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
-                     the sums out give up at once, as if the bound of their wait had run out (a forward of
-                     a few rows waits for nothing) */
+                     the sums out give up at once, as if the bound of their wait had run out (the kernels of
+                     a few rows wait for nothing) */
 } ssm_head_desc;
 
 /* Bytes of scratch of a call on the current device (at least 256; 0 if the arguments are invalid): a copy of
  * h (three times its bf16 size with fp32), one of W with fp32 or rows that are not aligned, and
  *   forward   rows * vocab / 16 bytes of sums (twice that for tiles of 128 words; next to none for a few rows)
  *   backward  a piece of G, 512 MiB at most (or 256 words of it), and fp32 sums of d_h and perhaps of d_W,
- *             up to 64 of them where there are few rows.
+ *             up to 64 of them where there are few rows; for a few rows 2 sums of d_h per SM.
  * grads: 0 for the forward, else bits 1 (d_h wanted) and 2 (d_W wanted) of the backward.  aligned: W's rows
  * (pointer and ld_w * element size) are 16-byte aligned; fp32 W may lie anywhere. */
 size_t ssm_head_workspace_size(const ssm_head_desc* desc, int grads, int aligned);

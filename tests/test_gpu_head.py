@@ -123,7 +123,7 @@ def test_distill(T, D, V, k, tau, io, entry_io):
 @pytest.mark.parametrize("D,V", [(8, 3), (72, 700), (515, 1001), (1030, 40), (2048, 300)])
 @pytest.mark.parametrize("T", [1, 2, 3, 4, 5, 8, 9])
 def test_a_few_rows(T, D, V, io):
-    """Up to 2 rows, 8 in fp32, the forward is a kernel of its own; rows that do not count among them."""
+    """Up to 2 and 4 rows, 8 in fp32, forward and backward are kernels of their own; rows that do not count among them."""
     i = _inputs(T, D, V, io, seed=T * D + V, ignored=0.0)
     if T > 2:
         i["target"][T // 2] = -100
