@@ -32,7 +32,7 @@ struct FewArgs {
   long long ld_w;
   const int64_t* target;
   const uint8_t* valid;
-  int* idx;
+  const int* idx;  // a teacher's
   HeadState* state;
   int* pos;
   float2* stats;  // [blocks][ld_stats]
@@ -118,8 +118,9 @@ template <typename IO, bool VEC, int R, int N> struct Words {
   }
 };
 
-// Which rows count: each block sees for itself, the first one writes it down.
-template <int R> __device__ __forceinline__ void look_at_rows(const FewArgs& a, int (&kind)[R]) {
+// Which rows count, and their target: each block sees for itself, the first one writes down the former.
+template <int R>
+__device__ __forceinline__ void look_at_rows(const FewArgs& a, int (&kind)[R], int (&target)[R]) {
   if (threadIdx.x >= R) return;
   const int t = threadIdx.x;
   int pos = kIgnored, word = kNoEntry;
@@ -133,12 +134,10 @@ template <int R> __device__ __forceinline__ void look_at_rows(const FewArgs& a, 
     } else {
       pos = a.valid[t] == 1 ? t : a.valid[t] == 2 ? kBadRow : kIgnored;
     }
-    if (blockIdx.x == 0) {
-      a.pos[t] = pos;
-      if (a.target) a.idx[t] = word;
-    }
+    if (blockIdx.x == 0) a.pos[t] = pos;
   }
   kind[t] = pos;
+  target[t] = word;
   const bool bad = __any_sync((1u << R) - 1u, pos == kBadRow);
   if (blockIdx.x == 0 && t == 0) a.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
 }
@@ -176,7 +175,7 @@ template <int R> struct Spread {
 template <typename IO, bool VEC, int R>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const FewArgs a) {
   extern __shared__ __align__(16) float h[];  // [R][padded], then the warps' sums
-  __shared__ int kind[R];
+  __shared__ int kind[R], target[R];
   asm volatile("griddepcontrol.launch_dependents;");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int padded = (a.cols + 7) / 8 * 8;
@@ -190,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
   for (int i = 0; i < kWords; i++) words[i] = max(min(from + i, to - 1), 0);
   batch.load(a, padded, words, 0);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  look_at_rows<R>(a, kind);
+  look_at_rows<R>(a, kind, target);
   __syncthreads();
   stage_rows<IO, R>(a, kind, padded, h);
   __syncthreads();
@@ -224,7 +223,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
   // the entries' logits, from the last warp on, which has the fewest words
   for (long long i = warps - 1 - me; i < a.rows * a.entries; i += warps) {
     const int row = (int)(i / a.entries);
-    const int word = kind[row] < 0 ? kNoEntry : a.target ? (int)a.target[row] : a.idx[i];
+    const int word = kind[row] < 0 ? kNoEntry : a.target ? target[row] : a.idx[i];
     if (word == kNoEntry) continue;
     const int one[1] = {word};
     Words<IO, VEC, 1, 1> x;
@@ -262,7 +261,7 @@ template <typename IO, bool VEC, int R>
 __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_bwd_kernel(const FewArgs a) {
   constexpr int kBatch = kWarps * kWords;
   extern __shared__ __align__(16) float h[];  // [R][padded], then the groups' sums [groups][R][padded]
-  __shared__ int kind[R];
+  __shared__ int kind[R], target[R];
   __shared__ float G[kBatch][R];
   __shared__ float lse[R], up[R];
   asm volatile("griddepcontrol.launch_dependents;");
@@ -271,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_bwd_kernel(co
   const int padded = (a.cols + 7) / 8 * 8, chunks = padded / 8;
   const int from = (int)((long long)blockIdx.x * a.vocab / gridDim.x),
             to = (int)((long long)(blockIdx.x + 1) * a.vocab / gridDim.x);
-  look_at_rows<R>(a, kind);
+  look_at_rows<R>(a, kind, target);
   __syncthreads();
   stage_rows<IO, R>(a, kind, padded, h);
   float* sums = h + R * padded;
@@ -283,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_bwd_kernel(co
   }
   __syncthreads();
   const int mine = lane / Spread<R>::kSame, row = mine % R;
-  const int* list = a.idx + (long long)row * a.entries;
+  const int* list = a.target ? &target[row] : a.idx + (long long)row * a.entries;
   const bool counts = row < a.rows && kind[row] >= 0;
   const int per = (kThreads / a.groups), group = threadIdx.x / per, first = threadIdx.x - group * per;
   for (int b0 = from; b0 < to; b0 += kBatch) {

@@ -302,6 +302,63 @@ def test_a_dirty_workspace_and_the_same_bits_every_time():
         assert torch.equal(p, q)
 
 
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 2, 4, 8])
+def test_a_few_rows_read_nothing_that_a_call_before_left(T, io):
+    """Whatever the workspace holds, call after call on other targets; with two calls at once; replayed."""
+    D, V = 16, 5003
+    i = _inputs(T, D, V, io, seed=31, ignored=0.0)
+    i["t_idx"], i["t_logit"] = _entries(T, V, 4, seed=8)
+    c = {k: v.cuda() for k, v in i.items()}
+    kind = binding.SSM_BF16 if io == "bf16" else binding.SSM_F32
+    n = max(head.ssm_head_workspace_size(T, D, V, io=kind, entries=4, grads=n) for n in (0, 1, 2, 3))
+
+    def once(target, ws=None, stream=None):
+        how = dict(ws=ws, stream=stream)
+        a = head.ssm_head_ce_fwd(c["h"], c["w"], target, **how)
+        g = head.ssm_head_ce_bwd(c["h"], c["w"], target, a.lse, c["d_loss"], **how)
+        b = head.ssm_head_distill_fwd(c["h"], c["w"], c["t_idx"], c["t_logit"], 2.0, **how)
+        k = head.ssm_head_distill_bwd(c["h"], c["w"], c["t_idx"], c["t_logit"], b.lse, c["d_loss"], 2.0,
+                                      **how)
+        return [*a, *g.values(), *b, *k.values()]
+
+    g = torch.Generator().manual_seed(5)
+    targets = [torch.randint(V, (T,), generator=g).cuda() for _ in range(12)]
+    ws = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    first = []
+    for y in targets:
+        want = torch.softmax(c["h"].double() @ c["w"].double().T, -1)
+        want[torch.arange(T), y] -= 1
+        want = (want * c["d_loss"].double()[:, None]).T @ c["h"].double()
+        got = once(y, ws)
+        # Every word of d_W: a row of it is at most sqrt(T) of all rows' d_loss h, which G and the result,
+        # each rounded to bf16 at most, leave within 2 x 2^-8 sqrt(8) = 2^-5.5.
+        off = (got[3].double() - want).norm(dim=1) / (c["d_loss"][:, None] * c["h"]).double().norm()
+        assert off.max().item() < 2 ** -5.4
+        first.append(got)
+    for fill in (0, 255, 127):
+        for y, want in zip(targets, first):
+            ws.fill_(fill)
+            for p, q in zip(want, once(y, ws)):
+                assert torch.equal(p, q)
+    torch.cuda.synchronize()
+    sides = torch.cuda.Stream(), torch.cuda.Stream()
+    both = [once(y, stream=s) for y in targets for s in sides]
+    torch.cuda.synchronize()
+    for j, again in enumerate(both):
+        for p, q in zip(first[j // 2], again):
+            assert torch.equal(p, q)
+    y = targets[0].clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = once(y)
+    for other, want in zip(targets, first):
+        y.copy_(other)
+        graph.replay()
+        for p, q in zip(want, held):
+            assert torch.equal(p, q)
+
+
 @pytest.mark.parametrize("io,T,V", [("bf16", 16384, 20000), ("f32", 8192, 12000)])
 def test_a_vocabulary_in_several_pieces(io, T, V):
     """More of G than is kept at a time; in 64 bits on the GPU."""
