@@ -27,7 +27,8 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ float nan_() { return __uint_as_float(0x7fc00000u); }
 
 // ---- a teacher's entries ------------------------------------------------------------------------
-// A warp per row.  An entry's place in the order is the number of smaller keys, counted: a key is the word
+// A warp per row; 4096 rows of 64 entries take 10 us (GB300), bound by the counting of places: k comparisons for
+// each entry.  An entry's place in the order is the number of smaller keys, counted: a key is the word
 // and, behind it, the entry's number, so that no two are alike.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t_idx, const T* t_logit,
@@ -165,7 +166,8 @@ __device__ __forceinline__ void copy8(const IO* x, int left, __nv_bfloat16* out,
 // ---- which rows count, and their copies --------------------------------------------------------------
 // A block takes `per_block` rows.  It looks at every row, which costs less than a launch of its own for a
 // count, so that it knows where its own go, and packs them, a warp per row; the last one also the rows
-// of zeros past them.  The blocks behind copy W.
+// of zeros past them.  The blocks behind copy W.  GB300, a start and an end of 4 us among them: 8192 x 768 bf16
+// 13 us, 4096 x 768 8; 1021 x 515 fp32 with W of 10007 words into three planes 13.5 (52 MB, 8 at the rate of a copy).
 constexpr int kRowThreads = 512;
 struct RowsArgs {
   const int64_t* target;
@@ -312,7 +314,7 @@ __device__ __forceinline__ Sum join(const Sum& a, const Sum& b, float scale) {
 }
 // A block of 1024 threads joins X rows' sums: 1024 / X slices of the tiles, each in order, then the slices,
 // a few per lane of a row's warp in order, then a tree.  X is 32, or 4 where that many rows do not fill the
-// SMs and the chain of loads is what counts.
+// SMs and the chain of loads is what counts.  4096 rows of 32768 words 9 us, 1021 of 10007 6 (GB300).
 template <int X>
 __global__ void __launch_bounds__(1024) head_loss_kernel(const float2* stats, int n_stats,
                                                          long long ld, const float* zt,
@@ -412,7 +414,8 @@ struct FinishArgs {
   long long n_w;
   int cols, padded_cols, last;
 };
-// A thread takes 8 columns of a row at a time, first of d_h's rows, then of d_W's.
+// A thread takes 8 columns of a row at a time, first of d_h's rows, then of d_W's.  Reads of the splits' sums
+// bound it: 18 us for 8192 x 768 of two pieces (GB300).
 template <typename IO, bool VEC_H, bool VEC_W>
 __global__ void __launch_bounds__(kThreads) head_finish_kernel(const FinishArgs a) {
   early_launch();

@@ -18,6 +18,17 @@
 // of a product), whose slots come free in between, so that a slot's next copy has more than a step's time.
 // The tensor cores truncate when they add, by the size of the sum: small products come before the large one,
 // and the sums are taken out every 64 columns and added in registers.
+//
+// GB300, us of a launch by itself and its rate (cuBLAS's bf16 product of 8192^3 on this GPU: 1908 TFLOP/s):
+//                                  kLogits        kGrad          kOut
+//   7370 x 768, 50000 words bf16   281  2010      2 x 165  1720  2 x 327  1730
+//   16384 x 1024, 32768 bf16       524  2100      2 x 292  1880  2 x 585  1880
+//   4096 x 768, 32768 bf16         108  1910      133      1550  222      1860
+//   1021 x 515, 10007 fp32          41  1540       49      1290   87      1450  (six products counted)
+// The tensor cores bound it, back to back the power limit (1500 - 1650 TFLOP/s).  kGrad's stores, 1 byte for each
+// 32 - 43 flops of a tile, are what it is slower by; fp32 lacks whole rounds of tiles (237 of 128 columns on 76
+// pairs) and a stage in nine (515 columns).  kOut with tiles of d_h and of d_W in one launch has one end
+// with idle SMs instead of two.
 #include "head.cuh"
 #include "pair.cuh"
 
@@ -255,6 +266,7 @@ template <int USE, int PLANES> struct Taker {
           for (int i = 0; i < 32; i++) v[i] -= i == at ? p : 0.0f;
           advance();
         }
+      // In pairs: of 32 separate products with rg behind ex2, nvcc 13.0.88 lost rg's sign.
       const f2_t rg2 = f2_pack(rg, rg);
 #pragma unroll
       for (int i = 0; i < 32; i += 2)
