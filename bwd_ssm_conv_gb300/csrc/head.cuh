@@ -27,6 +27,7 @@ struct HeadState {
   int count;     // packed rows
   float g_top;   // the largest finite |d_loss| of theirs (1 where there is none)
   float scale;   // what G lacks between the products: g_top tau
+  int tile;      // columns of a tile of Z
 };
 
 struct HeadRows {  // of a call, on the device
@@ -53,6 +54,26 @@ inline int head_part_shift(int vocab) {  // a part's words, as a power of two
   return shift;
 }
 
+// Z's tiles are 256, 192 or 128 words wide: what takes the fewest rounds of the pairs of CTAs, in time, for the
+// rows that count.
+struct HeadTiles {
+  int words;     // of a launch; 0: tiles of 256
+  int pairs;
+  float cost[3]; // of a tile of 256, 192 and 128
+};
+__host__ __device__ inline int head_tile(const HeadTiles& t, int rows) {
+  int best = kHeadTile;
+  float least = 0.0f;
+  if (t.words)
+    for (int i = 0; i < 3; i++) {
+      const int tile = kHeadTile - 64 * i,
+                units = (rows + kHeadTile - 1) / kHeadTile * ((t.words + tile - 1) / tile);
+      const float time = (float)((units + t.pairs - 1) / t.pairs) * t.cost[i];
+      if (i == 0 || time < least) least = time, best = tile;
+    }
+  return best;
+}
+
 inline int pad8(int n) { return (n + 7) / 8 * 8; }
 inline long long pad_rows(long long rows) { return (rows + 63) / 64 * 64; }
 
@@ -65,8 +86,9 @@ cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, co
 cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
                              const void* h, long long ld_h, const float* lse, const float* d_loss,
                              const void* w, long long ld_w, int* idx, const HeadRows& r,
-                             __nv_bfloat16* w_out, int sms, cudaStream_t st);
-// Loss and lse from the tiles' sums; zt: the entries' logits [rows][entries or 1].
+                             __nv_bfloat16* w_out, const HeadTiles& tiles, int sms, cudaStream_t st);
+// Loss and lse from the tiles' sums (n_stats of them; 0: two for each of the state's tiles); zt: the entries'
+// logits [rows][entries or 1].
 cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_stats,
                              const float* zt, const HeadLists& lists, const HeadRows& r,
                              float* loss, float* lse, int sms,
@@ -103,18 +125,18 @@ struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart
   long long rows, ld, plane;
   int cols;
 };
-// How a product is cut: columns of a tile (256 or 128), splits of the sum and their stages.
+// How a product with G is cut: columns of a tile (256 or 128), splits of the sum and their stages.
 struct HeadCut {
   int tile_n, splits, per;
 };
 // The sums of the vocabulary's tiles, stats [2 tiles][padded rows], and the entries' logits.
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const HeadLists& lists, int tile_n, float2* stats,
-                               float* zt, int sms, cudaStream_t st);
+                               const HeadRows& r, const HeadLists& lists, float2* stats, float* zt,
+                               int sms, cudaStream_t st);
 // G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [planes][padded rows][n].
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                             const HeadRows& r, const HeadLists& lists, int tile_n,
-                             __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st);
+                             const HeadRows& r, const HeadLists& lists, __nv_bfloat16* g, int v0, int n,
+                             int sms, cudaStream_t st);
 // The two products with G of the words v0 .. v0 + n, in one launch:
 //   h_part [splits][padded rows][padded cols] (+)= G W, the piece's words split, or without it rows src[]
 //   of d_h (with one split and one piece),

@@ -33,9 +33,14 @@ int num_sms() {
 
 // ---- how the products are cut ---------------------------------------------------------------------
 // Costs are in stages, the time of a 256 x 256 tile's step over 64 of the sum (six products for fp32).
+constexpr long long kFewRounds = 5;  // of tiles on the pairs of CTAs: below, their widths and splits are chosen
 double unit_cost(int io) { return io == SSM_F32 ? 0.7 : 3.0; }           // of a unit by itself
 double stage_bytes(int io) { return io == SSM_F32 ? 9.0e6 : 1.5e6; }     // that memory moves meanwhile
-double tile_cost(int tile_n, int io) { return tile_n == kHeadTile ? 1.0 : io == SSM_F32 ? 0.55 : 0.65; }
+double tile_cost(int tile_n, int io) {
+  if (tile_n == kHeadTile) return 1.0;
+  if (tile_n == 192) return io == SSM_F32 ? 0.8 : 0.85;
+  return io == SSM_F32 ? 0.55 : 0.65;
+}
 
 // Units of one or two kinds are dealt out to the pairs of CTAs in turn, the first kind first: the time of
 // the pair with the most to do.
@@ -55,15 +60,19 @@ double dealt(long long n0, double c0, long long n1, double c1, long long pairs) 
   return most;
 }
 
-// The tile's columns for Z: 128 where fewer tiles of 256 than pairs leave some of those idle.
-int logits_tile(long long rows, int cols, int words, int io, int sms) {
-  const long long pairs = sms / 2 > 0 ? sms / 2 : 1, m = (rows + kHeadTile - 1) / kHeadTile;
-  const int stages = (cols + kHeadBlock - 1) / kHeadBlock;
-  const auto time = [&](int tile) {
-    return dealt(m * ((words + tile - 1) / tile), stages * tile_cost(tile, io) + unit_cost(io), 0, 0.0,
-                 pairs);
-  };
-  return time(128) < time(256) ? 128 : 256;
+// Tiles of Z: narrower ones where there are few, as the last round then leaves a good part of the pairs idle.
+// The sums' warps of fp32 kGrad store G while no products run.
+HeadTiles tiles_of(long long rows, int cols, int words, int io, bool grad, int sms) {
+  const int pairs = sms / 2 > 0 ? sms / 2 : 1, stages = (cols + kHeadBlock - 1) / kHeadBlock;
+  HeadTiles t{words, pairs};
+  if ((rows + kHeadTile - 1) / kHeadTile * ((words + kHeadTile - 1) / kHeadTile) > kFewRounds * pairs)
+    t.words = 0;
+  for (int i = 0; i < 3; i++) {
+    const int tile = kHeadTile - 64 * i;
+    const double unit = io == SSM_F32 && grad ? 3.0 * tile / kHeadTile : unit_cost(io);
+    t.cost[i] = (float)(stages * tile_cost(tile, io) + unit);
+  }
+  return t;
 }
 
 struct Cuts {
@@ -81,7 +90,7 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
   Cuts best{};
   double least = -1.0;
   static constexpr int kSplits[] = {1, 2, 3, 4, 5, 6, 8, 10, 12, 16, 20, 24, 32, 48, 64};
-  const long long enough = 5 * pairs;
+  const long long enough = kFewRounds * pairs;
   for (int tile : {256, 128}) {
     const long long n = (cols + tile - 1) / tile;
     if (tile == 128 && m_w * n > enough && m_h * n > enough) break;
@@ -113,8 +122,9 @@ Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool severa
 // The workspace, by bytes from its start.
 struct Plan {
   size_t pos, src, idx, p, known, table, valid, rl, rg, h, w, stats, zt, g, dh, dw, bytes;
-  int planes, tile_z, n_stats, piece, pieces;
+  int planes, n_stats, piece, pieces;
   bool few;
+  HeadTiles tiles;
   Cuts cuts;
 };
 Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
@@ -153,9 +163,9 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   p.h = take((size_t)2 * p.planes * Tp * Dp);
   if (copy_w) p.w = take((size_t)2 * p.planes * d.vocab * Dp);
   if (!grads) {
-    p.tile_z = logits_tile(T, d.cols, d.vocab, d.io, sms);
-    p.n_stats = 2 * ((d.vocab + p.tile_z - 1) / p.tile_z);
-    p.stats = take((size_t)8 * p.n_stats * Tp);
+    p.tiles = tiles_of(T, d.cols, d.vocab, d.io, false, sms);
+    const int narrow = p.tiles.words ? kHeadTile / 2 : kHeadTile;
+    p.stats = take((size_t)8 * 2 * ((d.vocab + narrow - 1) / narrow) * Tp);
     p.zt = take(4 * T * n_e);
   } else {
     p.rl = take(4 * Tp);
@@ -168,7 +178,7 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.piece = (tiles + p.pieces - 1) / p.pieces * kHeadTile;
     p.pieces = (d.vocab + p.piece - 1) / p.piece;
     p.g = take((size_t)2 * p.planes * Tp * p.piece);
-    p.tile_z = logits_tile(T, d.cols, p.piece, d.io, sms);
+    p.tiles = tiles_of(T, d.cols, p.piece, d.io, true, sms);
     p.cuts = cuts_of(T, d.cols, p.piece, d.io, grads, p.pieces > 1, sms);
     if ((grads & 1) && (p.pieces > 1 || p.cuts.h.splits > 1))
       p.dh = take((size_t)4 * p.cuts.h.splits * Tp * Dp);
@@ -301,12 +311,13 @@ int run(Call c, bool distill, bool backward) {
   }
   __nv_bfloat16* w_out = copy_w ? (__nv_bfloat16*)(ws + p.w) : nullptr;
   SSM_DO(launch_head_rows(d, c.target, valid, c.h, c.ld_h, backward ? c.lse : nullptr,
-                          backward ? c.d_loss : nullptr, c.w, c.ld_w, lists.idx, r, w_out, sms, st));
+                          backward ? c.d_loss : nullptr, c.w, c.ld_w, lists.idx, r, w_out, p.tiles,
+                          sms, st));
   const HeadMatrix h{r.h, Tp, Dp, Tp * Dp, d.cols};
   const HeadMatrix w = copy_w ? HeadMatrix{w_out, d.vocab, Dp, (long long)d.vocab * Dp, d.cols} :
                                 HeadMatrix{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
   if (!backward) {
-    SSM_DO(launch_head_logits(d, h, w, r, lists, p.tile_z, stats, zt, sms, st));
+    SSM_DO(launch_head_logits(d, h, w, r, lists, stats, zt, sms, st));
     SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }
@@ -317,7 +328,7 @@ int run(Call c, bool distill, bool backward) {
   for (int i = 0; i < p.pieces; i++) {
     const int v0 = i * p.piece, n = d.vocab - v0 < p.piece ? d.vocab - v0 : p.piece;
     const bool last = i == p.pieces - 1;
-    SSM_DO(launch_head_grad(d, h, w, r, lists, p.tile_z, gp, v0, p.piece, sms, st));
+    SSM_DO(launch_head_grad(d, h, w, r, lists, gp, v0, p.piece, sms, st));
     SSM_DO(launch_head_out(d, g, h, w, r, out, v0, n, i > 0, sms, st));
     if (last || out.w_part)
       SSM_DO(launch_head_finish(d, r, out.h_part, p.cuts.h.splits, last ? c.d_h : nullptr, c.ld_d_h,

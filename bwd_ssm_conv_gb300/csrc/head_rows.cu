@@ -27,9 +27,9 @@ __device__ __forceinline__ float warp_max(float v) {
 __device__ __forceinline__ float nan_() { return __uint_as_float(0x7fc00000u); }
 
 // ---- a teacher's entries ------------------------------------------------------------------------
-// A warp per row; 4096 rows of 64 entries take 10 us (GB300), bound by the counting of places: k comparisons for
-// each entry.  An entry's place in the order is the number of smaller keys, counted: a key is the word
-// and, behind it, the entry's number, so that no two are alike.
+// A warp per row.  An entry's place in the order is the number of smaller keys, counted: a key is the word
+// and, behind it, the entry's number, so that no two are alike.  4096 rows of 64 entries take 8 - 9 us (GB300), 333 of
+// 17 4.3, most of it a start, an end and the chain of one row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t_idx, const T* t_logit,
                                                                 long long rows, int k, int vocab,
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
     const int4 x = keys[warp][o];
 #pragma unroll
     for (int j = 0; j < N; j++)
-      place[j] += (x.x < mine[j]) + (x.y < mine[j]) + (x.z < mine[j]) + (x.w < mine[j]);
+      if (32 * j < k)
+        place[j] += (x.x < mine[j]) + (x.y < mine[j]) + (x.z < mine[j]) + (x.w < mine[j]);
   }
   top = warp_max(top);
   bad = __any_sync(0xffffffffu, bad);
@@ -184,6 +185,7 @@ struct RowsArgs {
   __nv_bfloat16* w_out;
   int* idx;
   HeadRows r;
+  HeadTiles tiles;
 };
 enum RowKind { kCounts, kNone, kBad };
 // said: a row's target, or what `valid` holds of it.
@@ -254,6 +256,7 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
     r.state->count = all;
     r.state->g_top = top;
     r.state->scale = top * a.tau;
+    r.state->tile = head_tile(a.tiles, all > 0 ? all : 1);
   }
   // its own rows' places, kRowThreads of them at a time
   const int mine = before;
@@ -319,13 +322,14 @@ template <int X>
 __global__ void __launch_bounds__(1024) head_loss_kernel(const float2* stats, int n_stats,
                                                          long long ld, const float* zt,
                                                          const float* p, const float* known,
-                                                         long long rows, int entries, float scale,
-                                                         float tau, HeadRows r, float* loss,
+                                                         long long rows, int entries, int vocab,
+                                                         float scale, float tau, HeadRows r, float* loss,
                                                          float* lse) {
   constexpr int Y = 1024 / X;
   __shared__ float2 part[Y][X + 1];
   early_launch();
   wait_for_before();
+  if (n_stats == 0) n_stats = 2 * ((vocab + r.state->tile - 1) / r.state->tile);
   const int x = threadIdx.x % X, y = threadIdx.x / X;
   const long long first = (long long)blockIdx.x * X;
   const int pos = first + x < rows ? r.pos[first + x] : kIgnored;
@@ -502,7 +506,7 @@ cudaError_t launch_head_entries(const ssm_head_desc& d, const int64_t* t_idx, co
 cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, const uint8_t* valid,
                              const void* h, long long ld_h, const float* lse, const float* d_loss,
                              const void* w, long long ld_w, int* idx, const HeadRows& r,
-                             __nv_bfloat16* w_out, int sms, cudaStream_t st) {
+                             __nv_bfloat16* w_out, const HeadTiles& tiles, int sms, cudaStream_t st) {
   RowsArgs a{target, valid, d.rows, d.ignore_index, d.vocab, d.cols, pad8(d.cols)};
   const long long per = (d.rows + 255) / 256;  // at most 256 blocks, as each looks at every row
   a.per_block = per < kRowThreads / 32 ? kRowThreads / 32 : (int)per;
@@ -510,7 +514,7 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
   a.tau = d.entries ? d.temperature : 1.0f;
   a.h = h, a.ld_h = ld_h, a.lse = lse, a.d_loss = d_loss;
   a.w = w, a.ld_w = ld_w, a.w_out = w_out;
-  a.idx = idx, a.r = r;
+  a.idx = idx, a.r = r, a.tiles = tiles;
   const long long chunks = (long long)d.vocab * (a.padded_cols / 8);
   const long long copiers = w_out ? at_most((chunks + kRowThreads - 1) / kRowThreads, sms) : 0;
   const bool vec_h = vec_rows(h, ld_h, d.cols, d.io), vec_w = vec_rows(w, ld_w, d.cols, d.io);
@@ -536,8 +540,8 @@ cudaError_t launch_head_loss(const ssm_head_desc& d, const float2* stats, int n_
   const float tau = d.entries ? d.temperature : 1.0f;
   const int x = d.rows > 4 * sms ? 32 : 4;
   return go(x == 32 ? head_loss_kernel<32> : head_loss_kernel<4>, (d.rows + x - 1) / x, 1024, st, stats,
-            n_stats, pad_rows(d.rows), zt, lists.p, lists.known, d.rows, d.entries ? d.entries : 1, kLog2e / tau,
-            tau, r, loss, lse);
+            n_stats, pad_rows(d.rows), zt, lists.p, lists.known, d.rows, d.entries ? d.entries : 1,
+            d.vocab, kLog2e / tau, tau, r, loss, lse);
 }
 
 cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const float* h_part,

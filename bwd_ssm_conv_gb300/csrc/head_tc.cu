@@ -23,12 +23,14 @@
 //                                  kLogits        kGrad          kOut
 //   7370 x 768, 50000 words bf16   281  2010      2 x 165  1720  2 x 327  1730
 //   16384 x 1024, 32768 bf16       524  2100      2 x 292  1880  2 x 585  1880
-//   4096 x 768, 32768 bf16         108  1910      133      1550  222      1860
-//   1021 x 515, 10007 fp32          41  1540       49      1290   87      1450  (six products counted)
-// The tensor cores bound it, back to back the power limit (1500 - 1650 TFLOP/s).  kGrad's stores, 1 byte for each
-// 32 - 43 flops of a tile, are what it is slower by; fp32 lacks whole rounds of tiles (237 of 128 columns on 76
-// pairs) and a stage in nine (515 columns).  kOut with tiles of d_h and of d_W in one launch has one end
-// with idle SMs instead of two.
+//   3891 x 768, 32768 bf16         104  1880      133      1470  220      1780
+//   684 x 515, 10007 fp32           40  1030       50       850   90       940  (six products counted)
+//   300 x 256, 5003 fp32            14   330       18       260   18       510
+// The tensor cores bound it, back to back the power limit (1500 - 1650 TFLOP/s).  kGrad's stores are what it is
+// slower by (with fp32 no products run meanwhile); fp32 of few rows lacks whole tiles (768 of rows, 640 of
+// columns for 684 and 515), a stage in nine and even rounds of tiles.  Z's tiles may be of 256, 192 or 128 columns
+// (head_tile): with 256 and 128 alone 300 x 256 takes 15 and 20 us.  kOut with tiles of d_h and of d_W in one
+// launch has one end with idle SMs instead of two.
 #include "head.cuh"
 #include "pair.cuh"
 
@@ -66,7 +68,7 @@ struct Job {
   CUtensorMap a, b;
   int a_mn, b_mn;      // how the operands lie
   int m_fixed;         // rows of the result; 0: the packed rows
-  int n, tile_n;       // columns of the result, and of a tile (256 or 128)
+  int n, tile_n;       // columns of the result, and of a tile (256 or 128; 0: the state's, 192 too)
   int k_fixed;         // length of the sum; 0: the packed rows
   int per_split;       // stages of a split of the sum
   int b_row0;          // first row of b's in the tensor
@@ -172,7 +174,7 @@ __device__ __forceinline__ float pick(const float (&v)[32], int i) {
 template <int USE, int PLANES> struct Taker {
   const TcArgs& a;
   const Job& job;
-  const int row, col0;  // of the result: its row, and the first of its columns
+  const int row, col0, width;  // of the result: its row, and its columns
   const bool row_ok;
   float* turn;  // this warp's
   // kLogits, kGrad
@@ -182,9 +184,9 @@ template <int USE, int PLANES> struct Taker {
   float* dst = nullptr;
   float scale = 1.0f;
 
-  __device__ __forceinline__ Taker(const TcArgs& a, const Job& job, int row, int col0, int rows,
+  __device__ __forceinline__ Taker(const TcArgs& a, const Job& job, int row, int col0, int width, int rows,
                                    int split, float* turn)
-      : a(a), job(job), row(row), col0(col0), row_ok(row < rows), turn(turn) {
+      : a(a), job(job), row(row), col0(col0), width(width), row_ok(row < rows), turn(turn) {
     if constexpr (USE != kOut) {
       src = row_ok ? a.src[row] : -1;
       e = 0, next = kNoEntry;
@@ -276,7 +278,7 @@ template <int USE, int PLANES> struct Taker {
         for (int i = 0; i < 32; i++)
           if (word + i >= a.vocab) v[i] = 0.0f;
       }
-      if (!row_ok) return;
+      if (!row_ok || col0 + 32 * c >= job.n) return;  // tiles of 192 go past a piece's end
       __nv_bfloat16* g = a.g + (long long)row * a.ld_g + col0 + 32 * c;
 #pragma unroll
       for (int r = 0; r < PLANES; r++) {
@@ -364,7 +366,7 @@ template <int USE, int PLANES> struct Taker {
   __device__ __forceinline__ void done() {
     if constexpr (USE == kLogits)
       if (row_ok)
-        a.stats[(long long)((a.v0 + col0) / (job.tile_n / 2)) * a.ld_stats + row] =
+        a.stats[(long long)((a.v0 + col0) / width) * a.ld_stats + row] =
             make_float2(top, sum);
   }
 };
@@ -374,7 +376,7 @@ struct Unit {
   int job, mt, nt, split, begin, iters, tile_n;
 };
 struct Units {
-  int m[2], n[2], stages[2], rows[2], total[2];
+  int m[2], n[2], stages[2], rows[2], total[2], tile_n[2];
   __device__ __forceinline__ Units(const TcArgs& a, int count) {
 #pragma unroll
     for (int j = 0; j < 2; j++) {
@@ -382,8 +384,9 @@ struct Units {
       if (j >= a.jobs) continue;
       const Job& b = a.job[j];
       rows[j] = b.m_fixed ? b.m_fixed : count;
+      tile_n[j] = b.tile_n ? b.tile_n : a.state->tile;
       m[j] = (rows[j] + kHeadTile - 1) / kHeadTile;
-      n[j] = (b.n + b.tile_n - 1) / b.tile_n;
+      n[j] = (b.n + tile_n[j] - 1) / tile_n[j];
       const int k = b.k_fixed ? b.k_fixed : count;
       stages[j] = (k + kHeadBlock - 1) / kHeadBlock;
       total[j] = m[j] * n[j] * ((stages[j] + b.per_split - 1) / b.per_split);
@@ -403,7 +406,7 @@ struct Units {
     else x.mt = t / nj, x.nt = t - x.mt * nj;
     x.begin = x.split * b.per_split;
     x.iters = sj - x.begin < b.per_split ? sj - x.begin : b.per_split;
-    x.tile_n = b.tile_n;
+    x.tile_n = x.job ? tile_n[1] : tile_n[0];
     return x;
   }
 };
@@ -464,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         const int half = x.tile_n / 2;  // columns of B here
         const int m0 = x.mt * kHeadTile + rank * (kHeadTile / 2), n0 = x.nt * x.tile_n + rank * half;
         const bool a_mn = b.a_mn, b_mn = b.b_mn;
-        const uint32_t bytes = kOperand + (half >> 6) * kSlab;
+        const uint32_t bytes = kOperand + (half > 64 ? 2 : 1) * kSlab;  // of 96 columns all of the second slab
         for (int k = x.begin; k < x.begin + x.iters && ok; k++) {
 #pragma unroll
           for (int i = 0; i < PLANES; i++, it++, r.next()) {
@@ -583,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       const int rows = USE == kGrad ? (rows_here + 63) / 64 * 64 : rows_here;
       Taker<USE, PLANES> taker(a, a.job[x.job],
                                x.mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
-                               x.nt * x.tile_n + width * half, rows, x.split, turn);
+                               x.nt * x.tile_n + width * half, width, rows, x.split, turn);
       if constexpr (!SEG) {
         ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
         __syncwarp();
@@ -725,10 +728,8 @@ TcArgs args_of(const ssm_head_desc& d, const HeadRows& r, const HeadLists& lists
   return t;
 }
 // Z of the words from v0 on.
-bool logits_job(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w, int v0, int n,
-                int tile_n, Job& j) {
+bool logits_job(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w, int v0, int n, Job& j) {
   j.n = n;
-  j.tile_n = tile_n;
   j.k_fixed = d.cols;
   j.per_split = (d.cols + kHeadBlock - 1) / kHeadBlock;
   j.b_row0 = v0;
@@ -739,10 +740,10 @@ bool logits_job(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w
 }  // namespace
 
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const HeadLists& lists, int tile_n, float2* stats,
-                               float* zt, int sms, cudaStream_t st) {
+                               const HeadRows& r, const HeadLists& lists, float2* stats, float* zt,
+                               int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, lists);
-  if (!logits_job(d, h, w, 0, d.vocab, tile_n, t.job[0])) return cudaErrorInvalidValue;
+  if (!logits_job(d, h, w, 0, d.vocab, t.job[0])) return cudaErrorInvalidValue;
   t.stats = stats;
   t.ld_stats = h.rows;
   t.zt = zt;
@@ -750,10 +751,10 @@ cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, cons
 }
 
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                             const HeadRows& r, const HeadLists& lists, int tile_n,
-                             __nv_bfloat16* g, int v0, int n, int sms, cudaStream_t st) {
+                             const HeadRows& r, const HeadLists& lists, __nv_bfloat16* g, int v0, int n,
+                             int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, lists);
-  if (!logits_job(d, h, w, v0, n, tile_n, t.job[0])) return cudaErrorInvalidValue;
+  if (!logits_job(d, h, w, v0, n, t.job[0])) return cudaErrorInvalidValue;
   t.v0 = v0;
   t.rl = r.rl;
   t.rg = r.rg;

@@ -65,7 +65,8 @@ typedef struct {
 
 /* Bytes of scratch of a call on the current device (at least 256; 0 if the arguments are invalid): a copy of
  * h (three times its bf16 size with fp32), one of W with fp32 or rows that are not aligned, and
- *   forward   rows * vocab / 16 bytes of sums (twice that for tiles of 128 words; next to none for a few rows)
+ *   forward   rows * vocab / 16 bytes of sums (twice that up to 5 tiles of 256 x 256 for
+ *             each pair of SMs, which may be narrower ones; next to none for a few rows)
  *   backward  a piece of G, 512 MiB at most (or 256 words of it), and fp32 sums of d_h and perhaps of d_W,
  *             up to 64 of them where there are few rows; for a few rows 2 sums of d_h per SM.
  * grads: 0 for the forward, else bits 1 (d_h wanted) and 2 (d_W wanted) of the backward.  aligned: W's rows
