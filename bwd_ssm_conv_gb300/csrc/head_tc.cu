@@ -7,8 +7,9 @@
 // A pair of CTAs (tcgen05 cta_group::2) forms a 256 x 256 tile, 64 steps of the sum per stage: each CTA
 // holds 128 rows of A and 128 columns of B.  An operand is staged as it lies: [row][64 of the sum]
 // (K-major) or [64 of the sum][64 columns] slabs (MN-major), both from 64 x 64 boxes with the 128-byte
-// swizzle, so that neither G nor W nor h is ever transposed.  Pairs step over the tiles; two accumulators
-// in tensor memory alternate, so that a tile's results are taken out under the products of the next.
+// swizzle, so that neither G nor W nor h is ever transposed.  Pairs step over the tiles; two
+// accumulators in tensor memory (four where tiles are 128 columns wide) take turns, so that a tile's results
+// are taken out under the products of the next.
 //   warp 0      one thread copies the tiles by TMA (past the ends they read as 0)
 //   warp 1      one thread of the first CTA issues the MMAs; the second CTA's passes on that its copies
 //               have landed
@@ -24,13 +25,14 @@
 //   7370 x 768, 50000 words bf16   281  2010      2 x 165  1720  2 x 327  1730
 //   16384 x 1024, 32768 bf16       524  2100      2 x 292  1880  2 x 585  1880
 //   3891 x 768, 32768 bf16         104  1880      133      1470  220      1780
-//   684 x 515, 10007 fp32           40  1030       50       850   90       940  (six products counted)
+//   684 x 515, 10007 fp32           40  1030       50       850   87       970  (six products counted)
 //   300 x 256, 5003 fp32            14   330       18       260   18       510
 // The tensor cores bound it, back to back the power limit (1500 - 1650 TFLOP/s).  kGrad's stores are what it is
-// slower by (with fp32 no products run meanwhile); fp32 of few rows lacks whole tiles (768 of rows, 640 of
+// slower by (with fp32 few products run meanwhile); fp32 of few rows lacks whole tiles (768 of rows, 640 of
 // columns for 684 and 515), a stage in nine and even rounds of tiles.  Z's tiles may be of 256, 192 or 128 columns
 // (head_tile): with 256 and 128 alone 300 x 256 takes 15 and 20 us.  kOut with tiles of d_h and of d_W in one
-// launch has one end with idle SMs instead of two.
+// launch has one end with idle SMs instead of two, and four accumulators instead of two for 128 columns spare fp32 5 %
+// (684 x 515) to 13 % (8192 x 512 over 256 words).
 #include "head.cuh"
 #include "pair.cuh"
 
@@ -416,7 +418,7 @@ template <int USE, int PLANES, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
   constexpr int S = kSlots, kSeg = SEG ? kSegment<PLANES> : 1 << 30;
   extern __shared__ unsigned char raw[];
-  __shared__ uint64_t here[S], there[S], empty[S], ready[2], drained[2], last;
+  __shared__ uint64_t here[S], there[S], empty[S], ready[4], drained[4], last;
   __shared__ uint32_t tbase;
   __shared__ int bad;
   unsigned char* smem =
@@ -430,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
       mbar_init(&there[i], 1);
       mbar_init(&empty[i], 1);
     }
-    for (int b = 0; b < 2; b++) {
+    for (int b = 0; b < 4; b++) {
       mbar_init(&ready[b], 1);
       mbar_init(&drained[b], 2 * kSumWarps);
     }
@@ -454,6 +456,9 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
   const int count = a.state->count > 0 ? a.state->count : 1;
   const Units units(a, count);
   const int n_units = units.all();
+  // Accumulators: two of up to 256 columns or four of 128 (both products' tiles are alike), by turns.
+  const int acc_log = units.tile_n[0] > kHeadTile / 2 ? 1 : 2, acc_mask = (1 << acc_log) - 1;
+  const uint32_t acc_cols = kTmCols >> acc_log;
 
   if (warp < 4) {
     if constexpr (PLANES > 1) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegsFew));
@@ -510,9 +515,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
                        db0 = desc_of(smem_u32(smem) + kOperand, b_mn);
         const uint32_t sa = a_mn ? 2048 >> 4 : 32 >> 4, sb = b_mn ? 2048 >> 4 : 32 >> 4;
         for (int it = 0; it < iters && ok; seg++) {
-          const uint32_t d = tm + (seg & 1) * kHeadTile;
+          const uint32_t d = tm + (seg & acc_mask) * acc_cols;
           const int end = iters - it < kSeg ? iters : it + kSeg;
-          if (seg >= 2) ok = wait_for(&drained[seg & 1], ((seg >> 1) - 1) & 1, &bad);
+          if (seg > acc_mask)
+            ok = wait_for(&drained[seg & acc_mask], ((seg >> acc_log) - 1) & 1, &bad);
           bool first = true;
           // the product of slot i's A and slot j's B
           const auto mul = [&](int i, int j, bool add) {
@@ -550,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
             }
           }
           if (!ok) break;
-          if (elect_one()) Mma<2>::commit(&ready[seg & 1]);
+          if (elect_one()) Mma<2>::commit(&ready[seg & acc_mask]);
           __syncwarp();
         }
       }
@@ -588,11 +594,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
                                x.mt * kHeadTile + rank * (kHeadTile / 2) + 32 * quad + lane,
                                x.nt * x.tile_n + width * half, width, rows, x.split, turn);
       if constexpr (!SEG) {
-        ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
+        ok = wait_for(&ready[seg & acc_mask], (seg >> acc_log) & 1, &bad);
         __syncwarp();
         tmem_fence_after_sync();
         if (!ok) break;
-        const uint32_t t = tacc + (seg & 1) * kHeadTile;
+        const uint32_t t = tacc + (seg & acc_mask) * acc_cols;
 #pragma unroll 1
         for (int c = 0; c < chunks; c++) {
           float v[32];
@@ -600,7 +606,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           if (c == chunks - 1) {
             tmem_fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & 1));
+            if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & acc_mask));
           }
           taker.chunk(c, v);
           __syncwarp();
@@ -613,11 +619,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
 #pragma unroll
           for (int i = 0; i < 32; i++) acc[c][i] = 0.0f;
         for (int it = 0; it < iters && ok; it += kSeg, seg++) {
-          ok = wait_for(&ready[seg & 1], (seg >> 1) & 1, &bad);
+          ok = wait_for(&ready[seg & acc_mask], (seg >> acc_log) & 1, &bad);
           __syncwarp();
           tmem_fence_after_sync();
           if (!ok) break;
-          const uint32_t t = tacc + (seg & 1) * kHeadTile;
+          const uint32_t t = tacc + (seg & acc_mask) * acc_cols;
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             if (c >= chunks) break;
@@ -628,7 +634,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
           }
           tmem_fence_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & 1));
+          if (lane == 0) mbar_arrive_first<2>(first_drained + 8 * (seg & acc_mask));
         }
         if (!ok) break;
 #pragma unroll

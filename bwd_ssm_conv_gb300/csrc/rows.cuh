@@ -362,10 +362,10 @@ __device__ __forceinline__ void row_sum2(float& v, float& u, int tpr, float (*pa
 }
 
 // ---- rows ahead ---------------------------------------------------------------------------------
-// In the backwards and the layer norm's forward a thread's own chunks of the rows to come are copied to shared
-// memory while it works on the current one (cp.async, 8 columns at a time, RowPlan::slots rows in all).  It alone reads what it
-// copied, so no barrier is needed, and it may read a row twice, before and after the row's sum,
-// instead of holding it in registers.  With one slot (ring_slots) nothing is ahead: a row is copied as
+// In the backwards and the layer norm's forward a thread's own chunks of the rows to come are copied
+// to shared memory while it works on the current one (cp.async, 8 columns at a time, RowPlan::slots
+// rows in all).  It alone reads what it copied, so no barrier is needed, and it may read a row twice,
+// before and after the row's sum, instead of holding it in registers.  With one slot (ring_slots) nothing is ahead: a row is copied as
 // a whole and waited for.  Single columns (VEC = 1) are loaded one row ahead into registers instead, up
 // to 8 per thread (20000 x 1001 fp32, add_norm: forward 59 us, backward 123; read where they are used
 // 77 and 233); wider rows (and VEC = 8 without RING) are read where they are used (2000 x 12345 bf16

@@ -82,7 +82,8 @@ int ssm_add_norm_fwd(const ssm_norm_desc* desc, const void* x, long long ld_x,
                      uint8_t* x_e, int8_t* out_q, uint8_t* out_e, void* stream);
 
 /* Bytes of scratch the norms' backward needs for `sums` column sums (add_norm: 1, or 2 with
- * d_scale; add_layer_norm: one for each of d_w, d_b and d_scale; gated_norm: 1) on the current device; 0 if the arguments are invalid. */
+ * d_scale; add_layer_norm: one for each of d_w, d_b and d_scale; gated_norm: 1) on the current device; 0 if
+ * the arguments are invalid. */
 size_t ssm_norm_bwd_workspace_size(const ssm_norm_desc* desc, int sums);
 
 /* Backward.  Required: d_out, rstd (the forward's), and s as either res (the forward's res_out)
