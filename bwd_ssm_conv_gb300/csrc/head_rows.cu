@@ -508,7 +508,8 @@ cudaError_t launch_head_rows(const ssm_head_desc& d, const int64_t* target, cons
                              const void* w, long long ld_w, int* idx, const HeadRows& r,
                              __nv_bfloat16* w_out, const HeadTiles& tiles, int sms, cudaStream_t st) {
   RowsArgs a{target, valid, d.rows, d.ignore_index, d.vocab, d.cols, pad8(d.cols)};
-  const long long per = (d.rows + 255) / 256;  // at most 256 blocks, as each looks at every row
+  // at most 256 blocks, as each looks at every row (8192 x 512 fp32: 128 13.5 us, 256 12.3, 512 16.6)
+  const long long per = (d.rows + 255) / 256;
   a.per_block = per < kRowThreads / 32 ? kRowThreads / 32 : (int)per;
   a.row_blocks = (int)((d.rows + a.per_block - 1) / a.per_block);
   a.tau = d.entries ? d.temperature : 1.0f;
