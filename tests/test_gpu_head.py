@@ -303,6 +303,15 @@ def test_a_dirty_workspace_and_the_same_bits_every_time():
 
 
 @pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("ignored", [0.0, 0.35, 0.9])
+@pytest.mark.parametrize("T,D,V", [(333, 256, 5003), (600, 40, 9900), (1021, 64, 9985), (250, 130, 14500)])
+def test_as_many_tiles_as_a_few_rounds(T, D, V, ignored, io):
+    """The width of a tile then goes by the rows that count; tiles may go past the end of a piece."""
+    i = _inputs(T, D, V, io, seed=T + V, ignored=ignored)
+    _check(*_ce(i), i, _ce_rows(i))
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
 @pytest.mark.parametrize("T", [1, 2, 4, 8])
 def test_a_few_rows_read_nothing_that_a_call_before_left(T, io):
     """Whatever the workspace holds, call after call on other targets; with two calls at once; replayed."""
