@@ -703,7 +703,7 @@ cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
 }
 template <int USE> cudaError_t launch(const ssm_head_desc& d, const TcArgs& t, int sms, cudaStream_t st) {
   if (d.io == SSM_F32) return launch<USE, 3, true>(t, sms, st);
-  if constexpr (USE == kLogits)
+  if constexpr (USE != kOut)  // Z alike in both directions: lse is that of the forward's
     if (t.job[0].per_split > kSegment<1>) return launch<USE, 1, true>(t, sms, st);
   return launch<USE, 1, false>(t, sms, st);
 }
