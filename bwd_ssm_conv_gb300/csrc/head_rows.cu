@@ -28,7 +28,8 @@ __device__ __forceinline__ float nan_() { return __uint_as_float(0x7fc00000u); }
 
 // ---- a teacher's entries ------------------------------------------------------------------------
 // A warp per row.  An entry's place in the order is the number of smaller keys, counted: a key is the word
-// and, behind it, the entry's number, so that no two are alike.  4096 rows of 64 entries take 8 - 9 us (GB300), 333 of
+// and, behind it, the entry's number, so that no two are alike.  A logit's distance to the row's largest is
+// formed before it is divided by tau: t / tau of 7e6 (7 at 1e-6) would be good to half a unit.  4096 rows of 64 entries take 8 - 9 us (GB300), 333 of
 // 17 4.3, most of it a start, an end and the chain of one row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t_idx, const T* t_logit,
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
       const int64_t w = t_idx[row * k + i];
       bad = bad || w >= vocab;
       if (w >= 0 && w < vocab) word[j] = (int)w;
-      const float x = ld(t_logit + row * k + i) / tau;
+      const float x = ld(t_logit + row * k + i);
       if (word[j] >= 0) t[j] = x;
       mine[j] = word[j] >= 0 ? word[j] << kBits | i : kNone + i;
       odd = odd || t[j] != t[j];
@@ -88,7 +89,8 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
   float e[N], sum = 0.0f;
 #pragma unroll
   for (int j = 0; j < N; j++) {
-    e[j] = word[j] >= 0 && some ? expf(t[j] - top) : 0.0f;
+    t[j] = (t[j] - top) / tau;
+    e[j] = word[j] >= 0 && some ? expf(t[j]) : 0.0f;
     sum += e[j];
   }
   sum = warp_sum(sum);
@@ -97,7 +99,7 @@ __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t
 #pragma unroll
   for (int j = 0; j < N; j++) {
     e[j] = some ? e[j] / sum : 0.0f;
-    if (!(e[j] == 0.0f)) kn += e[j] * (t[j] - top - log_sum);
+    if (!(e[j] == 0.0f)) kn += e[j] * (t[j] - log_sum);
     if (lane + 32 * j < k) {
       lists.idx[row * k + place[j]] = word[j] >= 0 ? word[j] : kNoEntry;
       lists.p[row * k + place[j]] = e[j];

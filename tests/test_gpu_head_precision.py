@@ -1,5 +1,7 @@
 """What the head keeps of its digits, where the bounds of head_ref are wide: long sums, fp32 operands, losses
 near 0, temperatures, a few rows; against 64 bits on the GPU."""
+import math
+
 import pytest
 import torch
 
@@ -21,8 +23,8 @@ def _gradients(z, target, up, h, w):
 
 
 def test_logits_of_many_columns_are_alike_in_both_directions():
-    """65536 products of one sign: logits of 1160.  The tensor cores lose up to 2^-24 of a sum with each 16
-    products, 64 times between two emptyings (1024 columns): 2^-18 of a logit at most, 4.4e-3, nearly all of
+    """65536 products of one sign: logits of 1160.  The tensor cores lose up to 2^-23 of what they have
+    summed with each 16 products, 64 times between two emptyings (1024 columns): 2^-18 of a logit, 4.4e-3, nearly all of
     which is that of lse too, as both are the same sums.  Left in one sum the 4096 additions of the backward
     alone lost 0.3.  Besides G and the result are rounded to bf16, 2^-8 of their terms in all."""
     T, D, V = 70, 65536, 300
@@ -38,3 +40,36 @@ def test_logits_of_many_columns_are_alike_in_both_directions():
     want, size = _gradients(z, y, up, h, w)
     for n, v, s in zip(("d_h", "d_w"), want, size):
         assert float(((got[n].to(f64) - v).abs() / s).max()) < 2.0 ** -8 + 2.0 ** -8 + 4.4e-3
+
+
+@pytest.mark.parametrize("T", [3, 70])
+@pytest.mark.parametrize("tau", [1e-6, 1e-3, 1.0, 1e6])
+def test_a_teacher_is_as_exact_at_any_temperature(T, tau):
+    """Logits a few temperatures apart, around 7: their distances, exact to 2^-24, over tau are below 40, so that
+    p is good to 40 x 2^-23 and expf's two units, 5e-6.  The student is even (W is 0), so that nothing else is off."""
+    D, V, k = 16, 64, 5
+    g = torch.Generator().manual_seed(4)
+    h, w = torch.randn(T, D, generator=g).cuda(), torch.zeros(V, D).cuda()
+    t_logit = (7.0 + tau * 4 * torch.randn(T, k, generator=g)).cuda()
+    t_idx = torch.stack([torch.randperm(V, generator=g)[:k] for _ in range(T)]).cuda()
+    a = head.ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=tau)
+    got = head.ssm_head_distill_bwd(h, w, t_idx, t_logit, a.lse, torch.ones(T).cuda(), temperature=tau)
+    tau = float(torch.tensor(tau, dtype=torch.float32))  # as the call has it
+    t = t_logit.to(f64) / tau
+    assert float((t.amax(1) - t.amin(1)).max()) < 40
+    p = torch.softmax(t, 1)
+    want = (p * (torch.log_softmax(t, 1) + math.log(V))).sum(1)
+    assert float(((a.loss.to(f64) / tau ** 2 - want).abs() / want).max()) < 1e-5
+    G = torch.full((T, V), 1.0 / V, dtype=f64, device="cuda").scatter_add_(1, t_idx, -p) * tau
+    want = G.t() @ h.to(f64)
+    assert float((got["d_w"].to(f64) - want).norm() / want.norm()) < 1e-5
+
+
+@pytest.mark.parametrize("T", [3, 70])
+def test_a_teachers_logits_of_any_size(T):
+    """Their quotients by the temperature are past fp32, their distances take p to 1 and 0."""
+    t_logit = torch.tensor([1e35, 3e34, -2e37]).repeat(T, 1).cuda()
+    t_idx = torch.arange(3).repeat(T, 1).cuda()
+    h, w = torch.ones(T, 8).cuda(), torch.zeros(16, 8).cuda()
+    a = head.ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=1e-4)
+    assert float((a.loss.to(f64) / 1e-8 - math.log(16)).abs().max()) < 1e-5
