@@ -275,10 +275,12 @@ template <int USE, int PLANES> struct Taker {
 #pragma unroll
       for (int i = 0; i < 32; i += 2)
         f2_unpack(f2_mul(f2_pack(v[i], v[i + 1]), rg2), v[i], v[i + 1]);
-      if (word + 32 > a.vocab) {
+      // past the vocabulary, and in the rows of zeros past the packed ones, whatever W holds
+      const int left = src < 0 ? 0 : a.vocab - word;
+      if (left < 32) {
 #pragma unroll
         for (int i = 0; i < 32; i++)
-          if (word + i >= a.vocab) v[i] = 0.0f;
+          if (i >= left) v[i] = 0.0f;
       }
       if (!row_ok || col0 + 32 * c >= job.n) return;  // tiles of 192 go past a piece's end
       __nv_bfloat16* g = a.g + (long long)row * a.ld_g + col0 + 32 * c;

@@ -6,6 +6,7 @@ import pytest
 import torch
 
 from bwd_ssm_conv_gb300 import head
+from test_gpu_head import _ce, _inputs
 
 pytestmark = pytest.mark.gpu
 f64 = torch.float64
@@ -73,3 +74,15 @@ def test_a_teachers_logits_of_any_size(T):
     h, w = torch.ones(T, 8).cuda(), torch.zeros(16, 8).cuda()
     a = head.ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=1e-4)
     assert float((a.loss.to(f64) / 1e-8 - math.log(16)).abs().max()) < 1e-5
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 9, 300])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_no_row_that_counts_beside_weights_that_are_not_finite(T, io, bad):
+    i = _inputs(T, 72, 300, io, seed=7)
+    i["target"][:] = -100
+    i["w"][5] = bad
+    a, g = _ce(i)
+    for t in (a.loss, a.lse, g["d_h"], g["d_w"]):
+        assert bool((t == 0).all())
