@@ -262,7 +262,9 @@ template <int USE, int PLANES> struct Taker {
                                       fmaf(v[i], a.inv_tau, fmaf(v[i], a.inv_tau_rest, -rl)) * kLog2e;
         v[i] = ex2(min_nan(x, 0.0f));
       }
-      if constexpr (PLANES > 1)
+      // In braces: nvcc 13.0.88 drops an unrolled loop (`#pragma unroll`, whatever the optimisation level) that
+      // comes next behind a discarded `if constexpr (...) while (...)` without them, here the products with rg.
+      if constexpr (PLANES > 1) {
         while (next < word + 32) {
           const float p = prob();
           const int at = next - word;
@@ -270,7 +272,7 @@ template <int USE, int PLANES> struct Taker {
           for (int i = 0; i < 32; i++) v[i] -= i == at ? p : 0.0f;
           advance();
         }
-      // In pairs: of 32 separate products with rg behind ex2, nvcc 13.0.88 lost rg's sign.
+      }
       const f2_t rg2 = f2_pack(rg, rg);
 #pragma unroll
       for (int i = 0; i < 32; i += 2)
@@ -301,13 +303,14 @@ template <int USE, int PLANES> struct Taker {
           st_global32(g + r * a.plane_g + 16 * b, w);
         }
       }
-      if constexpr (PLANES == 1)  // cheaper than a subtraction from each: over what was stored for the word
+      if constexpr (PLANES == 1) {  // cheaper than a subtraction from each: over what was stored for the word
         while (next < word + 32) {
           const int at = next - word;
           float p = 0.0f;
           for (; next == word + at; advance()) p += prob();
           g[at] = __float2bfloat16_rn(pick(v, at) - p * rg);
         }
+      }
     } else if (job.part) {
       if (!row_ok) return;
 #pragma unroll

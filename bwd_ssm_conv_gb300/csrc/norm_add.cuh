@@ -54,11 +54,12 @@ __global__ void __launch_bounds__(MAXT, MINB) add_norm_fwd_kernel(const AddNormF
   const int step = gridDim.x * pl.rpb;  // rows stay below 2^31 - step
   const int more = kRing ? pl.slots - 1 : 1;  // rows ahead
   int half = 0, slot = 0;
-  if constexpr (kRing)
+  if constexpr (kRing) {
     for (int i = 0; i < pl.slots; i++) {
       x1.clear(i * bytes, okc, false);
       r1.clear(i * bytes, okc, false);
     }
+  }
   for (int i = 0; i < more; i++) ahead(blockIdx.x * pl.rpb + pos.slot + i * step, i);
   for (int base = blockIdx.x * pl.rpb; base < a.rows; base += step, half ^= 1) {
     const int row = base + pos.slot;
