@@ -57,13 +57,16 @@ constexpr int kSlots = 6;
 constexpr uint32_t kSlot = 2 * kOperand, kAtTurn = kSlots * kSlot;
 constexpr uint32_t kTurn = kSumWarps * 32 * 33 * 4, kSmem = kAtTurn + 1024;
 
-// Stages between two emptyings of the accumulator: as the tensor cores truncate when they add, by the size
-// of the sum.  Errors of lse and of d_W against 64 bits (plain fp32: 2e-7, 6.6e-7 and up):
+// Stages between two emptyings of the accumulator: as the tensor cores truncate when they add, by up to 2^-23 of
+// the sum for each 16 terms.  Errors of lse and of d_W against 64 bits (plain fp32: 2e-7, 6.6e-7 and up):
 //   fp32, 1021 x 515 over 10007 words: every 2 stages 3.2e-7 and 6.4e-7, every stage 0.7e-7 and 3.5e-7, for
 //     5 % of the time
 //   bf16, lse alone (G is rounded to bf16): all at once 768 columns 5.8e-7, 1024 7.4e-7, 2048 1.5e-6; every 12
 //     stages 4.8e-7 to 5.8e-7, which slows 1024 columns down
-template <int PLANES> constexpr int kSegment = PLANES > 1 ? 1 : 16;
+// The sums of bf16 gradients, over any number of rows or words, are emptied every 64 stages (4096 terms), which
+// leaves 1.5e-5 of a sum of one sign, 1/128 of the result's own rounding and less; all at once 65536 rows lost 2.4e-4.
+// It costs 0.4 % at most (8192 x 768 over 50000 words 1493 -> 1499 us; every 16 stages 1523).
+template <int USE, int PLANES> constexpr int kSegment = PLANES > 1 ? 1 : USE == kOut ? 64 : 16;
 
 // A product of a launch.
 struct Job {
@@ -421,7 +424,7 @@ struct Units {
 // SEG: sums are taken out in between (without it the kernel has half the registers).
 template <int USE, int PLANES, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
-  constexpr int S = kSlots, kSeg = SEG ? kSegment<PLANES> : 1 << 30;
+  constexpr int S = kSlots, kSeg = SEG ? kSegment<USE, PLANES> : 1 << 30;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t here[S], there[S], empty[S], ready[4], drained[4], last;
   __shared__ uint32_t tbase;
@@ -708,8 +711,8 @@ cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
 }
 template <int USE> cudaError_t launch(const ssm_head_desc& d, const TcArgs& t, int sms, cudaStream_t st) {
   if (d.io == SSM_F32) return launch<USE, 3, true>(t, sms, st);
-  if constexpr (USE != kOut)  // Z alike in both directions: lse is that of the forward's
-    if (t.job[0].per_split > kSegment<1>) return launch<USE, 1, true>(t, sms, st);
+  for (int j = 0; j < t.jobs; j++)
+    if (t.job[j].per_split > kSegment<USE, 1>) return launch<USE, 1, true>(t, sms, st);
   return launch<USE, 1, false>(t, sms, st);
 }
 

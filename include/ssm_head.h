@@ -28,8 +28,9 @@
  *
  * Arithmetic: products on the tensor cores with fp32 sums, fp32 operands as three bf16 terms each
  * (six products, which leave out 2^-24 of a product and less).  The tensor cores truncate as they
- * add, about 10^-8 of the sum for each 16 columns: sums are taken out every 64 columns with fp32 operands,
- * those of the logits every 1024 with bf16 ones, and added with rounding to nearest.  With bf16 operands G,
+ * add, up to 2^-23 of the sum for each 16 terms: sums are taken out every 64 terms with fp32 operands,
+ * with bf16 ones those of the logits every 1024 and those of the gradients every 4096, and added with rounding
+ * to nearest, so that long sums lose no more than short ones.  With bf16 operands G,
  * divided by the largest |d_loss|, is rounded to bf16 between the products, which gives d_h and d_W an error
  * of the size of their own rounding.  A few rows (bf16: 2 in the forward, 4 in
  * the backward; fp32: 8) are fp32 arithmetic throughout, G too.

@@ -86,3 +86,51 @@ def test_no_row_that_counts_beside_weights_that_are_not_finite(T, io, bad):
     a, g = _ce(i)
     for t in (a.loss, a.lse, g["d_h"], g["d_w"]):
         assert bool((t == 0).all())
+
+
+def _above_a_tie(n, cols, share, factor, seed):
+    """bf16 [n][cols] of values in [1, 2), whose sum over n times ``factor`` (an integer) lies above the middle
+    between two bf16 numbers by ``share`` of itself, or a little more."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randint(128, 256, (n, cols), generator=g, device="cuda")  # units of 2^-7
+    m = n // 8  # the rows that make up what the sum lacks
+    rest = x[m:].sum(0)
+    total = (rest + 192 * m) * factor
+    step = 2 ** (torch.floor(torch.log2(total.to(f64))).long() - 7)  # between two bf16 numbers
+    middle = total // step * step + step // 2
+    aim = torch.ceil(middle.to(f64) * (1 + share) / factor).long()
+    lack = aim - rest
+    x[:m] = lack // m
+    x[:m] += torch.arange(m, device="cuda")[:, None] < lack % m
+    assert bool((x.sum(0) == aim).all()) and 128 <= int(x.min()) and int(x.max()) < 256
+    return (x.to(f64) / 128).bfloat16()
+
+
+def _even(T, D, V, h, w):
+    """Gradients for logits of 0 and targets of 0: G is 141 x 2^-k, which is what bf16 makes of 1 / V."""
+    q = torch.tensor(1.0 / V).bfloat16().double()
+    assert float(q) * V == pytest.approx(1.0, abs=1e-3) and (float(q) * 2.0 ** 40) % 141 == 0
+    y, up = torch.zeros(T, dtype=torch.long, device="cuda"), torch.ones(T, device="cuda")
+    a = head.ssm_head_ce_fwd(h, w, y)
+    return float(q), head.ssm_head_ce_bwd(h, w, y, a.lse, up)
+
+
+# Sums of equal signs lose up to 2^-23 of what they are with each 16 terms: left in one sum the 29747 words
+# lose 2^-23 x 1859 / 2 = 1.1e-4 of it and the 65536 rows 2.4e-4; emptied every 4096 terms at most 256 additions
+# are lost by, 1.5e-5, and what is emptied is added with rounding to nearest (16 x 2^-24).  A sum that is 3e-5
+# above the middle between two bf16 numbers is then rounded up as it should be.
+def test_sums_over_many_words_are_rounded_as_they_should_be():
+    T, D, V = 8192, 2048, 29747
+    w = torch.zeros(V, D, dtype=torch.bfloat16, device="cuda")
+    w[1:] = _above_a_tie(V - 1, D, 3e-5, 141, seed=1)
+    q, g = _even(T, D, V, torch.zeros(T, D, dtype=torch.bfloat16, device="cuda"), w)
+    want = (w.to(f64).sum(0) * q).bfloat16()
+    assert int((g["d_h"] != want).sum()) == 0
+
+
+def test_sums_over_many_rows_are_rounded_as_they_should_be():
+    T, D, V = 65536, 4096, 3718
+    h = _above_a_tie(T, D, 3e-5, 141, seed=2)
+    q, g = _even(T, D, V, h, torch.zeros(V, D, dtype=torch.bfloat16, device="cuda"))
+    want = (h.to(f64).sum(0) * q).bfloat16()
+    assert int((g["d_w"][1:] != want).sum()) == 0
