@@ -74,6 +74,10 @@ __host__ __device__ inline int head_tile(const HeadTiles& t, int rows) {
   return best;
 }
 
+// bf16 terms of G between the products.
+inline int head_g_terms(const ssm_head_desc& d) {
+  return d.io == SSM_F32 ? 3 : d.flags & SSM_HEAD_FINE_G ? 2 : 1;
+}
 inline int pad8(int n) { return (n + 7) / 8 * 8; }
 inline long long pad_rows(long long rows) { return (rows + 63) / 64 * 64; }
 
@@ -125,7 +129,8 @@ struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart
   long long rows, ld, plane;
   int cols;
 };
-// How a product with G is cut: columns of a tile (256 or 128), splits of the sum and their stages.
+// How a product with G is cut: columns of a tile (256 or 128), splits of the sum and their stages (two for
+// each 64 of the sum where G has two terms).
 struct HeadCut {
   int tile_n, splits, per;
 };
@@ -133,7 +138,7 @@ struct HeadCut {
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
                                const HeadRows& r, const HeadLists& lists, float2* stats, float* zt,
                                int sms, cudaStream_t st);
-// G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [planes][padded rows][n].
+// G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [terms][padded rows][n].
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
                              const HeadRows& r, const HeadLists& lists, __nv_bfloat16* g, int v0, int n,
                              int sms, cudaStream_t st);

@@ -81,9 +81,10 @@ struct Cuts {
 };
 // The two products with G: pairs of numbers of splits, and both widths, as far as more units than a few for
 // each pair of CTAs could help.
-Cuts cuts_of(long long rows, int cols, int piece, int io, int grads, bool several, int sms) {
+Cuts cuts_of(long long rows, int cols, int piece, int io, bool fine, int grads, bool several, int sms) {
   const long long pairs = sms / 2 > 0 ? sms / 2 : 1, padded = pad_rows(rows);
-  const int st_h = piece / kHeadBlock, st_w = (int)(padded / kHeadBlock);
+  const int terms = fine ? 2 : 1;  // a stage for each
+  const int st_h = piece / kHeadBlock * terms, st_w = (int)(padded / kHeadBlock) * terms;
   const long long m_h = (rows + kHeadTile - 1) / kHeadTile, m_w = piece / kHeadTile;
   const double mb_h = 4.0 * padded * pad8(cols), mb_w = 4.0 * piece * pad8(cols);
   const auto per_of = [](int stages, int splits) { return (stages + splits - 1) / splits; };
@@ -172,14 +173,15 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
     p.rg = take(4 * Tp);
     // pieces of the vocabulary, alike
     const int tiles = (d.vocab + kHeadTile - 1) / kHeadTile;
-    long long most = kMaxPiece / (2 * p.planes * Tp) / kHeadTile;
+    const int terms = head_g_terms(d);
+    long long most = kMaxPiece / (2 * terms * Tp) / kHeadTile;
     if (most < 1) most = 1;
     p.pieces = (int)((tiles + most - 1) / most);
     p.piece = (tiles + p.pieces - 1) / p.pieces * kHeadTile;
     p.pieces = (d.vocab + p.piece - 1) / p.piece;
-    p.g = take((size_t)2 * p.planes * Tp * p.piece);
+    p.g = take((size_t)2 * terms * Tp * p.piece);
     p.tiles = tiles_of(T, d.cols, p.piece, d.io, true, sms);
-    p.cuts = cuts_of(T, d.cols, p.piece, d.io, grads, p.pieces > 1, sms);
+    p.cuts = cuts_of(T, d.cols, p.piece, d.io, terms == 2, grads, p.pieces > 1, sms);
     if ((grads & 1) && (p.pieces > 1 || p.cuts.h.splits > 1))
       p.dh = take((size_t)4 * p.cuts.h.splits * Tp * Dp);
     if ((grads & 2) && p.cuts.w.splits > 1)
@@ -194,7 +196,7 @@ Plan make_plan(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
 Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   struct Known {
     long long rows;
-    int cols, vocab, io, entries, grads, copy_w, sms;
+    int cols, vocab, io, entries, terms, grads, copy_w, sms;
     Plan plan;
   };
   constexpr int kPlans = 8;
@@ -202,11 +204,11 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
   static thread_local int next = 0;
   for (const Known& k : known)
     if (k.sms == sms && k.rows == d.rows && k.cols == d.cols && k.vocab == d.vocab && k.io == d.io &&
-        k.entries == d.entries && k.grads == grads && k.copy_w == (int)copy_w)
+        k.entries == d.entries && k.terms == head_g_terms(d) && k.grads == grads && k.copy_w == (int)copy_w)
       return k.plan;
   Known& k = known[next];
   next = (next + 1) % kPlans;
-  k = {d.rows, d.cols, d.vocab, d.io, d.entries, grads, (int)copy_w, sms,
+  k = {d.rows, d.cols, d.vocab, d.io, d.entries, head_g_terms(d), grads, (int)copy_w, sms,
        make_plan(d, grads, copy_w, sms)};
   return k.plan;
 }
@@ -214,7 +216,7 @@ Plan plan_of(const ssm_head_desc& d, int grads, bool copy_w, int sms) {
 int check(const ssm_head_desc* d, bool distill) {
   if (!d || d->rows <= 0 || d->cols <= 0 || d->vocab <= 0 || !io_size(d->io))
     return SSM_ERR_INVALID_ARG;
-  if (d->flags & ~(unsigned)SSM_DEBUG_NO_WAIT) return SSM_ERR_INVALID_ARG;
+  if (d->flags & ~(SSM_DEBUG_NO_WAIT | SSM_HEAD_FINE_G)) return SSM_ERR_INVALID_ARG;
   if (distill) {
     if (d->entries <= 0 || !io_size(d->entry_io)) return SSM_ERR_INVALID_ARG;
     if (!(d->temperature > 0.0f) || isinf(d->temperature)) return SSM_ERR_INVALID_ARG;

@@ -413,7 +413,7 @@ struct FinishArgs {
   void* d_h;
   long long ld_h;
   const float* w_part;
-  int w_per, words;
+  int w_per, words, g_stages;
   long long w_step;
   void* d_w;        // the first of the words
   void* all_w;      // the whole of d_W where this is the call's last kernel
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(kThreads) head_finish_kernel(const FinishArgs 
                   n = n_h + (a.w_part ? (long long)a.words * chunks : 0),
                   stride = (long long)gridDim.x * kThreads,
                   first = blockIdx.x * (long long)kThreads + threadIdx.x;
-  const int stages = ((state.count > 0 ? state.count : 1) + kHeadBlock - 1) / kHeadBlock;
+  const int stages = ((state.count > 0 ? state.count : 1) + kHeadBlock - 1) / kHeadBlock * a.g_stages;
   for (long long i = first; i < n; i += stride) {
     float v[8];
     if (i < n_h) {
@@ -556,6 +556,7 @@ cudaError_t launch_head_finish(const ssm_head_desc& d, const HeadRows& r, const 
   a.cols = d.cols, a.padded_cols = pad8(d.cols), a.last = last;
   a.h_part = h_part, a.h_splits = h_splits, a.h_step = pad_rows(d.rows) * a.padded_cols;
   a.rows = d.rows, a.d_h = d_h, a.ld_h = ld_d_h;
+  a.g_stages = head_g_terms(d) == 2 ? 2 : 1;
   a.w_part = w_part, a.w_per = w_per, a.words = n, a.w_step = (long long)piece * a.padded_cols;
   a.d_w = (char*)d_w + (size_t)v0 * d.cols * size;
   a.all_w = d_w, a.n_w = (long long)d.vocab * d.cols;

@@ -27,6 +27,8 @@
 //   3891 x 768, 32768 bf16         104  1880      133      1470  220      1780
 //   684 x 515, 10007 fp32           40  1030       50       850   87       970  (six products counted)
 //   300 x 256, 5003 fp32            14   330       18       260   18       510
+// G in two terms (SSM_HEAD_FINE_G): a stage for each, the smaller one first, with the other operand copied again;
+// the backward of 8192 x 768 over 50000 words 1.08 -> 2.13 ms, of 16384 x 1024 over 32768 1.86 -> 3.59.
 // The tensor cores bound it, back to back the power limit (1500 - 1650 TFLOP/s).  kGrad's stores are what it is
 // slower by (with fp32 few products run meanwhile); fp32 of few rows lacks whole tiles (768 of rows, 640 of
 // columns for 684 and 515), a stage in nine and even rounds of tiles.  Z's tiles may be of 256, 192 or 128 columns
@@ -75,7 +77,8 @@ struct Job {
   int m_fixed;         // rows of the result; 0: the packed rows
   int n, tile_n;       // columns of the result, and of a tile (256 or 128; 0: the state's, 192 too)
   int k_fixed;         // length of the sum; 0: the packed rows
-  int per_split;       // stages of a split of the sum
+  int a_terms;         // log2 of A's terms with bf16 operands: a stage for each, the smaller one first
+  int per_split;       // stages of a split of the sum (each of A's terms has its own)
   int b_row0;          // first row of b's in the tensor
   int m_first;         // unit order: m fastest (else n)
   // kOut: the splits' sums or, where there is one split, the result
@@ -109,6 +112,7 @@ struct TcArgs {
   const float *rl, *rg;
   __nv_bfloat16* g;
   long long ld_g, plane_g;
+  int fine;            // G in two terms with bf16 operands
   int io;
 };
 
@@ -304,6 +308,15 @@ template <int USE, int PLANES> struct Taker {
             }
           }
           st_global32(g + r * a.plane_g + 16 * b, w);
+          if (PLANES == 1 && a.fine) {  // what is left of them; v stays
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+              const int j = 16 * b + 2 * i;
+              w[i] = bf16x2_rn(v[j] - __uint_as_float(w[i] << 16),
+                               v[j + 1] - __uint_as_float(w[i] & 0xffff0000u));
+            }
+            st_global32(g + a.plane_g + 16 * b, w);
+          }
         }
       }
       if constexpr (PLANES == 1) {  // cheaper than a subtraction from each: over what was stored for the word
@@ -311,7 +324,10 @@ template <int USE, int PLANES> struct Taker {
           const int at = next - word;
           float p = 0.0f;
           for (; next == word + at; advance()) p += prob();
-          g[at] = __float2bfloat16_rn(pick(v, at) - p * rg);
+          const float x = pick(v, at) - p * rg;
+          const __nv_bfloat16 first = __float2bfloat16_rn(x);
+          g[at] = first;
+          if (a.fine) g[a.plane_g + at] = __float2bfloat16_rn(x - __bfloat162float(first));
         }
       }
     } else if (job.part) {
@@ -398,7 +414,7 @@ struct Units {
       m[j] = (rows[j] + kHeadTile - 1) / kHeadTile;
       n[j] = (b.n + tile_n[j] - 1) / tile_n[j];
       const int k = b.k_fixed ? b.k_fixed : count;
-      stages[j] = (k + kHeadBlock - 1) / kHeadBlock;
+      stages[j] = (k + kHeadBlock - 1) / kHeadBlock << b.a_terms;
       total[j] = m[j] * n[j] * ((stages[j] + b.per_split - 1) / b.per_split);
     }
   }
@@ -481,10 +497,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         const int m0 = x.mt * kHeadTile + rank * (kHeadTile / 2), n0 = x.nt * x.tile_n + rank * half;
         const bool a_mn = b.a_mn, b_mn = b.b_mn;
         const uint32_t bytes = kOperand + (half > 64 ? 2 : 1) * kSlab;  // of 96 columns all of the second slab
-        for (int k = x.begin; k < x.begin + x.iters && ok; k++) {
+        for (int stage = x.begin; stage < x.begin + x.iters && ok; stage++) {
+          const int k = stage >> b.a_terms;
 #pragma unroll
           for (int i = 0; i < PLANES; i++, it++, r.next()) {
             const int p = PLANES == 1 ? 0 : i == 0 ? 1 : i == 1 ? 0 : 2;
+            const int pa = PLANES == 1 ? b.a_terms & ~stage : p;
             if (it >= S) ok = ok && wait_for(&empty[r.s], r.phase ^ 1, &bad);
             if (!ok) break;
             if (elect_one()) {
@@ -493,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
 #pragma unroll
               for (int c = 0; c < 2; c++) {
                 tma_load_3d(to + c * kSlab, &b.a, a_mn ? m0 + 64 * c : 64 * k,
-                            a_mn ? 64 * k : m0 + 64 * c, p, &here[r.s]);
+                            a_mn ? 64 * k : m0 + 64 * c, pa, &here[r.s]);
                 if (64 * c < half)
                   tma_load_3d(to + kOperand + c * kSlab, &b.b, b_mn ? n0 + 64 * c : 64 * k,
                               b.b_row0 + (b_mn ? 64 * k : n0 + 64 * c), p, &here[r.s]);
@@ -775,6 +793,7 @@ cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const 
   t.g = g;
   t.ld_g = n;
   t.plane_g = h.rows * n;
+  t.fine = head_g_terms(d) == 2;
   return launch<kGrad>(d, t, sms, st);
 }
 
@@ -783,12 +802,13 @@ cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const H
                             bool add, int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, {});
   t.jobs = 0;
-  const int planes = planes_of(d), padded = pad8(d.cols);
+  const int planes = planes_of(d), terms = head_g_terms(d), padded = pad8(d.cols);
   const size_t size = d.io == SSM_F32 ? 4 : 2;
   if (o.d_w) {
     Job& j = t.job[t.jobs++];
-    if (!encode(&j.a, g, planes) || !encode(&j.b, h, planes)) return cudaErrorInvalidValue;
+    if (!encode(&j.a, g, terms) || !encode(&j.b, h, planes)) return cudaErrorInvalidValue;
     j.a_mn = j.b_mn = 1;
+    j.a_terms = terms == 2;
     j.m_fixed = n;
     j.n = d.cols;
     j.tile_n = o.w.tile_n;
@@ -802,8 +822,9 @@ cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const H
   }
   if (o.h_part || o.d_h) {
     Job& j = t.job[t.jobs++];
-    if (!encode(&j.a, g, planes) || !encode(&j.b, w, planes)) return cudaErrorInvalidValue;
+    if (!encode(&j.a, g, terms) || !encode(&j.b, w, planes)) return cudaErrorInvalidValue;
     j.b_mn = 1;
+    j.a_terms = terms == 2;
     j.n = d.cols;
     j.tile_n = o.h.tile_n;
     j.k_fixed = g.cols;

@@ -18,6 +18,7 @@ from . import binding, block
 from .binding import SSM_BF16, _check
 
 SSM_MAX_HEAD_ENTRIES = 128
+SSM_HEAD_FINE_G = 2
 
 EXPORTED = ("ssm_head_workspace_size", "ssm_head_ce_fwd", "ssm_head_ce_bwd", "ssm_head_distill_fwd",
             "ssm_head_distill_bwd")
@@ -62,11 +63,13 @@ def _calls():
     return block._B or block._calls()
 
 
-def ssm_head_workspace_size(rows, cols, vocab, io=SSM_BF16, entries=0, grads=0, aligned=True) -> int:
+def ssm_head_workspace_size(rows, cols, vocab, io=SSM_BF16, entries=0, grads=0, aligned=True,
+                            fine=False) -> int:
     """Bytes of ``ws``: ``entries`` 0 for cross entropy, ``grads`` 0 for the forward, else 1 (d_h) + 2
-    (d_w); ``aligned``: w's rows are 16-byte aligned."""
+    (d_w); ``aligned``: w's rows are 16-byte aligned; ``fine``: as the backward's."""
     return int(lib().ssm_head_workspace_size(
-        HeadDesc(rows, cols, vocab, io, entries, io, 1.0, -100, 0), grads, 1 if aligned else 0))
+        HeadDesc(rows, cols, vocab, io, entries, io, 1.0, -100, SSM_HEAD_FINE_G if fine else 0), grads,
+        1 if aligned else 0))
 
 
 def ssm_head_ce_fwd(h, w, target, ignore_index=-100, ws=None, out=None, stream=None,
@@ -86,13 +89,17 @@ def ssm_head_ce_fwd(h, w, target, ignore_index=-100, ws=None, out=None, stream=N
 
 
 def ssm_head_ce_bwd(h, w, target, lse, d_loss, ignore_index=-100, want_dh=True, want_dw=True, ws=None,
-                    out=None, stream=None, debug_flags=0) -> dict:
+                    out=None, stream=None, debug_flags=0, fine=False) -> dict:
     """Backward of ssm_head_ce_fwd, given its lse and the gradient d_loss [...] of each row's loss; returns
     {"d_h", "d_w"} in the type of h and w (None where not wanted).  ``out`` = a dict of preallocated
-    results with the same keys, optional."""
+    results with the same keys, optional.
+
+    ``fine`` (bf16): the gradient of the logits, which is rounded to bf16 between the products otherwise, is
+    kept to 16 bits in two terms, so that the results have no error but their own rounding; the backward
+    takes twice the time.  Up to 4 rows, and fp32 ones, are as exact in either case."""
     into = out if out is None else (out["d_h"], out["d_w"])
     r = _calls().head_ce_bwd(h, w, target, ignore_index, lse, d_loss, want_dh, want_dw, ws, into, stream,
-                             debug_flags)
+                             debug_flags | SSM_HEAD_FINE_G if fine else debug_flags)
     if type(r) is int:
         _check("ssm_head_ce_bwd", r)
     return {"d_h": r[0], "d_w": r[1]} if out is None else out
@@ -113,12 +120,13 @@ def ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=1.0, ws=None, out=Non
 
 
 def ssm_head_distill_bwd(h, w, t_idx, t_logit, lse, d_loss, temperature=1.0, want_dh=True,
-                         want_dw=True, ws=None, out=None, stream=None, debug_flags=0) -> dict:
+                         want_dw=True, ws=None, out=None, stream=None, debug_flags=0,
+                         fine=False) -> dict:
     """Backward of ssm_head_distill_fwd, given its lse and the gradient d_loss [...] of each row's loss
-    (the teacher's logits have none); results as in ssm_head_ce_bwd."""
+    (the teacher's logits have none); results and ``fine`` as in ssm_head_ce_bwd."""
     into = out if out is None else (out["d_h"], out["d_w"])
     r = _calls().head_distill_bwd(h, w, t_idx, t_logit, temperature, lse, d_loss, want_dh, want_dw, ws,
-                                  into, stream, debug_flags)
+                                  into, stream, debug_flags | SSM_HEAD_FINE_G if fine else debug_flags)
     if type(r) is int:
         _check("ssm_head_distill_bwd", r)
     return {"d_h": r[0], "d_w": r[1]} if out is None else out

@@ -31,9 +31,10 @@
  * add, up to 2^-23 of the sum for each 16 terms: sums are taken out every 64 terms with fp32 operands,
  * with bf16 ones those of the logits every 1024 and those of the gradients every 4096, and added with rounding
  * to nearest, so that long sums lose no more than short ones.  With bf16 operands G,
- * divided by the largest |d_loss|, is rounded to bf16 between the products, which gives d_h and d_W an error
- * of the size of their own rounding.  A few rows (bf16: 2 in the forward, 4 in
- * the backward; fp32: 8) are fp32 arithmetic throughout, G too.
+ * divided by the largest |d_loss|, is rounded to bf16 between the products (2^-8 of each of its values), which
+ * gives d_h and d_W an error of the size of their own rounding; with SSM_HEAD_FINE_G it is kept in two bf16 terms
+ * (2^-16), which takes twice the time and leaves d_h and d_W with their own rounding.  A few rows
+ * (bf16: 2 in the forward, 4 in the backward; fp32: 8) are fp32 arithmetic throughout, G too.
  */
 #ifndef SSM_HEAD_GB300_H
 #define SSM_HEAD_GB300_H
@@ -44,6 +45,7 @@
 extern "C" {
 #endif
 
+#define SSM_HEAD_FINE_G 2u /* of a descriptor's flags */
 #define SSM_MAX_HEAD_ENTRIES 128 /* teacher entries of a row (SSM_ERR_UNSUPPORTED beyond) */
 #define SSM_MAX_HEAD_COLS 65536
 #define SSM_MAX_HEAD_VOCAB (1 << 22)
@@ -59,7 +61,8 @@ typedef struct {
   int entry_io;   /* head_distill: ssm_dtype of t_logit */
   float temperature;      /* head_distill: tau > 0, finite */
   long long ignore_index; /* head_ce: the target of a row without a loss */
-  unsigned flags; /* 0, or ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
+  unsigned flags; /* SSM_HEAD_FINE_G: the backward of bf16 operands keeps G in two terms (no effect elsewhere);
+                     ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
                      the sums out give up at once, as if the bound of their wait had run out (the kernels of
                      a few rows wait for nothing) */
 } ssm_head_desc;
@@ -68,7 +71,7 @@ typedef struct {
  * h (three times its bf16 size with fp32), one of W with fp32 or rows that are not aligned, and
  *   forward   rows * vocab / 16 bytes of sums (twice that up to 5 tiles of 256 x 256 for
  *             each pair of SMs, which may be narrower ones; next to none for a few rows)
- *   backward  a piece of G, 512 MiB at most (or 256 words of it), and fp32 sums of d_h and perhaps of d_W,
+ *   backward  a piece of G, 512 MiB at most (or 256 words of it; the flags count), and fp32 sums of d_h and perhaps of d_W,
  *             up to 64 of them where there are few rows; for a few rows 2 sums of d_h per SM.
  * grads: 0 for the forward, else bits 1 (d_h wanted) and 2 (d_W wanted) of the backward.  aligned: W's rows
  * (pointer and ld_w * element size) are 16-byte aligned; fp32 W may lie anywhere. */

@@ -5,8 +5,10 @@ import math
 import pytest
 import torch
 
-from bwd_ssm_conv_gb300 import head
-from test_gpu_head import _ce, _inputs
+import head_ref as ref
+from bwd_ssm_conv_gb300 import binding, head
+from head_ref import within
+from test_gpu_head import _ce, _ce_rows, _entries, _inputs, _nan
 
 pytestmark = pytest.mark.gpu
 f64 = torch.float64
@@ -134,3 +136,87 @@ def test_sums_over_many_rows_are_rounded_as_they_should_be():
     q, g = _even(T, D, V, h, torch.zeros(V, D, dtype=torch.bfloat16, device="cuda"))
     want = (h.to(f64).sum(0) * q).bfloat16()
     assert int((g["d_w"][1:] != want).sum()) == 0
+
+
+def _within_fine(got, i, rows, lse, tau=1.0):
+    """Within the bounds of fp32 operands, whose G has 2^-22, and 2^-16 of each value of G besides; the results'
+    own rounding apart."""
+    h, w = i["h"].float(), i["w"].float()
+    want, bound = ref.head_bwd(h, w, rows[0], rows[1], lse.cpu(), i["d_loss"], tau)
+    z = torch.where(rows[1][:, None], h.to(f64), torch.zeros(1, dtype=f64)) @ w.to(f64).t() / tau
+    up = torch.where(rows[1], i["d_loss"].to(f64) * tau, torch.zeros(1, dtype=f64))[:, None]
+    G = ((torch.exp(z - lse.cpu().to(f64)[:, None]) - rows[0]) * up).abs()
+    h = torch.where(rows[1][:, None], h, torch.zeros(1))
+    for n, v, e, size in zip(("d_h", "d_w"), want, bound, (G @ w.to(f64).abs(), G.t() @ h.to(f64).abs())):
+        if got[n] is not None:
+            within(n, got[n], v, e + 2.0 ** -16 * size)
+
+
+FINE = [  # (T, D, V): one stage to several, splits of either sum, odd sizes
+    (5, 8, 40), (64, 64, 256), (70, 72, 700), (300, 515, 777), (129, 40, 5003), (900, 264, 300)]
+
+
+@pytest.mark.parametrize("T,D,V", FINE)
+def test_fine_gradients(T, D, V):
+    i = _inputs(T, D, V, "bf16", seed=T + V)
+    rows = _ce_rows(i)
+    h, w, y, up = (i[n].cuda() for n in ("h", "w", "target", "d_loss"))
+    a = head.ssm_head_ce_fwd(h, w, y)
+    got = head.ssm_head_ce_bwd(h, w, y, a.lse, up, fine=True,
+                               out=dict(d_h=_nan((T, D), h.dtype), d_w=_nan((V, D), h.dtype)))
+    _within_fine(got, i, rows, a.lse)
+    with pytest.raises(AssertionError, match="times its bound"):  # what it is there for
+        _within_fine(head.ssm_head_ce_bwd(h, w, y, a.lse, up), i, rows, a.lse)
+    # one gradient at a time, in a workspace of its size whatever that holds
+    for grads, n in ((1, "d_h"), (2, "d_w")):
+        ws = torch.full((head.ssm_head_workspace_size(T, D, V, grads=grads, aligned=D % 8 == 0, fine=True),),
+                        255, dtype=torch.uint8, device="cuda")
+        one = head.ssm_head_ce_bwd(h, w, y, a.lse, up, want_dh=grads == 1, want_dw=grads == 2, ws=ws,
+                                   fine=True)
+        _within_fine(one, i, rows, a.lse)
+        assert binding.ssm_scan_status(ws) == binding.SSM_OK
+
+
+@pytest.mark.parametrize("T,D,V,k,tau", [(33, 24, 20, 20, 1.0), (130, 72, 513, 64, 4.0), (300, 515, 777, 100, 0.7)])
+def test_fine_gradients_of_distillation(T, D, V, k, tau):
+    i = _inputs(T, D, V, "bf16", seed=T + k)
+    i["t_idx"], i["t_logit"] = _entries(T, V, k, seed=k)
+    rows = ref._p_of(i["t_idx"], i["t_logit"], tau, V)
+    h, w, t_idx, t_logit, up = (i[n].cuda() for n in ("h", "w", "t_idx", "t_logit", "d_loss"))
+    a = head.ssm_head_distill_fwd(h, w, t_idx, t_logit, temperature=tau)
+    got = head.ssm_head_distill_bwd(h, w, t_idx, t_logit, a.lse, up, temperature=tau, fine=True)
+    _within_fine(got, i, rows, a.lse, tau)
+
+
+def test_fine_gradients_in_several_pieces_and_where_they_make_no_difference():
+    T, D, V = 16384, 40, 9000  # 590 MB of G in two terms
+    i = _inputs(T, D, V, "bf16", seed=5, ignored=0.1)
+    h, w, y, up = (i[n].cuda() for n in ("h", "w", "target", "d_loss"))
+    a = head.ssm_head_ce_fwd(h, w, y)
+    got = head.ssm_head_ce_bwd(h, w, y, a.lse, up, fine=True)
+    some = y != -100
+    want, size = _gradients(h.to(f64) @ w.to(f64).t(), y.clamp(min=0), up * some, h, w)
+    # 2^-16 of G, 60 units of 2^-24 of its softmax, 260 additions by 2^-23 in a stretch of the sums
+    for n, v, s in zip(("d_h", "d_w"), want, size):
+        within(n, got[n], v.cpu(), ((2.0 ** -16 + 60 * 2.0 ** -24 + 130 * 2.0 ** -23) * s).cpu())
+    for T, io in ((4, "bf16"), (70, "f32"), (3, "f32")):
+        i = _inputs(T, 72, 300, io, seed=T, ignored=0.0)
+        h, w, y, up = (i[n].cuda() for n in ("h", "w", "target", "d_loss"))
+        a = head.ssm_head_ce_fwd(h, w, y)
+        p, q = (head.ssm_head_ce_bwd(h, w, y, a.lse, up, fine=fine) for fine in (False, True))
+        assert torch.equal(p["d_h"], q["d_h"]) and torch.equal(p["d_w"], q["d_w"])
+
+
+def test_a_fine_call_that_gives_up_reports_timeout():
+    T, D, V = 300, 72, 700
+    i = _inputs(T, D, V, "bf16", seed=6)
+    h, w, y, up = (i[n].cuda() for n in ("h", "w", "target", "d_loss"))
+    a = head.ssm_head_ce_fwd(h, w, y)
+    ws = torch.empty(head.ssm_head_workspace_size(T, D, V, grads=3, fine=True), dtype=torch.uint8,
+                     device="cuda")
+    g = head.ssm_head_ce_bwd(h, w, y, a.lse, up, ws=ws, fine=True, debug_flags=binding.SSM_DEBUG_NO_WAIT)
+    assert binding.ssm_scan_status(ws) == binding.SSM_ERR_TIMEOUT
+    assert bool(torch.isnan(g["d_h"]).all()) and bool(torch.isnan(g["d_w"]).all())
+    g = head.ssm_head_ce_bwd(h, w, y, a.lse, up, ws=ws, fine=True)
+    assert binding.ssm_scan_status(ws) == binding.SSM_OK
+    _within_fine(g, i, _ce_rows(i), a.lse)
