@@ -25,8 +25,7 @@ constexpr int kNoEntry = 0x7fffffff;        // fills a row's list of entries
 struct HeadState {
   int status;
   int count;     // packed rows
-  float g_top;   // the largest finite |d_loss| of theirs (1 where there is none)
-  float scale;   // what G lacks between the products: g_top tau
+  float scale;   // what G lacks between the products: tau times the largest finite |d_loss| of theirs (1: none)
   int tile;      // columns of a tile of Z
 };
 
@@ -34,7 +33,7 @@ struct HeadRows {  // of a call, on the device
   HeadState* state;
   int* pos;  // [rows]
   int* src;  // [padded rows], -1 past the packed ones
-  float *rl, *rg;  // backward, [padded rows]: lse, d_loss / g_top
+  float *rl, *rg;  // backward, [padded rows]: lse, d_loss over the largest
   __nv_bfloat16* h;  // [planes][padded rows][padded cols]
 };
 

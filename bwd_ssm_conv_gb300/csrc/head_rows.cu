@@ -256,7 +256,6 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
   if (blockIdx.x == 0 && threadIdx.x == 0) {
     r.state->status = bad ? SSM_ERR_INVALID_ARG : SSM_OK;
     r.state->count = all;
-    r.state->g_top = top;
     r.state->scale = top * a.tau;
     r.state->tile = head_tile(a.tiles, all > 0 ? all : 1);
   }
