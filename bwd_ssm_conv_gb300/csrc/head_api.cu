@@ -11,6 +11,7 @@ namespace {
 using namespace ssm;
 
 constexpr long long kMaxTotal = 1LL << 40;  // elements between a tensor's first and last row
+constexpr long long kMaxStride = 1LL << 40;  // bytes between two rows that TMA copies: below this
 constexpr long long kMaxLogits = 1LL << 40;  // rows times words: tiles are counted in 32 bits
 // Bytes of G at a time (a tile's columns at least).  Fewer and larger pieces leave fewer ends of launches with
 // idle SMs: 16384 x 1024 over 32768 words 2.97 ms at 96 MiB, 2.76 at 256, 2.64 at 512, 2.66 at 1024.
@@ -272,7 +273,8 @@ int run(Call c, bool distill, bool backward) {
   for (const int64_t* p : {c.target, c.t_idx})
     if (p && !aligned(p, 8)) return SSM_ERR_INVALID_ARG;
   if (distill && !aligned(c.t_logit, io_size(d.entry_io))) return SSM_ERR_INVALID_ARG;
-  if (c.ld_h > kMaxTotal / d.rows || c.ld_d_h > kMaxTotal / d.rows || c.ld_w > kMaxTotal / d.vocab)
+  if (c.ld_h > kMaxTotal / d.rows || c.ld_d_h > kMaxTotal / d.rows || c.ld_w > kMaxTotal / d.vocab ||
+      c.ld_w >= kMaxStride / (long long)size)
     return SSM_ERR_UNSUPPORTED;
   const int sms = num_sms();
   if (sms <= 0) return SSM_ERR_CUDA;

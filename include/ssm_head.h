@@ -11,7 +11,7 @@
  *                 d_h = G W,  d_W = G^T h
  *
  * Layouts: h and d_h [rows][cols], W [vocab][cols] (io), rows `ld_*` elements apart (0 means cols; at
- * least cols otherwise); d_W [vocab][cols] (io) contiguous; target int64 [rows]; t_idx int64 and t_logit
+ * least cols otherwise, those of W below 2^40 bytes); d_W [vocab][cols] (io) contiguous; target int64 [rows]; t_idx int64 and t_logit
  * (entry_io) [rows][entries], loss, lse and d_loss fp32 [rows], all contiguous.
  *
  * Rows without a loss: a target of ignore_index; a row without an entry.  Their loss, lse and gradient are
