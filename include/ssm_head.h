@@ -11,8 +11,9 @@
  *                 d_h = G W,  d_W = G^T h
  *
  * Layouts: h and d_h [rows][cols], W [vocab][cols] (io), rows `ld_*` elements apart (0 means cols; at
- * least cols otherwise, those of W below 2^40 bytes); d_W [vocab][cols] (io) contiguous; target int64 [rows]; t_idx int64 and t_logit
- * (entry_io) [rows][entries], loss, lse and d_loss fp32 [rows], all contiguous.
+ * least cols otherwise, those of W below 2^40 bytes); d_W [vocab][cols] (io) contiguous; target int64
+ * [rows]; t_idx int64 and t_logit (entry_io) [rows][entries], loss, lse and d_loss fp32 [rows], all
+ * contiguous.
  *
  * Rows without a loss: a target of ignore_index; a row without an entry.  Their loss, lse and gradient are
  * 0 and h is not read there, whatever it holds; they cost no product.  An entry with t_idx below 0 is not
@@ -34,7 +35,8 @@
  * divided by the largest |d_loss|, is rounded to bf16 between the products (2^-8 of each of its values), which
  * gives d_h and d_W an error of the size of their own rounding; with SSM_HEAD_FINE_G it is kept in two bf16 terms
  * (2^-16), which takes twice the time and leaves d_h and d_W with their own rounding.  A few rows
- * (bf16: 2 in the forward, 4 in the backward; fp32: 8) are fp32 arithmetic throughout, G too.
+ * (bf16: 2 in the forward, 4 in the backward; fp32: 8) are fp32 arithmetic throughout, G too, where they lie in the
+ * shared memory of a block: rows (as a power of two) * cols up to 18000 in the forward, 9216 in the backward.
  */
 #ifndef SSM_HEAD_GB300_H
 #define SSM_HEAD_GB300_H
