@@ -8,7 +8,7 @@ import torch
 import head_ref as ref
 from bwd_ssm_conv_gb300 import binding, head
 from head_ref import within
-from test_gpu_head import _ce, _ce_rows, _entries, _inputs, _nan
+from test_gpu_head import DT, _ce, _ce_rows, _check, _distill, _entries, _inputs, _nan
 
 pytestmark = pytest.mark.gpu
 f64 = torch.float64
@@ -220,3 +220,77 @@ def test_a_fine_call_that_gives_up_reports_timeout():
     g = head.ssm_head_ce_bwd(h, w, y, a.lse, up, ws=ws, fine=True)
     assert binding.ssm_scan_status(ws) == binding.SSM_OK
     _within_fine(g, i, _ce_rows(i), a.lse)
+
+
+@pytest.mark.parametrize("T,D,V", [(333, 256, 5003), (1021, 515, 10007), (40, 768, 3001)])
+def test_fp32_products_keep_all_three_terms(T, D, V):
+    """In the 2-norm, where errors of either sign do not add up as in a bound of each value: of G by its terms,
+    the softmax and the targets, 2^-24 (16 + 16) where lse and z / tau are rounded below 32 (uniformly:
+    1.1e-6 over sqrt 3), 2^-22 of the exponential and 3 x 2^-24 of the products left out; 1e-6 in all.  Without
+    either product with the third terms it is 3e-6 to 2e-5.  lse: half a unit, and as much of what is left out
+    of a logit."""
+    i = _inputs(T, D, V, "f32", seed=T)
+    a, g = _ce(i)
+    h, w, y, up = (i[n].cuda() for n in ("h", "w", "target", "d_loss"))
+    some = y != -100
+    z = h.to(f64) @ w.to(f64).t()
+    want = torch.logsumexp(z, 1)
+    assert float(want.abs().max()) < 32
+    assert float((a.lse - want)[some].norm() / want[some].norm()) < 2 * 2.0 ** -24
+    up = torch.where(some, up, 0.0 * up)
+    q = torch.softmax(z, 1)
+    P = torch.zeros_like(q)
+    P[torch.arange(T).cuda(), y.clamp(min=0)] = 1.0
+    up = up.to(f64)[:, None]
+    for n, left, right in (("d_h", lambda G: G, w), ("d_w", lambda G: G.t(), h)):
+        right = right.to(f64)
+        want = left((q - P) * up) @ right
+        size = torch.sqrt((left(q * up) @ right).norm() ** 2 + (left(P * up) @ right).norm() ** 2)
+        assert float((g[n] - want).norm() / size) < 1e-6, n
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 40])
+def test_a_loss_near_zero_keeps_its_digits(T, io):
+    """Two words, logits 32 and 32 - d that are exact: the loss is log(1 + exp(-d)), formed from one sum next to 1
+    (2^-24), an exponential (2^-22 of it and 2^-24 of its argument, 12) and a logarithm.  lse - z in fp32 is a
+    multiple of 2^-18, which the losses here are a third of that or more away from."""
+    losses = []
+    for eighths in range(72, 98):
+        h = torch.zeros(T, 8, dtype=DT[io])
+        h[:, 0] = 4
+        w = torch.zeros(2, 8, dtype=DT[io])
+        w[0, 0], w[1, 0] = 8, 8 - eighths / 32
+        assert 4 * float(w[1, 0]) == 32 - eighths / 8
+        want = math.log1p(math.exp(-eighths / 8))
+        if not 1 / 3 < want * 2 ** 18 % 1 < 2 / 3:
+            continue
+        losses.append(want)
+        a = head.ssm_head_ce_fwd(h.cuda(), w.cuda(), torch.zeros(T, dtype=torch.long).cuda())
+        assert float((a.loss.to(f64) - want).abs().max()) < 2.0 ** -24 + 2.0 ** -19 * want
+    assert len(losses) >= 6 and min(losses) < 2e-5 and max(losses) > 1e-4
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 4])
+@pytest.mark.parametrize("D,V", [(72, 700), (515, 1001), (1030, 40), (2304, 65)])
+def test_a_few_bf16_rows_keep_G_in_fp32(T, D, V):
+    """The bounds of fp32 operands, for what is stored in bf16."""
+    i = _inputs(T, D, V, "bf16", seed=T * D, ignored=0.0)
+    a, g = _ce(i)
+    rows = _ce_rows(i)
+    want, bound = ref.head_bwd(i["h"].float(), i["w"].float(), rows[0], rows[1], a.lse.cpu(), i["d_loss"])
+    for n, v, e in zip(("d_h", "d_w"), want, bound):
+        within(n, g[n], v, e)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [2, 70])
+@pytest.mark.parametrize("tau", [1e-6, 1e-4, 1e4, 1e6])
+def test_temperatures_up_to_their_limits(T, tau, io):
+    """Logits, the teacher's too, of a few temperatures."""
+    i = _inputs(T, 72, 300, io, seed=11)
+    i["h"] = (i["h"].float() * tau).to(DT[io])
+    i["t_idx"], t = _entries(T, 300, 9, seed=5)
+    i["t_logit"] = t * tau
+    exact = float(torch.tensor(tau, dtype=torch.float32))
+    _check(*_distill(i, tau), i, ref._p_of(i["t_idx"], i["t_logit"], exact, 300), exact)
