@@ -167,13 +167,18 @@ class Head:
                       W=(d_model ** -0.5 * torch.randn(vocab, d_model, generator=g)).to(device))
 
     def embed(self, tokens):
-        return self.p["W"].to(self.io)[tokens]
+        return self.p["W"][tokens].to(self.io)
 
-    def forward(self, h, residual, target, teacher=None, temperature=1.0):
+    def weights(self):
+        """A copy of W in the activations' type."""
+        return self.p["W"].to(self.io)
+
+    def forward(self, h, residual, target, teacher=None, temperature=1.0, W=None):
         """The loss of each row of h [...][d_model] and what backward needs.  target [...]: the next
-        tokens, -100 where there is none; or teacher: (t_idx, t_logit) of each row."""
+        tokens, -100 where there is none; or teacher: (t_idx, t_logit) of each row.  W: weights(), where more
+        than one call takes it."""
         a = ssm.ssm_add_layer_norm_fwd(h, self.p["w"], self.p["b"], residual, res_dtype=torch.float32)
-        W = self.p["W"].to(self.io)
+        W = self.weights() if W is None else W
         if teacher is None:
             r = ssm.ssm_head_ce_fwd(a.out, W, target)
         else:
@@ -250,12 +255,12 @@ def lm_step(blocks, head, tokens, save8=True, lr=0.0, teacher=None, temperature=
 def score(blocks, head, tokens):
     """The log-probability of each token of tokens [n_s][L] after the first, a token at a time."""
     n, L = tokens.shape
-    caches, out = [b.new_cache(n) for b in blocks], []
+    caches, W, out = [b.new_cache(n) for b in blocks], head.weights(), []
     for t in range(L - 1):
         x, stream = head.embed(tokens[:, t]), None
         for b, c in zip(blocks, caches):
             x, stream = b.decode(x, stream, c)
-        loss, _ = head.forward(x, stream, tokens[:, t + 1].contiguous())
+        loss, _ = head.forward(x, stream, tokens[:, t + 1].contiguous(), W=W)
         out.append(-loss)
     return torch.stack(out, 1)
 

@@ -1,6 +1,8 @@
-"""The example's language model as a whole: one step of it against 64-bit autograd of the same model."""
+"""The example's language model as a whole: one step of it against 64-bit autograd of the same model, and what
+embedding and scoring copy."""
 import pytest
 import torch
+from torch.utils._python_dispatch import TorchDispatchMode
 
 from test_gpu_block_example import SHAPE, _reference, mamba_block
 
@@ -50,3 +52,30 @@ def test_a_step_moves_every_parameter_by_its_gradient(distil):
         for n, v in m.p.items():
             moved = (was[n].to(f64) - v.to(f64)).cpu()
             assert float((moved - leaf[n].grad).norm() / leaf[n].grad.norm()) < 5e-4, (i, n)
+
+
+class _Copies(TorchDispatchMode):
+    """How many operations read or write a whole tensor of ``numel`` elements to make another of another type."""
+
+    def __init__(self, numel):
+        super().__init__()
+        self.numel, self.n = numel, 0
+
+    def __torch_dispatch__(self, func, types, args=(), kwargs=None):
+        out = func(*args, **(kwargs or {}))
+        if func is torch.ops.aten._to_copy.default and args[0].numel() == self.numel:
+            self.n += 1
+        return out
+
+
+def test_embedding_and_scoring_do_not_copy_the_weights_for_every_token():
+    blocks = [mamba_block.Block(SHAPE, seed=0)]
+    head = mamba_block.Head(SHAPE.d_model, VOCAB, seed=4)
+    tokens = _tokens(2, 9).cuda()
+    assert torch.equal(head.embed(tokens), head.p["W"].to(head.io)[tokens])
+    with _Copies(head.p["W"].numel()) as copies:
+        head.embed(tokens)
+    assert copies.n == 0
+    with _Copies(head.p["W"].numel()) as copies:
+        mamba_block.score(blocks, head, tokens)
+    assert copies.n == 1
