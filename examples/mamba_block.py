@@ -238,7 +238,7 @@ def lm_step(blocks, head, tokens, save8=True, lr=0.0, teacher=None, temperature=
         x, stream, k = b.forward(x, stream, save8)
         kept.append(k)
     loss, last = head.forward(x, stream, target, teacher, temperature)
-    rows = tokens.numel() if teacher is not None else tokens.shape[0] * (tokens.shape[1] - 1)
+    rows = tokens.numel() if teacher is not None else max(1, tokens.shape[0] * (tokens.shape[1] - 1))
     d_x, d_stream, g_head = head.backward(torch.full_like(loss, 1.0 / rows), last)
     for b, k in zip(reversed(blocks), reversed(kept)):
         d_x, d_stream, g = b.backward(d_x, d_stream, k)
@@ -255,14 +255,15 @@ def lm_step(blocks, head, tokens, save8=True, lr=0.0, teacher=None, temperature=
 def score(blocks, head, tokens):
     """The log-probability of each token of tokens [n_s][L] after the first, a token at a time."""
     n, L = tokens.shape
-    caches, W, out = [b.new_cache(n) for b in blocks], head.weights(), []
+    caches, W = [b.new_cache(n) for b in blocks], head.weights()
+    out = torch.empty(n, L - 1, device=tokens.device)
     for t in range(L - 1):
         x, stream = head.embed(tokens[:, t]), None
         for b, c in zip(blocks, caches):
             x, stream = b.decode(x, stream, c)
         loss, _ = head.forward(x, stream, tokens[:, t + 1].contiguous(), W=W)
-        out.append(-loss)
-    return torch.stack(out, 1)
+        out[:, t] = -loss
+    return out
 
 
 def main():

@@ -79,3 +79,18 @@ def test_embedding_and_scoring_do_not_copy_the_weights_for_every_token():
     with _Copies(head.p["W"].numel()) as copies:
         mamba_block.score(blocks, head, tokens)
     assert copies.n == 1
+
+
+@pytest.mark.parametrize("save8", [False, True])
+def test_sequences_of_one_token(save8):
+    """They have no next token: no scores, no loss, and nothing moves."""
+    blocks = [mamba_block.Block(SHAPE, seed=0)]
+    head = mamba_block.Head(SHAPE.d_model, VOCAB, seed=4)
+    tokens = _tokens(3, 1).cuda()
+    scores = mamba_block.score(blocks, head, tokens)
+    assert scores.shape == (3, 0) and scores.dtype == torch.float32 and scores.is_cuda
+    before = [{k: v.clone() for k, v in m.p.items()} for m in (*blocks, head)]
+    assert mamba_block.lm_step(blocks, head, tokens, save8=save8, lr=1.0) == 0.0
+    for m, was in zip((*blocks, head), before):
+        for n, v in m.p.items():
+            assert torch.equal(v, was[n]), n
