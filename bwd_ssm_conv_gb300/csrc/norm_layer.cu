@@ -6,7 +6,7 @@
 // Memory bounds it; with two sums of a row one after the other it is the loads in flight that have to cover
 // them, so rows of up to 8192 columns are copied ahead to shared memory (kRing), which the RMSNorm's forward with
 // its one sum goes without.  GB300: 32768 x 768 bf16 with an fp32 stream and both saved 48 us (45 at the rate of a
-// copy), 16384 x 768 all bf16 24 (20).  Odd widths (single columns, no copies ahead): 2047 x 1003 fp32 9.5 us,
+// copy), 16384 x 1024 all bf16 24 (20).  Odd widths (single columns, no copies ahead): 2047 x 1003 fp32 9.5 us,
 // bound by instructions, a load and a store for every 4 bytes.
 #include "norm_add.cuh"
 

@@ -4,7 +4,7 @@
 //   d_scale = sum_rows r x
 // A row is read once, copied ahead to shared memory, and its two sums are formed together over its threads.
 // Memory bounds it.  GB300: 32768 x 768 bf16 with an fp32 stream, d_s and d_scale 77 us (67 at the rate of a copy)
-// and 7 us for the column sums' join; 16384 x 768 all bf16 33 (25) and 7; 2047 x 1003 fp32 in single columns
+// and 7 us for the column sums' join; 16384 x 1024 all bf16 33 (25) and 7; 2047 x 1003 fp32 in single columns
 // 14.7 and 5, bound by instructions.
 // Each pair of types in a file of its own, as they take the compiler a minute each.
 #include "norm_add_bwd.cuh"
