@@ -135,8 +135,8 @@ struct HeadCut {
 };
 // The sums of the vocabulary's tiles, stats [2 tiles][padded rows], and the entries' logits.
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const HeadLists& lists, float2* stats, float* zt,
-                               int sms, cudaStream_t st);
+                               const HeadRows& r, const HeadLists& lists, const HeadTiles& tiles,
+                               float2* stats, float* zt, int sms, cudaStream_t st);
 // G of the words v0 .. v0 + n (n a multiple of 256; 0 past the vocabulary): g [terms][padded rows][n].
 cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
                              const HeadRows& r, const HeadLists& lists, __nv_bfloat16* g, int v0, int n,

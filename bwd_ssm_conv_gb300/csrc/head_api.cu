@@ -321,7 +321,7 @@ int run(Call c, bool distill, bool backward) {
   const HeadMatrix w = copy_w ? HeadMatrix{w_out, d.vocab, Dp, (long long)d.vocab * Dp, d.cols} :
                                 HeadMatrix{(const __nv_bfloat16*)c.w, d.vocab, c.ld_w, 0, d.cols};
   if (!backward) {
-    SSM_DO(launch_head_logits(d, h, w, r, lists, stats, zt, sms, st));
+    SSM_DO(launch_head_logits(d, h, w, r, lists, p.tiles, stats, zt, sms, st));
     SSM_DO(launch_head_loss(d, stats, p.n_stats, zt, lists, r, c.loss, c.lse_out, sms, st));
     return SSM_OK;
   }

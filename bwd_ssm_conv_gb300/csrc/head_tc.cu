@@ -63,12 +63,15 @@ constexpr uint32_t kTurn = kSumWarps * 32 * 33 * 4, kSmem = kAtTurn + 1024;
 // the sum for each 16 terms.  Errors of lse and of d_W against 64 bits (plain fp32: 2e-7, 6.6e-7 and up):
 //   fp32, 1021 x 515 over 10007 words: every 2 stages 3.2e-7 and 6.4e-7, every stage 0.7e-7 and 3.5e-7, for
 //     5 % of the time
-//   bf16, lse alone (G is rounded to bf16): all at once 768 columns 5.8e-7, 1024 7.4e-7, 2048 1.5e-6; every 12
-//     stages 4.8e-7 to 5.8e-7, which slows 1024 columns down
+//   bf16, lse and the loss (medians over random sizes of 700 - 1024 and 1025 - 2048 columns; plain fp32 1.9e-7 and
+//     3e-7): every 16 stages 5.9e-7 and 6.8e-7, 8 3.2e-7 and 3.5e-7, 4 1.6e-7 and 1.8e-7.  Every 8 stages the logits
+//     of 7370 x 768 over 50000 words take 326 us instead of 303, every 4 387; with few tiles (as where their widths
+//     are chosen) 4 cost nothing (64 x 768 over 32768 words 28.9, 1021 x 512 over 10000 29.0 at either).
+//   G of bf16 operands is rounded far more coarsely: its logits every 16 stages, as one sum up to 1024 columns.
 // The sums of bf16 gradients, over any number of rows or words, are emptied every 64 stages (4096 terms), which
 // leaves 1.5e-5 of a sum of one sign, 1/128 of the result's own rounding and less; all at once 65536 rows lost 2.4e-4.
 // It costs 0.4 % at most (8192 x 768 over 50000 words 1493 -> 1499 us; every 16 stages 1523).
-template <int USE, int PLANES> constexpr int kSegment = PLANES > 1 ? 1 : USE == kOut ? 64 : 16;
+constexpr int kSegmentLogits = 8, kSegmentFew = 4, kSegmentGrad = 16, kSegmentOut = 64;
 
 // A product of a launch.
 struct Job {
@@ -96,6 +99,7 @@ struct TcArgs {
   int jobs;
   HeadState* state;
   int no_wait;
+  int segment;  // bf16 operands: stages between two emptyings
   // kLogits, kGrad
   float scale;         // log2(e) / tau
   float inv_tau, inv_tau_rest;
@@ -440,7 +444,8 @@ struct Units {
 // SEG: sums are taken out in between (without it the kernel has half the registers).
 template <int USE, int PLANES, bool SEG>
 __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_constant__ TcArgs a) {
-  constexpr int S = kSlots, kSeg = SEG ? kSegment<USE, PLANES> : 1 << 30;
+  constexpr int S = kSlots;
+  const int kSeg = !SEG ? 1 << 30 : PLANES > 1 ? 1 : a.segment;
   extern __shared__ unsigned char raw[];
   __shared__ uint64_t here[S], there[S], empty[S], ready[4], drained[4], last;
   __shared__ uint32_t tbase;
@@ -730,7 +735,7 @@ cudaError_t launch(const TcArgs& t, int sms, cudaStream_t st) {
 template <int USE> cudaError_t launch(const ssm_head_desc& d, const TcArgs& t, int sms, cudaStream_t st) {
   if (d.io == SSM_F32) return launch<USE, 3, true>(t, sms, st);
   for (int j = 0; j < t.jobs; j++)
-    if (t.job[j].per_split > kSegment<USE, 1>) return launch<USE, 1, true>(t, sms, st);
+    if (t.job[j].per_split > t.segment) return launch<USE, 1, true>(t, sms, st);
   return launch<USE, 1, false>(t, sms, st);
 }
 
@@ -772,9 +777,10 @@ bool logits_job(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w
 }  // namespace
 
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
-                               const HeadRows& r, const HeadLists& lists, float2* stats, float* zt,
-                               int sms, cudaStream_t st) {
+                               const HeadRows& r, const HeadLists& lists, const HeadTiles& tiles,
+                               float2* stats, float* zt, int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, lists);
+  t.segment = tiles.words ? kSegmentFew : kSegmentLogits;
   if (!logits_job(d, h, w, 0, d.vocab, t.job[0])) return cudaErrorInvalidValue;
   t.stats = stats;
   t.ld_stats = h.rows;
@@ -787,6 +793,7 @@ cudaError_t launch_head_grad(const ssm_head_desc& d, const HeadMatrix& h, const 
                              int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, lists);
   if (!logits_job(d, h, w, v0, n, t.job[0])) return cudaErrorInvalidValue;
+  t.segment = kSegmentGrad;
   t.v0 = v0;
   t.rl = r.rl;
   t.rg = r.rg;
@@ -802,6 +809,7 @@ cudaError_t launch_head_out(const ssm_head_desc& d, const HeadMatrix& g, const H
                             bool add, int sms, cudaStream_t st) {
   TcArgs t = args_of(d, r, {});
   t.jobs = 0;
+  t.segment = kSegmentOut;
   const int planes = planes_of(d), terms = head_g_terms(d), padded = pad8(d.cols);
   const size_t size = d.io == SSM_F32 ? 4 : 2;
   if (o.d_w) {

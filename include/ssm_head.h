@@ -30,8 +30,8 @@
  * Arithmetic: products on the tensor cores with fp32 sums, fp32 operands as three bf16 terms each
  * (six products, which leave out 2^-24 of a product and less).  The tensor cores truncate as they
  * add, up to 2^-23 of the sum for each 16 terms: sums are taken out every 64 terms with fp32 operands,
- * with bf16 ones those of the logits every 1024 and those of the gradients every 4096, and added with rounding
- * to nearest, so that long sums lose no more than short ones.  With bf16 operands G,
+ * with bf16 ones those of the logits every 512 or 256 (the backward's every 1024) and those of the gradients
+ * every 4096, and added with rounding to nearest, so that long sums lose no more than short ones.  With bf16 operands G,
  * divided by the largest |d_loss|, is rounded to bf16 between the products (2^-8 of each of its values), which
  * gives d_h and d_W an error of the size of their own rounding; with SSM_HEAD_FINE_G it is kept in two bf16 terms
  * (2^-16), which takes twice the time and leaves d_h and d_W with their own rounding.  A few rows

@@ -27,8 +27,8 @@ def _gradients(z, target, up, h, w):
 
 def test_logits_of_many_columns_are_alike_in_both_directions():
     """65536 products of one sign: logits of 1160.  The tensor cores lose up to 2^-23 of what they have
-    summed with each 16 products, 64 times between two emptyings (1024 columns): 2^-18 of a logit, 4.4e-3, nearly all of
-    which is that of lse too, as both are the same sums.  Left in one sum the 4096 additions of the backward
+    summed with each 16 products, 64 times at most between two emptyings (1024 columns): 2^-18 of a logit, 4.4e-3,
+    part of which is that of lse too.  Left in one sum the 4096 additions of the backward
     alone lost 0.3.  Besides G and the result are rounded to bf16, 2^-8 of their terms in all."""
     T, D, V = 70, 65536, 300
     g = torch.Generator(device="cuda").manual_seed(3)
@@ -294,3 +294,19 @@ def test_temperatures_up_to_their_limits(T, tau, io):
     i["t_logit"] = t * tau
     exact = float(torch.tensor(tau, dtype=torch.float32))
     _check(*_distill(i, tau), i, ref._p_of(i["t_idx"], i["t_logit"], exact, 300), exact)
+
+
+@pytest.mark.parametrize("T,V,additions", [(70, 600, 16), (8192, 16000, 32)])
+@pytest.mark.parametrize("D", [768, 1024, 2040])
+def test_bf16_logits_are_as_good_as_fp32_sums(T, V, additions, D):
+    """Products of one sign.  An addition to a sum in tensor memory loses a quarter of 2^-23 of it on average, and
+    the sum grows evenly, so that n of them between two emptyings lose n / 2 x 2^-25 (16 with few tiles, 32 with
+    many); half a unit of lse, and one of the sums outside.  Of 64 additions 5.7e-7 to 6.3e-7 were lost."""
+    g = torch.Generator(device="cuda").manual_seed(D)
+    h = torch.rand(T, D, generator=g, device="cuda").add(1).bfloat16()
+    w = torch.rand(V, D, generator=g, device="cuda").add(1).mul(2.0 ** -6).bfloat16()
+    y = torch.randint(V, (T,), generator=g, device="cuda")
+    a = head.ssm_head_ce_fwd(h, w, y)
+    want = torch.cat([torch.logsumexp(p.to(f64) @ w.to(f64).t(), 1) for p in h.split(1024)])
+    off = float((a.lse.to(f64) - want).norm() / want.norm())
+    assert off < additions / 2 * 2.0 ** -25 + 3 * 2.0 ** -25, off
