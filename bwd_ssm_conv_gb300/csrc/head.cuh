@@ -73,9 +73,11 @@ __host__ __device__ inline int head_tile(const HeadTiles& t, int rows) {
   return best;
 }
 
-// bf16 terms of G between the products.
+// bf16 terms of G between the products.  With bf16 operands a second one leaves d_h and d_W with their own rounding.
+// A tile's rows get it in any case, as reading W and writing d_W is most of their time (768 columns, 32768 words,
+// us with one and two: 5 to 64 rows 62 and 69, 256 69 and 81, 512 86 and 118, 1024 123 and 192).
 inline int head_g_terms(const ssm_head_desc& d) {
-  return d.io == SSM_F32 ? 3 : d.flags & SSM_HEAD_FINE_G ? 2 : 1;
+  return d.io == SSM_F32 ? 3 : d.rows <= kHeadTile || d.flags & SSM_HEAD_FINE_G ? 2 : 1;
 }
 inline int pad8(int n) { return (n + 7) / 8 * 8; }
 inline long long pad_rows(long long rows) { return (rows + 63) / 64 * 64; }

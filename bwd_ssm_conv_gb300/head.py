@@ -94,10 +94,9 @@ def ssm_head_ce_bwd(h, w, target, lse, d_loss, ignore_index=-100, want_dh=True, 
     {"d_h", "d_w"} in the type of h and w (None where not wanted).  ``out`` = a dict of preallocated
     results with the same keys, optional.
 
-    ``fine`` (bf16): the gradient of the logits, which is rounded to bf16 between the products otherwise, is
-    kept to 16 bits in two terms, so that the results have no error but their own rounding; the backward
-    takes twice the time.  Up to 4 rows of up to 2304 columns, and fp32
-    rows, are as exact in either case."""
+    ``fine`` (bf16, more than 256 rows): the gradient of the logits, which is rounded to bf16 between the products
+    otherwise, is kept to 16 bits in two terms, so that the results have no error but their own rounding; the
+    backward takes twice the time.  Up to 256 rows, and fp32 ones, are as exact in either case."""
     into = out if out is None else (out["d_h"], out["d_w"])
     r = _calls().head_ce_bwd(h, w, target, ignore_index, lse, d_loss, want_dh, want_dw, ws, into, stream,
                              debug_flags | SSM_HEAD_FINE_G if fine else debug_flags)

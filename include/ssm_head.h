@@ -33,8 +33,9 @@
  * with bf16 ones those of the logits every 512 or 256 (the backward's every 1024) and those of the gradients
  * every 4096, and added with rounding to nearest, so that long sums lose no more than short ones.  With bf16 operands G,
  * divided by the largest |d_loss|, is rounded to bf16 between the products (2^-8 of each of its values), which
- * gives d_h and d_W an error of the size of their own rounding; with SSM_HEAD_FINE_G it is kept in two bf16 terms
- * (2^-16), which takes twice the time and leaves d_h and d_W with their own rounding.  A few rows
+ * gives d_h and d_W an error of the size of their own rounding; up to 256 rows, and with SSM_HEAD_FINE_G any
+ * number, it is kept in two bf16 terms (2^-16), which leaves d_h and d_W with their own rounding and takes twice the
+ * time where rows are many.  A few rows
  * (bf16: 2 in the forward, 4 in the backward; fp32: 8) are fp32 arithmetic throughout, G too, where they lie in the
  * shared memory of a block: rows (as a power of two) * cols up to 18000 in the forward, 9216 in the backward.
  */
@@ -63,7 +64,7 @@ typedef struct {
   int entry_io;   /* head_distill: ssm_dtype of t_logit */
   float temperature;      /* head_distill: tau > 0, finite */
   long long ignore_index; /* head_ce: the target of a row without a loss */
-  unsigned flags; /* SSM_HEAD_FINE_G: the backward of bf16 operands keeps G in two terms (no effect elsewhere);
+  unsigned flags; /* SSM_HEAD_FINE_G: the backward of more than 256 bf16 rows keeps G in two terms as that of fewer;
                      ssm.h's SSM_DEBUG_NO_WAIT, for tests of the error path only: the warps that take
                      the sums out give up at once, as if the bound of their wait had run out (the kernels of
                      a few rows wait for nothing) */
