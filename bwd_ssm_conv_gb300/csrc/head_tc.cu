@@ -22,9 +22,9 @@
 //
 // GB300, us of a launch by itself and its rate (cuBLAS's bf16 product of 8192^3 on this GPU: 1908 TFLOP/s):
 //                                  kLogits        kGrad          kOut
-//   7370 x 768, 50000 words bf16   281  2010      2 x 165  1720  2 x 327  1730
-//   16384 x 1024, 32768 bf16       524  2100      2 x 292  1880  2 x 585  1880
-//   3891 x 768, 32768 bf16         104  1880      133      1470  220      1780
+//   7370 x 768, 50000 words bf16   292  1940      2 x 164  1730  2 x 333  1700
+//   16384 x 1024, 32768 bf16       537  2050      2 x 298  1850  2 x 593  1850
+//   3891 x 768, 32768 bf16         114  1720      132      1480  220      1780
 //   684 x 515, 10007 fp32           40  1030       50       850   87       970  (six products counted)
 //   300 x 256, 5003 fp32            14   330       18       260   18       510
 // G in two terms (SSM_HEAD_FINE_G): a stage for each, the smaller one first, with the other operand copied again;
@@ -64,9 +64,10 @@ constexpr uint32_t kTurn = kSumWarps * 32 * 33 * 4, kSmem = kAtTurn + 1024;
 //   fp32, 1021 x 515 over 10007 words: every 2 stages 3.2e-7 and 6.4e-7, every stage 0.7e-7 and 3.5e-7, for
 //     5 % of the time
 //   bf16, lse and the loss (medians over random sizes of 700 - 1024 and 1025 - 2048 columns; plain fp32 1.9e-7 and
-//     3e-7): every 16 stages 5.9e-7 and 6.8e-7, 8 3.2e-7 and 3.5e-7, 4 1.6e-7 and 1.8e-7.  Every 8 stages the logits
-//     of 7370 x 768 over 50000 words take 326 us instead of 303, every 4 387; with few tiles (as where their widths
-//     are chosen) 4 cost nothing (64 x 768 over 32768 words 28.9, 1021 x 512 over 10000 29.0 at either).
+//     3e-7): every 16 stages 5.9e-7 and 6.8e-7, 8 3.2e-7 and 3.5e-7, 4 1.6e-7 and 1.8e-7.  Forward
+//     of 7370 x 768 over 50000 words at 16, 8 and 4: 293, 306 and 347 us, 16384 x 1024 over 32768 590, 601 and 664;
+//     with few tiles (as where their widths are chosen) 4 cost nothing (64 x 768 over 32768 words 29.0, 29.0 and
+//     27.3, 1021 x 512 over 10000 28.2, 29.0 and 27.0).
 //   G of bf16 operands is rounded far more coarsely: its logits every 16 stages, as one sum up to 1024 columns.
 // The sums of bf16 gradients, over any number of rows or words, are emptied every 64 stages (4096 terms), which
 // leaves 1.5e-5 of a sum of one sign, 1/128 of the result's own rounding and less; all at once 65536 rows lost 2.4e-4.
@@ -644,11 +645,15 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
         }
         seg++;
       } else {
+        // The first stretch of a sum is loaded in place, which is half of what these warps would do for sums of two
+        // (fp32, with one for each stage, is 3 % slower so).
         float acc[4][32];
+        if constexpr (PLANES > 1) {
 #pragma unroll
-        for (int c = 0; c < 4; c++)
+          for (int c = 0; c < 4; c++)
 #pragma unroll
-          for (int i = 0; i < 32; i++) acc[c][i] = 0.0f;
+            for (int i = 0; i < 32; i++) acc[c][i] = 0.0f;
+        }
         for (int it = 0; it < iters && ok; it += kSeg, seg++) {
           ok = wait_for(&ready[seg & acc_mask], (seg >> acc_log) & 1, &bad);
           __syncwarp();
@@ -658,10 +663,14 @@ __global__ void __launch_bounds__(kThreads, 1) head_tc_kernel(const __grid_const
 #pragma unroll
           for (int c = 0; c < 4; c++) {
             if (c >= chunks) break;
-            float v[32];
-            tmem_ld32(t + 32 * c, v);
+            if (PLANES == 1 && it == 0) {
+              tmem_ld32(t + 32 * c, acc[c]);
+            } else {
+              float v[32];
+              tmem_ld32(t + 32 * c, v);
 #pragma unroll
-            for (int i = 0; i < 32; i++) acc[c][i] += v[i];
+              for (int i = 0; i < 32; i++) acc[c][i] += v[i];
+            }
           }
           tmem_fence_before_sync();
           __syncwarp();
