@@ -53,6 +53,18 @@ inline int head_part_shift(int vocab) {  // a part's words, as a power of two
   return shift;
 }
 
+// Sums of the exponentials 2^((z - top) scale) of a row's words, without the one of the largest logit itself,
+// which is 1: next to it the others of a loss near 0 would lose their digits.
+struct HeadSum {
+  float top, rest;
+};
+__device__ __forceinline__ HeadSum join(const HeadSum& a, const HeadSum& b, float scale) {
+  const bool second = b.top > a.top;
+  const HeadSum &hi = second ? b : a, &lo = second ? a : b;
+  const float f = ex2((lo.top - (hi.top == -INFINITY ? 0.0f : hi.top)) * scale);  // 0 where lo has no words
+  return {hi.top, hi.rest + fmaf(f, lo.rest, f)};
+}
+
 // Z's tiles are 256, 192 or 128 words wide: what takes the fewest rounds of the pairs of CTAs, in time, for the
 // rows that count.
 struct HeadTiles {
@@ -135,7 +147,7 @@ struct HeadMatrix {  // [planes][rows][cols], rows ld elements apart
 struct HeadCut {
   int tile_n, splits, per;
 };
-// The sums of the vocabulary's tiles, stats [2 tiles][padded rows], and the entries' logits.
+// The sums of the vocabulary's tiles, stats [2 tiles][padded rows] (HeadSum), and the entries' logits.
 cudaError_t launch_head_logits(const ssm_head_desc& d, const HeadMatrix& h, const HeadMatrix& w,
                                const HeadRows& r, const HeadLists& lists, const HeadTiles& tiles,
                                float2* stats, float* zt, int sms, cudaStream_t st);

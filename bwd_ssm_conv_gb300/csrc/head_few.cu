@@ -196,7 +196,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
 
   constexpr int kSame = Spread<R>::kSame;
   const int mine = lane / kSame;
-  float top = -INFINITY, total = 0.0f;
+  HeadSum sum{-INFINITY, 0.0f};
   for (int w0 = from; w0 < to; w0 += kWords) {
     float d[kWords][R] = {};
     for (int c0 = 0; c0 < padded; c0 += 256 * batch.U) {
@@ -206,20 +206,13 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
 #pragma unroll
     for (int i = 0; i < kWords; i++) words[i] = min(w0 + kWords + i, to - 1);
     const float z = Spread<R>::over_lanes(d);
-    if (w0 + mine / R < to && lane % kSame == 0) {
-      const float above = fmaxf(top, z), base = above == -INFINITY ? 0.0f : above;
-      total = total * ex2((top - base) * a.scale) + ex2((z - base) * a.scale);
-      top = above;
-    }
+    if (w0 + mine / R < to && lane % kSame == 0) sum = join(sum, {z, 0.0f}, a.scale);
   }
   // over the lanes of a row, then the warps
 #pragma unroll
-  for (int off = 16; off >= R * kSame; off >>= 1) {
-    const float t = __shfl_xor_sync(0xffffffffu, top, off), u = __shfl_xor_sync(0xffffffffu, total, off);
-    const float above = fmaxf(top, t), base = above == -INFINITY ? 0.0f : above;
-    total = total * ex2((top - base) * a.scale) + u * ex2((t - base) * a.scale);
-    top = above;
-  }
+  for (int off = 16; off >= R * kSame; off >>= 1)
+    sum = join(sum, {__shfl_xor_sync(0xffffffffu, sum.top, off), __shfl_xor_sync(0xffffffffu, sum.rest, off)},
+               a.scale);
   // the entries' logits, from the last warp on, which has the fewest words
   for (long long i = warps - 1 - me; i < a.rows * a.entries; i += warps) {
     const int row = (int)(i / a.entries);
@@ -238,17 +231,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) head_few_kernel(const 
     if (lane == 0) a.zt[i] = v;
   }
   float2* sums = reinterpret_cast<float2*>(h + R * padded);
-  if (mine < R && lane % kSame == 0) sums[warp * R + mine] = make_float2(top, total);
+  if (mine < R && lane % kSame == 0) sums[warp * R + mine] = make_float2(sum.top, sum.rest);
   __syncthreads();
   if (threadIdx.x < R && (int)threadIdx.x < a.rows) {
-    top = -INFINITY, total = 0.0f;
+    sum = {-INFINITY, 0.0f};
     for (int w = 0; w < kWarps; w++) {
       const float2 v = sums[w * R + threadIdx.x];
-      const float above = fmaxf(top, v.x), base = above == -INFINITY ? 0.0f : above;
-      total = total * ex2((top - base) * a.scale) + v.y * ex2((v.x - base) * a.scale);
-      top = above;
+      sum = join(sum, {v.x, v.y}, a.scale);
     }
-    a.stats[blockIdx.x * a.ld_stats + threadIdx.x] = make_float2(top, total);
+    a.stats[blockIdx.x * a.ld_stats + threadIdx.x] = make_float2(sum.top, sum.rest);
   }
 }
 

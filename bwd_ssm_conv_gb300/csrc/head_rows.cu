@@ -309,13 +309,6 @@ __global__ void __launch_bounds__(kRowThreads) head_rows_kernel(const RowsArgs a
 }
 
 // ---- loss -------------------------------------------------------------------------------------------
-struct Sum {  // of the exponentials 2^((z - top) scale)
-  float top, sum;
-};
-__device__ __forceinline__ Sum join(const Sum& a, const Sum& b, float scale) {
-  const float top = fmaxf(a.top, b.top), at = top == -INFINITY ? 0.0f : top;
-  return {top, a.sum * ex2((a.top - at) * scale) + b.sum * ex2((b.top - at) * scale)};
-}
 // A block of 1024 threads joins X rows' sums: 1024 / X slices of the tiles, each in order, then the slices,
 // a few per lane of a row's warp in order, then a tree.  X is 32, or 4 where that many rows do not fill the
 // SMs and the chain of loads is what counts.  4096 rows of 32768 words 9 us, 1021 of 10007 6 (GB300).
@@ -334,14 +327,14 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const float2* stats, in
   const int x = threadIdx.x % X, y = threadIdx.x / X;
   const long long first = (long long)blockIdx.x * X;
   const int pos = first + x < rows ? r.pos[first + x] : kIgnored;
-  Sum s{-INFINITY, 0.0f};
+  HeadSum s{-INFINITY, 0.0f};
   if (pos >= 0)
 #pragma unroll 4
     for (int i = y; i < n_stats; i += Y) {
       const float2 v = stats[i * ld + pos];
       s = join(s, {v.x, v.y}, scale);
     }
-  part[y][x] = make_float2(s.top, s.sum);
+  part[y][x] = make_float2(s.top, s.rest);
   __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const long long row = first + warp;  // a warp per row from here
@@ -355,12 +348,13 @@ __global__ void __launch_bounds__(1024) head_loss_kernel(const float2* stats, in
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) {
     // the same order in both lanes
-    const Sum o{__shfl_xor_sync(0xffffffffu, s.top, off), __shfl_xor_sync(0xffffffffu, s.sum, off)};
+    const HeadSum o{__shfl_xor_sync(0xffffffffu, s.top, off),
+                    __shfl_xor_sync(0xffffffffu, s.rest, off)};
     s = lane & off ? join(o, s, scale) : join(s, o, scale);
   }
   const int at = r.pos[row];
-  // loss from distances to the largest logit: a loss near 0 keeps its digits
-  const float log_sum = logf(s.sum);
+  // loss from distances to the largest logit and the sum beside it: a loss near 0 keeps its digits
+  const float log_sum = log1pf(s.rest);
   float l = 0.0f;
   if (at >= 0)
     for (int j = lane; j < entries; j += 32) {

@@ -1,6 +1,6 @@
 // head_tc.cu -- the head's products on the tensor cores.  One kernel, three uses:
 //   kLogits  Z = h W^T, of which a tile leaves only what its row needs: the maximum, the sum of the
-//            exponentials below it, and the logits of the row's entries
+//            exponentials beside it, and the logits of the row's entries
 //   kGrad    Z again, turned into G = (softmax - p) d_loss, a piece of the vocabulary at a time
 //   kOut     d_h = G W (sums over the vocabulary), d_W = G^T h (sums over the rows)
 //
@@ -193,7 +193,7 @@ template <int USE, int PLANES> struct Taker {
   float* turn;  // this warp's
   // kLogits, kGrad
   int e, next, src;  // the row's next entry, from this thread's first column on
-  float top = -INFINITY, sum = 0.0f, rl = 0.0f, rg = 0.0f;
+  float top = -INFINITY, rest = 0.0f, rl = 0.0f, rg = 0.0f;
   // kOut
   float* dst = nullptr;
   float scale = 1.0f;
@@ -248,7 +248,9 @@ template <int USE, int PLANES> struct Taker {
       for (int i = 4; i < 32; i++) m[i & 3] = fmaxf(m[i & 3], v[i]);
       const float above = fmaxf(top, fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3])));
       const float at = above == -INFINITY ? 0.0f : above;
-      sum *= ex2((top - at) * a.scale);
+      const float one = above > top ? 1.0f : 0.0f;  // the largest so far is among these
+      const float f = ex2((top - at) * a.scale);
+      rest = fmaf(rest, f, one * f);
       top = above;
       // The distance first: logits may be so large that a product's rounding is not small.
       f2_t s[4] = {};
@@ -258,7 +260,16 @@ template <int USE, int PLANES> struct Taker {
         s[i & 3] = f2_add(s[i & 3], f2_ex2(f2_mul(f2_add(f2_pack(v[2 * i], v[2 * i + 1]), off), scale)));
       float s0, s1;
       f2_unpack(f2_add(f2_add(s[0], s[1]), f2_add(s[2], s[3])), s0, s1);
-      sum += s0 + s1;
+      float here = s0 + s1 - one;
+      // Where it is nearly all of them, the others by themselves (there is no second one like it then): next to it they
+      // would lose up to 6 roundings of 2^-24, which is 6e-6 of a sum of 2^-4.  Forward of 8192 x 768 over 50000 words
+      // with three rows in five of that kind 307 -> 311 us, 333 x 256 over 5003 fp32 25.3 -> 26.9.
+      if (one > 0.0f && here < 0.0625f) {
+        here = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; i++) here += v[i] == at ? 0.0f : ex2((v[i] - at) * a.scale);
+      }
+      rest += here;
       while (next < word + 32) {
         a.zt[(long long)src * a.entries + e] = pick(v, next - word);
         advance();
@@ -398,7 +409,7 @@ template <int USE, int PLANES> struct Taker {
     if constexpr (USE == kLogits)
       if (row_ok)
         a.stats[(long long)((a.v0 + col0) / width) * a.ld_stats + row] =
-            make_float2(top, sum);
+            make_float2(top, rest);
   }
 };
 

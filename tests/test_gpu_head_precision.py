@@ -315,3 +315,36 @@ def test_bf16_logits_are_as_good_as_fp32_sums(T, V, additions, D):
     want = torch.cat([torch.logsumexp(p.to(f64) @ w.to(f64).t(), 1) for p in h.split(1024)])
     off = float((a.lse.to(f64) - want).norm() / want.norm())
     assert off < additions / 2 * 2.0 ** -25 + 3 * 2.0 ** -25, off
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+@pytest.mark.parametrize("T,V", [(1, 300), (2, 20011), (8, 3001), (40, 3001), (300, 20011)])
+@pytest.mark.parametrize("distil", [False, True])
+def test_a_loss_far_below_one(T, V, distil, io):
+    """A word that is all but certain, every other logit 18 to 32 below it, all exact: the loss, 4e-7 to 3e-5, is
+    the others' sum without the 1 beside it.  An exponential is good to 2^-22, its argument, up to 32 log2(e), to
+    two roundings; a term is scaled by at most 20 more of the former as sums are joined; and 64 additions."""
+    g = torch.Generator().manual_seed(T + V)
+    tau = 2.0 if distil else 1.0
+    h = torch.zeros(T, 16)
+    h[:, 0], h[:, 1] = 4 * tau, 1
+    y = torch.randint(V, (T,), generator=g)
+    w = torch.zeros(V, 16)
+    w[:, 0] = -torch.randint(72, 128, (V,), generator=g) / 16  # 4.5 .. 7.9
+    top = int(y[0])  # one word for all rows
+    w[top, 0] = 0
+    y[:] = top
+    z = (h.to(f64) @ w.to(f64).t() / tau).cuda()
+    assert torch.equal(h.bfloat16().float(), h) and torch.equal(w.bfloat16().float(), w)
+    others = z.clone()
+    others[:, top] = -float("inf")
+    want = torch.log1p(torch.exp(others - z[:, top, None]).sum(1))
+    h, w = h.to(DT[io]).cuda(), w.to(DT[io]).cuda()
+    if distil:
+        idx, t = y[:, None].cuda(), torch.zeros(T, 1, device="cuda")
+        got, want = head.ssm_head_distill_fwd(h, w, idx, t, temperature=tau).loss, tau * tau * want
+    else:
+        got = head.ssm_head_ce_fwd(h, w, y.cuda()).loss
+    limit = 21 * 2.0 ** -22 + 2 * 32 * 2.0 ** -24 + 64 * 2.0 ** -24
+    off = float(((got.to(f64) - want) / want).abs().max())
+    assert float(want.max()) < 1e-3 and off < limit, (off, limit)
