@@ -24,7 +24,7 @@
 //                                  kLogits        kGrad          kOut
 //   7370 x 768, 50000 words bf16   292  1940      2 x 164  1730  2 x 333  1700
 //   16384 x 1024, 32768 bf16       537  2050      2 x 298  1850  2 x 593  1850
-//   3891 x 768, 32768 bf16         114  1720      132      1480  220      1780
+//   3891 x 768, 32768 bf16         116  1690      132      1480  220      1780
 //   684 x 515, 10007 fp32           40  1030       50       850   87       970  (six products counted)
 //   300 x 256, 5003 fp32            14   330       18       260   18       510
 // G in two terms (SSM_HEAD_FINE_G): a stage for each, the smaller one first, with the other operand copied again;

@@ -39,7 +39,10 @@
  * (bf16: 2 in the forward, 4 in the backward; fp32: 8) are fp32 arithmetic throughout, G too, where they lie in the
  * shared memory of a block: rows (as a power of two) * cols up to 18000 in the forward, 9216 in the backward.
  * lse is an fp32 number, so that the backward's softmax is good to 2^-24 |lse| of its values: for logits over tau
- * of 16, 1e-6, which shows in d_h and d_W of fp32 where softmax and target are nearly alike.
+ * of 16, 1e-6, which shows in d_h and d_W of fp32 where softmax and target are nearly alike.  The forward carries the
+ * sum beside the largest exponential by itself: a loss near 0 is as good as its logits.
+ * An infinite h or W gives an infinite logit with bf16 operands and with a few rows, and NaN with more fp32 rows, whose
+ * terms of it have no one sign.
  */
 #ifndef SSM_HEAD_GB300_H
 #define SSM_HEAD_GB300_H
