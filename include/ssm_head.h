@@ -41,8 +41,8 @@
  * lse is an fp32 number, so that the backward's softmax is good to 2^-24 |lse| of its values: for logits over tau
  * of 16, 1e-6, which shows in d_h and d_W of fp32 where softmax and target are nearly alike.  The forward carries the
  * sum beside the largest exponential by itself: a loss near 0 is as good as its logits.
- * An infinite h or W gives an infinite logit with bf16 operands and with a few rows, and NaN with more fp32 rows, whose
- * terms of it have no one sign.
+ * An infinite weight gives infinite logits with bf16 operands and with a few rows, and NaN with more fp32 rows, whose
+ * lower terms may be 0 or of the other sign there.
  */
 #ifndef SSM_HEAD_GB300_H
 #define SSM_HEAD_GB300_H
