@@ -29,8 +29,8 @@ __device__ __forceinline__ float nan_() { return __uint_as_float(0x7fc00000u); }
 // ---- a teacher's entries ------------------------------------------------------------------------
 // A warp per row.  An entry's place in the order is the number of smaller keys, counted: a key is the word
 // and, behind it, the entry's number, so that no two are alike.  A logit's distance to the row's largest is
-// formed before it is divided by tau: t / tau of 7e6 (7 at 1e-6) would be good to half a unit.  4096 rows of 64 entries take 8 - 9 us (GB300), 333 of
-// 17 4.3, most of it a start, an end and the chain of one row.
+// formed before it is divided by tau: t / tau of 7e6 (7 at 1e-6) would be good to half a unit.  4096 rows of 64
+// entries take 8 - 9 us (GB300), 333 of 17 4.3, most of it a start, an end and the chain of one row.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) head_entries_kernel(const int64_t* t_idx, const T* t_logit,
                                                                 long long rows, int k, int vocab,
